@@ -31,10 +31,12 @@ ERR_SCALE = 8
 ERR_TIMEOUT = 16
 
 # cache formats by record width (bytes a token occupies): the packed MXFP8 records
-# (uint8 [pages, block, 528 | 584]) and the plain caches of 512 elements a row
-# (float8_e4m3fn [pages, block, 512] -> record 512; bfloat16 [...] -> record 1024)
-RECORDS = (528, 584, 512, 1024)
+# (uint8 [pages, block, 528 | 584]), the packed MXFP4 record (uint8 [pages, block, 272]) and
+# the plain caches of 512 elements a row (float8_e4m3fn [pages, block, 512] -> record 512;
+# bfloat16 [...] -> record 1024)
+RECORDS = (528, 584, 512, 1024, 272)
 PACKED = (528, 584)
+MXFP4 = 272
 HEAD_DIM = 512
 
 
@@ -148,6 +150,18 @@ def lib() -> ctypes.CDLL:
                 L.gkr_sparse_logits.argtypes = [vp, i32, vp, ctypes.POINTER(CacheDesc), vp, i64,
                                                 i64, ctypes.c_float, vp, vp, vp, opt, vp]
                 L.gkr_sparse_logits.restype = ctypes.c_int
+                # q, H, k_cache, desc, indices, stride, Q, topk, sm_scale, out, lse, weights,
+                # stride, workspace, bytes, err, opts, stream
+                L.gkr_sparse_attention.argtypes = [vp, i32, vp, ctypes.POINTER(CacheDesc), vp, i64,
+                                                   i64, i64, ctypes.c_float, vp, vp, vp, i64, vp,
+                                                   i64, vp, opt, vp]
+                L.gkr_sparse_attention.restype = ctypes.c_int
+                L.gkr_sparse_attention_workspace.argtypes = [i32, i64, i64, ctypes.POINTER(i64)]
+                L.gkr_sparse_attention_workspace.restype = ctypes.c_int
+                # indices, stride, weights, stride, rows, length, keep, recent, kept,
+                # kept_weights, evicted, opts, stream
+                L.gkr_kv_evict.argtypes = [vp, i64, vp, i64, i64, i64, i64, i64, vp, vp, vp, opt, vp]
+                L.gkr_kv_evict.restype = ctypes.c_int
                 L.gkr_status_string.argtypes, L.gkr_status_string.restype = [ctypes.c_int], \
                     ctypes.c_char_p
                 L.gkr_last_cuda_error.argtypes, L.gkr_last_cuda_error.restype = [], i32
@@ -248,7 +262,8 @@ def record_rows(record: int) -> tuple[int, int, int]:
 def alloc_cache(num_pages: int, block_size: int, record: int, device="cuda",
                 page_stride_bytes: int | None = None, fill: int | None = None) -> torch.Tensor:
     """Allocate a paged cache whose stride(0) is the page stride (padded to the
-    record's alignment): uint8 [num_pages, block_size, record] for the packed records
+    record's alignment): uint8 [num_pages, block_size, record] for the packed records 528,
+    584 and 272
     (inside a page the bytes are a data region then a scale region, not row by row),
     float8_e4m3fn [num_pages, block_size, 512] for record 512, bfloat16
     [num_pages, block_size, 512] for record 1024.  `fill` sets every byte."""
@@ -258,7 +273,7 @@ def alloc_cache(num_pages: int, block_size: int, record: int, device="cuda",
     flat = torch.empty(num_pages * ps, dtype=torch.uint8, device=device)
     if fill is not None:
         flat.fill_(fill)
-    if record in PACKED:
+    if record in PACKED or record == MXFP4:
         return torch.as_strided(flat, (num_pages, block_size, record), (ps, record, 1))
     dt, es = (torch.float8_e4m3fn, 1) if record == 512 else (torch.bfloat16, 2)
     if ps % es:
@@ -276,14 +291,14 @@ def cache_bytes(k_cache: torch.Tensor) -> torch.Tensor:
 
 def _cache_desc(k_cache: torch.Tensor) -> CacheDesc:
     """The record width is the format selector: uint8 [pages, block, 528 | 584] are
-    the packed MXFP8 records; float8_e4m3fn / bfloat16 [pages, block, 512] the plain
+    the packed MXFP8 records, [pages, block, 272] the MXFP4 record; float8_e4m3fn / bfloat16 [pages, block, 512] the plain
     caches (records 512 / 1024)."""
     if k_cache.dim() != 3:
         raise ValueError("k_cache must be a 3-D paged cache [num_pages, block_size, width]")
     P, bs, w = k_cache.shape
     if k_cache.dtype == torch.uint8:
-        if w not in PACKED:
-            raise ValueError(f"unsupported paged KV record width {w} (expected 528 or 584)")
+        if w not in PACKED and w != MXFP4:
+            raise ValueError(f"unsupported paged KV record width {w} (expected 528, 584 or 272)")
         rec, es = w, 1
     elif k_cache.dtype in (torch.float8_e4m3fn, torch.bfloat16):
         if w != HEAD_DIM:
@@ -360,7 +375,7 @@ def kv_insert(kv: torch.Tensor, k_cache: torch.Tensor, slot_mapping: torch.Tenso
               record: int | None = None, err_flag: torch.Tensor | None = None,
               fp8_scale: torch.Tensor | None = None,
               launch_opts: LaunchOpts | None = None) -> None:
-    """RoPE + MXFP8 quantise + paged insert, in place into k_cache.
+    """RoPE + MXFP8 (MXFP4) quantise + paged insert, in place into k_cache.
 
     kv             bf16 [tokens, 512], contiguous; not modified.
     k_cache        uint8 [num_pages, block_size, record] (stride(0) = page stride), or a
@@ -369,7 +384,7 @@ def kv_insert(kv: torch.Tensor, k_cache: torch.Tensor, slot_mapping: torch.Tenso
     positions      int64, contiguous, covering every kv row.
     cos_sin_cache  fp32 [max_pos, 64], contiguous (cos 0..31 | sin 0..31).
     block_size     must equal k_cache.size(1).
-    record         528 / 584, or None to take it from k_cache.size(2).
+    record         528 / 584 / 272, or None to take it from k_cache.size(2).
     err_flag       optional int32 device tensor; error bits are OR-ed into element 0.
     fp8_scale      float32 device tensor of one element: required for an fp8 cache
                    (stored codes are e4m3(x / scale)), None otherwise.
@@ -516,3 +531,123 @@ def sparse_logits(q: torch.Tensor, k_cache: torch.Tensor, indices: torch.Tensor,
                                      _ptr(err_flag), _opts(launch_opts), stream)
     _raise(st)
     return out
+
+
+def _rows(t: torch.Tensor, dtype: torch.dtype, name: str) -> int:
+    """Row stride of a 2-D tensor whose rows are contiguous (a slice of wider rows will do)."""
+    _check(t.dtype == dtype and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1)
+           and (t.stride(0) >= t.shape[1] or t.shape[0] <= 1),
+           f"{name} must be a 2-D {dtype} tensor with contiguous rows".replace("torch.", ""))
+    return max(int(t.stride(0)), int(t.shape[1]))
+
+
+def sparse_attention_workspace(num_heads: int, num_queries: int, topk: int,
+                               device=None) -> int:
+    """Bytes of workspace a sparse_attention call of these sizes needs on a device."""
+    n = ctypes.c_int64()
+    with torch.cuda.device(device):
+        _raise(lib().gkr_sparse_attention_workspace(num_heads, num_queries, topk, ctypes.byref(n)))
+    return int(n.value)
+
+
+def sparse_attention(q: torch.Tensor, k_cache: torch.Tensor, indices: torch.Tensor,
+                     sm_scale: float, out: torch.Tensor | None = None,
+                     lse: torch.Tensor | None = None, weights: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None,
+                     err_flag: torch.Tensor | None = None,
+                     launch_opts: LaunchOpts | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Sparse decode attention over an MXFP4 cache (uint8 [num_pages, block_size, 272]).
+
+    With K[k] the bf16 row kv_gather returns for indices[i, k], key and value of every head:
+    out[i, h] = softmax over k of (sm_scale * q[i, h] . K[k]) times K, lse[i, h] the log of the
+    softmax's sum.  An index of -1 (or outside the cache) is no entry; a query without
+    entries gets zeros and -inf.
+
+    q          bf16 [Q, H, 512], contiguous, H <= 128.
+    indices    int32 [Q, topk], rows contiguous (a slice of wider rows will do).
+    out        bf16 [Q, H, 512], contiguous, not overlapping q (allocated when None).
+    lse        fp32 [Q, H], contiguous (allocated when None).
+    weights    fp32 [Q, topk], rows contiguous, or None: the attention that each entry
+               received, summed over the heads, is added to it in place.
+    workspace  contiguous uint8 CUDA tensor of sparse_attention_workspace() bytes or more, for
+               this call alone while it runs (allocated when None).
+    Returns (out, lse)."""
+    desc = _cache_desc(k_cache)
+    _check(desc.record == MXFP4, "sparse_attention reads the MXFP4 records (272 bytes)")
+    _check(q.dtype == torch.bfloat16 and q.dim() == 3 and q.shape[2] == HEAD_DIM
+           and q.is_contiguous(), "q must be a contiguous bf16 tensor [queries, heads, 512]")
+    istride = _rows(indices, torch.int32, "indices")
+    _check(indices.shape[0] == q.shape[0], "indices must have a row for each query")
+    Q, H, K = int(q.shape[0]), int(q.shape[1]), int(indices.shape[1])
+    _check(1 <= H <= 128, "sparse_attention takes 1 to 128 heads")
+    if out is None:
+        out = torch.empty_like(q)
+    if lse is None:
+        lse = torch.empty(Q, H, dtype=torch.float32, device=q.device)
+    _check(out.dtype == torch.bfloat16 and out.is_contiguous() and out.shape == q.shape,
+           "out must be a contiguous bf16 tensor of q's shape")
+    _check(lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == (Q, H),
+           "lse must be a contiguous fp32 tensor [queries, heads]")
+    wstride = 0
+    if weights is not None:
+        wstride = _rows(weights, torch.float32, "weights")
+        _check(weights.shape == indices.shape, "weights must have the shape of indices")
+    _check_err_flag(err_flag)
+    dev = _same_cuda_device(q, k_cache, indices, out, lse, weights, err_flag, workspace)
+    with torch.cuda.device(dev):
+        if workspace is None:
+            need = sparse_attention_workspace(H, Q, K, dev)
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        _check(workspace.dtype == torch.uint8 and workspace.is_contiguous(),
+               "workspace must be a contiguous uint8 tensor")
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        st = lib().gkr_sparse_attention(_ptr(q), H, _ptr(k_cache), ctypes.byref(desc),
+                                        _ptr(indices), istride, Q, K, float(sm_scale), _ptr(out),
+                                        _ptr(lse), _ptr(weights), wstride, _ptr(workspace),
+                                        workspace.numel(), _ptr(err_flag), _opts(launch_opts),
+                                        stream)
+    _raise(st)
+    return out, lse
+
+
+def kv_evict(indices: torch.Tensor, weights: torch.Tensor, keep: int, recent: int = 0,
+             kept: torch.Tensor | None = None, kept_weights: torch.Tensor | None = None,
+             evicted: torch.Tensor | None = None, launch_opts: LaunchOpts | None = None
+             ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """The records that a budget keeps, by accumulated attention weight.
+
+    indices   int32 [B, L], rows contiguous: each sequence's slots, oldest first (negative:
+              an empty entry).
+    weights   fp32 [B, L], rows contiguous: what sparse_attention has added up for them.
+    keep      records kept of each sequence at most, 0 .. L.
+    recent    the newest live records, kept whatever their weight, 0 .. keep; of the others
+              the heaviest stay (the older where weights are equal; NaN counts as lightest).
+
+    Returns (kept int32 [B, keep], kept_weights fp32 [B, keep], evicted int64 [B, L - keep]),
+    each in the list's order, padded with -1 (0 for the weights); contiguous tensors passed in
+    are written instead of new ones.  `evicted` can be the slot_mapping of the next
+    kv_insert, which skips -1.  No record moves."""
+    istride = _rows(indices, torch.int32, "indices")
+    wstride = _rows(weights, torch.float32, "weights")
+    _check(weights.shape == indices.shape, "weights must have the shape of indices")
+    B, L = int(indices.shape[0]), int(indices.shape[1])
+    keep, recent = int(keep), int(recent)
+    _check(0 <= recent <= keep <= L, "kv_evict needs 0 <= recent <= keep <= indices.shape[1]")
+
+    def buffer(t, n, dtype, name):
+        if t is None:
+            return torch.empty(B, n, dtype=dtype, device=indices.device)
+        _check(t.dtype == dtype and t.is_contiguous() and tuple(t.shape) == (B, n),
+               f"{name} must be a contiguous {dtype} tensor [{B}, {n}]".replace("torch.", ""))
+        return t
+    kept = buffer(kept, keep, torch.int32, "kept")
+    kept_weights = buffer(kept_weights, keep, torch.float32, "kept_weights")
+    evicted = buffer(evicted, L - keep, torch.int64, "evicted")
+    dev = _same_cuda_device(indices, weights, kept, kept_weights, evicted)
+    with torch.cuda.device(dev):
+        stream = torch.cuda.current_stream(dev).cuda_stream
+        st = lib().gkr_kv_evict(_ptr(indices), istride, _ptr(weights), wstride, B, L, keep,
+                                recent, _ptr(kept), _ptr(kept_weights), _ptr(evicted),
+                                _opts(launch_opts), stream)
+    _raise(st)
+    return kept, kept_weights, evicted

@@ -15,6 +15,7 @@ std::atomic<int> g_pdl{1};
 std::atomic<int> g_early_metadata{0};
 constexpr int64_t kDefaultStagedMin = 24576;
 constexpr int64_t kDefaultStreamMin = 131072;
+constexpr int64_t kMaxRows = INT64_C(1) << 24;   // queries, list entries of a call at most
 constexpr int32_t kMaxQHeads = 4096;   // query heads per token (padded) at most
 std::atomic<int64_t> g_staged_min{kDefaultStagedMin};
 std::atomic<int64_t> g_stream_min{kDefaultStreamMin};
@@ -40,6 +41,8 @@ bool record_rows(int32_t record, RecordRows* r) {
     // caches keep 512 elements a row: fp8 e4m3 (512 B) or bf16 (1024 B), pages aligned
     // to 512 B ("PR #56441 [Perf][DSpark] KV-only context insertion across V4.1 cache
     // formats", section "实现拆解" item 1).
+    // MXFP4 (the library's own record): 256 B e2m1 + 16 UE8M0, pages aligned to 512 B.
+    if (record == 272) { *r = {256, 16, 512}; return true; }
     if (record == 528) { *r = {512, 16, 512}; return true; }
     if (record == 584) { *r = {576, 8, 576}; return true; }
     if (record == 512) { *r = {512, 0, 512}; return true; }
@@ -47,7 +50,9 @@ bool record_rows(int32_t record, RecordRows* r) {
     return false;
 }
 
-bool packed(int32_t record) { return record == 528 || record == 584; }
+bool packed(int32_t record) { return record == 528 || record == 584 || record == 272; }
+// The records of the pages' compressed writer.
+bool compressed(int32_t record) { return record == 528 || record == 584; }
 
 // Packed records need block_size % 32 == 0 (the page geometry of the pages); the
 // plain caches take any block_size >= 1.
@@ -224,6 +229,7 @@ cudaError_t launch_insert(int32_t record, const gkr::InsertParams& p, cudaStream
     switch (record) {
         case 528: return gkr::launch_insert_v41(p, stream);
         case 584: return gkr::launch_insert_v4(p, stream);
+        case 272: return gkr::launch_insert_mxfp4(p, stream);
         case 512: return gkr::launch_insert_fp8(p, stream);
         default: return gkr::launch_insert_bf16(p, stream);
     }
@@ -233,6 +239,7 @@ cudaError_t launch_gather(int32_t record, const gkr::GatherParams& p, cudaStream
     switch (record) {
         case 528: return gkr::launch_gather_v41(p, stream);
         case 584: return gkr::launch_gather_v4(p, stream);
+        case 272: return gkr::launch_gather_mxfp4(p, stream);
         case 512: return gkr::launch_gather_fp8(p, stream);
         default: return gkr::launch_gather_bf16(p, stream);
     }
@@ -263,7 +270,7 @@ GKR_API gkr_status gkr_rope_quant_insert(const void* kv, int64_t num_tokens, voi
                                          int32_t* err_flag, const gkr_launch_opts* opts,
                                          cudaStream_t stream) {
     if (compress_ratio < 1 || (sanitize_nans != 0 && sanitize_nans != 1)) return GKR_EINVAL;
-    if (cache != nullptr && !packed(cache->record)) return GKR_EUNSUPPORTED_RECORD;
+    if (cache != nullptr && !compressed(cache->record)) return GKR_EUNSUPPORTED_RECORD;
     gkr::InsertParams p;
     const gkr_status st = prepare_insert(kv, num_tokens, k_cache, cache, slot_mapping,
                                          positions, cos_sin_cache, max_pos, nullptr, err_flag,
@@ -360,6 +367,7 @@ GKR_API gkr_status gkr_sparse_logits(const void* q, int32_t num_heads, const voi
     RecordRows rows;
     gkr_status st = check_cache(cache, &rows);
     if (st != GKR_OK) return st;
+    if (cache->record == 272) return GKR_EUNSUPPORTED_RECORD;   // read by gkr_sparse_attention
     Policy pol;
     st = resolve_policy(opts, &pol);
     if (st != GKR_OK) return st;
@@ -395,13 +403,110 @@ GKR_API gkr_status gkr_sparse_logits(const void* q, int32_t num_heads, const voi
     return cuda_status(gkr::launch_sparse_logits(cache->record, p, stream));
 }
 
+GKR_API gkr_status gkr_sparse_attention_workspace(int32_t num_heads, int64_t num_queries,
+                                                  int64_t topk, int64_t* bytes) {
+    if (bytes == nullptr || num_heads < 1 || num_heads > gkr::kAttentionMaxHeads ||
+        num_queries < 0 || num_queries > kMaxRows || topk < 0 || topk > kMaxRows)
+        return GKR_EINVAL;
+    *bytes = 0;
+    if (num_queries == 0) return GKR_OK;
+    return cuda_status(gkr::attention_workspace(num_heads, num_queries, topk, bytes));
+}
+
+GKR_API gkr_status gkr_sparse_attention(const void* q, int32_t num_heads, const void* k_cache,
+                                        const gkr_cache_desc* cache, const int32_t* indices,
+                                        int64_t index_stride, int64_t num_queries, int64_t topk,
+                                        float sm_scale, void* out, float* lse, float* weights,
+                                        int64_t weight_stride, void* workspace,
+                                        int64_t workspace_bytes, int32_t* err_flag,
+                                        const gkr_launch_opts* opts, cudaStream_t stream) {
+    RecordRows rows;
+    gkr_status st = check_cache(cache, &rows);
+    if (st != GKR_OK) return st;
+    if (cache->record != 272) return GKR_EUNSUPPORTED_RECORD;
+    Policy pol;
+    st = resolve_policy(opts, &pol);
+    if (st != GKR_OK) return st;
+    if (num_queries < 0 || num_queries > kMaxRows || topk < 0 || topk > kMaxRows ||
+        num_heads < 1 || num_heads > gkr::kAttentionMaxHeads || index_stride < topk ||
+        (weights != nullptr && weight_stride < topk) ||
+        !(sm_scale >= -3.40282347e38f && sm_scale <= 3.40282347e38f))
+        return GKR_EINVAL;
+    if (num_queries == 0) return GKR_OK;
+    if (!q || !k_cache || !out || !lse || (topk > 0 && !indices)) return GKR_EINVAL;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(out, 16) || !aligned(indices, 4) ||
+        !aligned(lse, 4) || !aligned(weights, 4) || !aligned(err_flag, 4))
+        return GKR_EALIGN;
+    int64_t need = 0;
+    const cudaError_t e = gkr::attention_workspace(num_heads, num_queries, topk, &need);
+    if (e != cudaSuccess) return cuda_status(e);
+    if (workspace_bytes < need || (need > 0 && !workspace)) return GKR_EINVAL;
+    if (need > 0 && !aligned(workspace, 16)) return GKR_EALIGN;
+    gkr::AttentionParams p;
+    p.q = q;
+    p.num_heads = num_heads;
+    p.cache = static_cast<const uint8_t*>(k_cache);
+    p.page_stride = cache->page_stride;
+    p.block_size = cache->block_size;
+    p.num_slots = static_cast<int32_t>(cache->num_pages * cache->block_size);
+    p.indices = indices;
+    p.index_stride = index_stride;
+    p.num_queries = num_queries;
+    p.topk = topk;
+    p.sm_scale = sm_scale;
+    p.out = out;
+    p.lse = lse;
+    p.weights = weights;
+    p.weight_stride = weight_stride;
+    p.workspace = workspace;
+    p.err = err_flag;
+    p.pdl = pol.pdl;
+    return cuda_status(gkr::launch_sparse_attention(p, stream));
+}
+
+GKR_API gkr_status gkr_kv_evict(const int32_t* indices, int64_t index_stride,
+                                const float* weights, int64_t weight_stride, int64_t num_rows,
+                                int64_t length, int64_t keep, int64_t recent, int32_t* kept,
+                                float* kept_weights, int64_t* evicted,
+                                const gkr_launch_opts* opts, cudaStream_t stream) {
+    Policy pol;
+    const gkr_status st = resolve_policy(opts, &pol);
+    if (st != GKR_OK) return st;
+    if (num_rows < 0 || num_rows > kMaxRows || length < 0 || length > kMaxRows || keep < 0 ||
+        keep > length || recent < 0 || recent > keep || index_stride < length ||
+        weight_stride < length)
+        return GKR_EINVAL;
+    if (num_rows == 0 || length == 0) return GKR_OK;
+    if (!indices || !weights || (keep > 0 && (!kept || !kept_weights)) ||
+        (keep < length && !evicted))
+        return GKR_EINVAL;
+    if (!aligned(indices, 4) || !aligned(weights, 4) || !aligned(kept, 4) ||
+        !aligned(kept_weights, 4) || !aligned(evicted, 8))
+        return GKR_EALIGN;
+    gkr::EvictParams p;
+    p.indices = indices;
+    p.index_stride = index_stride;
+    p.weights = weights;
+    p.weight_stride = weight_stride;
+    p.rows = num_rows;
+    p.length = static_cast<int32_t>(length);
+    p.keep = static_cast<int32_t>(keep);
+    p.recent = static_cast<int32_t>(recent);
+    p.kept = kept;
+    p.kept_weights = kept_weights;
+    p.evicted = evicted;
+    p.pdl = pol.pdl;
+    return cuda_status(gkr::launch_evict(p, stream));
+}
+
 GKR_API const char* gkr_status_string(gkr_status status) {
     switch (status) {
         case GKR_OK: return "ok";
         case GKR_EINVAL: return "invalid argument";
         case GKR_EUNSUPPORTED_RECORD:
-            return "unsupported record width (expected 528 or 584, or 512 / 1024 for the fp8 "
-                   "and bf16 caches; the compressed insert writes 528 / 584 only)";
+            return "unsupported record width (expected 528 or 584, 512 / 1024 for the fp8 and "
+                   "bf16 caches, or 272 for MXFP4; the compressed insert writes 528 / 584 "
+                   "only, the sparse logits read all but 272, the sparse attention 272 only)";
         case GKR_EBAD_PAGE_GEOMETRY:
             return "bad page geometry (page_stride below block_size * record or not a "
                    "multiple of the record's page alignment: 576 for 584, else 512)";

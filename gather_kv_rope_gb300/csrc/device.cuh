@@ -140,6 +140,36 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
 
 // (quantise8, the MXFP8 block quantiser, follows the two-wide fp32 helpers below.)
 
+// UE8M0 scale byte of an MXFP4 block: clamp(ceil(log2(amax / 6)), -127, 127) + 127.  As for
+// ue8m0_byte with 6 = 1.5 * 2^2: amax / 6 = ((1 + M/2^23) / 1.5) * 2^(E-129), the ratio in
+// [0.66, 1.34), so the ceiling is E - 129 plus one exactly when M > 0x400000.
+__device__ __forceinline__ uint32_t ue8m0_byte_e2m1(float amax) {
+    const uint32_t b = __float_as_uint(amax);
+    const uint32_t E = b >> 23;                    // amax >= 0
+    const int e = int(E) - 2 + int((b & 0x7FFFFFu) > 0x400000u);
+    return E == 255u ? 254u : (e > 0 ? uint32_t(e) : 0u);
+}
+
+// MXFP4 encode: 8 values with their block's scale byte -> one word of 8 e2m1 codes.  Each
+// value times the exact power of two 2^(127 - byte), then the nearest-even cast (the scale
+// rule keeps every finite product within +-6; an infinity saturates).  The even dims go to
+// nibbles 0..3 and the odd ones to nibbles 4..7, so that one shift and mask of the word
+// yields a pair of neighbouring dims in the two halves of a register (dequant8_e2m1).
+__device__ __forceinline__ uint32_t quantise8_e2m1(const float* f, uint32_t byte) {
+    const float k = inv_scale(byte);
+    uint32_t w;
+    // e2m1x2: the first source goes to the upper nibble
+    asm("{\n .reg .b8 a, b, c, d;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 a, %3, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %7, %5;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 c, %4, %2;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %6;\n"
+        " mov.b32 %0, {a, b, c, d};\n}"
+        : "=r"(w)
+        : "f"(__fmul_rn(f[0], k)), "f"(__fmul_rn(f[1], k)), "f"(__fmul_rn(f[2], k)),
+          "f"(__fmul_rn(f[3], k)), "f"(__fmul_rn(f[4], k)), "f"(__fmul_rn(f[5], k)),
+          "f"(__fmul_rn(f[6], k)), "f"(__fmul_rn(f[7], k)));
+    return w;
+}
+
 // ---------------------------------------------------------------- MXFP8 decode
 
 // d = a * b on packed bf16x2, rounded to nearest even (subnormals kept).
@@ -233,6 +263,44 @@ __device__ __forceinline__ uint4 dequant8(const uint2 c, uint32_t byte) {
     uint4 o;
     dequant4(c.x, d, o.x, o.y);
     dequant4(c.y, d, o.z, o.w);
+    return o;
+}
+
+// ---------------------------------------------------------------- MXFP4 decode
+
+// An e2m1 code s.EE.M moved to bf16 bit positions s.000000EE.M000000 reads as
+// (1 + M/2) * 2^(E-127) (E >= 1) or M * 2^-127 (E = 0): in both cases the e2m1 value times
+// 2^-126.  One bf16 multiply by 2^(byte - 1) then gives e2m1 * 2^(byte - 127), exactly
+// (subnormals kept).  2^(byte - 1) is a normal bf16 for byte <= 128; above that the factor
+// is split into 2^127 and 2^(byte - 128).
+constexpr uint32_t kE2m1OneStepByte = 128u;
+
+__device__ __forceinline__ uint32_t e2m1_factor(uint32_t byte) {   // byte <= 128
+    return (byte + 126u) * 0x00800080u;
+}
+// Pair i of a word: dims 2i (low half) and 2i + 1 (high half), times 2^-126.
+template <int i>
+__device__ __forceinline__ uint32_t e2m1_pair(uint32_t w) {
+    constexpr int kSign = 12 - 4 * i, kMag = 6 - 4 * i;   // left shifts of the nibble's fields
+    const uint32_t mag = kMag >= 0 ? w << (kMag >= 0 ? kMag : 0) : w >> (kMag < 0 ? -kMag : 0);
+    return ((w << kSign) & 0x80008000u) | (mag & 0x01C001C0u);
+}
+__device__ __forceinline__ uint4 dequant8_e2m1_scaled(uint32_t w, uint32_t factor) {
+    return make_uint4(bf16x2_mul(e2m1_pair<0>(w), factor), bf16x2_mul(e2m1_pair<1>(w), factor),
+                      bf16x2_mul(e2m1_pair<2>(w), factor), bf16x2_mul(e2m1_pair<3>(w), factor));
+}
+// Any scale byte (255, the UE8M0 NaN: NaN).
+__device__ __forceinline__ uint4 dequant8_e2m1(uint32_t w, uint32_t byte) {
+    if (__builtin_expect(byte <= kE2m1OneStepByte, 1))
+        return dequant8_e2m1_scaled(w, e2m1_factor(byte));
+    const uint32_t n = kBf16NaN | (kBf16NaN << 16);
+    if (byte == 255u) return make_uint4(n, n, n, n);
+    uint4 o = dequant8_e2m1_scaled(w, 254u * 0x00800080u);
+    const uint32_t m2 = (byte - 1u) * 0x00800080u;
+    o.x = bf16x2_mul(o.x, m2);
+    o.y = bf16x2_mul(o.y, m2);
+    o.z = bf16x2_mul(o.z, m2);
+    o.w = bf16x2_mul(o.w, m2);
     return o;
 }
 

@@ -98,6 +98,30 @@ __device__ __forceinline__ void encode_store_v4(const TokenLoads& L, uint8_t* da
     }
 }
 
+// MXFP4: 16 blocks of 32 dims as for V4.1, e2m1 codes.  `da` = data row + 4L (chunk B's
+// word goes to da + 128); `sl` = scale row + L/4.
+__device__ __forceinline__ void encode_store_mxfp4(const TokenLoads& L, uint8_t* da, uint8_t* sl,
+                                                   int lane) {
+    float a[8], b[8];
+    unpack_bf16x8(L.a, a);
+    unpack_bf16x8(L.b, b);
+    if (lane >= 24) rope4(b, L.c, L.s);  // dims 448..511 = pairs 4(L-24) .. 4(L-24)+3
+
+    float ma = amax8(a), mb = amax8(b);
+    ma = fmaxf(ma, __shfl_xor_sync(kFull, ma, 1));
+    mb = fmaxf(mb, __shfl_xor_sync(kFull, mb, 1));
+    ma = fmaxf(ma, __shfl_xor_sync(kFull, ma, 2));
+    mb = fmaxf(mb, __shfl_xor_sync(kFull, mb, 2));
+    const uint32_t ba = ue8m0_byte_e2m1(ma), bb = ue8m0_byte_e2m1(mb);
+
+    *reinterpret_cast<uint32_t*>(da) = quantise8_e2m1(a, ba);
+    *reinterpret_cast<uint32_t*>(da + 128) = quantise8_e2m1(b, bb);
+    if ((lane & 3) == 0) {
+        sl[0] = static_cast<uint8_t>(ba);
+        sl[8] = static_cast<uint8_t>(bb);
+    }
+}
+
 // bf16 cache row (1024 B): the row with dims 448..511 rotated, rounded to bf16.  Lane L
 // owns bytes [16L, 16L+16) (chunk A, copied) and [512+16L, 512+16L+16) (chunk B,
 // rotated on lanes 24..31).  `da` = row + 16L.
@@ -163,6 +187,7 @@ __device__ __forceinline__ void encode_store(const TokenLoads& L, uint8_t* da, u
                                              int lane, Scale sc) {
     if constexpr (kRecord == 528) encode_store_v41<kSanitize, kPackedQ>(L, da, sl, lane);
     else if constexpr (kRecord == 584) encode_store_v4<kSanitize, kPackedQ>(L, da, sl, lane);
+    else if constexpr (kRecord == 272) encode_store_mxfp4(L, da, sl, lane);
     else if constexpr (kRecord == 1024) encode_store_bf16(L, da, lane);
     else encode_store_fp8(L, da, lane, sc);
 }
@@ -184,9 +209,9 @@ struct ScaleRows {
     static constexpr int kRows = S == 0 ? 0 : 128 / S;   // rows per 128-byte line
     static constexpr int kBytes = S == 0 ? 16 : 128;     // staging bytes per warp
 
-    // This lane's first byte within a scale row (block L/4 for V4.1, L/8 for V4).
+    // This lane's first byte within a scale row (block L/4 for V4.1 and MXFP4, L/8 for V4).
     __device__ __forceinline__ static int lane_byte(int lane) {
-        return kRecord == 528 ? (lane >> 2) : (lane >> 3);
+        return kRecord == 528 || kRecord == 272 ? (lane >> 2) : (lane >> 3);
     }
 
     // Staging row of batch row r, offset to this lane's first byte (block L/4 or L/8).

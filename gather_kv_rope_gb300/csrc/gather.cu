@@ -1,5 +1,6 @@
-// Dequantise-and-gather of paged KV records back to bf16 [N, 512] (also from the two
-// plain caches: bf16 rows are copied, fp8 e4m3 rows multiplied by the cache's scale).
+// Dequantise-and-gather of paged KV records back to bf16 [N, 512] (also from MXFP4 records,
+// e2m1 codes with one UE8M0 scale per 32 dims, and from the two plain caches: bf16 rows are
+// copied, fp8 e4m3 rows multiplied by the cache's scale).
 //
 // Operation (page "PR #56893 [DSv4.1] Store the whole KV in MXFP8 (FlashMLA V4.1
 // record)", section "实现拆解" item 4: the gather reads a record by its width and
@@ -87,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, kRecord == 584 ? 6 : 8)
     LaneBases lb;
     lb.a = p.cache + Fmt<kRecord>::kLaneBytes * lane;
     lb.tail = p.cache + 448 + 16 * (lane >= 24 ? lane - 24 : 0);
-    lb.s = p.cache + (kRecord == 528 ? (lane >> 2) : (lane >> 3));
+    lb.s = p.cache + (kRecord == 528 || kRecord == 272 ? (lane >> 2) : (lane >> 3));
     Loaded<kRecord> r[U];
 #pragma unroll
     for (int u = 0; u < U; ++u)
@@ -117,6 +118,9 @@ cudaError_t launch_gather_v41(const GatherParams& p, cudaStream_t stream) {
 }
 cudaError_t launch_gather_v4(const GatherParams& p, cudaStream_t stream) {
     return launch<584, kPerWarp>(p, stream);
+}
+cudaError_t launch_gather_mxfp4(const GatherParams& p, cudaStream_t stream) {
+    return launch<272, kPerWarp>(p, stream);
 }
 cudaError_t launch_gather_fp8(const GatherParams& p, cudaStream_t stream) {
     return launch<512, kPerWarp>(p, stream);

@@ -1,5 +1,6 @@
 // RoPE + MXFP8 quantise + paged KV insert (V4.1 528 B and legacy V4 584 B records),
-// and the same rotation into the two plain KV-only caches (bf16 rows; fp8 e4m3 rows
+// the same rotation and block scaling into MXFP4 records (272 B: e2m1 codes, one UE8M0 byte
+// per 32 dims), and the rotation into the two plain KV-only caches (bf16 rows; fp8 e4m3 rows
 // with one fp32 scale: page "PR #56441 [Perf][DSpark] KV-only context insertion
 // across V4.1 cache formats", section "实现拆解" item 1).
 //
@@ -594,6 +595,9 @@ cudaError_t launch_insert_v41(const InsertParams& p, cudaStream_t stream) {
 }
 cudaError_t launch_insert_v4(const InsertParams& p, cudaStream_t stream) {
     return launch<584>(p, stream);
+}
+cudaError_t launch_insert_mxfp4(const InsertParams& p, cudaStream_t stream) {
+    return launch<272>(p, stream);
 }
 cudaError_t launch_insert_fp8(const InsertParams& p, cudaStream_t stream) {
     return launch<512>(p, stream);

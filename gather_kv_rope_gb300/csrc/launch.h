@@ -73,7 +73,46 @@ struct LogitsParams {
     int32_t pdl;
 };
 
-// Row geometry of the four cache formats ("record" = bytes a token occupies):
+// Validated arguments of one sparse attention launch over MXFP4 records.
+struct AttentionParams {
+    const void* q;             // bf16 [num_queries, num_heads, 512]
+    int32_t num_heads;         // 1 .. kAttentionMaxHeads
+    const uint8_t* cache;
+    int64_t page_stride;
+    int32_t block_size;
+    int32_t num_slots;
+    const int32_t* indices;    // row i at indices + i * index_stride, topk entries
+    int64_t index_stride;
+    int64_t num_queries;
+    int64_t topk;              // may be 0 (every query empty)
+    float sm_scale;
+    void* out;                 // bf16 [num_queries, num_heads, 512]
+    float* lse;                // fp32 [num_queries, num_heads]
+    float* weights;            // nullable; row i at weights + i * weight_stride
+    int64_t weight_stride;
+    void* workspace;           // attention_workspace() bytes
+    int32_t* err;              // nullable
+    int32_t pdl;
+};
+
+// Validated arguments of one eviction launch.
+struct EvictParams {
+    const int32_t* indices;    // row r at indices + r * index_stride, `length` entries
+    int64_t index_stride;
+    const float* weights;      // row r at weights + r * weight_stride
+    int64_t weight_stride;
+    int64_t rows;
+    int32_t length;            // >= 1
+    int32_t keep;              // 0 .. length
+    int32_t recent;            // 0 .. keep
+    int32_t* kept;             // [rows, keep]
+    float* kept_weights;       // [rows, keep]
+    int64_t* evicted;          // [rows, length - keep]
+    int32_t pdl;
+};
+
+// Row geometry of the five cache formats ("record" = bytes a token occupies):
+//   272  MXFP4 record: 256 B e2m1 data row + 16 B scale row;
 //   528  V4.1 MXFP8 record: 512 B e4m3 data row + 16 B scale row;
 //   584  V4 record: 576 B data row (448 e4m3 + 64 bf16) + 8 B scale row;
 //   512  fp8 e4m3 row, one fp32 scale for the whole cache, no scale row;
@@ -82,10 +121,13 @@ struct LogitsParams {
 template <int kRecord>
 struct Fmt {
     static constexpr uint32_t D =
-        kRecord == 528 ? 512u : kRecord == 584 ? 576u : static_cast<uint32_t>(kRecord);
-    static constexpr uint32_t S = kRecord == 528 ? 16u : kRecord == 584 ? 8u : 0u;
-    // bytes of a row that lane L owns at 8L-dim granularity: 8 e4m3 or 16 bf16 bytes
-    static constexpr int kLaneBytes = kRecord == 1024 ? 16 : 8;
+        kRecord == 272 ? 256u
+                       : kRecord == 528 ? 512u
+                                        : kRecord == 584 ? 576u : static_cast<uint32_t>(kRecord);
+    static constexpr uint32_t S =
+        kRecord == 528 || kRecord == 272 ? 16u : kRecord == 584 ? 8u : 0u;
+    // bytes of a row that lane L owns at 8L-dim granularity: 4 e2m1, 8 e4m3 or 16 bf16 bytes
+    static constexpr int kLaneBytes = kRecord == 1024 ? 16 : kRecord == 272 ? 4 : 8;
     static constexpr bool kPacked = kRecord == 528 || kRecord == 584;
 };
 
@@ -172,6 +214,7 @@ __host__ __device__ inline WarpItems warp_items(const WorkMap& m, int64_t gw) {
 
 cudaError_t launch_insert_v41(const InsertParams& p, cudaStream_t stream);
 cudaError_t launch_insert_v4(const InsertParams& p, cudaStream_t stream);
+cudaError_t launch_insert_mxfp4(const InsertParams& p, cudaStream_t stream);
 cudaError_t launch_insert_fp8(const InsertParams& p, cudaStream_t stream);
 cudaError_t launch_insert_bf16(const InsertParams& p, cudaStream_t stream);
 // Compressed-KV insert: only group-boundary tokens are written; NaN -> 0 if sanitize.
@@ -180,15 +223,24 @@ cudaError_t launch_rope_quant_insert_v41(const InsertParams& p, bool sanitize,
 cudaError_t launch_rope_quant_insert_v4(const InsertParams& p, bool sanitize,
                                         cudaStream_t stream);
 // Query heads normed and rotated, padded heads zeroed, and the KV rows inserted (any of
-// the four cache formats), in one launch.
+// the five cache formats), in one launch.
 cudaError_t launch_qnorm_rope_kv_insert(int32_t record, const InsertParams& p,
                                         const QSideParams& qp, cudaStream_t stream);
 // Sparse decode logits from the cache records, gathered and dequantised on chip.
 cudaError_t launch_sparse_logits(int32_t record, const LogitsParams& p, cudaStream_t stream);
 int32_t logits_chunk_keys(int32_t record);   // keys per work item
 int32_t logits_max_heads();    // heads per query at most
+// Sparse decode attention over MXFP4 records, and the bytes of workspace it needs on the
+// current device.
+cudaError_t launch_sparse_attention(const AttentionParams& p, cudaStream_t stream);
+cudaError_t attention_workspace(int32_t num_heads, int64_t num_queries, int64_t topk,
+                                int64_t* bytes);
+constexpr int32_t kAttentionMaxHeads = 128;
+// The records each row keeps by weight, and the slots it frees.
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);
 cudaError_t launch_gather_v41(const GatherParams& p, cudaStream_t stream);
 cudaError_t launch_gather_v4(const GatherParams& p, cudaStream_t stream);
+cudaError_t launch_gather_mxfp4(const GatherParams& p, cudaStream_t stream);
 cudaError_t launch_gather_fp8(const GatherParams& p, cudaStream_t stream);
 cudaError_t launch_gather_bf16(const GatherParams& p, cudaStream_t stream);
 

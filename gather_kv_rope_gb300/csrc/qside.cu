@@ -335,6 +335,7 @@ cudaError_t launch_qnorm_rope_kv_insert(int32_t record, const InsertParams& p,
     switch (record) {
         case 528: return launch<528>(p, qp, stream);
         case 584: return launch<584>(p, qp, stream);
+        case 272: return launch<272>(p, qp, stream);
         case 512: return launch<512>(p, qp, stream);
         default: return launch<1024>(p, qp, stream);
     }

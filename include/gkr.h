@@ -12,7 +12,11 @@
  *                  rotated (bf16 out, padded heads zeroed) beside the KV insert, in one
  *                  launch;
  *   gkr_sparse_logits: the dequant-gather fused into its consumer: sparse decode
- *                  logits q . k over each query's top-k records, dequantised on chip.
+ *                  logits q . k over each query's top-k records, dequantised on chip;
+ *   gkr_sparse_attention: the whole of sparse decode attention over 4-bit (MXFP4)
+ *                  records: logits, softmax, value product, and on request the attention
+ *                  each record received;
+ *   gkr_kv_evict:  the records a budget keeps by that attention, and the slots it frees.
  *
  * Operations follow these passages (page title, section):
  *   "PR #56893 [DSv4.1] Store the whole KV in MXFP8 (FlashMLA V4.1 record)",
@@ -65,7 +69,8 @@ extern "C" {
 typedef enum gkr_status {
     GKR_OK = 0,
     GKR_EINVAL = 1,               /* null pointer, negative count, bad block size, ... */
-    GKR_EUNSUPPORTED_RECORD = 2,  /* record width not 528, 584, 512 or 1024             */
+    GKR_EUNSUPPORTED_RECORD = 2,  /* record width not 528, 584, 512, 1024 or 272, or one
+                                     that this call does not take                       */
     GKR_EBAD_PAGE_GEOMETRY = 3,   /* page stride too small or not a multiple of align   */
     GKR_EALIGN = 4,               /* a pointer is not aligned as documented             */
     GKR_ECUDA = 5                 /* the launch failed; see gkr_last_cuda_error()       */
@@ -93,9 +98,13 @@ typedef enum gkr_status {
  *   record 512 (fp8):  D = 512 e4m3 codes of x / scale, S = 0; the scale is one
  *                      fp32 for the whole cache, passed as fp8_scale; align 512.
  *   record 1024 (bf16): D = 1024 (512 little-endian bf16), S = 0; align 512.
+ *   record 272 (MXFP4, the library's own): D = 256 (e2m1 codes of dims 0..511), S = 16
+ *                      (one UE8M0 byte per 32-dim block); align 512.  The data row is 64
+ *                      little-endian words; word w holds dims 8w .. 8w + 7, the even ones
+ *                      in its nibbles 0..3 and the odd ones in its nibbles 4..7.
  * A slot s lives in page s / block_size, row s % block_size.
- * Requirements: record in {528, 584, 512, 1024}; block_size > 0, and a multiple
- * of 32 for 528 / 584; num_pages > 0; page_stride >= block_size * record and a
+ * Requirements: record in {528, 584, 512, 1024, 272}; block_size > 0, and a multiple
+ * of 32 for 528 / 584 / 272; num_pages > 0; page_stride >= block_size * record and a
  * multiple of the record's page alignment; num_pages * block_size < 2^31.
  */
 typedef struct gkr_cache_desc {
@@ -155,6 +164,9 @@ GKR_API gkr_status gkr_record_rows(int32_t record, int32_t *data_row_bytes,
  *     and each value is stored as e4m3(x / 2^(b - 127)), round to nearest even,
  *     saturating at +-448 (an infinite amax gives b = 254 and +-inf -> +-448);
  *   for 584 the rotated dims 448..511 are stored as bf16 (round to nearest even);
+ *   record 272 stores e2m1(x / 2^(b - 127)), round to nearest even, with
+ *     b = clamp(ceil(log2(amax / 6)), -127, 127) + 127 for each 32 dims (an infinite amax
+ *     gives b = 254 and +-inf -> +-6);
  *   record 1024 stores the rotated row as bf16 (dims 0..447 unchanged);
  *   record 512 stores e4m3(fl32(x / *fp8_scale)) for all 512 dims (one IEEE fp32
  *     division, then the saturating nearest-even cast).
@@ -278,8 +290,9 @@ GKR_API gkr_status gkr_qnorm_rope_kv_insert(const void *q_in, int32_t num_heads,
  *     528: out[i, d] = bf16(e4m3(data[d]) * 2^(scale[d / 32] - 127));
  *     584: d < 448 as above with scale[d / 64]; d >= 448 copies the stored bf16.
  *     1024: out[i, :] = the stored bf16 row;
- *     512: out[i, d] = bf16(fl32(e4m3(data[d]) * *fp8_scale)).
- *   For 528 / 584 the product is exact in fp32 and rounded once to bf16 (nearest
+ *     512: out[i, d] = bf16(fl32(e4m3(data[d]) * *fp8_scale));
+ *     272: out[i, d] = bf16(e2m1(code d) * 2^(scale[d / 32] - 127)).
+ *   For 528 / 584 / 272 the product is exact in fp32 and rounded once to bf16 (nearest
  *   even, subnormals kept).  An e4m3 NaN code (0x7F / 0xFF) or scale byte 255 (the
  *   UE8M0 NaN) yields the bf16 NaN 0x7FC0.
  *
@@ -305,8 +318,8 @@ GKR_API gkr_status gkr_kv_gather(const void *k_cache, const gkr_cache_desc *cach
  * marking an invalid entry, and FP8 entries are dequantised to bf16 for the matrix
  * product).  For query i, head h < num_heads and entry k < topk:
  *   out[i, h, k] = fl32(sm_scale * sum_d q[i, h, d] * K[d])
- * where K = the bf16 row gkr_kv_gather returns for indices[i, k] (any of the four
- * records); indices[i, k] == -1 gives -inf, an index < -1 or past the cache gives -inf
+ * where K = the bf16 row gkr_kv_gather returns for indices[i, k] (any record but 272,
+ * which gkr_sparse_attention reads: GKR_EUNSUPPORTED_RECORD); indices[i, k] == -1 gives -inf, an index < -1 or past the cache gives -inf
  * and sets GKR_ERR_INDEX; an fp8 cache whose scale is not a positive finite number gives
  * -inf everywhere and GKR_ERR_SCALE.  The gathered rows stay on chip (shared memory) and
  * the products run on the tensor cores (bf16 x bf16, fp32 accumulation over the 512
@@ -330,6 +343,80 @@ GKR_API gkr_status gkr_sparse_logits(const void *q, int32_t num_heads, const voi
                                      int64_t num_queries, int64_t topk, float sm_scale,
                                      const float *fp8_scale, float *out, int32_t *err_flag,
                                      const gkr_launch_opts *opts, cudaStream_t stream);
+
+/*
+ * sparse_attention: sparse decode attention over an MXFP4 cache (FlashMLA overview page,
+ * DSA section: a decode query attends to the cache entries its index row lists, -1 marking
+ * an invalid one, entries dequantised to bf16 for the matrix products; the latent row is key
+ * and value of every head).  For query i, head h < num_heads, entry k < topk, with K[k]
+ * the bf16 row gkr_kv_gather returns for indices[i, k]:
+ *   s[k] = sm_scale * q[i, h] . K[k];
+ *   lse[i, h] = log(sum over the valid k of exp(s[k]));
+ *   out[i, h, :] = bf16(sum over the valid k of exp(s[k] - lse[i, h]) * K[k, :]);
+ *   with weights: weights[i, k] += sum over h of exp(s[k] - lse[i, h]) for the valid k.
+ * An index of -1 is no entry; one < -1 or past the cache is none either and sets
+ * GKR_ERR_INDEX.  A query without a valid entry gets zeros and lse -inf; weights of
+ * invalid entries are not touched.  Entries may repeat; each counts.
+ * Arithmetic: bf16 products with fp32 sums, fp32 softmax statistics; the probabilities are
+ * rounded to bf16 (relative to a running maximum) for the value product.  Results do not
+ * depend on the order of execution: every sum has a fixed order.
+ *
+ * q               device, bf16 [num_queries, num_heads, 512] row-major, 16-byte aligned.
+ * num_heads       1 .. 128.
+ * k_cache         device, the cache described by *cache (record 272 only), 16-byte aligned.
+ * indices         device, int32; row i starts at indices + i * index_stride (index_stride
+ *                 >= topk).
+ * num_queries     0 .. 2^24 (0 enqueues nothing); topk 0 .. 2^24 (0: every query is empty).
+ * sm_scale        finite.
+ * out             device, bf16 [num_queries, num_heads, 512], 16-byte aligned; not
+ *                 overlapping any input.
+ * lse             device, fp32 [num_queries, num_heads].
+ * weights         device, fp32, row i at weights + i * weight_stride (weight_stride >=
+ *                 topk), added to in place; or NULL.
+ * workspace       device, at least gkr_sparse_attention_workspace() bytes, 16-byte aligned
+ *                 (may be NULL when that is 0); its contents need no preparation.  Calls
+ *                 that may run at the same time need one each.
+ * workspace_bytes its size.
+ * err_flag        device int32 or NULL; GKR_ERR_INDEX / GKR_ERR_TIMEOUT.
+ * opts, stream    as for the other entry points.
+ */
+GKR_API gkr_status gkr_sparse_attention(const void *q, int32_t num_heads, const void *k_cache,
+                                        const gkr_cache_desc *cache, const int32_t *indices,
+                                        int64_t index_stride, int64_t num_queries, int64_t topk,
+                                        float sm_scale, void *out, float *lse, float *weights,
+                                        int64_t weight_stride, void *workspace,
+                                        int64_t workspace_bytes, int32_t *err_flag,
+                                        const gkr_launch_opts *opts, cudaStream_t stream);
+
+/* Workspace of a gkr_sparse_attention call of these sizes on the current device. */
+GKR_API gkr_status gkr_sparse_attention_workspace(int32_t num_heads, int64_t num_queries,
+                                                  int64_t topk, int64_t *bytes);
+
+/*
+ * kv_evict: which records of each sequence a budget keeps, by the attention they have
+ * received (an extension of the library; the pages have no counterpart).  Row r is one
+ * sequence's list, oldest first: entry p holds the slot indices[r, p] (negative: empty) and
+ * weights[r, p].  Of the live entries the last `recent` are kept, and of the others those
+ * with the largest weights (the lowest p where weights are equal) until `keep` are kept in
+ * all.  A NaN weight ranks below every number; -0 ranks with 0.
+ *   kept[r, :]          the kept slots in the row's order, then -1;
+ *   kept_weights[r, :]  their weights, then 0;
+ *   evicted[r, :]       the other live slots in the row's order, then -1 (int64: usable as
+ *                       the slot_mapping of an insert, which skips -1).
+ * No record moves: slots are the unit of allocation, and a freed one can be written next.
+ *
+ * indices, weights       device; rows at index_stride / weight_stride elements (>= length).
+ * num_rows, length       0 .. 2^24 each (0 of either enqueues nothing).
+ * keep, recent           0 <= recent <= keep <= length.
+ * kept, kept_weights     device, int32 / fp32 [num_rows, keep] (may be NULL when keep is 0).
+ * evicted                device, int64 [num_rows, length - keep] (may be NULL when empty).
+ * The outputs overlap no input.
+ */
+GKR_API gkr_status gkr_kv_evict(const int32_t *indices, int64_t index_stride,
+                                const float *weights, int64_t weight_stride, int64_t num_rows,
+                                int64_t length, int64_t keep, int64_t recent, int32_t *kept,
+                                float *kept_weights, int64_t *evicted,
+                                const gkr_launch_opts *opts, cudaStream_t stream);
 
 /*
  * Process-wide defaults of the launch options (gkr_launch_opts fields left at -1 take
@@ -391,7 +478,8 @@ GKR_API int32_t gkr_last_cuda_error(void);
  * gkr_set_early_metadata / gkr_get_early_metadata.  3.0.0: every launching entry point
  * takes a gkr_launch_opts pointer before the stream; gkr_qnorm_rope_kv_insert.
  * 3.1.0: gkr_sparse_logits.  3.2.0: gkr_qnorm_rope_kv_insert takes q_scale (an e4m3
- * query output). */
+ * query output).  Record 272, gkr_sparse_attention and gkr_kv_evict were added to 3.2.0
+ * without a change to any call it had; their symbols tell a library that has them. */
 GKR_API int32_t gkr_version(void);
 
 #ifdef __cplusplus
