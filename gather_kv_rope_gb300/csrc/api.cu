@@ -432,6 +432,8 @@ GKR_API gkr_status gkr_sparse_attention(const void* q, int32_t num_heads, const 
         (weights != nullptr && weight_stride < topk) ||
         !(sm_scale >= -3.40282347e38f && sm_scale <= 3.40282347e38f))
         return GKR_EINVAL;
+    // runs of chunks (64 entries) are counted in 32 bits
+    if (num_queries * ((topk + 63) / 64) > INT64_C(0x7FFFFFFF)) return GKR_EINVAL;
     if (num_queries == 0) return GKR_OK;
     if (!q || !k_cache || !out || !lse || (topk > 0 && !indices)) return GKR_EINVAL;
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(out, 16) || !aligned(indices, 4) ||

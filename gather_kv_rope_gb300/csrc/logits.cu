@@ -36,11 +36,9 @@
 // Every wait on an mbarrier sleeps in try_wait (a suspend hint, so waiting warps take no
 // issue slots) and is bounded (20 ms of %globaltimer): past it the CTA sets
 // GKR_ERR_TIMEOUT, stops waiting, still frees its tensor memory and returns.
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include "device.cuh"
 #include "launch.h"
+#include "tensor.cuh"
 
 namespace gkr {
 
@@ -61,7 +59,6 @@ constexpr int kMmaWarp = kProducerWarps + kEpilogueWarps;   // warp 20: tcgen05.
                                                             // allocates and frees TMEM too
 constexpr int kKeysPerWarp = kN / kProducerWarps;           // keys of a group per producer
 constexpr int kLogitThreads = (kMmaWarp + 1) * 32;          // 21 warps: up to 80 registers
-constexpr int kRowBytes = 128;           // one swizzle row: 64 bf16 of K
 constexpr int kBBytes = kN * kHalfK * 2; // 32 KB per stage
 constexpr uint32_t kTmemCols = 512;      // accumulators at columns 0 and 128, A at 256
 constexpr uint32_t kACol = 2 * kChunk;   // A: 512 bf16 a row, two to a column
@@ -71,8 +68,6 @@ constexpr int kTileBytes = kEpilogueWarps * kTileWarpBytes;
 constexpr int kWindow = 32 / kKeysPerWarp;  // groups whose indices one register holds
 constexpr int kSmemLimit = 227 * 1024;   // shared memory a CTA may use
 constexpr int32_t kErrIndex = 4;
-constexpr int32_t kErrTimeout = 16;
-constexpr uint64_t kWaitNs = 20000000;    // a wait gives up after 20 ms (a normal one takes us)
 
 // A producer warp's ring of raw records: kSlots groups of kKeysPerWarp records, each as
 // the cache holds it (data row, then scale row) at a 16-byte aligned stride; as many
@@ -101,130 +96,12 @@ static_assert(Raw<528>::slots >= 3 && Raw<584>::slots >= 3 && Raw<512>::slots >=
               "a ring of at least one group; one validity bit per ring record; whole "
               "groups per index window");
 
-// ------------------------------------------------------------- tcgen05 / mbarrier PTX
-
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_init_fence() {
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-}
-// True once the phase with the given parity has completed.  A thread whose phase is not
-// complete is suspended until it completes or kSuspendNs have passed: a waiting warp then
-// takes no issue slots from the warps that work (spinning without the hint cost ~2 % of
-// the sparse logits).
-constexpr uint32_t kSuspendNs = 20000;
-__device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p;\n"
-        " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(bar), "r"(parity), "r"(kSuspendNs)
-        : "memory");
-    return done != 0u;
-}
-__device__ __forceinline__ uint64_t global_ns() {
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-// Wait for the phase with the given parity to complete; false once kWaitNs have passed.
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
-    while (!mbar_try_wait(bar, parity))
-        if (global_ns() - t0 > kWaitNs) return false;
-    return true;
-}
-__device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem),
-                 "r"(ncols)
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_relinquish() {
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
-                 : "memory");
-}
-__device__ __forceinline__ void tc_fence_before_sync() {
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after_sync() {
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-// Make this thread's shared-memory stores visible to the tensor cores (async proxy).
-__device__ __forceinline__ void fence_async_smem() {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-// D[tmem] (+)= A[tmem] * B[smem]^T, bf16 inputs, fp32 accumulator; one thread.  A sits in
-// tensor memory with row i in lane i and its K values two to a 32-bit column (the lower
-// half holds the even k), so the K = 16 of one instruction span 8 columns.
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                            uint32_t idesc, uint32_t accumulate) {
-    asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-// Arrive on the mbarrier once every tcgen05 operation this thread issued has completed.
-__device__ __forceinline__ void mma_commit(uint32_t bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                     bar)
-                 : "memory");
-}
-// 16 consecutive fp32 accumulator columns of this thread's lane.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-        "%11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-// 16 consecutive 32-bit columns of this thread's lane (tcgen05.wait::st before handing
-// them to the tensor cores).
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint4 (&v)[4]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-        "%11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-        "r"(v[0].x), "r"(v[0].y), "r"(v[0].z), "r"(v[0].w), "r"(v[1].x), "r"(v[1].y),
-        "r"(v[1].z), "r"(v[1].w), "r"(v[2].x), "r"(v[2].y), "r"(v[2].z), "r"(v[2].w),
-        "r"(v[3].x), "r"(v[3].y), "r"(v[3].z), "r"(v[3].w)
-        : "memory");
-}
-__device__ __forceinline__ void tmem_st_wait() {
-    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
 // Instruction descriptor of kind::f16: fp32 accumulator (bits 4-5 = 1), bf16 A and B
 // (bits 7-9, 10-12 = 1), both K-major (bits 15, 16 = 0), N >> 3 at bits 17-22, M >> 4 at
 // bits 24-28.
 constexpr uint32_t kIdesc = (1u << 4) | (1u << 7) | (1u << 10) |
                             (static_cast<uint32_t>(kN >> 3) << 17) |
                             (static_cast<uint32_t>(kM >> 4) << 24);
-
-// Shared-memory matrix descriptor of the K-major B operand with the 128-byte swizzle: start
-// address >> 4 (bits 0-13), leading offset (unused by this layout; 1) at bits 16-29,
-// stride between 8-row groups (1024 bytes) >> 4 at bits 32-45, descriptor version 1 at
-// bits 46-47, swizzle mode 128B (2) at bits 61-63.  The operand's rows are 128 bytes (64
-// bf16 of K); row r of an 8-row group sits at r * 128 in its 1024-byte group, and its
-// 16-byte piece c at position c ^ r.
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
-    return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1) << 16) |
-           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) |
-           (static_cast<uint64_t>(2) << 61);
-}
 
 // Byte offset of the 16-byte piece holding dims [8c, 8c+8) of K block kb (dims 64kb..) of
 // row r in an operand of `rows` rows: K blocks of rows x 128 bytes, 8-row swizzle groups.
@@ -251,34 +128,6 @@ struct alignas(8) Barriers {
     uint32_t tmem_base;
     int32_t timed_out;
 };
-
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-    asm volatile(
-        "{\n .reg .b64 state;\n mbarrier.arrive.shared::cta.b64 state, [%0];\n}\n" ::"r"(bar)
-        : "memory");
-}
-
-// A wait that records a timeout instead of hanging: after the first failure the thread
-// stops waiting (its results are discarded, see GKR_ERR_TIMEOUT).
-__device__ __forceinline__ void wait_or_flag(uint32_t bar, uint32_t parity, bool& ok) {
-    if (ok) ok = mbar_wait(bar, parity);
-}
-
-// The same for a whole warp: lane 0 waits, the warp follows it (__syncwarp orders the
-// lanes' later accesses after lane 0's acquire); every lane gets the outcome.
-__device__ __forceinline__ void warp_wait_or_flag(uint32_t bar, uint32_t parity, bool& ok,
-                                                  int lane) {
-    if (lane == 0) wait_or_flag(bar, parity, ok);
-    ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
-    __syncwarp();
-}
-
-// One arrival for a whole warp: every lane's earlier shared-memory writes (each lane has
-// fenced them for the async proxy) are ordered before lane 0's arrive by __syncwarp.
-__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar);
-}
 
 __device__ __forceinline__ void prefetch_l2(const void* p) {
     asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
@@ -688,21 +537,6 @@ __global__ void __launch_bounds__(kLogitThreads, 1)
     __syncthreads();
     if (threadIdx.x == 0 && bars->timed_out != 0) report(p.err, kErrTimeout);
     if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
-}
-
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no link to the driver
-// library); null when the driver does not provide it.
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-    static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                             &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess)
-            f = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-    }();
-    return fn;
 }
 
 // The logits [num_queries, num_heads, topk] fp32 as a 3-D tensor map with 32 x 32 x 1 boxes

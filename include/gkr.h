@@ -366,7 +366,8 @@ GKR_API gkr_status gkr_sparse_logits(const void *q, int32_t num_heads, const voi
  * k_cache         device, the cache described by *cache (record 272 only), 16-byte aligned.
  * indices         device, int32; row i starts at indices + i * index_stride (index_stride
  *                 >= topk).
- * num_queries     0 .. 2^24 (0 enqueues nothing); topk 0 .. 2^24 (0: every query is empty).
+ * num_queries     0 .. 2^24 (0 enqueues nothing); topk 0 .. 2^24 (0: every query is empty);
+ *                 num_queries * ceil(topk / 64) < 2^31.
  * sm_scale        finite.
  * out             device, bf16 [num_queries, num_heads, 512], 16-byte aligned; not
  *                 overlapping any input.

@@ -100,6 +100,7 @@ def test_attention_refusals(gkr):
     assert attend(gkr, d, Q=0, q=None, cache=None, idx=None, out=None, lse=None) == 0
     for bad in (dict(H=0), dict(H=129), dict(Q=-1), dict(Q=(1 << 24) + 1), dict(topk=-1),
                 dict(topk=(1 << 24) + 1, istride=1 << 25), dict(istride=63),
+                dict(Q=1 << 24, topk=1 << 20, istride=1 << 20),
                 dict(weights=A, wstride=63), dict(scale=float("inf")), dict(scale=float("nan")),
                 dict(q=None), dict(cache=None), dict(idx=None), dict(out=None), dict(lse=None),
                 dict(opts=gkr.LaunchOpts())):
