@@ -424,6 +424,9 @@ GKR_API gkr_status gkr_sparse_attention(const void* q, int32_t num_heads, const 
     gkr_status st = check_cache(cache, &rows);
     if (st != GKR_OK) return st;
     if (cache->record != 272) return GKR_EUNSUPPORTED_RECORD;
+    // rows of 256 bytes are counted in 32 bits
+    if ((cache->page_stride >> 8) > INT64_C(0x7FFFFFFF) / cache->num_pages)
+        return GKR_EBAD_PAGE_GEOMETRY;
     Policy pol;
     st = resolve_policy(opts, &pol);
     if (st != GKR_OK) return st;

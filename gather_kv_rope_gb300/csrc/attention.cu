@@ -48,20 +48,30 @@ constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kPairHeads = 64;           // heads (rows) of each CTA of the pair
 constexpr int kChunkKeys = 64;           // records per chunk
 constexpr int kOwnKeys = 32;             // of which a CTA dequantises this many in full
-constexpr int kStages = 4;               // chunks in flight
+constexpr int kStages = 3;               // chunks of dequantised records in flight
+constexpr int kRawStages = 3;            // chunks of raw records in flight
 constexpr int kSoftmaxWarps = 4;         // warps 0..3: warp w owns tensor-memory lanes 32w ..
-constexpr int kProducerWarps = 8;        // warps 4..11: gather and dequantise
-constexpr int kMmaWarp = kSoftmaxWarps + kProducerWarps;    // warp 12: products (rank 0)
-constexpr int kLoadWarp = kMmaWarp + 1;                     // warp 13: query tiles
-constexpr int kAttendThreads = (kLoadWarp + 1) * 32;
+constexpr int kOwnWarps = 8;             // dequantise the CTA's own records for q . K
+constexpr int kRefillWarps = 4;          // dequantise the other CTA's records for p . K
+constexpr int kFirstOwn = kSoftmaxWarps;
+constexpr int kFirstRefill = kFirstOwn + kOwnWarps;
+constexpr int kMmaWarp = kFirstRefill + kRefillWarps;       // products (rank 0)
+constexpr int kGatherWarps = 3;          // raw records: own in two halves, the others' half
+constexpr int kFirstGather = kMmaWarp + 1;
+constexpr int kIndexRing = 8;            // chunks of indices (kept as many) a gather warp holds,
+constexpr int kIndexAhead = 6;           // and has on their way
+constexpr int kAttendThreads = (kFirstGather + kGatherWarps) * 32;   // 20 warps: up to 96 registers
 constexpr uint32_t kBlockBytes = kOwnKeys * kRowBytes;      // 64 dims of the stage's 32 rows
 constexpr uint32_t kHalfBytes = 4 * kBlockBytes;            // 256 dims
 constexpr uint32_t kStageBytes = 2 * kHalfBytes;
 constexpr uint32_t kQBlockBytes = kPairHeads * kRowBytes;   // 64 dims of the query tile
-constexpr uint32_t kQBytes = 8 * kQBlockBytes;
+constexpr int kQTmemBlocks = 6;          // blocks of 64 dims of the query in tensor memory
+constexpr uint32_t kQBytes = (8 - kQTmemBlocks) * kQBlockBytes;   // and in shared memory
 constexpr uint32_t kPBytes = kPairHeads * kRowBytes;        // probabilities of a chunk, bf16
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 256;          // logits: two buffers of 32 columns; output at 0
+constexpr uint32_t kQCol = 320;          // the query's first 384 dims, two to a column
+static_assert(kQCol + kQTmemBlocks * 32 <= kTmemCols, "tensor memory");
 // A new maximum replaces the running one only when it is this much larger (in powers of two):
 // probabilities then stay below 2^8, and the accumulator is rarely rescaled.
 constexpr float kLag = 8.0f;
@@ -86,85 +96,130 @@ struct Cut {
     int64_t total;
     int32_t pairs;
     __host__ __device__ int64_t begin(int64_t g) const { return total * g / pairs; }
-    __host__ __device__ int64_t owner(int64_t chunk) const { return ((chunk + 1) * pairs - 1) / total; }
 };
 
 // Shared memory of a CTA, from a 1024-byte boundary.
-constexpr uint32_t kOffStages = kQBytes;
+constexpr uint32_t kOffNext = kQBytes;                      // the next query's first blocks
+constexpr uint32_t kOffStages = kOffNext + kQTmemBlocks * kQBlockBytes;
 constexpr uint32_t kOffP = kOffStages + kStages * kStageBytes;
-constexpr uint32_t kOffMax = kOffP + 2 * kPBytes;           // [2][128] row maxima
+constexpr uint32_t kOffRaw = kOffP + 2 * kPBytes;
+// raw stage: the codes of the 32 own records in two blocks of 32 rows of 128 bytes (one for each
+// half of the dims), those of the other CTA's 32 records in this CTA's half in a third, all with
+// the 128-byte swizzle (eight rows' pieces lie in different banks); then the scale rows
+constexpr uint32_t kRawBlock = kOwnKeys * 128;
+constexpr uint32_t kRawOth = 2 * kRawBlock;
+constexpr uint32_t kRawOwnScales = kRawOth + kRawBlock;
+constexpr uint32_t kRawOthScales = kRawOwnScales + kOwnKeys * 16;
+constexpr uint32_t kRawBytes = kRawOthScales + kOwnKeys * 16;
+constexpr uint32_t kOffMax = kOffRaw + kRawStages * kRawBytes;   // [2][128] row maxima
 constexpr uint32_t kOffSum = kOffMax + 2 * 128 * 4;         // [128] row sums
-constexpr uint32_t kOffBars = kOffSum + 128 * 4;
+constexpr uint32_t kOffIndex = kOffSum + 128 * 4;           // [gather warp][kIndexRing][32]
+constexpr uint32_t kOffLive = kOffIndex + kGatherWarps * kIndexRing * 128;   // [kIndexRing][CTA] masks
+constexpr uint32_t kOffBars = kOffLive + kIndexRing * 2 * 4;
+static_assert(kRawStages + kStages + 1 < kIndexRing && kIndexAhead < kIndexRing,
+              "the softmax reads a chunk's masks before they are replaced");
 
 struct alignas(8) PairBarriers {
     // in the leader: arrivals of both CTAs
-    uint64_t full_k[kStages];    // producers: the chunk's records are in place for q . K
-    uint64_t full_v[kStages];    // producers: ... and for p . K
+    uint64_t full_k[kStages];    // own warps: the chunk's records are in place for q . K
+    uint64_t full_v[kStages];    // refill warps: ... and for p . K
     uint64_t p_full[2];          // softmax: the logits are read, the probabilities written
-    uint64_t q_full;             // the query tiles have arrived
+    uint64_t q_full;             // softmax: a query is in place for q . K
     // in each CTA
+    uint64_t q_next;             // the next query's first blocks are in shared memory
+    uint64_t q_live;             // this query's last blocks are
+    uint64_t raw_own[kRawStages], raw_own_empty[kRawStages];   // raw records: landed, read
+    uint64_t raw_oth[kRawStages], raw_oth_empty[kRawStages];
     uint64_t s_full[2];          // products: the logits of a chunk are complete
     uint64_t stage_empty[kStages];   // products: p . K has read the stage
     uint64_t o_done[2];          // products: p . K of a chunk is complete
-    uint64_t q_free;             // products: q . K of a query's last chunk is complete
-    uint64_t q_tma;              // this CTA's query tile has arrived
     uint32_t tmem_base;
     int32_t timed_out;
 };
 constexpr size_t kAttendSmem = 1024 + kOffBars + sizeof(PairBarriers);
 static_assert(kAttendSmem <= 227 * 1024, "a CTA's shared memory");
 
+// 2^x within 2^-22; results below 2^-126 kept (factors that rescale what may be large) ...
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// ... or, in one instruction, flushed to zero (a probability: kLift puts those below 2^-142).
+__device__ __forceinline__ float exp2_flush(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 
-// One lane's part of a record: 32 dims, their scale byte.
-struct Unit {
-    uint4 codes;
-    uint32_t scale;
+__device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+                 "r"(v.w)
+                 : "memory");
+}
+
+__device__ __forceinline__ uint4 lds16_at(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// A stage of a ring and the parity of its current round.
+template <int N>
+struct Ring {
+    int s = 0;
+    uint32_t parity = 0;
+    __device__ __forceinline__ void next() {
+        if (++s == N) {
+            s = 0;
+            parity ^= 1u;
+        }
+    }
 };
 
-// Unit u of the record in slot idx; zeros (the value 0) for an entry that is none.
-__device__ __forceinline__ Unit load_unit(const AttentionParams& p, const uint8_t* base,
-                                          int32_t row, int u) {
-    Unit r;
-    r.codes = make_uint4(0u, 0u, 0u, 0u);
-    r.scale = 0u;
-    if (base != nullptr) {
-        r.codes = ldg_na16(base + row * 256 + u * 16);
-        r.scale = ldg_u8(base + static_cast<int64_t>(p.block_size) * 256 + row * 16 + u);
-    }
-    return r;
-}
-// The page (null: no entry) and row of slot idx.
-__device__ __forceinline__ const uint8_t* record_page(const AttentionParams& p, int32_t idx,
-                                                      int32_t& row) {
-    row = 0;
-    if (idx < 0 || idx >= p.num_slots) return nullptr;
-    uint32_t page, r;
-    page_row(static_cast<uint32_t>(idx), static_cast<uint32_t>(p.block_size), page, r);
-    row = static_cast<int32_t>(r);
-    return p.cache + static_cast<int64_t>(page) * p.page_stride;
-}
-// The unit's 32 bf16 values into row r of a block of 64 dims: 16-byte pieces c0 .. c0 + 3.
-__device__ __forceinline__ void store_unit(uint8_t* block, int r, int c0, const Unit& t) {
-    uint8_t* const row = block + (r >> 3) * 1024 + (r & 7) * kRowBytes;
-    const uint32_t w[4] = {t.codes.x, t.codes.y, t.codes.z, t.codes.w};
-    if (__builtin_expect(t.scale <= kE2m1OneStepByte, 1)) {
-        const uint32_t f = e2m1_factor(t.scale);
+// The rare scales (above 2, or the NaN), out of the way of the common path.
+__device__ __noinline__ void store_unit_far(uint32_t out, uint4 codes, uint32_t scale) {
+    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            st16(row + (((c0 + j) ^ (r & 7)) << 4), dequant8_e2m1_scaled(w[j], f));
+    for (int j = 0; j < 4; ++j) sts16(out ^ (j << 4), dequant8_e2m1(w[j], scale));
+}
+// A unit's 32 dims (16 bytes of codes, a scale byte) as bf16 into four 16-byte pieces of a
+// swizzled row: piece j of the unit lies at the first one's address with j in bits 4 and 5
+// flipped.
+__device__ __forceinline__ void store_unit(uint32_t codes, uint32_t scale, uint32_t out) {
+    const uint4 c = lds16_at(codes);
+    uint32_t s;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(s) : "r"(scale) : "memory");
+    if (__builtin_expect(s <= kE2m1OneStepByte, 1)) {
+        const uint32_t f = e2m1_factor(s);
+        sts16(out, dequant8_e2m1_scaled(c.x, f));
+        sts16(out ^ 16u, dequant8_e2m1_scaled(c.y, f));
+        sts16(out ^ 32u, dequant8_e2m1_scaled(c.z, f));
+        sts16(out ^ 48u, dequant8_e2m1_scaled(c.w, f));
     } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            st16(row + (((c0 + j) ^ (r & 7)) << 4), dequant8_e2m1(w[j], t.scale));
+        store_unit_far(out, c, s);
     }
 }
 
-// Eight fp32 values, scaled, as bf16.
+// Named barriers of the warps of one role: one thread waits on the mbarriers, the others here,
+// where a waiting warp takes no issue slots.  Instruction supply bounds a kernel of so many roles
+// before anything else does: with every warp polling for itself and each role's loop unrolled
+// in full, the warps ran 11200 instructions a chunk and missed the instruction cache on 17 % of
+// its requests.  So the waits are few, the loops short, and roles that do the same share
+// their code.  The waiting threads sit in warps on other schedulers than the one that
+// issues the products.
+constexpr int kPollThread = 32;   // of the softmax warps
+constexpr int kOwnBar = 1, kRefillBar = 2, kSoftmaxBar = 3, kHeadsBar = 4;   // and 5
+__device__ __forceinline__ void group_sync(int bar, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
+}
+
+// Eight fp32 values as bf16, and scaled.
+__device__ __forceinline__ uint4 pack8(const float* v) {
+    return make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]),
+                      pack_bf16x2_rn(v[4], v[5]), pack_bf16x2_rn(v[6], v[7]));
+}
 __device__ __forceinline__ uint4 pack8(const float* v, float f) {
     return make_uint4(pack_bf16x2_rn(__fmul_rn(v[0], f), __fmul_rn(v[1], f)),
                       pack_bf16x2_rn(__fmul_rn(v[2], f), __fmul_rn(v[3], f)),
@@ -172,8 +227,27 @@ __device__ __forceinline__ uint4 pack8(const float* v, float f) {
                       pack_bf16x2_rn(__fmul_rn(v[6], f), __fmul_rn(v[7], f)));
 }
 
+// Row `row` of a query tile (blocks of 64 rows of 64 dims, 128-byte swizzle) into this thread's
+// lane of tensor memory at `dst`.  A is read by the tensor cores from both halves of the lanes,
+// each of which produces half of the columns, so both hold every row.
+__device__ __forceinline__ void query_to_tmem(uint32_t tile, int row, uint32_t dst) {
+    const uint32_t src = tile + row * kRowBytes + ((row & 7) << 4);
+#pragma unroll 1
+    for (int b = 0; b < kQTmemBlocks; ++b) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {   // 32 dims
+            uint4 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = lds16_at((src ^ ((4 * h + i) << 4)) + b * kQBlockBytes);
+            tmem_st16(dst + 32 * b + 16 * h, v);
+        }
+    }
+    tmem_st_wait();
+}
+
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
-    attend_kernel(const AttentionParams p, const Cut cut, const __grid_constant__ CUtensorMap q_map) {
+    attend_kernel(const AttentionParams p, const Cut cut, const __grid_constant__ CUtensorMap q_map,
+                  const __grid_constant__ CUtensorMap cache_map) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -191,18 +265,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(smem_addr(&bars->full_k[s]), 2 * kProducerWarps);
-            mbar_init(smem_addr(&bars->full_v[s]), 2 * kProducerWarps);
+            mbar_init(smem_addr(&bars->full_k[s]), 2 * kOwnWarps);
+            mbar_init(smem_addr(&bars->full_v[s]), 2 * kRefillWarps);
             mbar_init(smem_addr(&bars->stage_empty[s]), 1);
+        }
+        for (int s = 0; s < kRawStages; ++s) {
+            mbar_init(smem_addr(&bars->raw_own[s]), 2 + 32);   // two halves, the scales' copies
+            mbar_init(smem_addr(&bars->raw_oth[s]), 1 + 32);
+            mbar_init(smem_addr(&bars->raw_own_empty[s]), kOwnWarps);
+            mbar_init(smem_addr(&bars->raw_oth_empty[s]), kRefillWarps);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(smem_addr(&bars->p_full[b]), 2 * kSoftmaxWarps);
             mbar_init(smem_addr(&bars->s_full[b]), 1);
             mbar_init(smem_addr(&bars->o_done[b]), 1);
         }
-        mbar_init(smem_addr(&bars->q_full), 2);
-        mbar_init(smem_addr(&bars->q_free), 1);
-        mbar_init(smem_addr(&bars->q_tma), 1);
+        mbar_init(smem_addr(&bars->q_full), 2 * kSoftmaxWarps);
+        mbar_init(smem_addr(&bars->q_next), 1);
+        mbar_init(smem_addr(&bars->q_live), 1);
         bars->timed_out = 0;
         mbar_init_fence();
     }
@@ -212,181 +292,222 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     __syncthreads();
     cluster_sync();   // the other CTA's barriers exist
     tc_fence_after_sync();
-    const uint32_t tmem = bars->tmem_base;
-    bool ok = true;
+    // All 512 columns are this CTA's, so they begin at address 0: a constant, which keeps the
+    // products' addresses in uniform registers.
+    constexpr uint32_t tmem = 0;
+    bool ok = bars->tmem_base == 0;
 
     // chunk j of this pair: query and chunk within it, counted
     int64_t qi = c0 / cut.per_query;
     int64_t ci = c0 - qi * cut.per_query;
 
-    if (warp >= kSoftmaxWarps && warp < kMmaWarp) {
-        // ------------------------------------------------------------- producers
-        // A lane handles one of the CTA's 32 records (row r) and one of the other CTA's (row r
-        // too): two units of the first, one of the second.  Eight lanes of a store have eight
-        // rows of one swizzle group, so their pieces fall into different banks; the four
-        // lanes of a record read 64 contiguous bytes.
-        const int pw = warp - kSoftmaxWarps;
-        const int r = (pw & 3) * 8 + (lane & 7);
-        const int u_own = (pw >> 2) * 8 + (lane >> 3);                      // and + 4
-        const int u_oth = static_cast<int>(rank) * 8 + (pw >> 2) * 4 + (lane >> 3);
-        const int k_own = static_cast<int>(rank) * kOwnKeys + r;
-        const int k_oth = (1 - static_cast<int>(rank)) * kOwnKeys + r;
-        // blocks of 64 dims hold two units
-        const uint32_t own_a = (u_own >> 1) * kBlockBytes, own_b = own_a + 2 * kBlockBytes;
-        const int c_own = (u_own & 1) * 4, c_oth = (u_oth & 1) * 4;
-        // the half of the stage whose dims the other CTA multiplies
-        const uint32_t oth = (rank == 0 ? kHalfBytes : 0u) +
-                             ((u_oth - static_cast<int>(rank) * 8) >> 1) * kBlockBytes;
-        const uint32_t full_k = map_rank(smem_addr(&bars->full_k[0]), 0);
-        const uint32_t full_v = map_rank(smem_addr(&bars->full_v[0]), 0);
-
-        // indices of chunk j, the records of chunks j - 1 and j - 2 on their way
-        int32_t i_own = -1, i_oth = -1, i_oth2 = -1;
-        int j_idx = 0;
-        auto next_indices = [&]() {
-            i_oth2 = i_oth;
-            i_own = i_oth = -1;
-            if (j_idx < n) {
-                const int32_t* const row = p.indices + qi * p.index_stride;
-                const int64_t k = ci * kChunkKeys;
-                if (k + k_own < p.topk) i_own = __ldg(row + k + k_own);
-                if (k + k_oth < p.topk) i_oth = __ldg(row + k + k_oth);
-                if (++ci == cut.per_query) {
-                    ci = 0;
-                    ++qi;
-                }
-            }
-            ++j_idx;
-        };
-        Unit a, b, o;         // being stored: chunk j + 1's own units, chunk j's other
-        Unit na, nb, no;      // on their way: one chunk later
-        auto load_own = [&](int32_t idx) {
-            int32_t row;
-            const uint8_t* const base = record_page(p, idx, row);
-            na = load_unit(p, base, row, u_own);
-            nb = load_unit(p, base, row, u_own + 4);
-        };
-        auto load_oth = [&](int32_t idx) {
-            int32_t row;
-            const uint8_t* const base = record_page(p, idx, row);
-            no = load_unit(p, base, row, u_oth);
-        };
-        next_indices();       // chunk 0
-        load_own(i_own);
-        a = na;
-        b = nb;
-        next_indices();       // chunk 1
-        o = Unit{};
+    if (warp >= kFirstOwn && warp < kMmaWarp) {
+        // ------------------------------------------------------------- dequantisation
+        // Eight warps put the CTA's own records, in full, into a stage for q . K; four replace
+        // the half of it whose dims the other CTA multiplies by the other records' half.  Both
+        // run the same instructions (see kOwnBar).  A lane takes two units of 32 dims of record
+        // r.  Eight lanes have eight rows of one swizzle group, so what they load and what
+        // they store lies in different banks.
+        const bool own = warp < kFirstRefill;
+        const int w = own ? warp - kFirstOwn : warp - kFirstRefill;
+        const int r = (w & 3) * 8 + (lane & 7);
+        const int u = (w >> 2) * 8 + (lane >> 3);           // and + 4: two blocks of 64 dims on
+        const uint32_t src = (own ? (w >> 2) * kRawBlock : kRawOth) + r * 128 +
+                             (((lane >> 3) ^ (r & 7)) << 4);
+        const uint32_t src_s = (own ? kRawOwnScales : kRawOthScales + rank * 8) + r * 16 + u;
+        const uint32_t dst = kOffStages + (own || rank != 0 ? 0u : kHalfBytes) +
+                             (u >> 1) * kBlockBytes + r * kRowBytes + (((u & 1) * 4 ^ (r & 7)) << 4);
+        const uint32_t full = map_rank(smem_addr(own ? &bars->full_k[0] : &bars->full_v[0]), 0);
+        const uint32_t raw_full = smem_addr(own ? &bars->raw_own[0] : &bars->raw_oth[0]);
+        const uint32_t raw_empty = smem_addr(own ? &bars->raw_own_empty[0] : &bars->raw_oth_empty[0]);
+        const uint32_t raw0 = smem_addr(smem + kOffRaw);
+        const uint32_t out0 = smem_addr(smem) + dst;
+        const int bar = own ? kOwnBar : kRefillBar, threads = own ? kOwnWarps * 32 : kRefillWarps * 32;
+        Ring<kStages> st;
+        Ring<kRawStages> rw;
 #pragma unroll 1
-        for (int j = -1; j < n; ++j) {
-            load_own(i_own);                       // chunk j + 2
-            load_oth(i_oth2);                      // chunk j + 1
-            next_indices();                        // chunk j + 3
-            if (j + 1 < n) {
-                const int s = (j + 1) & (kStages - 1);
-                if (j + 1 >= kStages)
-                    warp_wait_or_flag(smem_addr(&bars->stage_empty[s]),
-                                      (((j + 1) / kStages) - 1) & 1, ok, lane);
-                uint8_t* const st = smem + kOffStages + s * kStageBytes;
-                store_unit(st + own_a, r, c_own, a);
-                store_unit(st + own_b, r, c_own, b);
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(full_k + 8 * s);
+        for (int j = 0; j < n; ++j) {
+            if (w == (own ? 2 : 3) && lane == 0) {
+                wait_quiet(raw_full + 8 * rw.s, rw.parity, ok);
+                // the stage is free; q . K has read what is replaced
+                if (!own || j >= kStages)
+                    wait_quiet(own ? smem_addr(&bars->stage_empty[st.s]) : smem_addr(&bars->s_full[j & 1]),
+                               own ? st.parity ^ 1u : (j >> 1) & 1, ok);
             }
-            if (j >= 0) {
-                const int s = j & (kStages - 1);
-                warp_wait_or_flag(smem_addr(&bars->s_full[j & 1]), (j >> 1) & 1, ok, lane);
-                store_unit(smem + kOffStages + s * kStageBytes + oth, r, c_oth, o);
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(full_v + 8 * s);
+            group_sync(bar, threads);
+            const uint32_t raw = raw0 + rw.s * kRawBytes, out = out0 + st.s * kStageBytes;
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h)
+                store_unit(raw + (src ^ (h << 6)), raw + src_s + 4 * h, out + h * 2 * kBlockBytes);
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(raw_empty + 8 * rw.s);
+                mbar_arrive_cluster(full + 8 * st.s);
             }
-            a = na;
-            b = nb;
-            o = no;
+            st.next();
+            rw.next();
         }
-    } else if (warp == kLoadWarp) {
-        // ------------------------------------------------------------- query tiles
-        if (lane == 0) {
-            uint32_t loads = 0;
-            for (int j = 0; j < n; ++j) {
-                if (j == 0 || ci == 0) {
-                    // the tile may go once the last chunk of the query before is multiplied
-                    if (j > 0) wait_or_flag(smem_addr(&bars->q_free), (loads - 1) & 1, ok);
-                    const uint32_t bar = smem_addr(&bars->q_tma);
-                    if (ok) {
-                        mbar_expect_tx(bar, kQBytes);
-                        for (int kb = 0; kb < 8; ++kb)
-                            tma_load_3d(smem_addr(smem) + kb * kQBlockBytes, &q_map, bar, 64 * kb,
-                                        static_cast<int32_t>(rank) * kPairHeads,
-                                        static_cast<int32_t>(qi));
-                        wait_or_flag(bar, loads & 1, ok);
-                    }
-                    ++loads;
-                    mbar_arrive_cluster(map_rank(smem_addr(&bars->q_full), 0));
-                }
+    } else if (warp >= kFirstGather) {
+        // ------------------------------------------------------------- raw records
+        // Three warps run this: one for each half of the own records' dims, one for this CTA's
+        // half of the others'.  The indices come into a ring in shared memory six chunks ahead
+        // (a global load takes more than a chunk's time), lane i decodes record i of the
+        // chunk's 32, eight lanes have the copy engine gather four half-rows each, and every
+        // lane copies its record's 16 scale bytes.  An entry that is none gets scale bytes
+        // 0 and whatever codes slot 0 has: finite values, which the softmax masks.
+        const int g = warp - kFirstGather;
+        const bool own = g < 2;
+        const uint32_t cta = own ? rank : 1u - rank;        // whose records
+        const int key = static_cast<int>(cta) * kOwnKeys + lane;
+        const uint32_t full = smem_addr(own ? &bars->raw_own[0] : &bars->raw_oth[0]);
+        const uint32_t empty = smem_addr(own ? &bars->raw_own_empty[0] : &bars->raw_oth_empty[0]);
+        const uint32_t raw0 = smem_addr(smem + kOffRaw);
+        const int32_t x = static_cast<int32_t>(own ? g : rank) * 128;
+        const uint32_t dst = g * kRawBlock + lane * 512;    // lane < 8: rows 4 lane .. + 3
+        const uint32_t scale_dst = (own ? kRawOwnScales : kRawOthScales) + 16 * lane;
+        const uint32_t ring = smem_addr(smem + kOffIndex) + g * kIndexRing * 128 + 4 * lane;
+        int ahead = 0;                                      // the next chunk to fetch indices of
+        auto fetch = [&]() {
+            if (ahead < n) {
+                const uint32_t to = ring + (ahead & (kIndexRing - 1)) * 128;
+                const int64_t k = ci * kChunkKeys + key;
+                if (k < p.topk) cp_async4(to, p.indices + qi * p.index_stride + k);
+                else asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(-1) : "memory");
                 if (++ci == cut.per_query) {
                     ci = 0;
                     ++qi;
                 }
+                ++ahead;
             }
+            cp_async_commit();
+        };
+#pragma unroll 1
+        for (int i = 0; i < kIndexAhead; ++i) fetch();
+        bool bad = false;
+        Ring<kRawStages> rw;
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+            cp_async_wait<kIndexAhead - 1>();               // chunk j's indices are here
+            int32_t idx;
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(idx) : "r"(ring + (j & (kIndexRing - 1)) * 128) : "memory");
+            const bool is = idx >= 0 && idx < p.num_slots;
+            bad |= !is && idx != -1;
+            const uint32_t live = __ballot_sync(kFull, is);
+            uint32_t page, r;
+            page_row(is ? static_cast<uint32_t>(idx) : 0u, static_cast<uint32_t>(p.block_size), page, r);
+            const int64_t at = static_cast<int64_t>(page) * p.page_stride;
+            const int32_t row = static_cast<int32_t>(at >> 8) + static_cast<int32_t>(r);
+            int32_t r4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) r4[i] = __shfl_sync(kFull, row, (4 * lane + i) & 31);
+            if (lane == 0 && j >= kRawStages) wait_quiet(empty + 8 * rw.s, rw.parity ^ 1u, ok);
+            __syncwarp();
+            const uint32_t raw = raw0 + rw.s * kRawBytes, bar = full + 8 * rw.s;
+            if (g != 1) {
+                if (lane == 0)
+                    reinterpret_cast<uint32_t*>(smem + kOffLive)[(j & (kIndexRing - 1)) * 2 + cta] = live;
+                cp_async16_or_zeros(raw + scale_dst,
+                                    p.cache + at + static_cast<int64_t>(p.block_size) * 256 + r * 16u, is);
+                cp_async_arrive(bar);
+            }
+            if (lane == 0) mbar_expect_tx(bar, kRawBlock);
+            __syncwarp();
+            if (lane < 8) tma_gather4(raw + dst, &cache_map, bar, x, r4[0], r4[1], r4[2], r4[3]);
+            fetch();
+            rw.next();
         }
+        if (g != 1 && rank == 0 && __any_sync(kFull, bad) && lane == 0) report(p.err, kErrIndex);
+        // the copies in flight land before the CTA leaves: the dequantising warps wait for them,
+        // and where they have given up, this does
+        cp_async_wait<0>();
+        for (int j = n > kRawStages ? n - kRawStages : 0; j < n; ++j)
+            if (lane == 0) wait_quiet(full + 8 * (j % kRawStages), (j / kRawStages) & 1, ok);
         __syncwarp();
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------- products
-        if (lane == 0 && rank == 0) {
+        // The whole warp runs this, one lane issues (elect_lane).
+        if (rank == 0) {
+            const uint32_t elected = elect_lane();
             const uint64_t q_desc = sw128_desc(smem_addr(smem));
+            const uint64_t k_desc0 = sw128_desc(smem_addr(smem + kOffStages));
+            const uint64_t v_desc0 = sw128_mn_desc(smem_addr(smem + kOffStages), kBlockBytes);
+            const uint64_t p_desc0 = sw128_desc(smem_addr(smem + kOffP));
             uint32_t loads = 0;
-            bool first = true;    // chunk j - 1 opens its query in this pair
-            auto output = [&](int j, bool fresh) {
-                const int s = j & (kStages - 1);
-                wait_or_flag_cluster(smem_addr(&bars->full_v[s]), (j / kStages) & 1, ok);
-                wait_or_flag_cluster(smem_addr(&bars->p_full[j & 1]), (j >> 1) & 1, ok);
-                tc_fence_after_sync();
-                const uint64_t a = sw128_desc(smem_addr(smem + kOffP + (j & 1) * kPBytes));
-                const uint64_t b = sw128_mn_desc(smem_addr(smem + kOffStages + s * kStageBytes),
-                                                 kBlockBytes);
+            Ring<kStages> sk, sv;
+            // q . K runs one chunk ahead of p . K within a query; jq, jo: their next chunks,
+            // ci and co: those within the query
+            int64_t co = ci;
+            bool fresh = true;    // chunk jo opens its query in this pair
+            int jq = 0, jo = 0;
+#pragma unroll 1
+            while (jo < n) {
+                const bool opens = jq == 0 || ci == 0;
+                if (jq < n && jq - jo < 2 && !(opens && jo < jq)) {
+                    if (opens) {
+                        wait_quiet(smem_addr(&bars->q_full), loads & 1, ok);
+                        ++loads;
+                    }
+                    wait_quiet(smem_addr(&bars->full_k[sk.s]), sk.parity, ok);
+                    __syncwarp();
+                    tc_fence_after_sync();
+                    const uint32_t d = tmem + kSCol + 32 * (jq & 1);
+                    uint64_t a = q_desc, b = k_desc0 + sk.s * (kStageBytes >> 4);
+                    uint32_t at = tmem + kQCol;
+#pragma unroll 1
+                    for (int kb = 0; kb < kQTmemBlocks; ++kb) {       // 64 dims
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {        // 16 records
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16_ts_pair(d, at + 8 * k, b + 2 * k, kIdescS, k != 0 ? 1u : kb, elected);
+                        at += 32;
+                        b += kBlockBytes >> 4;
+                    }
+#pragma unroll 1
+                    for (int kb = kQTmemBlocks; kb < 8; ++kb) {
 #pragma unroll
-                    for (int d = 0; d < 2; ++d) {    // 128 of each CTA's 256 dims
-                        const uint32_t off = (k >> 1) * kHalfBytes + (k & 1) * 2048 + d * 2 * kBlockBytes;
-                        mma_bf16_ss_pair(tmem + 128 * d, a + 2 * k, b + (off >> 4), kIdescO,
-                                         (fresh && k == 0) ? 0u : 1u);
+                        for (int k = 0; k < 4; ++k)
+                            mma_bf16_ss_pair(d, a + 2 * k, b + 2 * k, kIdescS, 1u, elected);
+                        a += kQBlockBytes >> 4;
+                        b += kBlockBytes >> 4;
+                    }
+                    mma_commit_pair(smem_addr(&bars->s_full[jq & 1]), elected);
+                    if (++ci == cut.per_query) ci = 0;
+                    sk.next();
+                    ++jq;
+                } else {
+                    wait_quiet(smem_addr(&bars->full_v[sv.s]), sv.parity, ok);
+                    wait_quiet(smem_addr(&bars->p_full[jo & 1]), (jo >> 1) & 1, ok);
+                    __syncwarp();
+                    tc_fence_after_sync();
+                    uint64_t a = p_desc0 + (jo & 1) * (kPBytes >> 4);
+                    uint64_t b = v_desc0 + sv.s * (kStageBytes >> 4);
+                    uint32_t acc = fresh ? 0u : 1u;
+#pragma unroll 1
+                    for (int k = 0; k < 2; ++k) {        // records of CTA k, 16 at a time
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)  // 128 of each CTA's 256 dims
+                                mma_bf16_ss_pair(tmem + 128 * h, a + 2 * i,
+                                                 b + ((i * 2048 + h * 2 * kBlockBytes) >> 4), kIdescO,
+                                                 i != 0 ? 1u : acc, elected);
+                        }
+                        a += 4;
+                        b += kHalfBytes >> 4;
+                        acc = 1u;
+                    }
+                    mma_commit_pair(smem_addr(&bars->stage_empty[sv.s]), elected);
+                    mma_commit_pair(smem_addr(&bars->o_done[jo & 1]), elected);
+                    sv.next();
+                    ++jo;
+                    fresh = false;
+                    if (++co == cut.per_query) {
+                        co = 0;
+                        fresh = true;
                     }
                 }
-                mma_commit_pair(smem_addr(&bars->stage_empty[s]));
-                mma_commit_pair(smem_addr(&bars->o_done[j & 1]));
-            };
-            for (int j = 0; j < n; ++j) {
-                const bool opens = j == 0 || ci == 0;
-                if (opens) {   // finish the query before, then wait for the new one's tile
-                    if (j > 0) output(j - 1, first);
-                    wait_or_flag_cluster(smem_addr(&bars->q_full), loads & 1, ok);
-                    ++loads;
-                }
-                const int s = j & (kStages - 1);
-                wait_or_flag_cluster(smem_addr(&bars->full_k[s]), (j / kStages) & 1, ok);
-                tc_fence_after_sync();
-                const uint64_t b = sw128_desc(smem_addr(smem + kOffStages + s * kStageBytes));
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    mma_bf16_ss_pair(tmem + kSCol + 32 * (j & 1),
-                                     q_desc + (((k >> 2) * kQBlockBytes + (k & 3) * 32) >> 4),
-                                     b + (((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4), kIdescS,
-                                     k != 0 ? 1u : 0u);
-                mma_commit_pair(smem_addr(&bars->s_full[j & 1]));
-                if (++ci == cut.per_query) {
-                    ci = 0;
-                    if (j + 1 < n) mma_commit_pair(smem_addr(&bars->q_free));
-                }
-                if (!opens) output(j - 1, first);
-                first = opens;
             }
-            output(n - 1, first);
         }
-        __syncwarp();
     } else {
         // ------------------------------------------------------------- softmax, epilogue
         // Lane L of the 128: head L % 64 of this CTA; of a chunk the records of CTA L / 64; of
@@ -400,34 +521,71 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         const int self = half * 64 + row, peer = self ^ 64;
         const uint32_t p_full = map_rank(smem_addr(&bars->p_full[0]), 0);
         const float scale = __fmul_rn(p.sm_scale, kLog2e);   // logits in powers of two
-        auto pair_sync = [&]() {   // the two warps that share their heads
-            asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp & 1)) : "memory");
+        auto pair_sync = [&]() { group_sync(kHeadsBar + (warp & 1), 64); };   // the two warps of a head
+        const uint32_t q_full = map_rank(smem_addr(&bars->q_full), 0);
+        // A query's first 384 dims wait in shared memory since the query before was moved, and go
+        // to tensor memory; the last 128 come straight to where q . K reads them.
+        const int64_t q_last = (c0 + n - 1) / cut.per_query;
+        uint32_t q_parity = 0;
+        auto fetch_next = [&](int64_t q) {   // one thread
+            mbar_expect_tx(smem_addr(&bars->q_next), kQTmemBlocks * kQBlockBytes);
+#pragma unroll 1
+            for (int b = 0; b < kQTmemBlocks; ++b)
+                tma_load_3d(smem_addr(smem) + kOffNext + b * kQBlockBytes, &q_map,
+                            smem_addr(&bars->q_next), 64 * b, static_cast<int32_t>(rank) * kPairHeads,
+                            static_cast<int32_t>(q));
         };
-        auto index_of = [&](int64_t q, int64_t c) -> int32_t {
-            const int64_t k = c * kChunkKeys + half * kOwnKeys + lane;
-            return k < p.topk ? __ldg(p.indices + q * p.index_stride + k) : -1;
+        auto query = [&](int64_t q) {
+            if (threadIdx.x == kPollThread) {
+                mbar_expect_tx(smem_addr(&bars->q_live), kQBytes);
+#pragma unroll 1
+                for (int b = kQTmemBlocks; b < 8; ++b)
+                    tma_load_3d(smem_addr(smem) + (b - kQTmemBlocks) * kQBlockBytes, &q_map,
+                                smem_addr(&bars->q_live), 64 * b, static_cast<int32_t>(rank) * kPairHeads,
+                                static_cast<int32_t>(q));
+                wait_quiet(smem_addr(&bars->q_next), q_parity, ok);
+            }
+            group_sync(kSoftmaxBar, kSoftmaxWarps * 32);
+            query_to_tmem(smem_addr(smem) + kOffNext, row, tmem + lanes + kQCol);
+            fence_async_smem();   // what was read is read, before the copy engine writes there
+            tc_fence_before_sync();
+            group_sync(kSoftmaxBar, kSoftmaxWarps * 32);
+            if (threadIdx.x == kPollThread) {
+                if (q < q_last) fetch_next(q + 1);
+                wait_quiet(smem_addr(&bars->q_live), q_parity, ok);
+            }
+            if (lane == 0) mbar_arrive_cluster(q_full);
+            q_parity ^= 1u;
         };
-        bool bad = false;
+        if (threadIdx.x == kPollThread) fetch_next(qi);
+        query(qi);
         float m = -INFINITY, l = 0.0f;
         bool fresh = true;         // no chunk of this query is in the accumulator
         int64_t seg = ci;          // the segment's first chunk
-        int32_t idx = index_of(qi, ci);
+#pragma unroll 1
         for (int j = 0; j < n; ++j) {
-            const bool is = idx >= 0 && idx < p.num_slots;
-            bad |= !is && idx != -1;
-            const uint32_t live = __ballot_sync(kFull, is);
             const bool last = j + 1 == n || ci + 1 == cut.per_query;   // of this segment
-            if (j + 1 < n) idx = ci + 1 == cut.per_query ? index_of(qi + 1, 0) : index_of(qi, ci + 1);
-            warp_wait_or_flag(smem_addr(&bars->s_full[j & 1]), (j >> 1) & 1, ok, lane);
+            // q . K of this chunk is complete, and with it, issued before, p . K of chunk j - 2:
+            // the probabilities' buffer is free
+            if (threadIdx.x == kPollThread) wait_quiet(smem_addr(&bars->s_full[j & 1]), (j >> 1) & 1, ok);
+            group_sync(kSoftmaxBar, kSoftmaxWarps * 32);
             tc_fence_after_sync();
+            const uint32_t live =
+                reinterpret_cast<const uint32_t*>(smem + kOffLive)[(j & (kIndexRing - 1)) * 2 + half];
             float v[32];
             tmem_ld32(tmem + lanes + kSCol + 32 * (j & 1), v);
-            float top = -INFINITY;
+            const uint64_t scale2 = f32x2(scale, scale);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                v[i] = (live >> i) & 1u ? __fmul_rn(v[i], scale) : -INFINITY;
-                top = fmaxf(top, v[i]);
+            for (int i = 0; i < 32; i += 2)
+                f32x2_split(mul_f32x2(f32x2(v[i], v[i + 1]), scale2), v[i], v[i + 1]);
+            if (live != kFull) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (((live >> i) & 1u) == 0u) v[i] = -INFINITY;
             }
+            float top = fmaxf(v[0], v[1]);
+#pragma unroll
+            for (int i = 2; i < 32; i += 2) top = fmaxf(top, fmaxf(v[i], v[i + 1]));
             maxima[(j & 1) * 128 + self] = top;
             pair_sync();
             top = fmaxf(top, maxima[(j & 1) * 128 + peer]);
@@ -438,8 +596,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 l = __fmul_rn(l, fix);
                 if (!fresh) {
                     // the products of the chunk before are in the accumulator
-                    warp_wait_or_flag(smem_addr(&bars->o_done[(j - 1) & 1]), ((j - 1) >> 1) & 1, ok,
-                                      lane);
+                    if (lane == 0) wait_quiet(smem_addr(&bars->o_done[(j - 1) & 1]), ((j - 1) >> 1) & 1, ok);
+                    __syncwarp();
                     tc_fence_after_sync();
 #pragma unroll 1
                     for (int c = 0; c < 256; c += 32) {
@@ -453,74 +611,93 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 }
             }
             const float ref = m == -INFINITY ? 0.0f : __fsub_rn(m, kLift);
-            float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            const uint64_t ref2 = f32x2(-ref, -ref);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                v[i] = exp2_approx(__fsub_rn(v[i], ref));
-                sum[i & 3] = __fadd_rn(sum[i & 3], v[i]);
+            for (int i = 0; i < 32; i += 2) {
+                f32x2_split(add_f32x2(f32x2(v[i], v[i + 1]), ref2), v[i], v[i + 1]);
+                v[i] = exp2_flush(v[i]);
+                v[i + 1] = exp2_flush(v[i + 1]);
             }
-            l = __fadd_rn(l, __fadd_rn(__fadd_rn(sum[0], sum[1]), __fadd_rn(sum[2], sum[3])));
-            // the buffer's last reader, the value product of chunk j - 2
-            if (j >= 2)
-                warp_wait_or_flag(smem_addr(&bars->o_done[j & 1]), ((j >> 1) - 1) & 1, ok, lane);
+            uint64_t sum2 = add_f32x2(f32x2(v[0], v[1]), f32x2(v[2], v[3]));
+            uint64_t sum2b = add_f32x2(f32x2(v[4], v[5]), f32x2(v[6], v[7]));
+#pragma unroll
+            for (int i = 8; i < 32; i += 4) {
+                sum2 = add_f32x2(sum2, f32x2(v[i], v[i + 1]));
+                sum2b = add_f32x2(sum2b, f32x2(v[i + 2], v[i + 3]));
+            }
+            float sum_a, sum_b;
+            f32x2_split(add_f32x2(sum2, sum2b), sum_a, sum_b);
+            l = __fadd_rn(l, __fadd_rn(sum_a, sum_b));
             uint8_t* const prow = smem + kOffP + (j & 1) * kPBytes + (row >> 3) * 1024 +
                                   (row & 7) * kRowBytes;
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-                st16(prow + (((half * 4 + c) ^ (row & 7)) << 4), pack8(v + 8 * c, 1.0f));
+                st16(prow + (((half * 4 + c) ^ (row & 7)) << 4), pack8(v + 8 * c));
             fence_async_smem();
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive_cluster(p_full + 8 * (j & 1));
             fresh = false;
             if (last) {
+                // q . K of this query is complete: the next one may take its place, and is
+                // multiplied while this one is written out
+                if (j + 1 < n) query(qi + 1);
                 sums[self] = l;
                 pair_sync();
                 const float total = __fadd_rn(half == 0 ? l : sums[peer], half == 0 ? sums[peer] : l);
                 pair_sync();   // read before the next segment's sums
-                warp_wait_or_flag(smem_addr(&bars->o_done[j & 1]), (j >> 1) & 1, ok, lane);
+                if (lane == 0) wait_quiet(smem_addr(&bars->o_done[j & 1]), (j >> 1) & 1, ok);
+                ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
                 tc_fence_after_sync();
                 const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
                 const bool whole = seg == 0 && ci + 1 == cut.per_query;
-                const float lse2 = total == 0.0f ? -INFINITY : __fadd_rn(__fsub_rn(m, kLift), log2f(total));
-                const bool mine = head < p.num_heads && ok;
-                if (whole) {
-                    uint8_t* const out = static_cast<uint8_t*>(p.out) +
-                                         (qi * p.num_heads + head) * 1024 + half * 512;
+                const float lse2 =
+                    total == 0.0f ? -INFINITY : __fadd_rn(__fsub_rn(m, kLift), log2f(total));
+                // A piece that does not begin its query is its pair's first: slot 0.  Rows leave
+                // through the warp's quarter of the probabilities' buffers, free now, so that
+                // eight lanes write 128 bytes of one row.
+                const int64_t slot = 2 * pair + (seg == 0 ? 1 : 0);
+                float* const pieces = static_cast<float*>(p.workspace);
+                const int64_t at = (whole ? qi : slot) * p.num_heads;
+                uint8_t* const dst = whole ? static_cast<uint8_t*>(p.out) + at * 1024 + half * 512
+                                           : reinterpret_cast<uint8_t*>(pieces + at * 512) + half * 1024;
+                const int64_t dst_row = whole ? 1024 : 2048;
+                const uint32_t st = smem_addr(smem + kOffP) + warp * 4096;
+                const int head0 = static_cast<int>(rank) * kPairHeads + (warp & 1) * 32;
 #pragma unroll 1
-                    for (int c = 0; c < 256; c += 32) {
-                        float t[32];
-                        tmem_ld32(tmem + lanes + c, t);
-                        if (mine) {
+                for (int c = 0; c < 256; c += whole ? 64 : 32) {   // 128 bytes of each row
+                    float t[32];
+                    tmem_ld32(tmem + lanes + c, t);
+                    const uint32_t mine = st + lane * 128 + ((lane & 7) << 4);
+                    if (whole) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                st16(out + 2 * c + 16 * i,
-                                     total == 0.0f ? make_uint4(0u, 0u, 0u, 0u) : pack8(t + 8 * i, inv));
-                        }
-                    }
-                    if (mine && half == 0)
-                        p.lse[qi * p.num_heads + head] = __fmul_rn(lse2, kLn2);
-                } else {
-                    // a piece that does not begin its query is its pair's first: slot 0
-                    const int64_t slot = 2 * pair + (seg == 0 ? 1 : 0);
-                    float* const rows = static_cast<float*>(p.workspace);
-                    float* const dst = rows + (slot * p.num_heads + head) * 512 + half * 256;
-#pragma unroll 1
-                    for (int c = 0; c < 256; c += 32) {
-                        float t[32];
-                        tmem_ld32(tmem + lanes + c, t);
-                        if (mine) {
+                        for (int i = 0; i < 4; ++i) sts16(mine ^ (i << 4), pack8(t + 8 * i, inv));
+                        tmem_ld32(tmem + lanes + c + 32, t);
 #pragma unroll
-                            for (int i = 0; i < 32; i += 4)
-                                *reinterpret_cast<float4*>(dst + c + i) =
-                                    total == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
-                                                  : make_float4(__fmul_rn(t[i], inv), __fmul_rn(t[i + 1], inv),
-                                                                __fmul_rn(t[i + 2], inv), __fmul_rn(t[i + 3], inv));
-                        }
+                        for (int i = 0; i < 4; ++i) sts16(mine ^ ((4 + i) << 4), pack8(t + 8 * i, inv));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            sts16(mine ^ (i << 4),
+                                  make_uint4(__float_as_uint(__fmul_rn(t[4 * i], inv)),
+                                             __float_as_uint(__fmul_rn(t[4 * i + 1], inv)),
+                                             __float_as_uint(__fmul_rn(t[4 * i + 2], inv)),
+                                             __float_as_uint(__fmul_rn(t[4 * i + 3], inv))));
                     }
-                    if (mine && half == 0)
-                        rows[2 * static_cast<int64_t>(cut.pairs) * p.num_heads * 512 +
-                             slot * p.num_heads + head] = lse2;
+                    __syncwarp();
+                    uint8_t* const to = dst + (whole ? 2 : 4) * c + (lane & 7) * 16;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = 4 * i + (lane >> 3);
+                        const uint4 v = lds16_at(st + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+                        if (head0 + r < p.num_heads && ok) st16(to + (head0 + r) * dst_row, v);
+                    }
+                    __syncwarp();
+                }
+                if (half == 0 && head < p.num_heads && ok) {
+                    if (whole) p.lse[at + head] = __fmul_rn(lse2, kLn2);
+                    else
+                        pieces[2 * static_cast<int64_t>(cut.pairs) * p.num_heads * 512 + at + head] = lse2;
                 }
                 tc_fence_before_sync();
                 m = -INFINITY;
@@ -533,8 +710,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 ++qi;
             }
         }
-        if (rank == 0 && (warp == 0 || warp == 2) && __any_sync(kFull, bad) && lane == 0)
-            report(p.err, kErrIndex);
     }
     if (!ok) atomicOr(&bars->timed_out, 1);
     tc_fence_before_sync();
@@ -544,44 +719,76 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     if (warp == kMmaWarp) tmem_dealloc_pair(tmem, kTmemCols);
 }
 
-// Joins the pieces of each cut query: out = sum_i exp2(lse_i - lse) rows_i.  A block of 128
-// threads takes one head, four dims a thread, of the query that pair g's run begins inside of,
-// if g is the second pair on it.
-__global__ void __launch_bounds__(128) join_kernel(const AttentionParams p, const Cut cut) {
-    const int64_t g = 1 + blockIdx.x / p.num_heads;
-    const int head = static_cast<int>(blockIdx.x % p.num_heads);
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kFull, v, d));
+    return v;
+}
+
+// The queries that the cut runs through: query, its first pair and how many work on it.
+constexpr int kMaxPairs = 128;
+struct Cuts {
+    int32_t n;
+    int32_t query[kMaxPairs - 1];
+    int16_t first[kMaxPairs - 1], pairs[kMaxPairs - 1];
+};
+
+// Joins the pieces of each cut query: out = sum_i exp2(lse_i - lse) rows_i.  A block takes one
+// head of one query, four dims a thread; with many pieces, four groups of 128 threads take
+// every fourth piece and add up in shared memory.
+template <int kGroups>
+__global__ void __launch_bounds__(128 * kGroups)
+    join_kernel(const AttentionParams p, const int32_t pairs, const __grid_constant__ Cuts cuts) {
+    __shared__ float4 part[kGroups > 1 ? kGroups : 1][kGroups > 1 ? 128 : 1];
+    const int32_t c = blockIdx.x / p.num_heads;
+    const int32_t head = blockIdx.x - c * p.num_heads;
+    const int g0 = cuts.first[c], n = cuts.pairs[c];
+    const int d = threadIdx.x & 127, group = threadIdx.x >> 7;
     pdl_wait_previous();
     pdl_release_next();
-    const int64_t qi = cut.begin(g) / cut.per_query;
-    const int64_t g0 = cut.owner(qi * cut.per_query);
-    if (g != g0 + 1) return;
-    const int64_t g1 = cut.owner((qi + 1) * cut.per_query - 1);
-    if (g1 == g0) return;   // finished by its pair
     const float* const rows = static_cast<const float*>(p.workspace);
-    const float* const lses = rows + 2 * static_cast<int64_t>(cut.pairs) * p.num_heads * 512 + head;
+    const float* const lses = rows + 2 * static_cast<int64_t>(pairs) * p.num_heads * 512 + head;
     // the first piece ends its pair's run (slot 1), the others begin theirs (slot 0)
-    auto slot = [&](int64_t i) -> int64_t { return 2 * i + (i == g0 ? 1 : 0); };
+    auto slot = [&](int i) -> int32_t { return (2 * (g0 + i) + (i == 0 ? 1 : 0)) * p.num_heads; };
+    // the pieces' log-sum-exps, one a lane
+    const int lane = threadIdx.x & 31;
     float m = -INFINITY;
-    for (int64_t i = g0; i <= g1; ++i) m = fmaxf(m, lses[slot(i) * p.num_heads]);
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, lses[slot(i)]);
+#pragma unroll
+    for (int x = 16; x >= 1; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
     const float ref = m == -INFINITY ? 0.0f : m;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float sum = 0.0f;
+    for (int i = lane; i < n; i += 32) sum = __fadd_rn(sum, exp2_approx(__fsub_rn(lses[slot(i)], ref)));
+    sum = warp_sum(sum);
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-    for (int64_t i = g0; i <= g1; ++i) {
-        const float w = exp2_approx(__fsub_rn(lses[slot(i) * p.num_heads], ref));
+    for (int i = group; i < n; i += kGroups) {
+        const float w = exp2_approx(__fsub_rn(lses[slot(i)], ref));
         const float4 t = *reinterpret_cast<const float4*>(
-            rows + (slot(i) * p.num_heads + head) * 512 + 4 * threadIdx.x);
-        sum = __fadd_rn(sum, w);
+            rows + (static_cast<int64_t>(slot(i)) + head) * 512 + 4 * d);
         acc.x = __fmaf_rn(w, t.x, acc.x);
         acc.y = __fmaf_rn(w, t.y, acc.y);
         acc.z = __fmaf_rn(w, t.z, acc.z);
         acc.w = __fmaf_rn(w, t.w, acc.w);
     }
+    if constexpr (kGroups > 1) {
+        part[group][d] = acc;
+        __syncthreads();
+        if (group != 0) return;
+#pragma unroll
+        for (int i = 1; i < kGroups; ++i) {
+            const float4 t = part[i][d];
+            acc.x = __fadd_rn(acc.x, t.x);
+            acc.y = __fadd_rn(acc.y, t.y);
+            acc.z = __fadd_rn(acc.z, t.z);
+            acc.w = __fadd_rn(acc.w, t.w);
+        }
+    }
     const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
     const uint2 v = make_uint2(pack_bf16x2_rn(__fmul_rn(acc.x, inv), __fmul_rn(acc.y, inv)),
                                pack_bf16x2_rn(__fmul_rn(acc.z, inv), __fmul_rn(acc.w, inv)));
-    const int64_t at = qi * p.num_heads + head;
-    st8(static_cast<uint8_t*>(p.out) + at * 1024 + 8 * threadIdx.x, v);
+    const int64_t at = static_cast<int64_t>(cuts.query[c]) * p.num_heads + head;
+    st8(static_cast<uint8_t*>(p.out) + at * 1024 + 8 * d, v);
     if (threadIdx.x == 0)
         p.lse[at] = sum == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(m, log2f(sum)), kLn2);
 }
@@ -589,11 +796,6 @@ __global__ void __launch_bounds__(128) join_kernel(const AttentionParams p, cons
 constexpr int kHeadsPerBlock = 8;
 constexpr int kTile = 32;
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kFull, v, d));
-    return v;
-}
 // Records k0 .. k0 + 31 of query qi as bf16 rows of 1024 bytes in `rows` (zeros for an entry
 // that is none); returns the bits of the valid ones.  Every thread of the block calls it.
 __device__ __forceinline__ uint32_t load_tile(const AttentionParams& p, int64_t qi, int64_t k0,
@@ -728,6 +930,7 @@ cudaError_t make_cut(int64_t num_queries, int64_t topk, Cut* cut) {
     if (e != cudaSuccess) return e;
     cut->per_query = topk == 0 ? 1 : (topk + kChunkKeys - 1) / kChunkKeys;
     cut->total = num_queries * cut->per_query;
+    if (pairs > kMaxPairs) pairs = kMaxPairs;
     cut->pairs = static_cast<int32_t>(cut->total < pairs ? cut->total : pairs);
     return cudaSuccess;
 }
@@ -737,6 +940,22 @@ bool has_pieces(const Cut& cut) {
     for (int32_t g = 1; g < cut.pairs; ++g)
         if (cut.begin(g) % cut.per_query != 0) return true;
     return false;
+}
+
+// The queries that pairs' runs begin inside of.
+void find_cuts(const Cut& cut, Cuts* cuts, int* most) {
+    cuts->n = 0;
+    *most = 0;
+    for (int32_t g = 1; g < cut.pairs; ++g) {
+        const int64_t begin = cut.begin(g), q = begin / cut.per_query;
+        if (begin - q * cut.per_query == 0) continue;
+        if (cuts->n == 0 || cuts->query[cuts->n - 1] != q) {
+            cuts->query[cuts->n] = static_cast<int32_t>(q);
+            cuts->first[cuts->n] = static_cast<int16_t>(g - 1);
+            cuts->pairs[cuts->n++] = 1;
+        }
+        if (++cuts->pairs[cuts->n - 1] > *most) *most = cuts->pairs[cuts->n - 1];
+    }
 }
 
 // The queries [num_queries, num_heads, 512] as a 3-D tensor map with boxes of 64 dims x 64
@@ -756,6 +975,23 @@ cudaError_t q_tensor_map(const AttentionParams& p, CUtensorMap* map) {
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// The cache as rows of 256 bytes (every data row is one: pages start at multiples of 512), read
+// in half-rows with the 128-byte swizzle; a box is one row high, as four-row gathers want it.
+cudaError_t cache_tensor_map(const AttentionParams& p, CUtensorMap* map) {
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (encode == nullptr) return cudaErrorNotSupported;
+    const int64_t pages = p.num_slots / p.block_size;
+    const cuuint64_t dims[2] = {256, static_cast<cuuint64_t>(pages * (p.page_stride >> 8))};
+    const cuuint64_t strides[1] = {256};
+    const cuuint32_t box[2] = {128, 1};
+    const cuuint32_t step[2] = {1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p.cache),
+                              dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 }  // namespace
 
 cudaError_t attention_workspace(int32_t num_heads, int64_t num_queries, int64_t topk,
@@ -772,15 +1008,21 @@ cudaError_t launch_sparse_attention(const AttentionParams& p, cudaStream_t strea
     Cut cut;
     cudaError_t e = make_cut(p.num_queries, p.topk, &cut);
     if (e != cudaSuccess) return e;
-    CUtensorMap map;
-    e = q_tensor_map(p, &map);
+    CUtensorMap q_map, cache_map;
+    e = q_tensor_map(p, &q_map);
+    if (e == cudaSuccess) e = cache_tensor_map(p, &cache_map);
     if (e != cudaSuccess) return e;
     e = launch_kernel(attend_kernel, 2 * static_cast<int64_t>(cut.pairs), kAttendThreads, kAttendSmem,
-                      stream, p.pdl, p, cut, map);
+                      stream, p.pdl, p, cut, q_map, cache_map);
     if (e != cudaSuccess) return e;
-    if (has_pieces(cut)) {
-        e = launch_kernel(join_kernel, static_cast<int64_t>(cut.pairs - 1) * p.num_heads, 128, 0,
-                          stream, p.pdl, p, cut);
+    Cuts cuts;
+    int most = 0;
+    find_cuts(cut, &cuts, &most);
+    if (cuts.n > 0) {
+        const int64_t blocks = static_cast<int64_t>(cuts.n) * p.num_heads;
+        // four groups from eight pieces on: measured at 128 heads, ...
+        e = most >= 8 ? launch_kernel(join_kernel<4>, blocks, 512, 0, stream, p.pdl, p, cut.pairs, cuts)
+                      : launch_kernel(join_kernel<1>, blocks, 128, 0, stream, p.pdl, p, cut.pairs, cuts);
         if (e != cudaSuccess) return e;
     }
     if (p.weights == nullptr || p.topk == 0) return e;

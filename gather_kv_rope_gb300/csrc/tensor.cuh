@@ -152,6 +152,23 @@ __device__ __forceinline__ void warp_wait_or_flag(uint32_t bar, uint32_t parity,
     __syncwarp();
 }
 
+// wait_or_flag for kernels whose warps run different code and wait at the same time: a poll is
+// a few instructions, because the polls of waiting warps compete for issue slots and
+// instruction fetches with the warps that work, and the limit is counted in SM clocks
+// (40 million: 20 ms at 2 GHz): reading %globaltimer takes 5 us and holds up the SM's global
+// loads behind it.
+constexpr int64_t kWaitClocks = 40000000;
+__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity) {
+    const int64_t t0 = clock64();
+    do {
+        if (mbar_try_wait(bar, parity)) return true;
+    } while (clock64() - t0 <= kWaitClocks);
+    return false;
+}
+__device__ __forceinline__ void wait_quiet(uint32_t bar, uint32_t parity, bool& ok) {
+    if (ok && !mbar_try_wait(bar, parity)) ok = mbar_wait_slow(bar, parity);
+}
+
 // One arrival for a whole warp: every lane's earlier shared-memory writes (each lane has
 // fenced them for the async proxy) are ordered before lane 0's arrive by __syncwarp.
 __device__ __forceinline__ void warp_arrive(uint32_t bar, int lane) {
@@ -195,40 +212,33 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
                      : "memory");
 }
-// Arrive on an mbarrier anywhere in the cluster (a map_rank address).
+// Arrive on an mbarrier anywhere in the cluster (a map_rank address).  What the arrivals of
+// these kernels announce is read by the tensor cores of the arriving CTA's own SM, for which
+// the writer has fenced it (fence_async_smem); no memory is handed from CTA to CTA, so the
+// default release at CTA scope does (a release at cluster scope, and waits that acquire at it,
+// cost the sparse attention a full memory barrier per arrival: see attention.cu).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// mbar_wait for arrivals that come from the other CTA too.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n .reg .pred p;\n"
-        " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(done)
-        : "r"(bar), "r"(parity), "r"(kSuspendNs)
-        : "memory");
-    return done != 0u;
-}
-__device__ __forceinline__ void wait_or_flag_cluster(uint32_t bar, uint32_t parity, bool& ok) {
-    if (!ok || mbar_try_wait_cluster(bar, parity)) return;
-    const uint64_t t0 = global_ns();
-    while (!mbar_try_wait_cluster(bar, parity))
-        if (global_ns() - t0 > kWaitNs) {
-            ok = false;
-            return;
-        }
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                  : "memory");
 }
+// TMA gather of four rows r0 .. r3 of a 2-D map with a box one row high, from element x on.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int32_t x, int32_t r0, int32_t r1, int32_t r2,
+                                            int32_t r3) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3)
+        : "memory");
+}
 // TMA load of a 3-D box at (x, y, z) into this CTA's shared memory, counted on `bar`.
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
                                             int32_t x, int32_t y, int32_t z) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], "
         "[%1, {%3, %4, %5}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
         : "memory");
@@ -245,22 +255,43 @@ __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
                  : "memory");
 }
-// D[tmem] (+)= A[smem] * B[smem]^T over the pair, bf16 inputs, fp32 accumulator; one thread.
+// One lane of a converged warp (warp-uniform code around it keeps addresses and descriptors in
+// uniform registers, where tcgen05 wants them).
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t e;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+    return e;
+}
+// D[tmem] (+)= A[smem] * B[smem]^T over the pair, bf16 inputs, fp32 accumulator; the whole warp
+// calls it, the elected lane issues.
 __device__ __forceinline__ void mma_bf16_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                                 uint32_t idesc, uint32_t accumulate) {
+                                                 uint32_t idesc, uint32_t accumulate,
+                                                 uint32_t elected) {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "{\n .reg .pred p, e;\n setp.ne.b32 e, %5, 0;\n setp.ne.b32 p, %4, 0;\n"
+        " @e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
         : "memory");
 }
-// Arrive on the mbarrier at this offset in both CTAs once every tcgen05 operation this thread
-// issued has completed.
-__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+// The same with A in tensor memory: K's values two to a column (the lower half the even k), 16
+// of them in 8 columns, the CTA's 64 rows in lanes 0 .. 63 and again in lanes 64 .. 127.
+__device__ __forceinline__ void mma_bf16_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                                 uint32_t idesc, uint32_t accumulate,
+                                                 uint32_t elected) {
     asm volatile(
-        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-        "[%0], %1;" ::"r"(bar),
-        "h"(static_cast<uint16_t>(3))
+        "{\n .reg .pred p, e;\n setp.ne.b32 e, %5, 0;\n setp.ne.b32 p, %4, 0;\n"
+        " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+        : "memory");
+}
+// Arrive on the mbarrier at this offset in both CTAs once every tcgen05 operation the elected
+// lane issued has completed.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar, uint32_t elected) {
+    asm volatile(
+        "{\n .reg .pred e;\n setp.ne.b32 e, %2, 0;\n"
+        " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
+        ".b64 [%0], %1;\n}" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3)), "r"(elected)
         : "memory");
 }
 // 32 consecutive 32-bit columns of this thread's lane; tcgen05.wait::ld before their use.
