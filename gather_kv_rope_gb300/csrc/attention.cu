@@ -178,12 +178,6 @@ struct Ring {
     }
 };
 
-// The rare scales (above 2, or the NaN), out of the way of the common path.
-__device__ __noinline__ void store_unit_far(uint32_t out, uint4 codes, uint32_t scale) {
-    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sts16(out ^ (j << 4), dequant8_e2m1(w[j], scale));
-}
 // A unit's 32 dims (16 bytes of codes, a scale byte) as bf16 into four 16-byte pieces of a
 // swizzled row: piece j of the unit lies at the first one's address with j in bits 4 and 5
 // flipped.
@@ -191,15 +185,11 @@ __device__ __forceinline__ void store_unit(uint32_t codes, uint32_t scale, uint3
     const uint4 c = lds16_at(codes);
     uint32_t s;
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(s) : "r"(scale) : "memory");
-    if (__builtin_expect(s <= kE2m1OneStepByte, 1)) {
-        const uint32_t f = e2m1_factor(s);
-        sts16(out, dequant8_e2m1_scaled(c.x, f));
-        sts16(out ^ 16u, dequant8_e2m1_scaled(c.y, f));
-        sts16(out ^ 32u, dequant8_e2m1_scaled(c.z, f));
-        sts16(out ^ 48u, dequant8_e2m1_scaled(c.w, f));
-    } else {
-        store_unit_far(out, c, s);
-    }
+    const uint32_t f = e2m1_factor(s);
+    sts16(out, dequant8_e2m1(c.x, f));
+    sts16(out ^ 16u, dequant8_e2m1(c.y, f));
+    sts16(out ^ 32u, dequant8_e2m1(c.z, f));
+    sts16(out ^ 48u, dequant8_e2m1(c.w, f));
 }
 
 // Named barriers of the warps of one role: one thread waits on the mbarriers, the others here,
@@ -433,6 +423,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
             const uint64_t k_desc0 = sw128_desc(smem_addr(smem + kOffStages));
             const uint64_t v_desc0 = sw128_mn_desc(smem_addr(smem + kOffStages), kBlockBytes);
             const uint64_t p_desc0 = sw128_desc(smem_addr(smem + kOffP));
+            const uint32_t q_lo = static_cast<uint32_t>(q_desc), k_lo = static_cast<uint32_t>(k_desc0);
+            const uint32_t v_lo = static_cast<uint32_t>(v_desc0), p_lo = static_cast<uint32_t>(p_desc0);
             uint32_t loads = 0;
             Ring<kStages> sk, sv;
             // q . K runs one chunk ahead of p . K within a query; jq, jo: their next chunks,
@@ -452,24 +444,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                     __syncwarp();
                     tc_fence_after_sync();
                     const uint32_t d = tmem + kSCol + 32 * (jq & 1);
-                    uint64_t a = q_desc, b = k_desc0 + sk.s * (kStageBytes >> 4);
-                    uint32_t at = tmem + kQCol;
-#pragma unroll 1
-                    for (int kb = 0; kb < kQTmemBlocks; ++kb) {       // 64 dims
+                    // one addition a product: the lower half of the descriptor (start addresses
+                    // stay below 2^14 sixteen-byte units, so nothing carries), the rest constant
+                    const uint32_t b = k_lo + sk.s * (kStageBytes >> 4);
+                    if (elected) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_bf16_ts_pair(d, at + 8 * k, b + 2 * k, kIdescS, k != 0 ? 1u : kb, elected);
-                        at += 32;
-                        b += kBlockBytes >> 4;
+                        for (int k = 0; k < 32; ++k) {       // 16 dims
+                            const uint64_t bk = desc_at(k_desc0, b + (((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4));
+                            if (k < 4 * kQTmemBlocks)
+                                mma_bf16_ts_pair(d, tmem + kQCol + 8 * k, bk, kIdescS, k != 0);
+                            else
+                                mma_bf16_ss_pair(d, desc_at(q_desc, q_lo + ((((k >> 2) - kQTmemBlocks) * kQBlockBytes + (k & 3) * 32) >> 4)),
+                                                 bk, kIdescS, true);
+                        }
                     }
-#pragma unroll 1
-                    for (int kb = kQTmemBlocks; kb < 8; ++kb) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            mma_bf16_ss_pair(d, a + 2 * k, b + 2 * k, kIdescS, 1u, elected);
-                        a += kQBlockBytes >> 4;
-                        b += kBlockBytes >> 4;
-                    }
+                    __syncwarp();
                     mma_commit_pair(smem_addr(&bars->s_full[jq & 1]), elected);
                     if (++ci == cut.per_query) ci = 0;
                     sk.next();
@@ -479,23 +468,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                     wait_quiet(smem_addr(&bars->p_full[jo & 1]), (jo >> 1) & 1, ok);
                     __syncwarp();
                     tc_fence_after_sync();
-                    uint64_t a = p_desc0 + (jo & 1) * (kPBytes >> 4);
-                    uint64_t b = v_desc0 + sv.s * (kStageBytes >> 4);
-                    uint32_t acc = fresh ? 0u : 1u;
-#pragma unroll 1
-                    for (int k = 0; k < 2; ++k) {        // records of CTA k, 16 at a time
+                    const uint32_t a = p_lo + (jo & 1) * (kPBytes >> 4);
+                    const uint32_t b = v_lo + sv.s * (kStageBytes >> 4);
+                    if (elected) {
 #pragma unroll
-                        for (int i = 0; i < 2; ++i) {
+                        for (int k = 0; k < 4; ++k) {            // 16 records; k / 2: of which CTA
 #pragma unroll
-                            for (int h = 0; h < 2; ++h)  // 128 of each CTA's 256 dims
-                                mma_bf16_ss_pair(tmem + 128 * h, a + 2 * i,
-                                                 b + ((i * 2048 + h * 2 * kBlockBytes) >> 4), kIdescO,
-                                                 i != 0 ? 1u : acc, elected);
+                            for (int h = 0; h < 2; ++h)          // 128 of each CTA's 256 dims
+                                mma_bf16_ss_pair(tmem + 128 * h, desc_at(p_desc0, a + 2 * k),
+                                                 desc_at(v_desc0, b + (((k >> 1) * kHalfBytes + (k & 1) * 2048 +
+                                                                        h * 2 * kBlockBytes) >> 4)),
+                                                 kIdescO, k != 0 || !fresh);
                         }
-                        a += 4;
-                        b += kHalfBytes >> 4;
-                        acc = 1u;
                     }
+                    __syncwarp();
                     mma_commit_pair(smem_addr(&bars->stage_empty[sv.s]), elected);
                     mma_commit_pair(smem_addr(&bars->o_done[jo & 1]), elected);
                     sv.next();
@@ -814,8 +800,8 @@ __device__ __forceinline__ uint32_t load_tile(const AttentionParams& p, int64_t 
             const uint32_t* const data =
                 reinterpret_cast<const uint32_t*>(base + static_cast<int64_t>(row) * 256);
             const uint8_t* const sc = base + static_cast<int64_t>(p.block_size) * 256 + row * 16;
-            a = dequant8_e2m1(__ldg(data + lane), __ldg(sc + (lane >> 2)));
-            b = dequant8_e2m1(__ldg(data + 32 + lane), __ldg(sc + 8 + (lane >> 2)));
+            a = dequant8_e2m1(__ldg(data + lane), e2m1_factor(__ldg(sc + (lane >> 2))));
+            b = dequant8_e2m1(__ldg(data + 32 + lane), e2m1_factor(__ldg(sc + 8 + (lane >> 2))));
             if (lane == 0) atomicOr(valid, 1u << r);
         } else if (idx != -1 && lane == 0) {
             report(p.err, kErrIndex);

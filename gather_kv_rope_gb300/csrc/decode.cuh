@@ -112,8 +112,8 @@ __device__ __forceinline__ void convert(const Loaded<kRecord>& r, int lane, floa
             oa = dequant8_scaled(r.a, scale);
             ob = dequant8_scaled(r.b, scale);
         } else if constexpr (kRecord == 272) {
-            oa = dequant8_e2m1(r.a, r.s & 0xFFu);
-            ob = dequant8_e2m1(r.b, r.s >> 8);
+            oa = dequant8_e2m1(r.a, e2m1_factor(r.s & 0xFFu));
+            ob = dequant8_e2m1(r.b, e2m1_factor(r.s >> 8));
         } else if constexpr (kRecord == 528) {
             oa = dequant8(r.a, r.s & 0xFFu);
             ob = dequant8(r.b, r.s >> 8);

@@ -270,13 +270,16 @@ __device__ __forceinline__ uint4 dequant8(const uint2 c, uint32_t byte) {
 
 // An e2m1 code s.EE.M moved to bf16 bit positions s.000000EE.M000000 reads as
 // (1 + M/2) * 2^(E-127) (E >= 1) or M * 2^-127 (E = 0): in both cases the e2m1 value times
-// 2^-126.  One bf16 multiply by 2^(byte - 1) then gives e2m1 * 2^(byte - 127), exactly
-// (subnormals kept).  2^(byte - 1) is a normal bf16 for byte <= 128; above that the factor
-// is split into 2^127 and 2^(byte - 128).
-constexpr uint32_t kE2m1OneStepByte = 128u;
+// 2^-126.  A bf16 multiply by 2^127 and one by 2^(byte - 128) give e2m1 * 2^(byte - 127), both
+// exact (subnormals kept) up to the overflow to infinity.  (One multiply by 2^(byte - 1) would
+// do for scales up to 2, but latents with outliers have blocks above that: a second path for
+// them cost the sparse attention a quarter of its time.)
 
-__device__ __forceinline__ uint32_t e2m1_factor(uint32_t byte) {   // byte <= 128
-    return (byte + 126u) * 0x00800080u;
+// 2^(byte - 128) in both halves; byte 255, the UE8M0 NaN, gives the NaN that makes every
+// product one.
+__device__ __forceinline__ uint32_t e2m1_factor(uint32_t byte) {
+    const uint32_t b = byte >= 2u ? (byte - 1u) << 7 : 0x20u << byte;   // 2^-128, 2^-127 subnormal
+    return (byte == 255u ? kBf16NaN : b) * 0x00010001u;
 }
 // Pair i of a word: dims 2i (low half) and 2i + 1 (high half), times 2^-126.
 template <int i>
@@ -285,23 +288,14 @@ __device__ __forceinline__ uint32_t e2m1_pair(uint32_t w) {
     const uint32_t mag = kMag >= 0 ? w << (kMag >= 0 ? kMag : 0) : w >> (kMag < 0 ? -kMag : 0);
     return ((w << kSign) & 0x80008000u) | (mag & 0x01C001C0u);
 }
-__device__ __forceinline__ uint4 dequant8_e2m1_scaled(uint32_t w, uint32_t factor) {
-    return make_uint4(bf16x2_mul(e2m1_pair<0>(w), factor), bf16x2_mul(e2m1_pair<1>(w), factor),
-                      bf16x2_mul(e2m1_pair<2>(w), factor), bf16x2_mul(e2m1_pair<3>(w), factor));
+template <int i>
+__device__ __forceinline__ uint32_t e2m1_value(uint32_t w, uint32_t factor) {
+    return bf16x2_mul(bf16x2_mul(e2m1_pair<i>(w), 254u * 0x00800080u), factor);
 }
-// Any scale byte (255, the UE8M0 NaN: NaN).
-__device__ __forceinline__ uint4 dequant8_e2m1(uint32_t w, uint32_t byte) {
-    if (__builtin_expect(byte <= kE2m1OneStepByte, 1))
-        return dequant8_e2m1_scaled(w, e2m1_factor(byte));
-    const uint32_t n = kBf16NaN | (kBf16NaN << 16);
-    if (byte == 255u) return make_uint4(n, n, n, n);
-    uint4 o = dequant8_e2m1_scaled(w, 254u * 0x00800080u);
-    const uint32_t m2 = (byte - 1u) * 0x00800080u;
-    o.x = bf16x2_mul(o.x, m2);
-    o.y = bf16x2_mul(o.y, m2);
-    o.z = bf16x2_mul(o.z, m2);
-    o.w = bf16x2_mul(o.w, m2);
-    return o;
+// Eight codes (one word) and their block's factor -> eight bf16 values.
+__device__ __forceinline__ uint4 dequant8_e2m1(uint32_t w, uint32_t factor) {
+    return make_uint4(e2m1_value<0>(w, factor), e2m1_value<1>(w, factor), e2m1_value<2>(w, factor),
+                      e2m1_value<3>(w, factor));
 }
 
 // ---------------------------------------------------------------- fp8 rows with one scale

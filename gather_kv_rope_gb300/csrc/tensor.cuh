@@ -161,7 +161,9 @@ constexpr int64_t kWaitClocks = 40000000;
 __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity) {
     const int64_t t0 = clock64();
     do {
-        if (mbar_try_wait(bar, parity)) return true;
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
     } while (clock64() - t0 <= kWaitClocks);
     return false;
 }
@@ -262,26 +264,27 @@ __device__ __forceinline__ uint32_t elect_lane() {
     asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(e));
     return e;
 }
-// D[tmem] (+)= A[smem] * B[smem]^T over the pair, bf16 inputs, fp32 accumulator; the whole warp
-// calls it, the elected lane issues.
+// A descriptor with its lower half replaced.
+__device__ __forceinline__ uint64_t desc_at(uint64_t desc, uint32_t lo) {
+    return (desc & 0xFFFFFFFF00000000u) | lo;
+}
+// D[tmem] (+)= A[smem] * B[smem]^T over the pair, bf16 inputs, fp32 accumulator; one thread.
 __device__ __forceinline__ void mma_bf16_ss_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                                 uint32_t idesc, uint32_t accumulate,
-                                                 uint32_t elected) {
+                                                 uint32_t idesc, bool accumulate) {
     asm volatile(
-        "{\n .reg .pred p, e;\n setp.ne.b32 e, %5, 0;\n setp.ne.b32 p, %4, 0;\n"
-        " @e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
         : "memory");
 }
 // The same with A in tensor memory: K's values two to a column (the lower half the even k), 16
 // of them in 8 columns, the CTA's 64 rows in lanes 0 .. 63 and again in lanes 64 .. 127.
 __device__ __forceinline__ void mma_bf16_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                                 uint32_t idesc, uint32_t accumulate,
-                                                 uint32_t elected) {
+                                                 uint32_t idesc, bool accumulate) {
     asm volatile(
-        "{\n .reg .pred p, e;\n setp.ne.b32 e, %5, 0;\n setp.ne.b32 p, %4, 0;\n"
-        " @e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
         : "memory");
 }
 // Arrive on the mbarrier at this offset in both CTAs once every tcgen05 operation the elected
