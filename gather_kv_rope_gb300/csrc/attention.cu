@@ -50,7 +50,8 @@ constexpr int kChunkKeys = 64;           // records per chunk
 constexpr int kOwnKeys = 32;             // of which a CTA dequantises this many in full
 constexpr int kStages = 3;               // chunks of dequantised records in flight
 constexpr int kRawStages = 3;            // chunks of raw records in flight
-constexpr int kSoftmaxWarps = 4;         // warps 0..3: warp w owns tensor-memory lanes 32w ..
+constexpr int kSoftmaxWarps = 8;         // warps 0..7: warp w has tensor-memory lanes 32 (w % 4) ..
+                                         // and half w / 4 of their columns
 constexpr int kOwnWarps = 8;             // dequantise the CTA's own records for q . K
 constexpr int kRefillWarps = 4;          // dequantise the other CTA's records for p . K
 constexpr int kFirstOwn = kSoftmaxWarps;
@@ -60,7 +61,7 @@ constexpr int kGatherWarps = 3;          // raw records: own in two halves, the 
 constexpr int kFirstGather = kMmaWarp + 1;
 constexpr int kIndexRing = 8;            // chunks of indices (kept as many) a gather warp holds,
 constexpr int kIndexAhead = 6;           // and has on their way
-constexpr int kAttendThreads = (kFirstGather + kGatherWarps) * 32;   // 20 warps: up to 96 registers
+constexpr int kAttendThreads = (kFirstGather + kGatherWarps) * 32;   // 24 warps: up to 80 registers
 constexpr uint32_t kBlockBytes = kOwnKeys * kRowBytes;      // 64 dims of the stage's 32 rows
 constexpr uint32_t kHalfBytes = 4 * kBlockBytes;            // 256 dims
 constexpr uint32_t kStageBytes = 2 * kHalfBytes;
@@ -72,12 +73,16 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 256;          // logits: two buffers of 32 columns; output at 0
 constexpr uint32_t kQCol = 320;          // the query's first 384 dims, two to a column
 static_assert(kQCol + kQTmemBlocks * 32 <= kTmemCols, "tensor memory");
-// A new maximum replaces the running one only when it is this much larger (in powers of two):
-// probabilities then stay below 2^8, and the accumulator is rarely rescaled.
-constexpr float kLag = 8.0f;
+// A new maximum replaces the running one only when it is this much larger (in powers of two), for
+// any of the 32 heads of a warp: rescaling the accumulator takes longer than a chunk's softmax
+// (1400 cycles), and at 8, with the logits of heavy-tailed latents, every second chunk had some
+// head that rose.  The reference does not touch the precision of floating-point terms, only
+// their range: probabilities stay below 2^(kLag + kLift) = 2^48, and an output of fewer than
+// 2^24 records below 2^55 each cannot overflow.
+constexpr float kLag = 32.0f;
 // Probabilities are taken as exp2(s - m + kLift): bf16 ends at 2^-133, and without the lift terms
 // that the output still shows (it ends there too) would be rounded away before they are
-// multiplied by a record's values and summed.  At most 2^24 with kLag, far from overflow.
+// multiplied by a record's values and summed.
 constexpr float kLift = 16.0f;
 
 // kind::f16 over the pair, M = 128, fp32 accumulator, bf16 A and B (fields as in logits.cu):
@@ -111,9 +116,9 @@ constexpr uint32_t kRawOth = 2 * kRawBlock;
 constexpr uint32_t kRawOwnScales = kRawOth + kRawBlock;
 constexpr uint32_t kRawOthScales = kRawOwnScales + kOwnKeys * 16;
 constexpr uint32_t kRawBytes = kRawOthScales + kOwnKeys * 16;
-constexpr uint32_t kOffMax = kOffRaw + kRawStages * kRawBytes;   // [2][128] row maxima
-constexpr uint32_t kOffSum = kOffMax + 2 * 128 * 4;         // [128] row sums
-constexpr uint32_t kOffIndex = kOffSum + 128 * 4;           // [gather warp][kIndexRing][32]
+constexpr uint32_t kOffMax = kOffRaw + kRawStages * kRawBytes;   // [4][64] maxima of a head
+constexpr uint32_t kOffSum = kOffMax + 256 * 4;             // [4][64] sums of a head
+constexpr uint32_t kOffIndex = kOffSum + 256 * 4;           // [gather warp][kIndexRing][32]
 constexpr uint32_t kOffLive = kOffIndex + kGatherWarps * kIndexRing * 128;   // [kIndexRing][CTA] masks
 constexpr uint32_t kOffBars = kOffLive + kIndexRing * 2 * 4;
 static_assert(kRawStages + kStages + 1 < kIndexRing && kIndexAhead < kIndexRing,
@@ -220,10 +225,11 @@ __device__ __forceinline__ uint4 pack8(const float* v, float f) {
 // Row `row` of a query tile (blocks of 64 rows of 64 dims, 128-byte swizzle) into this thread's
 // lane of tensor memory at `dst`.  A is read by the tensor cores from both halves of the lanes,
 // each of which produces half of the columns, so both hold every row.
-__device__ __forceinline__ void query_to_tmem(uint32_t tile, int row, uint32_t dst) {
+// This call moves blocks `first` .. `first` + 2.
+__device__ __forceinline__ void query_to_tmem(uint32_t tile, int row, int first, uint32_t dst) {
     const uint32_t src = tile + row * kRowBytes + ((row & 7) << 4);
 #pragma unroll 1
-    for (int b = 0; b < kQTmemBlocks; ++b) {
+    for (int b = first; b < first + kQTmemBlocks / 2; ++b) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {   // 32 dims
             uint4 v[4];
@@ -496,18 +502,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         }
     } else {
         // ------------------------------------------------------------- softmax, epilogue
-        // Lane L of the 128: head L % 64 of this CTA; of a chunk the records of CTA L / 64; of
-        // the output the dims 256 (L / 64) ...  The two lanes of a head exchange their maxima.
+        // Tensor-memory lane L: head L % 64 of this CTA; of a chunk the records of CTA L / 64; of
+        // the output the dims 256 (L / 64) ...  Two warps share a lane, one for each half of its
+        // columns (records, dims), so four threads have a head; they exchange maxima and sums.
+        const int quarter = warp & 3, part = warp >> 2;
         const int row = (warp & 1) * 32 + lane;
-        const int half = warp >> 1;
+        const int half = quarter >> 1;
         const int head = static_cast<int>(rank) * kPairHeads + row;
-        const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-        float* const maxima = reinterpret_cast<float*>(smem + kOffMax);
-        float* const sums = reinterpret_cast<float*>(smem + kOffSum);
-        const int self = half * 64 + row, peer = self ^ 64;
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        float* const maxima = reinterpret_cast<float*>(smem + kOffMax) + row;
+        float* const sums = reinterpret_cast<float*>(smem + kOffSum) + row;
+        const int self = (part * 2 + half) * 64;
         const uint32_t p_full = map_rank(smem_addr(&bars->p_full[0]), 0);
         const float scale = __fmul_rn(p.sm_scale, kLog2e);   // logits in powers of two
-        auto pair_sync = [&]() { group_sync(kHeadsBar + (warp & 1), 64); };   // the two warps of a head
+        auto head_any = [&](bool mine) -> bool {             // whether any of them says so
+            uint32_t any;
+            asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %1, 0;\n barrier.red.or.pred p, %2, 128, p;\n"
+                         " selp.u32 %0, 1, 0, p;\n}" : "=r"(any)
+                         : "r"(mine ? 1u : 0u), "r"(kHeadsBar + (warp & 1)) : "memory");
+            return any != 0u;
+        };
+        auto head_sync = [&]() { group_sync(kHeadsBar + (warp & 1), 128); };   // the warps of a head
         const uint32_t q_full = map_rank(smem_addr(&bars->q_full), 0);
         // A query's first 384 dims wait in shared memory since the query before was moved, and go
         // to tensor memory; the last 128 come straight to where q . K reads them.
@@ -532,7 +547,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 wait_quiet(smem_addr(&bars->q_next), q_parity, ok);
             }
             group_sync(kSoftmaxBar, kSoftmaxWarps * 32);
-            query_to_tmem(smem_addr(smem) + kOffNext, row, tmem + lanes + kQCol);
+            query_to_tmem(smem_addr(smem) + kOffNext, row, part * kQTmemBlocks / 2, tmem + lanes + kQCol);
             fence_async_smem();   // what was read is read, before the copy engine writes there
             tc_fence_before_sync();
             group_sync(kSoftmaxBar, kSoftmaxWarps * 32);
@@ -551,42 +566,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
             const bool last = j + 1 == n || ci + 1 == cut.per_query;   // of this segment
+            const uint32_t live =
+                (reinterpret_cast<const uint32_t*>(smem + kOffLive)[(j & (kIndexRing - 1)) * 2 + half] >>
+                 (16 * part)) & 0xFFFFu;
             // q . K of this chunk is complete, and with it, issued before, p . K of chunk j - 2:
             // the probabilities' buffer is free
-            if (threadIdx.x == kPollThread) wait_quiet(smem_addr(&bars->s_full[j & 1]), (j >> 1) & 1, ok);
-            group_sync(kSoftmaxBar, kSoftmaxWarps * 32);
+            wait_quiet(smem_addr(&bars->s_full[j & 1]), (j >> 1) & 1, ok);
+            __syncwarp();
             tc_fence_after_sync();
-            const uint32_t live =
-                reinterpret_cast<const uint32_t*>(smem + kOffLive)[(j & (kIndexRing - 1)) * 2 + half];
-            float v[32];
-            tmem_ld32(tmem + lanes + kSCol + 32 * (j & 1), v);
+            float v[16];
+            tmem_ld16(tmem + lanes + kSCol + 32 * (j & 1) + 16 * part, v);
             const uint64_t scale2 = f32x2(scale, scale);
 #pragma unroll
-            for (int i = 0; i < 32; i += 2)
+            for (int i = 0; i < 16; i += 2)
                 f32x2_split(mul_f32x2(f32x2(v[i], v[i + 1]), scale2), v[i], v[i + 1]);
-            if (live != kFull) {
+            if (live != 0xFFFFu) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
+                for (int i = 0; i < 16; ++i)
                     if (((live >> i) & 1u) == 0u) v[i] = -INFINITY;
             }
             float top = fmaxf(v[0], v[1]);
 #pragma unroll
-            for (int i = 2; i < 32; i += 2) top = fmaxf(top, fmaxf(v[i], v[i + 1]));
-            maxima[(j & 1) * 128 + self] = top;
-            pair_sync();
-            top = fmaxf(top, maxima[(j & 1) * 128 + peer]);
-            const bool rise = top > m + kLag || (m == -INFINITY && top > m);
-            if (__any_sync(kFull, rise)) {
+            for (int i = 2; i < 16; i += 2) top = fmaxf(top, fmaxf(v[i], v[i + 1]));
+            // Rarely a logit is far above its head's reference; the head's four threads learn of
+            // it by the barrier alone, and only then exchange their maxima.
+            if (head_any(top > m + kLag || (m == -INFINITY && top > m))) {
+                maxima[self] = top;
+                head_sync();
+                top = fmaxf(fmaxf(maxima[0], maxima[64]), fmaxf(maxima[128], maxima[192]));
+                head_sync();   // read before they are written again
+                const bool rise = top > m + kLag || (m == -INFINITY && top > m);
                 const float fix = rise ? exp2_approx(__fsub_rn(m, top)) : 1.0f;
                 if (rise) m = top;
                 l = __fmul_rn(l, fix);
                 if (!fresh) {
                     // the products of the chunk before are in the accumulator
-                    if (lane == 0) wait_quiet(smem_addr(&bars->o_done[(j - 1) & 1]), ((j - 1) >> 1) & 1, ok);
+                    wait_quiet(smem_addr(&bars->o_done[(j - 1) & 1]), ((j - 1) >> 1) & 1, ok);
                     __syncwarp();
                     tc_fence_after_sync();
 #pragma unroll 1
-                    for (int c = 0; c < 256; c += 32) {
+                    for (int c = 128 * part; c < 128 * part + 128; c += 32) {
                         float t[32];
                         tmem_ld32(tmem + lanes + c, t);
 #pragma unroll
@@ -599,26 +618,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
             const float ref = m == -INFINITY ? 0.0f : __fsub_rn(m, kLift);
             const uint64_t ref2 = f32x2(-ref, -ref);
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
+            for (int i = 0; i < 16; i += 2) {
                 f32x2_split(add_f32x2(f32x2(v[i], v[i + 1]), ref2), v[i], v[i + 1]);
                 v[i] = exp2_flush(v[i]);
                 v[i + 1] = exp2_flush(v[i + 1]);
             }
             uint64_t sum2 = add_f32x2(f32x2(v[0], v[1]), f32x2(v[2], v[3]));
-            uint64_t sum2b = add_f32x2(f32x2(v[4], v[5]), f32x2(v[6], v[7]));
 #pragma unroll
-            for (int i = 8; i < 32; i += 4) {
-                sum2 = add_f32x2(sum2, f32x2(v[i], v[i + 1]));
-                sum2b = add_f32x2(sum2b, f32x2(v[i + 2], v[i + 3]));
-            }
+            for (int i = 4; i < 16; i += 4)
+                sum2 = add_f32x2(sum2, add_f32x2(f32x2(v[i], v[i + 1]), f32x2(v[i + 2], v[i + 3])));
             float sum_a, sum_b;
-            f32x2_split(add_f32x2(sum2, sum2b), sum_a, sum_b);
+            f32x2_split(sum2, sum_a, sum_b);
             l = __fadd_rn(l, __fadd_rn(sum_a, sum_b));
-            uint8_t* const prow = smem + kOffP + (j & 1) * kPBytes + (row >> 3) * 1024 +
-                                  (row & 7) * kRowBytes;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-                st16(prow + (((half * 4 + c) ^ (row & 7)) << 4), pack8(v + 8 * c));
+            const uint32_t prow = smem_addr(smem + kOffP) + (j & 1) * kPBytes + row * kRowBytes +
+                                  ((half * 4 + part * 2 ^ (row & 7)) << 4);
+            sts16(prow, pack8(v));
+            sts16(prow ^ 16u, pack8(v + 8));
             fence_async_smem();
             tc_fence_before_sync();
             __syncwarp();
@@ -629,9 +644,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 // multiplied while this one is written out
                 if (j + 1 < n) query(qi + 1);
                 sums[self] = l;
-                pair_sync();
-                const float total = __fadd_rn(half == 0 ? l : sums[peer], half == 0 ? sums[peer] : l);
-                pair_sync();   // read before the next segment's sums
+                head_sync();
+                const float total = __fadd_rn(__fadd_rn(sums[0], sums[64]), __fadd_rn(sums[128], sums[192]));
+                head_sync();   // read before the next segment's sums
                 if (lane == 0) wait_quiet(smem_addr(&bars->o_done[j & 1]), (j >> 1) & 1, ok);
                 ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
                 tc_fence_after_sync();
@@ -640,30 +655,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 const float lse2 =
                     total == 0.0f ? -INFINITY : __fadd_rn(__fsub_rn(m, kLift), log2f(total));
                 // A piece that does not begin its query is its pair's first: slot 0.  Rows leave
-                // through the warp's quarter of the probabilities' buffers, free now, so that
-                // eight lanes write 128 bytes of one row.
+                // through the warp's eighth of the probabilities' buffers, free now, so that
+                // four lanes write 64 bytes of one row.
                 const int64_t slot = 2 * pair + (seg == 0 ? 1 : 0);
                 float* const pieces = static_cast<float*>(p.workspace);
                 const int64_t at = (whole ? qi : slot) * p.num_heads;
-                uint8_t* const dst = whole ? static_cast<uint8_t*>(p.out) + at * 1024 + half * 512
-                                           : reinterpret_cast<uint8_t*>(pieces + at * 512) + half * 1024;
                 const int64_t dst_row = whole ? 1024 : 2048;
-                const uint32_t st = smem_addr(smem + kOffP) + warp * 4096;
+                uint8_t* const dst = (whole ? static_cast<uint8_t*>(p.out)
+                                            : reinterpret_cast<uint8_t*>(pieces)) +
+                                     at * dst_row + (2 * half + part) * (dst_row >> 2);
+                const uint32_t st = smem_addr(smem + kOffP) + warp * 2048;
+                const uint32_t mine = st + lane * 64 + (((lane >> 1) & 3) << 4);
                 const int head0 = static_cast<int>(rank) * kPairHeads + (warp & 1) * 32;
+                const int step = whole ? 32 : 16;
 #pragma unroll 1
-                for (int c = 0; c < 256; c += whole ? 64 : 32) {   // 128 bytes of each row
-                    float t[32];
-                    tmem_ld32(tmem + lanes + c, t);
-                    const uint32_t mine = st + lane * 128 + ((lane & 7) << 4);
+                for (int c = 0; c < 128; c += step) {           // 64 bytes of each row
+                    float t[16];
+                    tmem_ld16(tmem + lanes + 128 * part + c, t);
                     if (whole) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) sts16(mine ^ (i << 4), pack8(t + 8 * i, inv));
-                        tmem_ld32(tmem + lanes + c + 32, t);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) sts16(mine ^ ((4 + i) << 4), pack8(t + 8 * i, inv));
+                        sts16(mine, pack8(t, inv));
+                        sts16(mine ^ 16u, pack8(t + 8, inv));
+                        tmem_ld16(tmem + lanes + 128 * part + c + 16, t);
+                        sts16(mine ^ 32u, pack8(t, inv));
+                        sts16(mine ^ 48u, pack8(t + 8, inv));
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
+                        for (int i = 0; i < 4; ++i)
                             sts16(mine ^ (i << 4),
                                   make_uint4(__float_as_uint(__fmul_rn(t[4 * i], inv)),
                                              __float_as_uint(__fmul_rn(t[4 * i + 1], inv)),
@@ -671,16 +688,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                                              __float_as_uint(__fmul_rn(t[4 * i + 3], inv))));
                     }
                     __syncwarp();
-                    uint8_t* const to = dst + (whole ? 2 : 4) * c + (lane & 7) * 16;
+                    uint8_t* const to = dst + c * (whole ? 2 : 4) + (lane & 3) * 16;
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = 4 * i + (lane >> 3);
-                        const uint4 v = lds16_at(st + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-                        if (head0 + r < p.num_heads && ok) st16(to + (head0 + r) * dst_row, v);
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 8 * i + (lane >> 2);
+                        const uint4 x = lds16_at(st + r * 64 + (((lane ^ (r >> 1)) & 3) << 4));
+                        if (head0 + r < p.num_heads && ok) st16(to + (head0 + r) * dst_row, x);
                     }
                     __syncwarp();
                 }
-                if (half == 0 && head < p.num_heads && ok) {
+                if (half == 0 && part == 0 && head < p.num_heads && ok) {
                     if (whole) p.lse[at + head] = __fmul_rn(lse2, kLn2);
                     else
                         pieces[2 * static_cast<int64_t>(cut.pairs) * p.num_heads * 512 + at + head] = lse2;
