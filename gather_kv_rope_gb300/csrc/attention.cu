@@ -70,6 +70,7 @@ constexpr int kQTmemBlocks = 6;          // blocks of 64 dims of the query in te
 constexpr uint32_t kQBytes = (8 - kQTmemBlocks) * kQBlockBytes;   // and in shared memory
 constexpr uint32_t kPBytes = kPairHeads * kRowBytes;        // probabilities of a chunk, bf16
 constexpr uint32_t kTmemCols = 512;
+constexpr int kMaxHeadsTile = 128;
 constexpr uint32_t kSCol = 256;          // logits: two buffers of 32 columns; output at 0
 constexpr uint32_t kQCol = 320;          // the query's first 384 dims, two to a column
 static_assert(kQCol + kQTmemBlocks * 32 <= kTmemCols, "tensor memory");
@@ -796,93 +797,320 @@ __global__ void __launch_bounds__(128 * kGroups)
         p.lse[at] = sum == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(m, log2f(sum)), kLn2);
 }
 
-constexpr int kHeadsPerBlock = 8;
-constexpr int kTile = 32;
+// ---------------------------------------------------------------- weights
+//
+// weights[i, k] += sum over h of exp(s[i, h, k] - lse[i, h]): the logits once more, now that
+// every head's lse is known (keeping them would take num_heads * 4 bytes an entry, 64 times
+// what the record has).  Here the records are the rows of the product (M = 128) and the heads
+// its columns, so a thread has all heads of one record and sums them in its registers, in the
+// heads' order.  One CTA an SM; a tile is 128 records of one query.
+//   * one warp fetches indices, scale rows and, four half-rows a lane, the codes;
+//   * 16 warps dequantise 64 dims of the tile at a time (16 KB, three stages);
+//   * one thread multiplies them by the query's heads, which lie in shared memory, into one of
+//     two accumulators;
+//   * four warps turn the accumulator into the records' sums and add them to the weights.
 
-// Records k0 .. k0 + 31 of query qi as bf16 rows of 1024 bytes in `rows` (zeros for an entry
-// that is none); returns the bits of the valid ones.  Every thread of the block calls it.
-__device__ __forceinline__ uint32_t load_tile(const AttentionParams& p, int64_t qi, int64_t k0,
-                                              uint8_t* rows, uint32_t* valid, int warp, int lane) {
-    __syncthreads();   // the previous tile has been read
-    if (threadIdx.x == 0) *valid = 0;
-    __syncthreads();
-    for (int r = warp; r < kTile; r += kHeadsPerBlock) {
-        const int64_t k = k0 + r;
-        const int32_t idx = k < p.topk ? __ldg(p.indices + qi * p.index_stride + k) : -1;
-        uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-        if (idx >= 0 && idx < p.num_slots) {
-            uint32_t page, row;
-            page_row(static_cast<uint32_t>(idx), static_cast<uint32_t>(p.block_size), page, row);
-            const uint8_t* const base = p.cache + static_cast<int64_t>(page) * p.page_stride;
-            const uint32_t* const data =
-                reinterpret_cast<const uint32_t*>(base + static_cast<int64_t>(row) * 256);
-            const uint8_t* const sc = base + static_cast<int64_t>(p.block_size) * 256 + row * 16;
-            a = dequant8_e2m1(__ldg(data + lane), e2m1_factor(__ldg(sc + (lane >> 2))));
-            b = dequant8_e2m1(__ldg(data + 32 + lane), e2m1_factor(__ldg(sc + 8 + (lane >> 2))));
-            if (lane == 0) atomicOr(valid, 1u << r);
-        } else if (idx != -1 && lane == 0) {
-            report(p.err, kErrIndex);
-        }
-        st16(rows + r * 1024 + 16 * lane, a);
-        st16(rows + r * 1024 + 512 + 16 * lane, b);
-    }
-    __syncthreads();
-    return *valid;
-}
+constexpr int kTileKeys = 128;
+constexpr int kWSoftWarps = 4;                              // warp w: tensor-memory lanes 32w ..
+constexpr int kWDequantWarps = 16;
+constexpr int kWMmaWarp = kWSoftWarps + kWDequantWarps;
+constexpr int kWGatherWarp = kWMmaWarp + 1;
+constexpr int kWeightThreads = (kWGatherWarp + 1) * 32;
+constexpr int kWRaw = 2;                                    // half-rows (128 bytes) of a tile in flight
+constexpr int kWStages = 3;                                 // 64 dims of a tile
+constexpr int kWIndexRing = 4, kWIndexAhead = 3;            // tiles of indices
+constexpr uint32_t kWStageBytes = kTileKeys * kRowBytes;
+constexpr uint32_t kWOffStages = kMaxHeadsTile * 1024;      // after the query: 8 blocks of 64 dims
+constexpr uint32_t kWOffRaw = kWOffStages + kWStages * kWStageBytes;
+constexpr uint32_t kWRawBytes = kTileKeys * 128;
+constexpr uint32_t kWOffScales = kWOffRaw + kWRaw * kWRawBytes;        // [2 tiles][128][16]
+constexpr uint32_t kWOffLse = kWOffScales + 2 * kTileKeys * 16;        // [128] lse in powers of two
+constexpr uint32_t kWOffIndex = kWOffLse + kMaxHeadsTile * 4;          // [kWIndexRing][128]
+constexpr uint32_t kWOffLive = kWOffIndex + kWIndexRing * kTileKeys * 4;   // [8][4]
+constexpr uint32_t kWOffBars = kWOffLive + 8 * 16;
 
-// This lane's 16 dims of a row's dot product with x, summed over the warp.
-__device__ __forceinline__ float dot(const float (&x)[16], const uint8_t* row, int lane) {
-    float v[16];
-    unpack_bf16x8(lds16(row + 16 * lane), v);
-    unpack_bf16x8(lds16(row + 512 + 16 * lane), v + 8);
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) s = __fmaf_rn(x[i], v[i], s);
-    return warp_sum(s);
-}
+struct alignas(8) WeightBarriers {
+    uint64_t q_full, q_free;                 // the query is in place; its last product is done
+    uint64_t raw[kWRaw], raw_empty[kWRaw];   // half-rows landed (the first half's with the scales); read
+    uint64_t scales_empty[2];                // a tile's scales are read
+    uint64_t a_full[kWStages], a_empty[kWStages];
+    uint64_t acc_full[2], acc_empty[2];
+    uint32_t tmem_base;
+    int32_t timed_out;
+};
+constexpr size_t kWeightSmem = 1024 + kWOffBars + sizeof(WeightBarriers);
+static_assert(kWeightSmem <= 227 * 1024, "a CTA's shared memory");
 
-__device__ __forceinline__ void load_head(const AttentionParams& p, int64_t qi, int h, int lane,
-                                          float (&x)[16]) {
-    const uint8_t* const row = static_cast<const uint8_t*>(p.q) + (qi * p.num_heads + h) * 1024;
-    unpack_bf16x8(*reinterpret_cast<const uint4*>(row + 16 * lane), x);
-    unpack_bf16x8(*reinterpret_cast<const uint4*>(row + 512 + 16 * lane), x + 8);
-}
-
-// weights[qi, k] += sum over the heads of exp(s - lse): the logits once more, now that each
-// head's lse is known; a block takes 32 entries of a query, a warp every eighth head.
-__global__ void __launch_bounds__(kHeadsPerBlock * 32) weight_kernel(const AttentionParams p,
-                                                                     const int64_t tiles) {
-    __shared__ __align__(16) uint8_t rows[kTile * 1024];
-    __shared__ uint32_t valid;
-    __shared__ float part[kHeadsPerBlock][32];
-    const int lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kWeightThreads, 1)
+    weight_kernel(const AttentionParams p, const int64_t tiles, const int32_t n_pad,
+                  const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap cache_map) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* const smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    WeightBarriers* const bars = reinterpret_cast<WeightBarriers*>(smem + kWOffBars);
     const int warp = threadIdx.x >> 5;
-    const int64_t qi = blockIdx.x / tiles;
-    const int64_t k0 = (blockIdx.x - qi * tiles) * kTile;
+    const int lane = threadIdx.x & 31;
+    // tiles i0 .. i0 + n - 1 of all queries' tiles, one query after another
+    const int64_t total = p.num_queries * tiles;
+    const int64_t i0 = total * blockIdx.x / gridDim.x;
+    const int n = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x - i0);
+
+    if (warp == kWMmaWarp) {
+        tmem_alloc(smem_addr(&bars->tmem_base), 256);
+        tmem_relinquish();
+    }
+    if (threadIdx.x == 0) {
+        mbar_init(smem_addr(&bars->q_full), 1);
+        mbar_init(smem_addr(&bars->q_free), 1);
+        for (int s = 0; s < kWRaw; ++s) {
+            mbar_init(smem_addr(&bars->raw[s]), 1 + 32);
+            mbar_init(smem_addr(&bars->raw_empty[s]), kWDequantWarps);
+        }
+        for (int s = 0; s < kWStages; ++s) {
+            mbar_init(smem_addr(&bars->a_full[s]), kWDequantWarps);
+            mbar_init(smem_addr(&bars->a_empty[s]), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_addr(&bars->scales_empty[s]), kWDequantWarps);
+            mbar_init(smem_addr(&bars->acc_full[s]), 1);
+            mbar_init(smem_addr(&bars->acc_empty[s]), kWSoftWarps);
+        }
+        bars->timed_out = 0;
+        mbar_init_fence();
+    }
     pdl_wait_previous();
     pdl_release_next();
-    const uint32_t live = load_tile(p, qi, k0, rows, &valid, warp, lane);
-    const float scale = __fmul_rn(p.sm_scale, kLog2e);
-    float sum = 0.0f;
-    for (int h = warp; h < p.num_heads; h += kHeadsPerBlock) {
-        float x[16];
-        load_head(p, qi, h, lane, x);
-        const float lse = __fmul_rn(p.lse[qi * p.num_heads + h], kLog2e);
-        float s = -INFINITY;
-        for (int k = 0; k < kTile; ++k) {
-            const float d = dot(x, rows + k * 1024, lane);
-            if (lane == k && ((live >> k) & 1u) != 0u) s = __fmul_rn(d, scale);
-        }
-        if (((live >> lane) & 1u) != 0u) sum = __fadd_rn(sum, exp2_approx(__fsub_rn(s, lse)));
-    }
-    part[warp][lane] = sum;
+    tc_fence_before_sync();
     __syncthreads();
-    if (warp == 0 && ((live >> lane) & 1u) != 0u) {
-        float t = part[0][lane];
-        for (int w = 1; w < kHeadsPerBlock; ++w) t = __fadd_rn(t, part[w][lane]);
-        float* const dst = p.weights + qi * p.weight_stride + k0 + lane;
-        *dst = __fadd_rn(*dst, t);
+    tc_fence_after_sync();
+    const uint32_t tmem = bars->tmem_base;
+    bool ok = true;
+    int64_t qi = i0 / tiles;
+    int64_t ti = i0 - qi * tiles;
+
+    if (warp >= kWSoftWarps && warp < kWMmaWarp) {
+        // ------------------------------------------------------------- dequantisation
+        // A stage is 128 records x 64 dims; a warp takes eight records, a lane 16 dims of one.
+        const int w = warp - kWSoftWarps;
+        const int r = w * 8 + (lane & 7);
+        const int v = lane >> 3;
+        const uint32_t raw0 = smem_addr(smem + kWOffRaw) + r * 128 + (v & 1) * 8;
+        const uint32_t scale0 = smem_addr(smem + kWOffScales) + r * 16 + (v >> 1);
+        const uint32_t dst = smem_addr(smem + kWOffStages) + r * kRowBytes + ((2 * v ^ (r & 7)) << 4);
+        Ring<kWRaw> rw;
+        Ring<kWStages> st;
+        int filled = 0;
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+#pragma unroll 1
+            for (int h = 0; h < 8; ++h) {   // 64 dims
+                if (w == 2 && lane == 0) {
+                    if ((h & 3) == 0) wait_quiet(smem_addr(&bars->raw[rw.s]), rw.parity, ok);
+                    if (filled >= kWStages) wait_quiet(smem_addr(&bars->a_empty[st.s]), st.parity ^ 1u, ok);
+                    ++filled;
+                }
+                group_sync(kOwnBar, kWDequantWarps * 32);
+                uint32_t w0, w1, s;
+                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1)
+                             : "r"(raw0 + rw.s * kWRawBytes + (((h & 3) * 2 + (v >> 1) ^ (r & 7)) << 4)) : "memory");
+                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(s)
+                             : "r"(scale0 + (j & 1) * kTileKeys * 16 + 2 * h) : "memory");
+                const uint32_t f = e2m1_factor(s), out = dst + st.s * kWStageBytes;
+                sts16(out, dequant8_e2m1(w0, f));
+                sts16(out ^ 16u, dequant8_e2m1(w1, f));
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    if ((h & 3) == 3) mbar_arrive(smem_addr(&bars->raw_empty[rw.s]));
+                    if (h == 7) mbar_arrive(smem_addr(&bars->scales_empty[j & 1]));
+                    mbar_arrive(smem_addr(&bars->a_full[st.s]));
+                }
+                if ((h & 3) == 3) rw.next();
+                st.next();
+            }
+        }
+    } else if (warp == kWGatherWarp) {
+        // ------------------------------------------------------------- raw records
+        // Lane i has records 4i .. 4i + 3 of the tile.
+        const uint32_t ring = smem_addr(smem + kWOffIndex) + 16 * lane;
+        int ahead = 0;
+        auto fetch = [&]() {
+            if (ahead < n) {
+                const uint32_t to = ring + (ahead % kWIndexRing) * kTileKeys * 4;
+                const int32_t* const row = p.indices + qi * p.index_stride;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t k = ti * kTileKeys + 4 * lane + i;
+                    if (k < p.topk) cp_async4(to + 4 * i, row + k);
+                    else asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + 4 * i), "r"(-1) : "memory");
+                }
+                if (++ti == tiles) {
+                    ti = 0;
+                    ++qi;
+                }
+                ++ahead;
+            }
+            cp_async_commit();
+        };
+#pragma unroll 1
+        for (int i = 0; i < kWIndexAhead; ++i) fetch();
+        Ring<kWRaw> rw;
+        int half_rows = 0;
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+            cp_async_wait<kWIndexAhead - 1>();
+            const uint4 idx4 = lds16_at(ring + (j % kWIndexRing) * kTileKeys * 4);
+            const int32_t idx[4] = {static_cast<int32_t>(idx4.x), static_cast<int32_t>(idx4.y),
+                                    static_cast<int32_t>(idx4.z), static_cast<int32_t>(idx4.w)};
+            int32_t r4[4];
+            const uint8_t* scales[4];
+            uint32_t live = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const bool is = idx[i] >= 0 && idx[i] < p.num_slots;   // else: finite values, not used
+                live |= is ? 1u << i : 0u;
+                uint32_t page, r;
+                page_row(is ? static_cast<uint32_t>(idx[i]) : 0u, static_cast<uint32_t>(p.block_size), page, r);
+                const int64_t at = static_cast<int64_t>(page) * p.page_stride;
+                r4[i] = static_cast<int32_t>(at >> 8) + static_cast<int32_t>(r);
+                scales[i] = p.cache + at + static_cast<int64_t>(p.block_size) * 256 + r * 16u;
+            }
+            smem[kWOffLive + (j & 7) * 32 + lane] = static_cast<uint8_t>(live);
+#pragma unroll 1
+            for (int h = 0; h < 2; ++h) {
+                if (lane == 0) {
+                    if (half_rows >= kWRaw) wait_quiet(smem_addr(&bars->raw_empty[rw.s]), rw.parity ^ 1u, ok);
+                    if (h == 0 && j >= 2) wait_quiet(smem_addr(&bars->scales_empty[j & 1]), ((j >> 1) - 1) & 1, ok);
+                }
+                __syncwarp();
+                const uint32_t bar = smem_addr(&bars->raw[rw.s]);
+                if (h == 0) {
+                    const uint32_t to = smem_addr(smem + kWOffScales) + (j & 1) * kTileKeys * 16 + 64 * lane;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) cp_async16_or_zeros(to + 16 * i, scales[i], (live >> i & 1u) != 0u);
+                }
+                cp_async_arrive(bar);
+                if (lane == 0) mbar_expect_tx(bar, kWRawBytes);
+                __syncwarp();
+                tma_gather4(smem_addr(smem + kWOffRaw) + rw.s * kWRawBytes + 512 * lane, &cache_map, bar, h * 128,
+                            r4[0], r4[1], r4[2], r4[3]);
+                rw.next();
+                ++half_rows;
+            }
+            fetch();
+        }
+        // the copies in flight land before the CTA leaves
+        cp_async_wait<0>();
+        for (int i = half_rows > kWRaw ? half_rows - kWRaw : 0; i < half_rows; ++i)
+            if (lane == 0) wait_quiet(smem_addr(&bars->raw[i % kWRaw]), (i / kWRaw) & 1, ok);
+        __syncwarp();
+    } else if (warp == kWMmaWarp) {
+        // ------------------------------------------------------------- products
+        const uint32_t elected = elect_lane();
+        const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n_pad >> 3) << 17) |
+                               (static_cast<uint32_t>(128 >> 4) << 24);
+        const uint64_t a_desc = sw128_desc(smem_addr(smem + kWOffStages));
+        const uint64_t q_desc = sw128_desc(smem_addr(smem));
+        const uint32_t a_lo = static_cast<uint32_t>(a_desc), q_lo = static_cast<uint32_t>(q_desc);
+        const uint32_t q_block = static_cast<uint32_t>(n_pad) * kRowBytes;   // 64 dims of the query
+        Ring<kWStages> st;
+        uint32_t loads = 0;
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+            if (j == 0 || ti == 0) {   // the next query, once the last product of the one before is done
+                if (j > 0) wait_quiet(smem_addr(&bars->q_free), (loads - 1) & 1, ok);
+                __syncwarp();
+                if (elected && ok) {
+                    mbar_expect_tx(smem_addr(&bars->q_full), 8 * q_block);
+#pragma unroll 1
+                    for (int b = 0; b < 8; ++b)
+                        tma_load_3d(smem_addr(smem) + b * q_block, &q_map, smem_addr(&bars->q_full), 64 * b, 0,
+                                    static_cast<int32_t>(qi));
+                }
+                wait_quiet(smem_addr(&bars->q_full), loads & 1, ok);
+                ++loads;
+            }
+            if (j >= 2) wait_quiet(smem_addr(&bars->acc_empty[j & 1]), ((j >> 1) - 1) & 1, ok);
+#pragma unroll 1
+            for (int h = 0; h < 8; ++h) {
+                wait_quiet(smem_addr(&bars->a_full[st.s]), st.parity, ok);
+                __syncwarp();
+                tc_fence_after_sync();
+                if (elected) {
+                    const uint32_t a = a_lo + st.s * (kWStageBytes >> 4);
+                    const uint32_t q = q_lo + ((h * q_block) >> 4);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16_ss(tmem + 128 * (j & 1), desc_at(a_desc, a + 2 * k), desc_at(q_desc, q + 2 * k),
+                                    idesc, h != 0 || k != 0);
+                    mma_commit(smem_addr(&bars->a_empty[st.s]));
+                }
+                __syncwarp();
+                st.next();
+            }
+            if (elected) mma_commit(smem_addr(&bars->acc_full[j & 1]));
+            if (++ti == tiles) {
+                ti = 0;
+                ++qi;
+                if (elected && j + 1 < n) mma_commit(smem_addr(&bars->q_free));
+            }
+            __syncwarp();
+        }
+    } else {
+        // ------------------------------------------------------------- sums
+        float* const lse = reinterpret_cast<float*>(smem + kWOffLse);
+        const float scale = __fmul_rn(p.sm_scale, kLog2e);
+        const uint64_t scale2 = f32x2(scale, scale);
+        const int key = warp * 32 + lane;
+#pragma unroll 1
+        for (int j = 0; j < n; ++j) {
+            if (j == 0 || ti == 0) {
+                group_sync(kSoftmaxBar, kWSoftWarps * 32);   // the query before is read
+                const int h = threadIdx.x;                   // 0 .. 127
+                lse[h] = h < p.num_heads
+                             ? __fmul_rn(-kLog2e, p.lse[qi * p.num_heads + h])
+                             : -INFINITY;                    // no head: exp2(-inf) = 0
+                group_sync(kSoftmaxBar, kWSoftWarps * 32);
+            }
+            wait_quiet(smem_addr(&bars->acc_full[j & 1]), (j >> 1) & 1, ok);
+            __syncwarp();
+            tc_fence_after_sync();
+            const bool live = (smem[kWOffLive + (j & 7) * 32 + (key >> 2)] >> (key & 3) & 1) != 0;
+            uint64_t sum2 = f32x2(0.0f, 0.0f);
+#pragma unroll 1
+            for (int c = 0; c < n_pad; c += 16) {
+                float v[16];
+                tmem_ld16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + 128 * (j & 1) + c, v);
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const float4 m = *reinterpret_cast<const float4*>(lse + c + i);
+                    float a, b;
+                    f32x2_split(fma_f32x2(f32x2(v[i], v[i + 1]), scale2, f32x2(m.x, m.y)), a, b);
+                    sum2 = add_f32x2(sum2, f32x2(exp2_flush(a), exp2_flush(b)));
+                    f32x2_split(fma_f32x2(f32x2(v[i + 2], v[i + 3]), scale2, f32x2(m.z, m.w)), a, b);
+                    sum2 = add_f32x2(sum2, f32x2(exp2_flush(a), exp2_flush(b)));
+                }
+            }
+            tc_fence_before_sync();
+            warp_arrive(smem_addr(&bars->acc_empty[j & 1]), lane);
+            ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
+            if (live && ok) {
+                float even, odd;
+                f32x2_split(sum2, even, odd);
+                float* const dst = p.weights + qi * p.weight_stride + ti * kTileKeys + key;
+                *dst = __fadd_rn(*dst, __fadd_rn(even, odd));
+            }
+            if (++ti == tiles) {
+                ti = 0;
+                ++qi;
+            }
+        }
     }
+    if (!ok) atomicOr(&bars->timed_out, 1);
+    tc_fence_before_sync();
+    __syncthreads();
+    if (threadIdx.x == 0 && bars->timed_out != 0) report(p.err, kErrTimeout);
+    if (warp == kWMmaWarp) tmem_dealloc(tmem, 256);
 }
 
 // The pairs of CTAs that the current device holds at once (cached per device).
@@ -961,15 +1189,15 @@ void find_cuts(const Cut& cut, Cuts* cuts, int* most) {
     }
 }
 
-// The queries [num_queries, num_heads, 512] as a 3-D tensor map with boxes of 64 dims x 64
+// The queries [num_queries, num_heads, 512] as a 3-D tensor map with boxes of 64 dims x `heads`
 // heads and the 128-byte swizzle; heads past num_heads read as zeros.
-cudaError_t q_tensor_map(const AttentionParams& p, CUtensorMap* map) {
+cudaError_t q_tensor_map(const AttentionParams& p, int heads, CUtensorMap* map) {
     const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (encode == nullptr) return cudaErrorNotSupported;
     const cuuint64_t dims[3] = {512, static_cast<cuuint64_t>(p.num_heads),
                                 static_cast<cuuint64_t>(p.num_queries)};
     const cuuint64_t strides[2] = {1024, static_cast<cuuint64_t>(1024) * p.num_heads};
-    const cuuint32_t box[3] = {64, kPairHeads, 1};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(heads), 1};
     const cuuint32_t step[3] = {1, 1, 1};
     const CUresult r =
         encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p.q), dims, strides, box,
@@ -1012,7 +1240,7 @@ cudaError_t launch_sparse_attention(const AttentionParams& p, cudaStream_t strea
     cudaError_t e = make_cut(p.num_queries, p.topk, &cut);
     if (e != cudaSuccess) return e;
     CUtensorMap q_map, cache_map;
-    e = q_tensor_map(p, &q_map);
+    e = q_tensor_map(p, kPairHeads, &q_map);
     if (e == cudaSuccess) e = cache_tensor_map(p, &cache_map);
     if (e != cudaSuccess) return e;
     e = launch_kernel(attend_kernel, 2 * static_cast<int64_t>(cut.pairs), kAttendThreads, kAttendSmem,
@@ -1029,9 +1257,17 @@ cudaError_t launch_sparse_attention(const AttentionParams& p, cudaStream_t strea
         if (e != cudaSuccess) return e;
     }
     if (p.weights == nullptr || p.topk == 0) return e;
-    const int64_t tiles = (p.topk + kTile - 1) / kTile;
-    return launch_kernel(weight_kernel, p.num_queries * tiles, kHeadsPerBlock * 32, 0, stream,
-                         p.pdl, p, tiles);
+    const int n_pad = (p.num_heads + 15) / 16 * 16;   // columns of the product
+    e = q_tensor_map(p, n_pad, &q_map);
+    if (e != cudaSuccess) return e;
+    int64_t warps = 0;
+    e = resident_warps(reinterpret_cast<const void*>(weight_kernel), kWeightThreads, kWeightSmem, &warps);
+    if (e != cudaSuccess) return e;
+    const int64_t ctas = warps / (kWeightThreads / 32);
+    const int64_t tiles = (p.topk + kTileKeys - 1) / kTileKeys;
+    const int64_t blocks = p.num_queries * tiles < ctas ? p.num_queries * tiles : ctas;
+    return launch_kernel(weight_kernel, blocks, kWeightThreads, kWeightSmem, stream, p.pdl, p, tiles,
+                         n_pad, q_map, cache_map);
 }
 
 }  // namespace gkr
