@@ -16,6 +16,7 @@ std::atomic<int> g_early_metadata{0};
 constexpr int64_t kDefaultStagedMin = 24576;
 constexpr int64_t kDefaultStreamMin = 131072;
 constexpr int64_t kMaxRows = INT64_C(1) << 24;   // queries, list entries of a call at most
+constexpr int64_t kMaxList = INT64_C(1) << 21;   // entries of an eviction list at most
 constexpr int32_t kMaxQHeads = 4096;   // query heads per token (padded) at most
 std::atomic<int64_t> g_staged_min{kDefaultStagedMin};
 std::atomic<int64_t> g_stream_min{kDefaultStreamMin};
@@ -477,7 +478,7 @@ GKR_API gkr_status gkr_kv_evict(const int32_t* indices, int64_t index_stride,
     Policy pol;
     const gkr_status st = resolve_policy(opts, &pol);
     if (st != GKR_OK) return st;
-    if (num_rows < 0 || num_rows > kMaxRows || length < 0 || length > kMaxRows || keep < 0 ||
+    if (num_rows < 0 || num_rows > kMaxRows || length < 0 || length > kMaxList || keep < 0 ||
         keep > length || recent < 0 || recent > keep || index_stride < length ||
         weight_stride < length)
         return GKR_EINVAL;

@@ -407,7 +407,7 @@ GKR_API gkr_status gkr_sparse_attention_workspace(int32_t num_heads, int64_t num
  * No record moves: slots are the unit of allocation, and a freed one can be written next.
  *
  * indices, weights       device; rows at index_stride / weight_stride elements (>= length).
- * num_rows, length       0 .. 2^24 each (0 of either enqueues nothing).
+ * num_rows, length       0 .. 2^24, 0 .. 2^21 (0 of either enqueues nothing).
  * keep, recent           0 <= recent <= keep <= length.
  * kept, kept_weights     device, int32 / fp32 [num_rows, keep] (may be NULL when keep is 0).
  * evicted                device, int64 [num_rows, length - keep] (may be NULL when empty).

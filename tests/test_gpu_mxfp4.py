@@ -367,7 +367,7 @@ def evict_check(gkr, idx, w, keep, recent, pad=0):
 
 
 @pytest.mark.parametrize("B,L", [(1, 1), (3, 2), (2, 31), (5, 33), (2, 1000), (3, 1024), (2, 1025),
-                                 (1, 4097), (4, 2049), (1, 40001)])
+                                 (1, 4097), (4, 2049), (1, 40001), (2, 8192), (2, 8193), (1, 20000)])
 def test_evict_sizes(gkr, B, L):
     rng = np.random.default_rng(B * L)
     idx = rng.permutation(B * L * 2)[:B * L].reshape(B, L).astype(np.int32)
@@ -415,3 +415,17 @@ def test_evict_given_outputs(gkr):
     got = gkr.kv_evict(torch.from_numpy(idx).to(DEV), torch.from_numpy(w).to(DEV), 60, 10, *bufs)
     assert all(a is b for a, b in zip(got, bufs))
     assert all(np.array_equal(x.cpu().numpy(), y) for x, y in zip(got, plain.evict(idx, w, 60, 10)))
+
+
+@pytest.mark.parametrize("L", [8200, 300000])
+def test_evict_ties_across_parts(gkr, L):
+    """Rows split over a cluster: ties, empty entries and the newest ones anywhere; and rows too long
+    for their keys to be held."""
+    rng = np.random.default_rng(L)
+    idx = np.arange(3 * L, dtype=np.int32).reshape(3, L)
+    idx[1, rng.random(L) < 0.5] = -1
+    idx[2, : L // 2] = -1
+    w = rng.integers(0, 3, (3, L)).astype(np.float32)
+    w[2] = 1.0
+    for keep, recent in [(L // 2, 0), (L // 3, L // 4), (L - 1, 7), (5, 5)]:
+        evict_check(gkr, idx, w, keep, recent)
