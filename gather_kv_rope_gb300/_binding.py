@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import contextvars
 import ctypes
+import functools
 import threading
 from pathlib import Path
 
@@ -316,6 +317,25 @@ def _check(cond: bool, msg: str) -> None:
         raise ValueError(msg)
 
 
+# The current stream's handle without a Stream object around it (2 us a call); the public way
+# where torch lacks it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _call(dev: torch.device, fn, *args) -> None:
+    """fn(*args, stream) with `dev` current and its current stream; raises for a bad status.  The
+    device is switched only where it is another one: the small calls are bound by the host."""
+    index = dev.index
+    if index == torch.cuda.current_device():
+        st = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, _raw_stream(index))
+    if st != GKR_OK:
+        _raise(st)
+
+
 def _ptr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
@@ -395,13 +415,9 @@ def kv_insert(kv: torch.Tensor, k_cache: torch.Tensor, slot_mapping: torch.Tenso
     _check_fp8_scale(desc, fp8_scale)
     if fp8_scale is not None:
         _same_cuda_device(kv, fp8_scale)
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
-        st = lib().gkr_kv_insert(_ptr(kv), T, _ptr(k_cache), ctypes.byref(desc),
-                                 _ptr(slot_mapping), _ptr(positions), _ptr(cos_sin_cache),
-                                 cos_sin_cache.shape[0], _ptr(fp8_scale), _ptr(err_flag),
-                                 _opts(launch_opts), stream)
-    _raise(st)
+    _call(dev, lib().gkr_kv_insert, kv.data_ptr(), T, k_cache.data_ptr(), ctypes.byref(desc),
+          slot_mapping.data_ptr(), positions.data_ptr(), cos_sin_cache.data_ptr(),
+          cos_sin_cache.shape[0], _ptr(fp8_scale), _ptr(err_flag), _opts(launch_opts))
 
 
 def rope_quant_insert(kv: torch.Tensor, k_cache: torch.Tensor, slot_mapping: torch.Tensor,
@@ -418,14 +434,10 @@ def rope_quant_insert(kv: torch.Tensor, k_cache: torch.Tensor, slot_mapping: tor
     desc, T, dev = _insert_args(kv, k_cache, slot_mapping, positions, cos_sin_cache,
                                 block_size, record, err_flag)
     _check(desc.record in PACKED, "the compressed insert writes the packed 528 / 584 records")
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
-        st = lib().gkr_rope_quant_insert(_ptr(kv), T, _ptr(k_cache), ctypes.byref(desc),
-                                         _ptr(slot_mapping), _ptr(positions),
-                                         _ptr(cos_sin_cache), cos_sin_cache.shape[0],
-                                         int(compress_ratio), 1 if sanitize_nans else 0,
-                                         _ptr(err_flag), _opts(launch_opts), stream)
-    _raise(st)
+    _call(dev, lib().gkr_rope_quant_insert, kv.data_ptr(), T, k_cache.data_ptr(),
+          ctypes.byref(desc), slot_mapping.data_ptr(), positions.data_ptr(),
+          cos_sin_cache.data_ptr(), cos_sin_cache.shape[0], int(compress_ratio),
+          1 if sanitize_nans else 0, _ptr(err_flag), _opts(launch_opts))
 
 
 def kv_gather(k_cache: torch.Tensor, indices: torch.Tensor, out: torch.Tensor,
@@ -443,12 +455,8 @@ def kv_gather(k_cache: torch.Tensor, indices: torch.Tensor, out: torch.Tensor,
            "out must be a contiguous bf16 tensor of shape indices.shape + (512,)")
     _check_err_flag(err_flag)
     dev = _same_cuda_device(k_cache, indices, out, err_flag, fp8_scale)
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
-        st = lib().gkr_kv_gather(_ptr(k_cache), ctypes.byref(desc), _ptr(indices),
-                                 indices.numel(), _ptr(out), _ptr(fp8_scale), _ptr(err_flag),
-                                 _opts(launch_opts), stream)
-    _raise(st)
+    _call(dev, lib().gkr_kv_gather, k_cache.data_ptr(), ctypes.byref(desc), indices.data_ptr(),
+          indices.numel(), out.data_ptr(), _ptr(fp8_scale), _ptr(err_flag), _opts(launch_opts))
     return out
 
 
@@ -489,15 +497,11 @@ def qnorm_rope_kv_insert(q: torch.Tensor, kv: torch.Tensor, k_cache: torch.Tenso
            "q_out must be a contiguous tensor [tokens, num_heads_padded, 512] of bf16 "
            "(e4m3 codes: float8_e4m3fn or uint8 with q_scale)")
     _same_cuda_device(kv, q, q_out, fp8_scale, q_scale)
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
-        st = lib().gkr_qnorm_rope_kv_insert(_ptr(q), H, Hp, _ptr(q_out), _ptr(q_scale), float(eps),
-                                            1 if apply_q_norm else 0, _ptr(kv), T, _ptr(k_cache),
-                                            ctypes.byref(desc), _ptr(slot_mapping),
-                                            _ptr(positions), _ptr(cos_sin_cache),
-                                            cos_sin_cache.shape[0], _ptr(fp8_scale),
-                                            _ptr(err_flag), _opts(launch_opts), stream)
-    _raise(st)
+    _call(dev, lib().gkr_qnorm_rope_kv_insert, q.data_ptr(), H, Hp, q_out.data_ptr(),
+          _ptr(q_scale), float(eps), 1 if apply_q_norm else 0, kv.data_ptr(), T,
+          k_cache.data_ptr(), ctypes.byref(desc), slot_mapping.data_ptr(), positions.data_ptr(),
+          cos_sin_cache.data_ptr(), cos_sin_cache.shape[0], _ptr(fp8_scale), _ptr(err_flag),
+          _opts(launch_opts))
     return q_out
 
 
@@ -524,30 +528,36 @@ def sparse_logits(q: torch.Tensor, k_cache: torch.Tensor, indices: torch.Tensor,
            "out must be a contiguous fp32 tensor [queries, heads, topk]")
     _check_err_flag(err_flag)
     dev = _same_cuda_device(q, k_cache, indices, out, err_flag, fp8_scale)
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
-        st = lib().gkr_sparse_logits(_ptr(q), H, _ptr(k_cache), ctypes.byref(desc), _ptr(indices),
-                                     Q, K, float(sm_scale), _ptr(fp8_scale), _ptr(out),
-                                     _ptr(err_flag), _opts(launch_opts), stream)
-    _raise(st)
+    _call(dev, lib().gkr_sparse_logits, q.data_ptr(), H, k_cache.data_ptr(), ctypes.byref(desc),
+          indices.data_ptr(), Q, K, float(sm_scale), _ptr(fp8_scale), out.data_ptr(),
+          _ptr(err_flag), _opts(launch_opts))
     return out
 
 
 def _rows(t: torch.Tensor, dtype: torch.dtype, name: str) -> int:
     """Row stride of a 2-D tensor whose rows are contiguous (a slice of wider rows will do)."""
-    _check(t.dtype == dtype and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] <= 1)
-           and (t.stride(0) >= t.shape[1] or t.shape[0] <= 1),
-           f"{name} must be a 2-D {dtype} tensor with contiguous rows".replace("torch.", ""))
-    return max(int(t.stride(0)), int(t.shape[1]))
+    if t.dtype == dtype and t.dim() == 2:
+        rows, cols = t.shape
+        stride, step = t.stride()
+        if (step == 1 or cols <= 1) and (stride >= cols or rows <= 1):
+            return max(stride, cols)
+    raise ValueError(f"{name} must be a 2-D {dtype} tensor with contiguous rows".replace("torch.", ""))
+
+
+@functools.lru_cache(maxsize=256)
+def _attention_workspace(num_heads: int, num_queries: int, topk: int, index: int) -> int:
+    n = ctypes.c_int64()
+    with torch.cuda.device(index):
+        _raise(lib().gkr_sparse_attention_workspace(num_heads, num_queries, topk, ctypes.byref(n)))
+    return int(n.value)
 
 
 def sparse_attention_workspace(num_heads: int, num_queries: int, topk: int,
                                device=None) -> int:
     """Bytes of workspace a sparse_attention call of these sizes needs on a device."""
-    n = ctypes.c_int64()
-    with torch.cuda.device(device):
-        _raise(lib().gkr_sparse_attention_workspace(num_heads, num_queries, topk, ctypes.byref(n)))
-    return int(n.value)
+    dev = torch.device("cuda" if device is None else device)
+    index = torch.cuda.current_device() if dev.index is None else dev.index
+    return _attention_workspace(int(num_heads), int(num_queries), int(topk), index)
 
 
 def sparse_attention(q: torch.Tensor, k_cache: torch.Tensor, indices: torch.Tensor,
@@ -581,9 +591,9 @@ def sparse_attention(q: torch.Tensor, k_cache: torch.Tensor, indices: torch.Tens
     Q, H, K = int(q.shape[0]), int(q.shape[1]), int(indices.shape[1])
     _check(1 <= H <= 128, "sparse_attention takes 1 to 128 heads")
     if out is None:
-        out = torch.empty_like(q)
+        out = q.new_empty((Q, H, HEAD_DIM))
     if lse is None:
-        lse = torch.empty(Q, H, dtype=torch.float32, device=q.device)
+        lse = q.new_empty((Q, H), dtype=torch.float32)
     _check(out.dtype == torch.bfloat16 and out.is_contiguous() and out.shape == q.shape,
            "out must be a contiguous bf16 tensor of q's shape")
     _check(lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == (Q, H),
@@ -594,19 +604,15 @@ def sparse_attention(q: torch.Tensor, k_cache: torch.Tensor, indices: torch.Tens
         _check(weights.shape == indices.shape, "weights must have the shape of indices")
     _check_err_flag(err_flag)
     dev = _same_cuda_device(q, k_cache, indices, out, lse, weights, err_flag, workspace)
-    with torch.cuda.device(dev):
-        if workspace is None:
-            need = sparse_attention_workspace(H, Q, K, dev)
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is None:
+        workspace = q.new_empty(_attention_workspace(H, Q, K, dev.index), dtype=torch.uint8)
+    else:
         _check(workspace.dtype == torch.uint8 and workspace.is_contiguous(),
                "workspace must be a contiguous uint8 tensor")
-        stream = torch.cuda.current_stream(dev).cuda_stream
-        st = lib().gkr_sparse_attention(_ptr(q), H, _ptr(k_cache), ctypes.byref(desc),
-                                        _ptr(indices), istride, Q, K, float(sm_scale), _ptr(out),
-                                        _ptr(lse), _ptr(weights), wstride, _ptr(workspace),
-                                        workspace.numel(), _ptr(err_flag), _opts(launch_opts),
-                                        stream)
-    _raise(st)
+    _call(dev, lib().gkr_sparse_attention, q.data_ptr(), H, k_cache.data_ptr(), ctypes.byref(desc),
+          indices.data_ptr(), istride, Q, K, float(sm_scale), out.data_ptr(), lse.data_ptr(),
+          _ptr(weights), wstride, workspace.data_ptr(), workspace.numel(), _ptr(err_flag),
+          _opts(launch_opts))
     return out, lse
 
 
@@ -636,7 +642,7 @@ def kv_evict(indices: torch.Tensor, weights: torch.Tensor, keep: int, recent: in
 
     def buffer(t, n, dtype, name):
         if t is None:
-            return torch.empty(B, n, dtype=dtype, device=indices.device)
+            return indices.new_empty((B, n), dtype=dtype)
         _check(t.dtype == dtype and t.is_contiguous() and tuple(t.shape) == (B, n),
                f"{name} must be a contiguous {dtype} tensor [{B}, {n}]".replace("torch.", ""))
         return t
@@ -644,10 +650,7 @@ def kv_evict(indices: torch.Tensor, weights: torch.Tensor, keep: int, recent: in
     kept_weights = buffer(kept_weights, keep, torch.float32, "kept_weights")
     evicted = buffer(evicted, L - keep, torch.int64, "evicted")
     dev = _same_cuda_device(indices, weights, kept, kept_weights, evicted)
-    with torch.cuda.device(dev):
-        stream = torch.cuda.current_stream(dev).cuda_stream
-        st = lib().gkr_kv_evict(_ptr(indices), istride, _ptr(weights), wstride, B, L, keep,
-                                recent, _ptr(kept), _ptr(kept_weights), _ptr(evicted),
-                                _opts(launch_opts), stream)
-    _raise(st)
+    _call(dev, lib().gkr_kv_evict, indices.data_ptr(), istride, weights.data_ptr(), wstride, B, L,
+          keep, recent, kept.data_ptr(), kept_weights.data_ptr(), evicted.data_ptr(),
+          _opts(launch_opts))
     return kept, kept_weights, evicted
