@@ -8,8 +8,9 @@
 // every number, -0 with 0.
 //
 // The weight of the last entry to be kept is found by its bits: a weight's 32 bits map to an
-// unsigned key in the order of the values, and three passes, each counting the keys that share
-// the bits found so far by their next 11 (11, 10) bits, fix those.  Then each entry's fate is
+// unsigned key in the order of the values, and four passes, each counting the keys that share
+// the bits found so far by their next 8 bits, fix those.  (Weights are few powers of two apart:
+// eight copies of the counters, taken by the lane, keep most additions off each other's.)  Then each entry's fate is
 // known -- kept if newer, or above that key, or equal to it and among the first `ties` such --
 // and its place is a count of bits: entries are handled as words of 32 bits (live, competing,
 // kept), one ballot each, and prefix sums run over the words.  Counts are whole numbers, so the
@@ -27,8 +28,7 @@ namespace gkr {
 
 namespace {
 
-constexpr int kEvictThreads = 1024;
-constexpr int kBins = 2048;
+constexpr int kBins = 256, kCopies = 8;
 // Keys kept in shared memory up to this many entries a CTA; longer parts read the weights again
 // for each pass.
 constexpr int kCachedKeys = 36864;
@@ -42,6 +42,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 // Exclusive prefix of v over the block's threads; *total = the sum.
+template <int kThreads>
 __device__ __forceinline__ int32_t block_prefix(int32_t v, int32_t* shared, int warp, int lane,
                                                 int32_t* total) {
     int32_t x = v;
@@ -53,20 +54,21 @@ __device__ __forceinline__ int32_t block_prefix(int32_t v, int32_t* shared, int 
     __syncthreads();   // the last use of `shared` is over
     if (lane == 31) shared[warp] = x;
     __syncthreads();
-    const int32_t w = shared[lane];   // 32 warps
+    const int32_t w = lane < kThreads / 32 ? shared[lane] : 0;
     *total = __reduce_add_sync(kFull, w);
     return x - v + __reduce_add_sync(kFull, lane < warp ? w : 0);
 }
 
 // Exclusive prefix sums of the popcounts of bits[0 .. n) into out; returns their total.
+template <int kThreads>
 __device__ __forceinline__ int32_t scan_words(const uint32_t* bits, int32_t* out, int n,
                                               int32_t* shared, int warp, int lane) {
-    const int per = (n + kEvictThreads - 1) / kEvictThreads;
+    const int per = (n + kThreads - 1) / kThreads;
     const int a = threadIdx.x * per, b = a + per < n ? a + per : n;
     int32_t sum = 0;
     for (int i = a; i < b; ++i) sum += __popc(bits[i]);
     int32_t total;
-    int32_t x = block_prefix(sum, shared, warp, lane, &total);
+    int32_t x = block_prefix<kThreads>(sum, shared, warp, lane, &total);
     for (int i = a; i < b; ++i) {
         out[i] = x;
         x += __popc(bits[i]);
@@ -88,16 +90,33 @@ __device__ __forceinline__ int32_t read_peer(const int32_t* p, uint32_t rank) {
     return v;
 }
 
-struct EvictShared {
+// Entries of words w0, w0 + step, ...: their slots (-1 past the part's end) and weights, all loads on
+// their way before the first is used.
+constexpr int kBatch = 8;
+__device__ __forceinline__ void load_batch(const int32_t* idx, const float* wts, int w0, int step,
+                                           int n, int32_t len, int lane, int32_t (&s)[kBatch],
+                                           float (&x)[kBatch]) {
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+        const int32_t i = 32 * (w0 + step * u) + lane;
+        const bool is = w0 + step * u < n && i < len;
+        s[u] = is ? __ldg(idx + i) : -1;
+        x[u] = is ? __ldg(wts + i) : 0.0f;
+    }
+}
+
+struct alignas(16) EvictShared {
     int32_t scan[32];
     int32_t live, strict, tied;          // this CTA's counts, read by the others
     int32_t found[2];
-    int32_t hist[3][kBins];              // one a pass: the others read it at their own time
+    int32_t sum[4][kBins];               // counts, one array a pass: the others read it at their own time
+    alignas(16) int32_t hist[kBins][kCopies];
 };
 
 // words: words of 32 entries of a CTA's part (the same for all CTAs of a row; the last may have
 // less to do); cached: its keys lie in shared memory.
-__global__ void __launch_bounds__(kEvictThreads, 1)
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads, 1)
     evict_kernel(const EvictParams p, const int32_t words, const int32_t cluster, const bool cached) {
     extern __shared__ __align__(16) uint8_t dynamic[];
     EvictShared& sh = *reinterpret_cast<EvictShared*>(dynamic);
@@ -106,6 +125,7 @@ __global__ void __launch_bounds__(kEvictThreads, 1)
     int32_t* const live_before = reinterpret_cast<int32_t*>(some + words);
     int32_t* const some_before = live_before + words;
     uint32_t* const keys = reinterpret_cast<uint32_t*>(some_before + words);
+    constexpr int kWarps = kThreads / 32;
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
     const uint32_t rank = cluster > 1 ? cluster_rank() : 0u;
@@ -132,16 +152,22 @@ __global__ void __launch_bounds__(kEvictThreads, 1)
         return __reduce_add_sync(kFull, v);
     };
 
-    for (int w = warp; w < n; w += 32) {
-        const int32_t i = 32 * w + lane;
-        const bool is = i < len && __ldg(idx + i) >= 0;
-        if (cached) keys[i] = is ? weight_key(__ldg(wts + i)) : 0u;
-        const uint32_t b = __ballot_sync(kFull, is);
-        if (lane == 0) live[w] = b;
+    for (int w0 = warp; w0 < n; w0 += kWarps * kBatch) {
+        int32_t s[kBatch];
+        float x[kBatch];
+        load_batch(idx, wts, w0, kWarps, n, len, lane, s, x);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int w = w0 + kWarps * u;
+            const uint32_t b = __ballot_sync(kFull, s[u] >= 0);
+            if (w < n) {                                 // warp-uniform
+                if (cached) keys[32 * w + lane] = s[u] >= 0 ? weight_key(x[u]) : 0u;
+                if (lane == 0) live[w] = b;
+            }
+        }
     }
-    for (int i = threadIdx.x; i < 3 * kBins; i += kEvictThreads) sh.hist[0][i] = 0;
     __syncthreads();
-    int32_t mine = scan_words(live, live_before, n, sh.scan, warp, lane);
+    int32_t mine = scan_words<kThreads>(live, live_before, n, sh.scan, warp, lane);
     if (threadIdx.x == 0) sh.live = mine;
     sync();
     int32_t live0;                                       // live entries before this part
@@ -149,7 +175,7 @@ __global__ void __launch_bounds__(kEvictThreads, 1)
     const int32_t fresh = p.recent < all ? p.recent : all;   // protected entries
     const int32_t old = all - fresh;                         // the first `old` live ones compete
     const int32_t room = p.keep - fresh < old ? p.keep - fresh : old;
-    for (int w = threadIdx.x; w < n; w += kEvictThreads)
+    for (int w = threadIdx.x; w < n; w += kThreads)
         some[w] = lowest_bits(live[w], old - live0 - live_before[w]);
     __syncthreads();
 
@@ -157,43 +183,50 @@ __global__ void __launch_bounds__(kEvictThreads, 1)
     uint32_t key = 0, mask = 0;
     int32_t ties = room;
     if (room < old) {
-        for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-            const uint32_t digit = pass == 2 ? 1023u : 2047u;
-            int32_t* const hist = sh.hist[pass];
-            for (int w = warp; w < n; w += 32) {
+        for (int pass = 0; pass < 4; ++pass) {
+            const int shift = 24 - 8 * pass;
+            for (int i = threadIdx.x; i < kBins * kCopies; i += kThreads) sh.hist[0][i] = 0;
+            __syncthreads();
+            for (int w = warp; w < n; w += kWarps) {
                 if ((some[w] >> lane & 1u) != 0u) {
                     const int32_t i = 32 * w + lane;
                     const uint32_t k = cached ? keys[i] : weight_key(__ldg(wts + i));
-                    if ((k & mask) == key) atomicAdd(&hist[k >> shift & digit], 1);
+                    if ((k & mask) == key) atomicAdd(&sh.hist[k >> shift & 255u][lane & (kCopies - 1)], 1);
                 }
             }
-            sync();
-            // bins from the top: a thread has bins 2047 - 2t and 2046 - 2t
-            const int t = threadIdx.x, b1 = kBins - 1 - 2 * t, b0 = b1 - 1;
-            int32_t h1 = hist[b1], h0 = hist[b0];
+            __syncthreads();
+            // bins from the top: thread t < 256 has bin 255 - t
+            const int bin = kBins - 1 - static_cast<int>(threadIdx.x);
+            int32_t h = 0;
+            if (bin >= 0) {
+                const uint4 a = lds16(&sh.hist[bin][0]), b = lds16(&sh.hist[bin][4]);
+                h = static_cast<int32_t>(a.x + a.y + a.z + a.w + b.x + b.y + b.z + b.w);
+                sh.sum[pass][bin] = h;
+            }
             if (cluster > 1) {
-                h1 = h0 = 0;
-                for (int c = 0; c < cluster; ++c) {
-                    h1 += read_peer(hist + b1, c);
-                    h0 += read_peer(hist + b0, c);
+                sync();
+                if (bin >= 0) {
+                    int32_t v[kMaxCluster];
+#pragma unroll
+                    for (int c = 0; c < kMaxCluster; ++c)   // all on their way before the first is used
+                        v[c] = c < cluster ? read_peer(&sh.sum[pass][bin], c) : 0;
+                    h = 0;
+#pragma unroll
+                    for (int c = 0; c < kMaxCluster; ++c) h += v[c];
                 }
             }
             int32_t total;
-            const int32_t above = block_prefix(h0 + h1, sh.scan, warp, lane, &total);
+            const int32_t above = block_prefix<kThreads>(h, sh.scan, warp, lane, &total);
             // the first bin, from the top, that brings the count to `ties` (to more than 0 where
             // that is 0: nothing is kept, and the top bin serves)
             const int32_t want = ties > 0 ? ties : 1;
-            if (above < want && above + h1 >= want) {
-                sh.found[0] = b1;
+            if (above < want && above + h >= want) {
+                sh.found[0] = bin;
                 sh.found[1] = ties - above;
-            } else if (above + h1 < want && above + h1 + h0 >= want) {
-                sh.found[0] = b0;
-                sh.found[1] = ties - above - h1;
             }
             __syncthreads();
             key |= static_cast<uint32_t>(sh.found[0]) << shift;
-            mask |= digit << shift;
+            mask |= 255u << shift;
             ties = sh.found[1];
             __syncthreads();
         }
@@ -202,7 +235,7 @@ __global__ void __launch_bounds__(kEvictThreads, 1)
     // competing entries above the key, and those equal to it
     int32_t strict = 0, tied = 0;
     if (room < old) {
-        for (int w = warp; w < n; w += 32) {
+        for (int w = warp; w < n; w += kWarps) {
             const uint32_t c = some[w];
             const int32_t i = 32 * w + lane;
             const bool is = (c >> lane & 1u) != 0u;
@@ -243,68 +276,69 @@ __global__ void __launch_bounds__(kEvictThreads, 1)
         }
         // this part's ties in order; then the kept words
         int32_t run = tied0;
-        for (int w0 = 0; w0 < n; w0 += kEvictThreads) {
+        for (int w0 = 0; w0 < n; w0 += kThreads) {
             const int w = w0 + threadIdx.x;
             const uint32_t equal = w < n ? some[w] : 0u;
             int32_t total;
-            const int32_t x = run + block_prefix(__popc(equal), sh.scan, warp, lane, &total);
+            const int32_t x = run + block_prefix<kThreads>(__popc(equal), sh.scan, warp, lane, &total);
             run += total;
             if (w < n) some[w] = static_cast<uint32_t>(some_before[w]) | lowest_bits(equal, ties - x);
         }
         __syncthreads();
     } else {                                             // every live entry stays
-        for (int w = threadIdx.x; w < n; w += kEvictThreads) some[w] = live[w];
+        for (int w = threadIdx.x; w < n; w += kThreads) some[w] = live[w];
         kept0 = live0;
         __syncthreads();
     }
-    scan_words(some, some_before, n, sh.scan, warp, lane);
+    scan_words<kThreads>(some, some_before, n, sh.scan, warp, lane);
 
     int32_t* const kept = p.kept + r * p.keep;
     float* const kept_w = p.kept_weights + r * p.keep;
     int64_t* const gone = p.evicted + r * (p.length - p.keep);
-    for (int w = warp; w < n; w += 32) {
-        const uint32_t l = live[w], k = some[w], below = (1u << lane) - 1u;
-        if ((l >> lane & 1u) != 0u) {
-            const int32_t i = 32 * w + lane;
-            const int32_t s = __ldg(idx + i);
-            const int32_t a = kept0 + some_before[w] + __popc(k & below);
-            if ((k >> lane & 1u) != 0u) {
-                kept[a] = s;
-                kept_w[a] = __ldg(wts + i);
-            } else {
-                gone[live0 + live_before[w] + __popc(l & below) - a] = s;
+    for (int w0 = warp; w0 < n; w0 += kWarps * kBatch) {
+        int32_t s[kBatch];
+        float x[kBatch];
+        load_batch(idx, wts, w0, kWarps, n, len, lane, s, x);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int w = w0 + kWarps * u;
+            if (w < n && s[u] >= 0) {
+                const uint32_t l = live[w], k = some[w], below = (1u << lane) - 1u;
+                const int32_t a = kept0 + some_before[w] + __popc(k & below);
+                if ((k >> lane & 1u) != 0u) {
+                    kept[a] = s[u];
+                    kept_w[a] = x[u];
+                } else {
+                    gone[live0 + live_before[w] + __popc(l & below) - a] = s[u];
+                }
             }
         }
     }
     // what is left of the row's outputs, spread over its CTAs
     const int32_t kept_all = fresh + room;
-    for (int32_t i = kept_all + rank * kEvictThreads + threadIdx.x; i < p.keep; i += cluster * kEvictThreads) {
+    for (int32_t i = kept_all + rank * kThreads + threadIdx.x; i < p.keep; i += cluster * kThreads) {
         kept[i] = -1;
         kept_w[i] = 0.0f;
     }
-    for (int32_t i = all - kept_all + rank * kEvictThreads + threadIdx.x; i < p.length - p.keep;
-         i += cluster * kEvictThreads)
+    for (int32_t i = all - kept_all + rank * kThreads + threadIdx.x; i < p.length - p.keep;
+         i += cluster * kThreads)
         gone[i] = -1;
     if (cluster > 1) cluster_sync();                     // no CTA leaves while another reads its counts
 }
 
-}  // namespace
-
-cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
-    // CTAs a row: one for each 8192 entries, at most eight
-    int32_t cluster = 1;
-    while (cluster < kMaxCluster && p.length > 8192 * cluster) cluster *= 2;
+template <int kThreads>
+cudaError_t launch(const EvictParams& p, int32_t cluster, cudaStream_t stream) {
     const int32_t words = (p.length + 32 * cluster - 1) / (32 * cluster);
     const bool cached = words * 32 <= kCachedKeys;
     const size_t smem = sizeof(EvictShared) + static_cast<size_t>(words) * (cached ? 16 + 128 : 16);
     // raises the kernel's limit once per device
     int64_t warps = 0;
-    const cudaError_t e = resident_warps(reinterpret_cast<const void*>(evict_kernel), kEvictThreads,
+    const cudaError_t e = resident_warps(reinterpret_cast<const void*>(evict_kernel<kThreads>), kThreads,
                                          sizeof(EvictShared) + kCachedKeys / 32 * 144, &warps);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.rows * cluster));
-    cfg.blockDim = dim3(kEvictThreads);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -316,7 +350,17 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, evict_kernel, p, words, cluster, cached);
+    return cudaLaunchKernelEx(&cfg, evict_kernel<kThreads>, p, words, cluster, cached);
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
+    // CTAs a row: one for each 8192 entries, at most eight; few threads wait less for each other
+    // where the entries are few
+    int32_t cluster = 1;
+    while (cluster < kMaxCluster && p.length > 8192 * cluster) cluster *= 2;
+    return p.length <= 4096 ? launch<256>(p, 1, stream) : launch<1024>(p, cluster, stream);
 }
 
 }  // namespace gkr
