@@ -283,6 +283,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         bars->timed_out = 0;
         mbar_init_fence();
     }
+    if (threadIdx.x == kFirstGather * 32) prefetch_map(&cache_map);
+    if (threadIdx.x == kPollThread) prefetch_map(&q_map);
     pdl_wait_previous();
     pdl_release_next();
     tc_fence_before_sync();
@@ -351,8 +353,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         // half of the others'.  The indices come into a ring in shared memory six chunks ahead
         // (a global load takes more than a chunk's time), lane i decodes record i of the
         // chunk's 32, eight lanes have the copy engine gather four half-rows each, and every
-        // lane copies its record's 16 scale bytes.  An entry that is none gets scale bytes
-        // 0 and whatever codes slot 0 has: finite values, which the softmax masks.
+        // lane copies its record's 16 scale bytes.  An entry that is none gets scale bytes 0
+        // and whatever codes are there -- the first record's of its four, or, where none of the
+        // four is one, those of an earlier chunk: finite values, which the softmax masks.  (One
+        // slot read in their place by every SM takes 4 us a chunk to answer.)
         const int g = warp - kFirstGather;
         const bool own = g < 2;
         const uint32_t cta = own ? rank : 1u - rank;        // whose records
@@ -395,9 +399,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
             page_row(is ? static_cast<uint32_t>(idx) : 0u, static_cast<uint32_t>(p.block_size), page, r);
             const int64_t at = static_cast<int64_t>(page) * p.page_stride;
             const int32_t row = static_cast<int32_t>(at >> 8) + static_cast<int32_t>(r);
+            const uint32_t four = lane < 8 ? live >> (4 * lane) & 15u : 0u;   // this lane's rows
             int32_t r4[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) r4[i] = __shfl_sync(kFull, row, (4 * lane + i) & 31);
+            for (int i = 0; i < 4; ++i)
+                r4[i] = __shfl_sync(kFull, row, (4 * lane + ((four >> i & 1u) != 0u ? i : __ffs(four) - 1)) & 31);
+            const uint32_t bytes = __popc(__ballot_sync(kFull, four != 0u)) * 512u;
             if (lane == 0 && j >= kRawStages) wait_quiet(empty + 8 * rw.s, rw.parity ^ 1u, ok);
             __syncwarp();
             const uint32_t raw = raw0 + rw.s * kRawBytes, bar = full + 8 * rw.s;
@@ -408,9 +415,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                                     p.cache + at + static_cast<int64_t>(p.block_size) * 256 + r * 16u, is);
                 cp_async_arrive(bar);
             }
-            if (lane == 0) mbar_expect_tx(bar, kRawBlock);
+            if (lane == 0) mbar_expect_tx(bar, bytes);
             __syncwarp();
-            if (lane < 8) tma_gather4(raw + dst, &cache_map, bar, x, r4[0], r4[1], r4[2], r4[3]);
+            if (four != 0u) tma_gather4(raw + dst, &cache_map, bar, x, r4[0], r4[1], r4[2], r4[3]);
             fetch();
             rw.next();
         }
@@ -967,7 +974,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
             uint32_t live = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const bool is = idx[i] >= 0 && idx[i] < p.num_slots;   // else: finite values, not used
+                const bool is = idx[i] >= 0 && idx[i] < p.num_slots;   // else: as in attend_kernel
                 live |= is ? 1u << i : 0u;
                 uint32_t page, r;
                 page_row(is ? static_cast<uint32_t>(idx[i]) : 0u, static_cast<uint32_t>(p.block_size), page, r);
@@ -975,6 +982,12 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
                 r4[i] = static_cast<int32_t>(at >> 8) + static_cast<int32_t>(r);
                 scales[i] = p.cache + at + static_cast<int64_t>(p.block_size) * 256 + r * 16u;
             }
+            const int some = live != 0u ? __ffs(live) - 1 : 0;
+            const int32_t r_some = some == 0 ? r4[0] : some == 1 ? r4[1] : some == 2 ? r4[2] : r4[3];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if ((live >> i & 1u) == 0u) r4[i] = r_some;
+            const uint32_t bytes = __popc(__ballot_sync(kFull, live != 0u)) * 512u;
             smem[kWOffLive + (j & 7) * 32 + lane] = static_cast<uint8_t>(live);
 #pragma unroll 1
             for (int h = 0; h < 2; ++h) {
@@ -990,10 +1003,11 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
                     for (int i = 0; i < 4; ++i) cp_async16_or_zeros(to + 16 * i, scales[i], (live >> i & 1u) != 0u);
                 }
                 cp_async_arrive(bar);
-                if (lane == 0) mbar_expect_tx(bar, kWRawBytes);
+                if (lane == 0) mbar_expect_tx(bar, bytes);
                 __syncwarp();
-                tma_gather4(smem_addr(smem + kWOffRaw) + rw.s * kWRawBytes + 512 * lane, &cache_map, bar, h * 128,
-                            r4[0], r4[1], r4[2], r4[3]);
+                if (live != 0u)
+                    tma_gather4(smem_addr(smem + kWOffRaw) + rw.s * kWRawBytes + 512 * lane, &cache_map, bar,
+                                h * 128, r4[0], r4[1], r4[2], r4[3]);
                 rw.next();
                 ++half_rows;
             }
