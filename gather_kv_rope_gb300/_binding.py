@@ -292,24 +292,30 @@ def cache_bytes(k_cache: torch.Tensor) -> torch.Tensor:
 
 def _cache_desc(k_cache: torch.Tensor) -> CacheDesc:
     """The record width is the format selector: uint8 [pages, block, 528 | 584] are
-    the packed MXFP8 records, [pages, block, 272] the MXFP4 record; float8_e4m3fn / bfloat16 [pages, block, 512] the plain
-    caches (records 512 / 1024)."""
-    if k_cache.dim() != 3:
+    the packed MXFP8 records, [pages, block, 272] the MXFP4 record; float8_e4m3fn /
+    bfloat16 [pages, block, 512] the plain caches (records 512 / 1024)."""
+    return _desc_of(k_cache.shape, k_cache.stride(), k_cache.dtype)
+
+
+# One descriptor for each geometry, only ever read: building it for every call took 1 us.
+@functools.lru_cache(maxsize=256)
+def _desc_of(shape, stride, dtype) -> CacheDesc:
+    if len(shape) != 3:
         raise ValueError("k_cache must be a 3-D paged cache [num_pages, block_size, width]")
-    P, bs, w = k_cache.shape
-    if k_cache.dtype == torch.uint8:
+    P, bs, w = shape
+    if dtype == torch.uint8:
         if w not in PACKED and w != MXFP4:
             raise ValueError(f"unsupported paged KV record width {w} (expected 528, 584 or 272)")
         rec, es = w, 1
-    elif k_cache.dtype in (torch.float8_e4m3fn, torch.bfloat16):
+    elif dtype in (torch.float8_e4m3fn, torch.bfloat16):
         if w != HEAD_DIM:
-            raise ValueError(f"a {k_cache.dtype} cache must have width 512, not {w}")
-        rec, es = (512, 1) if k_cache.dtype == torch.float8_e4m3fn else (1024, 2)
+            raise ValueError(f"a {dtype} cache must have width 512, not {w}")
+        rec, es = (512, 1) if dtype == torch.float8_e4m3fn else (1024, 2)
     else:
         raise ValueError("k_cache must be uint8 (packed records), float8_e4m3fn or bfloat16")
-    if k_cache.stride(2) != 1 or k_cache.stride(1) != w:
+    if stride[2] != 1 or stride[1] != w:
         raise ValueError("k_cache must have stride(2) == 1 and stride(1) == its width")
-    return CacheDesc(rec, bs, P, k_cache.stride(0) * es)
+    return CacheDesc(rec, bs, P, stride[0] * es)
 
 
 def _check(cond: bool, msg: str) -> None:
@@ -368,23 +374,28 @@ def _check_err_flag(err_flag):
 def _insert_args(kv, k_cache, slot_mapping, positions, cos_sin_cache, block_size, record,
                  err_flag):
     desc = _cache_desc(k_cache)
-    if record is not None:
-        _check(int(record) == desc.record,
-               f"record {record} does not match k_cache width {desc.record}")
-    _check(int(block_size) == desc.block_size,
-           f"block_size {block_size} != k_cache.size(1) {desc.block_size}")
-    _check(kv.dtype == torch.bfloat16 and kv.dim() == 2 and kv.shape[1] == HEAD_DIM
-           and kv.is_contiguous(), "kv must be a contiguous bf16 tensor [tokens, 512]")
-    _check(slot_mapping.dtype == torch.int64 and slot_mapping.dim() == 1
-           and slot_mapping.is_contiguous(), "slot_mapping must be a contiguous int64 [T] tensor")
-    _check(positions.dtype == torch.int64 and positions.dim() == 1 and positions.is_contiguous(),
-           "positions must be a contiguous int64 1-D tensor")
+    if record is not None and int(record) != desc.record:
+        raise ValueError(f"record {record} does not match k_cache width {desc.record}")
+    if int(block_size) != desc.block_size:
+        raise ValueError(f"block_size {block_size} != k_cache.size(1) {desc.block_size}")
+    rows = kv.shape
+    if kv.dtype != torch.bfloat16 or len(rows) != 2 or rows[1] != HEAD_DIM \
+            or not kv.is_contiguous():
+        raise ValueError("kv must be a contiguous bf16 tensor [tokens, 512]")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.dim() != 1 \
+            or not slot_mapping.is_contiguous():
+        raise ValueError("slot_mapping must be a contiguous int64 [T] tensor")
+    if positions.dtype != torch.int64 or positions.dim() != 1 or not positions.is_contiguous():
+        raise ValueError("positions must be a contiguous int64 1-D tensor")
     T = slot_mapping.shape[0]
-    _check(kv.shape[0] >= T, "kv has fewer rows than slot_mapping")
-    _check(positions.shape[0] >= kv.shape[0], "positions must cover every kv row")
-    _check(cos_sin_cache.dtype == torch.float32 and cos_sin_cache.dim() == 2
-           and cos_sin_cache.shape[1] == 64 and cos_sin_cache.is_contiguous(),
-           "cos_sin_cache must be a contiguous fp32 tensor [max_pos, 64]")
+    if rows[0] < T:
+        raise ValueError("kv has fewer rows than slot_mapping")
+    if positions.shape[0] < rows[0]:
+        raise ValueError("positions must cover every kv row")
+    table = cos_sin_cache.shape
+    if cos_sin_cache.dtype != torch.float32 or len(table) != 2 or table[1] != 64 \
+            or not cos_sin_cache.is_contiguous():
+        raise ValueError("cos_sin_cache must be a contiguous fp32 tensor [max_pos, 64]")
     _check_err_flag(err_flag)
     dev = _same_cuda_device(kv, k_cache, slot_mapping, positions, cos_sin_cache, err_flag)
     return desc, T, dev
@@ -448,11 +459,11 @@ def kv_gather(k_cache: torch.Tensor, indices: torch.Tensor, out: torch.Tensor,
     An index of -1 writes zeros.  An fp8 cache needs its fp8_scale.  Returns out."""
     desc = _cache_desc(k_cache)
     _check_fp8_scale(desc, fp8_scale)
-    _check(indices.dtype == torch.int32 and indices.is_contiguous(),
-           "indices must be a contiguous int32 tensor")
-    _check(out.dtype == torch.bfloat16 and out.is_contiguous()
-           and tuple(out.shape) == tuple(indices.shape) + (HEAD_DIM,),
-           "out must be a contiguous bf16 tensor of shape indices.shape + (512,)")
+    if indices.dtype != torch.int32 or not indices.is_contiguous():
+        raise ValueError("indices must be a contiguous int32 tensor")
+    if out.dtype != torch.bfloat16 or not out.is_contiguous() \
+            or out.shape != indices.shape + (HEAD_DIM,):
+        raise ValueError("out must be a contiguous bf16 tensor of shape indices.shape + (512,)")
     _check_err_flag(err_flag)
     dev = _same_cuda_device(k_cache, indices, out, err_flag, fp8_scale)
     _call(dev, lib().gkr_kv_gather, k_cache.data_ptr(), ctypes.byref(desc), indices.data_ptr(),
@@ -584,20 +595,25 @@ def sparse_attention(q: torch.Tensor, k_cache: torch.Tensor, indices: torch.Tens
     Returns (out, lse)."""
     desc = _cache_desc(k_cache)
     _check(desc.record == MXFP4, "sparse_attention reads the MXFP4 records (272 bytes)")
-    _check(q.dtype == torch.bfloat16 and q.dim() == 3 and q.shape[2] == HEAD_DIM
-           and q.is_contiguous(), "q must be a contiguous bf16 tensor [queries, heads, 512]")
+    shape = q.shape
+    if q.dtype != torch.bfloat16 or len(shape) != 3 or shape[2] != HEAD_DIM \
+            or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bf16 tensor [queries, heads, 512]")
     istride = _rows(indices, torch.int32, "indices")
-    _check(indices.shape[0] == q.shape[0], "indices must have a row for each query")
-    Q, H, K = int(q.shape[0]), int(q.shape[1]), int(indices.shape[1])
-    _check(1 <= H <= 128, "sparse_attention takes 1 to 128 heads")
+    Q, H, _ = shape
+    rows, K = indices.shape
+    if rows != Q:
+        raise ValueError("indices must have a row for each query")
+    if not 1 <= H <= 128:
+        raise ValueError("sparse_attention takes 1 to 128 heads")
     if out is None:
-        out = q.new_empty((Q, H, HEAD_DIM))
+        out = torch.empty_like(q)
+    elif out.dtype != torch.bfloat16 or not out.is_contiguous() or out.shape != shape:
+        raise ValueError("out must be a contiguous bf16 tensor of q's shape")
     if lse is None:
-        lse = q.new_empty((Q, H), dtype=torch.float32)
-    _check(out.dtype == torch.bfloat16 and out.is_contiguous() and out.shape == q.shape,
-           "out must be a contiguous bf16 tensor of q's shape")
-    _check(lse.dtype == torch.float32 and lse.is_contiguous() and tuple(lse.shape) == (Q, H),
-           "lse must be a contiguous fp32 tensor [queries, heads]")
+        lse = torch.empty(Q, H, dtype=torch.float32, device=q.device)
+    elif lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != (Q, H):
+        raise ValueError("lse must be a contiguous fp32 tensor [queries, heads]")
     wstride = 0
     if weights is not None:
         wstride = _rows(weights, torch.float32, "weights")
@@ -605,15 +621,25 @@ def sparse_attention(q: torch.Tensor, k_cache: torch.Tensor, indices: torch.Tens
     _check_err_flag(err_flag)
     dev = _same_cuda_device(q, k_cache, indices, out, lse, weights, err_flag, workspace)
     if workspace is None:
-        workspace = q.new_empty(_attention_workspace(H, Q, K, dev.index), dtype=torch.uint8)
-    else:
-        _check(workspace.dtype == torch.uint8 and workspace.is_contiguous(),
-               "workspace must be a contiguous uint8 tensor")
+        workspace = torch.empty(_attention_workspace(H, Q, K, dev.index), dtype=torch.uint8,
+                                device=dev)
+    elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
     _call(dev, lib().gkr_sparse_attention, q.data_ptr(), H, k_cache.data_ptr(), ctypes.byref(desc),
           indices.data_ptr(), istride, Q, K, float(sm_scale), out.data_ptr(), lse.data_ptr(),
           _ptr(weights), wstride, workspace.data_ptr(), workspace.numel(), _ptr(err_flag),
           _opts(launch_opts))
     return out, lse
+
+
+def _buffer(t, rows: int, cols: int, dtype: torch.dtype, name: str, like: torch.Tensor):
+    """A given output after its checks, or a new one beside `like`."""
+    if t is None:
+        return torch.empty(rows, cols, dtype=dtype, device=like.device)
+    if t.dtype != dtype or not t.is_contiguous() or t.shape != (rows, cols):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor [{rows}, {cols}]"
+                         .replace("torch.", ""))
+    return t
 
 
 def kv_evict(indices: torch.Tensor, weights: torch.Tensor, keep: int, recent: int = 0,
@@ -635,20 +661,16 @@ def kv_evict(indices: torch.Tensor, weights: torch.Tensor, keep: int, recent: in
     kv_insert, which skips -1.  No record moves."""
     istride = _rows(indices, torch.int32, "indices")
     wstride = _rows(weights, torch.float32, "weights")
-    _check(weights.shape == indices.shape, "weights must have the shape of indices")
-    B, L = int(indices.shape[0]), int(indices.shape[1])
+    B, L = indices.shape
+    if weights.shape != (B, L):
+        raise ValueError("weights must have the shape of indices")
     keep, recent = int(keep), int(recent)
-    _check(0 <= recent <= keep <= L, "kv_evict needs 0 <= recent <= keep <= indices.shape[1]")
+    if not 0 <= recent <= keep <= L:
+        raise ValueError("kv_evict needs 0 <= recent <= keep <= indices.shape[1]")
 
-    def buffer(t, n, dtype, name):
-        if t is None:
-            return indices.new_empty((B, n), dtype=dtype)
-        _check(t.dtype == dtype and t.is_contiguous() and tuple(t.shape) == (B, n),
-               f"{name} must be a contiguous {dtype} tensor [{B}, {n}]".replace("torch.", ""))
-        return t
-    kept = buffer(kept, keep, torch.int32, "kept")
-    kept_weights = buffer(kept_weights, keep, torch.float32, "kept_weights")
-    evicted = buffer(evicted, L - keep, torch.int64, "evicted")
+    kept = _buffer(kept, B, keep, torch.int32, "kept", indices)
+    kept_weights = _buffer(kept_weights, B, keep, torch.float32, "kept_weights", indices)
+    evicted = _buffer(evicted, B, L - keep, torch.int64, "evicted", indices)
     dev = _same_cuda_device(indices, weights, kept, kept_weights, evicted)
     _call(dev, lib().gkr_kv_evict, indices.data_ptr(), istride, weights.data_ptr(), wstride, B, L,
           keep, recent, kept.data_ptr(), kept_weights.data_ptr(), evicted.data_ptr(),
