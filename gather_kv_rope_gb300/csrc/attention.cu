@@ -96,12 +96,17 @@ constexpr uint32_t kIdescS = idesc(kChunkKeys, false);
 constexpr uint32_t kIdescO = idesc(256, true);
 
 // The cut of a call's chunks over the pairs: pair g takes chunks [total * g / pairs,
-// total * (g + 1) / pairs) of the queries' chunks taken one query after another.
+// total * (g + 1) / pairs) of the queries' chunks taken one query after another, or, with
+// `each` > 0, `each` whole queries.
 struct Cut {
     int64_t per_query;   // chunks of a query, >= 1
     int64_t total;
+    int64_t each;
     int32_t pairs;
-    __host__ __device__ int64_t begin(int64_t g) const { return total * g / pairs; }
+    __host__ __device__ int64_t begin(int64_t g) const {
+        const int64_t b = each > 0 ? each * per_query * g : total * g / pairs;
+        return b < total ? b : total;
+    }
 };
 
 // Shared memory of a CTA, from a 1024-byte boundary.
@@ -738,6 +743,7 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // The queries that the cut runs through: query, its first pair and how many work on it.
 constexpr int kMaxPairs = 128;
+constexpr int64_t kCutChunks = 11;
 struct Cuts {
     int32_t n;
     int32_t query[kMaxPairs - 1];
@@ -1177,6 +1183,17 @@ cudaError_t make_cut(int64_t num_queries, int64_t topk, Cut* cut) {
     cut->total = num_queries * cut->per_query;
     if (pairs > kMaxPairs) pairs = kMaxPairs;
     cut->pairs = static_cast<int32_t>(cut->total < pairs ? cut->total : pairs);
+    cut->each = 0;
+    // Whole queries, as many for each pair, where that leaves the longest run at most kCutChunks
+    // longer than the even cut: about what the pieces' fp32 rows and the kernel that joins them
+    // cost.  128 heads x 128 queries x 2048 entries on 76 pairs: runs of 64 chunks whole 77 us a
+    // call, of 54 cut 88 us; 64 queries x 2049: 33 whole 82, 28 cut 96 (with weights); 37 x 1531
+    // entries, 16 heads: 24 whole 31, 12 cut 27.
+    const int64_t each = (num_queries + pairs - 1) / pairs;
+    if (each * cut->per_query <= (cut->total + pairs - 1) / pairs + kCutChunks) {
+        cut->each = each;
+        cut->pairs = static_cast<int32_t>((num_queries + each - 1) / each);
+    }
     return cudaSuccess;
 }
 
