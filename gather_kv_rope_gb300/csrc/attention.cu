@@ -817,50 +817,65 @@ __global__ void __launch_bounds__(128 * kGroups)
 // what the record has).  Here the records are the rows of the product (M = 128) and the heads
 // its columns, so a thread has all heads of one record and sums them in its registers, in the
 // heads' order.  One CTA an SM; a tile is 128 records of one query.
-//   * one warp fetches indices, scale rows and, four half-rows a lane, the codes;
-//   * 16 warps dequantise 64 dims of the tile at a time (16 KB, three stages);
+//   * four warps fetch indices, scale rows and, a quarter-row (64 bytes) at a time, the codes;
+//   * 16 warps dequantise 64 dims of the tile at a time (16 KB a stage), eight warps each stage;
 //   * one thread multiplies them by the query's heads, which lie in shared memory, into one of
 //     two accumulators;
 //   * four warps turn the accumulator into the records' sums and add them to the weights.
+// Measured at 64 queries of 128 heads and 2049 entries: 31 us, against 45 us with one group of
+// 16 warps a stage, one stage less and whole half-rows.  The products alone are 17 GFLOP
+// (9 us); what is left is the dequantisation's instructions and the latencies between a stage's
+// filling, its product and its next filling: two or three stages are all that shared memory
+// holds beside 128 heads.
 
 constexpr int kTileKeys = 128;
 constexpr int kWSoftWarps = 4;                              // warp w: tensor-memory lanes 32w ..
 constexpr int kWDequantWarps = 16;
 constexpr int kWMmaWarp = kWSoftWarps + kWDequantWarps;
-constexpr int kWGatherWarp = kWMmaWarp + 1;
-constexpr int kWeightThreads = (kWGatherWarp + 1) * 32;
-constexpr int kWRaw = 2;                                    // half-rows (128 bytes) of a tile in flight
-constexpr int kWStages = 3;                                 // 64 dims of a tile
+constexpr int kWGatherWarps = 4;
+constexpr int kWFirstGather = kWMmaWarp + 1;
+constexpr int kWeightThreads = (kWFirstGather + kWGatherWarps) * 32;
+constexpr int kWGroups = 2;                                 // of dequantisation warps
+constexpr int kWGroupWarps = kWDequantWarps / kWGroups;
 constexpr int kWIndexRing = 4, kWIndexAhead = 3;            // tiles of indices
-constexpr uint32_t kWStageBytes = kTileKeys * kRowBytes;
-constexpr uint32_t kWOffStages = kMaxHeadsTile * 1024;      // after the query: 8 blocks of 64 dims
-constexpr uint32_t kWOffRaw = kWOffStages + kWStages * kWStageBytes;
-constexpr uint32_t kWRawBytes = kTileKeys * 128;
-constexpr uint32_t kWOffScales = kWOffRaw + kWRaw * kWRawBytes;        // [2 tiles][128][16]
-constexpr uint32_t kWOffLse = kWOffScales + 2 * kTileKeys * 16;        // [128] lse in powers of two
-constexpr uint32_t kWOffIndex = kWOffLse + kMaxHeadsTile * 4;          // [kWIndexRing][128]
-constexpr uint32_t kWOffLive = kWOffIndex + kWIndexRing * kTileKeys * 4;   // [8][4]
-constexpr uint32_t kWOffBars = kWOffLive + 8 * 16;
+constexpr uint32_t kWStageBytes = kTileKeys * kRowBytes;    // 64 dims of a tile
+constexpr uint32_t kWRawBytes = kTileKeys * 64;             // quarter-rows of a tile: 128 dims
 
-struct alignas(8) WeightBarriers {
-    uint64_t q_full, q_free;                 // the query is in place; its last product is done
-    uint64_t raw[kWRaw], raw_empty[kWRaw];   // half-rows landed (the first half's with the scales); read
-    uint64_t scales_empty[2];                // a tile's scales are read
-    uint64_t a_full[kWStages], a_empty[kWStages];
-    uint64_t acc_full[2], acc_empty[2];
-    uint32_t tmem_base;
-    int32_t timed_out;
+// Shared memory for queries of up to kHeads heads: the query, stages, quarter-rows in flight,
+// scales, heads' lse, indices, live bits, barriers.
+template <int kHeads>
+struct WeightSmem {
+    static constexpr int kStages = kHeads <= 64 ? 4 : 3;
+    static constexpr int kRaw = kHeads <= 64 ? 8 : 5;
+    struct alignas(8) Barriers {
+        uint64_t q_full, q_free;               // the query is in place; its last product is done
+        uint64_t raw[kRaw], raw_empty[kRaw];   // quarter-rows landed (the first with the scales); read
+        uint64_t scales_empty[2];              // a tile's scales are read
+        uint64_t a_full[kStages], a_empty[kStages];
+        uint64_t acc_full[2], acc_empty[2];
+        uint32_t tmem_base;
+        int32_t timed_out;
+    };
+    static constexpr uint32_t kStagesAt = kHeads * 1024;
+    static constexpr uint32_t kRawAt = kStagesAt + kStages * kWStageBytes;
+    static constexpr uint32_t kScalesAt = kRawAt + kRaw * kWRawBytes;          // [2 tiles][128][16]
+    static constexpr uint32_t kLseAt = kScalesAt + 2 * kTileKeys * 16;         // [kHeads] lse in powers of two
+    static constexpr uint32_t kIndexAt = kLseAt + kHeads * 4;                  // [kWIndexRing][128]
+    static constexpr uint32_t kLiveAt = kIndexAt + kWIndexRing * kTileKeys * 4;   // [8][4] bits
+    static constexpr uint32_t kBarsAt = kLiveAt + 8 * 16;
+    static constexpr size_t kBytes = 1024 + kBarsAt + sizeof(Barriers);
+    static_assert(kBytes <= 227 * 1024, "a CTA's shared memory");
 };
-constexpr size_t kWeightSmem = 1024 + kWOffBars + sizeof(WeightBarriers);
-static_assert(kWeightSmem <= 227 * 1024, "a CTA's shared memory");
 
+template <int kHeads>
 __global__ void __launch_bounds__(kWeightThreads, 1)
     weight_kernel(const AttentionParams p, const int64_t tiles, const int32_t n_pad,
-                  const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap cache_map) {
+                  const __grid_constant__ CUtensorMap q_map) {
+    using M = WeightSmem<kHeads>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    WeightBarriers* const bars = reinterpret_cast<WeightBarriers*>(smem + kWOffBars);
+    typename M::Barriers* const bars = reinterpret_cast<typename M::Barriers*>(smem + M::kBarsAt);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
     // tiles i0 .. i0 + n - 1 of all queries' tiles, one query after another
@@ -875,12 +890,12 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     if (threadIdx.x == 0) {
         mbar_init(smem_addr(&bars->q_full), 1);
         mbar_init(smem_addr(&bars->q_free), 1);
-        for (int s = 0; s < kWRaw; ++s) {
-            mbar_init(smem_addr(&bars->raw[s]), 1 + 32);
+        for (int s = 0; s < M::kRaw; ++s) {
+            mbar_init(smem_addr(&bars->raw[s]), kWGatherWarps * (1 + 32));
             mbar_init(smem_addr(&bars->raw_empty[s]), kWDequantWarps);
         }
-        for (int s = 0; s < kWStages; ++s) {
-            mbar_init(smem_addr(&bars->a_full[s]), kWDequantWarps);
+        for (int s = 0; s < M::kStages; ++s) {
+            mbar_init(smem_addr(&bars->a_full[s]), kWGroupWarps);
             mbar_init(smem_addr(&bars->a_empty[s]), 1);
         }
         for (int s = 0; s < 2; ++s) {
@@ -903,60 +918,66 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
 
     if (warp >= kWSoftWarps && warp < kWMmaWarp) {
         // ------------------------------------------------------------- dequantisation
-        // A stage is 128 records x 64 dims; a warp takes eight records, a lane 16 dims of one.
+        // Eight warps fill every other stage, eight the ones between, so that one group's loads,
+        // stores and waits lie behind the other's arithmetic.  A warp takes 16 records, a lane
+        // 32 dims of one: one scale and one 16-byte read.
         const int w = warp - kWSoftWarps;
-        const int r = w * 8 + (lane & 7);
-        const int v = lane >> 3;
-        const uint32_t raw0 = smem_addr(smem + kWOffRaw) + r * 128 + (v & 1) * 8;
-        const uint32_t scale0 = smem_addr(smem + kWOffScales) + r * 16 + (v >> 1);
-        const uint32_t dst = smem_addr(smem + kWOffStages) + r * kRowBytes + ((2 * v ^ (r & 7)) << 4);
-        Ring<kWRaw> rw;
-        Ring<kWStages> st;
-        int filled = 0;
+        const int group = w / kWGroupWarps;
+        const int r = (w % kWGroupWarps) * 16 + (lane & 7) + 8 * (lane >> 4);
+        const int v = (lane >> 3) & 1;
+        const uint32_t raw0 = smem_addr(smem + M::kRawAt) + r * 64 + (((2 * group + v) ^ (r >> 1 & 3)) << 4);
+        const uint32_t scale0 = smem_addr(smem + M::kScalesAt) + r * 16 + 2 * group + v;
+        const uint32_t dst0 = smem_addr(smem + M::kStagesAt) + r * kRowBytes;
+        Ring<M::kRaw> rw;
+        int stage = group;                 // every other one of the ring's
+        uint32_t turn = 0;                 // of the ring
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
 #pragma unroll 1
-            for (int h = 0; h < 8; ++h) {   // 64 dims
-                if (w == 2 && lane == 0) {
-                    if ((h & 3) == 0) wait_quiet(smem_addr(&bars->raw[rw.s]), rw.parity, ok);
-                    if (filled >= kWStages) wait_quiet(smem_addr(&bars->a_empty[st.s]), st.parity ^ 1u, ok);
-                    ++filled;
-                }
-                group_sync(kOwnBar, kWDequantWarps * 32);
-                uint32_t w0, w1, s;
-                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w0), "=r"(w1)
-                             : "r"(raw0 + rw.s * kWRawBytes + (((h & 3) * 2 + (v >> 1) ^ (r & 7)) << 4)) : "memory");
+            for (int h = 0; h < 4; ++h) {   // 128 dims: 64 for each group
+                // every warp waits for itself: at a barrier of the warps each stage took as long
+                // as the slowest of them
+                wait_quiet(smem_addr(&bars->raw[rw.s]), rw.parity, ok);
+                if (turn > 0) wait_quiet(smem_addr(&bars->a_empty[stage]), (turn - 1) & 1, ok);
+                __syncwarp();
+                const uint4 codes = lds16_at(raw0 + rw.s * kWRawBytes);
+                uint32_t s;
                 asm volatile("ld.shared.u8 %0, [%1];" : "=r"(s)
-                             : "r"(scale0 + (j & 1) * kTileKeys * 16 + 2 * h) : "memory");
-                const uint32_t f = e2m1_factor(s), out = dst + st.s * kWStageBytes;
-                sts16(out, dequant8_e2m1(w0, f));
-                sts16(out ^ 16u, dequant8_e2m1(w1, f));
+                             : "r"(scale0 + (j & 1) * kTileKeys * 16 + 4 * h) : "memory");
+                const uint32_t f = e2m1_factor(s), dst = dst0 + stage * kWStageBytes;
+                sts16(dst + (((4 * v + 0) ^ (r & 7)) << 4), dequant8_e2m1(codes.x, f));
+                sts16(dst + (((4 * v + 1) ^ (r & 7)) << 4), dequant8_e2m1(codes.y, f));
+                sts16(dst + (((4 * v + 2) ^ (r & 7)) << 4), dequant8_e2m1(codes.z, f));
+                sts16(dst + (((4 * v + 3) ^ (r & 7)) << 4), dequant8_e2m1(codes.w, f));
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    if ((h & 3) == 3) mbar_arrive(smem_addr(&bars->raw_empty[rw.s]));
-                    if (h == 7) mbar_arrive(smem_addr(&bars->scales_empty[j & 1]));
-                    mbar_arrive(smem_addr(&bars->a_full[st.s]));
+                    mbar_arrive(smem_addr(&bars->raw_empty[rw.s]));
+                    if (h == 3) mbar_arrive(smem_addr(&bars->scales_empty[j & 1]));
+                    mbar_arrive(smem_addr(&bars->a_full[stage]));
                 }
-                if ((h & 3) == 3) rw.next();
-                st.next();
+                rw.next();
+                stage += kWGroups;
+                if (stage >= M::kStages) {
+                    stage -= M::kStages;
+                    ++turn;
+                }
             }
         }
-    } else if (warp == kWGatherWarp) {
+    } else if (warp >= kWFirstGather) {
         // ------------------------------------------------------------- raw records
-        // Lane i has records 4i .. 4i + 3 of the tile.
-        const uint32_t ring = smem_addr(smem + kWOffIndex) + 16 * lane;
+        // A warp has 32 records of the tile: a lane finds one's row, four lanes copy a
+        // quarter-row.  Four warps: one alone took 110 cycles a copy instruction, 1800 a quarter
+        // of the tile, which then set the pace.
+        const int rec = (warp - kWFirstGather) * 32;
+        const uint32_t ring = smem_addr(smem + M::kIndexAt) + 4 * (rec + lane);
         int ahead = 0;
         auto fetch = [&]() {
             if (ahead < n) {
                 const uint32_t to = ring + (ahead % kWIndexRing) * kTileKeys * 4;
-                const int32_t* const row = p.indices + qi * p.index_stride;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int64_t k = ti * kTileKeys + 4 * lane + i;
-                    if (k < p.topk) cp_async4(to + 4 * i, row + k);
-                    else asm volatile("st.shared.b32 [%0], %1;" ::"r"(to + 4 * i), "r"(-1) : "memory");
-                }
+                const int64_t k = ti * kTileKeys + rec + lane;
+                if (k < p.topk) cp_async4(to, p.indices + qi * p.index_stride + k);
+                else asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(-1) : "memory");
                 if (++ti == tiles) {
                     ti = 0;
                     ++qi;
@@ -967,73 +988,61 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         };
 #pragma unroll 1
         for (int i = 0; i < kWIndexAhead; ++i) fetch();
-        Ring<kWRaw> rw;
-        int half_rows = 0;
+        const int c = lane & 3;   // 16-byte chunk of the quarter-row
+        const uint32_t to0 = smem_addr(smem + M::kRawAt) + (rec + (lane >> 2)) * 64 + ((c ^ (lane >> 3 & 3)) << 4);
+        Ring<M::kRaw> rw;
+        int quarters = 0;
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
             cp_async_wait<kWIndexAhead - 1>();
-            const uint4 idx4 = lds16_at(ring + (j % kWIndexRing) * kTileKeys * 4);
-            const int32_t idx[4] = {static_cast<int32_t>(idx4.x), static_cast<int32_t>(idx4.y),
-                                    static_cast<int32_t>(idx4.z), static_cast<int32_t>(idx4.w)};
-            int32_t r4[4];
-            const uint8_t* scales[4];
-            uint32_t live = 0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const bool is = idx[i] >= 0 && idx[i] < p.num_slots;   // else: as in attend_kernel
-                live |= is ? 1u << i : 0u;
-                uint32_t page, r;
-                page_row(is ? static_cast<uint32_t>(idx[i]) : 0u, static_cast<uint32_t>(p.block_size), page, r);
-                const int64_t at = static_cast<int64_t>(page) * p.page_stride;
-                r4[i] = static_cast<int32_t>(at >> 8) + static_cast<int32_t>(r);
-                scales[i] = p.cache + at + static_cast<int64_t>(p.block_size) * 256 + r * 16u;
-            }
-            const int some = live != 0u ? __ffs(live) - 1 : 0;
-            const int32_t r_some = some == 0 ? r4[0] : some == 1 ? r4[1] : some == 2 ? r4[2] : r4[3];
+            int32_t slot;
+            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(slot)
+                         : "r"(ring + (j % kWIndexRing) * kTileKeys * 4) : "memory");
+            const bool is = slot >= 0 && slot < p.num_slots;
+            const uint32_t live = __ballot_sync(kFull, is);
+            uint32_t page, row;
+            page_row(is ? static_cast<uint32_t>(slot) : 0u, static_cast<uint32_t>(p.block_size), page, row);
+            const int64_t at = static_cast<int64_t>(page) * p.page_stride;
+            const int32_t rows = static_cast<int32_t>(at >> 8) + static_cast<int32_t>(row);   // of 256 bytes
+            const uint8_t* const scales = p.cache + at + static_cast<int64_t>(p.block_size) * 256 + row * 16u;
+            const uint8_t* from[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                if ((live >> i & 1u) == 0u) r4[i] = r_some;
-            const uint32_t bytes = __popc(__ballot_sync(kFull, live != 0u)) * 512u;
-            smem[kWOffLive + (j & 7) * 32 + lane] = static_cast<uint8_t>(live);
+                from[i] = p.cache + 16 * c +
+                          static_cast<int64_t>(__shfl_sync(kFull, rows, 8 * i + (lane >> 2))) * 256;
 #pragma unroll 1
-            for (int h = 0; h < 2; ++h) {
-                if (lane == 0) {
-                    if (half_rows >= kWRaw) wait_quiet(smem_addr(&bars->raw_empty[rw.s]), rw.parity ^ 1u, ok);
-                    if (h == 0 && j >= 2) wait_quiet(smem_addr(&bars->scales_empty[j & 1]), ((j >> 1) - 1) & 1, ok);
-                }
-                __syncwarp();
-                const uint32_t bar = smem_addr(&bars->raw[rw.s]);
+            for (int h = 0; h < 4; ++h) {
+                if (quarters >= M::kRaw) wait_quiet(smem_addr(&bars->raw_empty[rw.s]), rw.parity ^ 1u, ok);
                 if (h == 0) {
-                    const uint32_t to = smem_addr(smem + kWOffScales) + (j & 1) * kTileKeys * 16 + 64 * lane;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) cp_async16_or_zeros(to + 16 * i, scales[i], (live >> i & 1u) != 0u);
+                    if (j >= 2) wait_quiet(smem_addr(&bars->scales_empty[j & 1]), ((j >> 1) - 1) & 1, ok);
+                    cp_async16_or_zeros(smem_addr(smem + M::kScalesAt) + ((j & 1) * kTileKeys + rec + lane) * 16,
+                                        scales, is);
+                    if (lane == 0)
+                        *reinterpret_cast<uint32_t*>(smem + M::kLiveAt + (j & 7) * 16 + rec / 8) = live;
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    cp_async16_or_zeros(to0 + rw.s * kWRawBytes + i * 512, from[i] + 64 * h,
+                                        (live >> (8 * i + (lane >> 2)) & 1u) != 0u);
+                const uint32_t bar = smem_addr(&bars->raw[rw.s]);
                 cp_async_arrive(bar);
-                if (lane == 0) mbar_expect_tx(bar, bytes);
-                __syncwarp();
-                if (live != 0u)
-                    tma_gather4(smem_addr(smem + kWOffRaw) + rw.s * kWRawBytes + 512 * lane, &cache_map, bar,
-                                h * 128, r4[0], r4[1], r4[2], r4[3]);
+                if (lane == 0) mbar_arrive(bar);
                 rw.next();
-                ++half_rows;
+                ++quarters;
             }
             fetch();
         }
-        // the copies in flight land before the CTA leaves
-        cp_async_wait<0>();
-        for (int i = half_rows > kWRaw ? half_rows - kWRaw : 0; i < half_rows; ++i)
-            if (lane == 0) wait_quiet(smem_addr(&bars->raw[i % kWRaw]), (i / kWRaw) & 1, ok);
-        __syncwarp();
+        cp_async_wait<0>();   // the copies in flight land before the CTA leaves
     } else if (warp == kWMmaWarp) {
         // ------------------------------------------------------------- products
         const uint32_t elected = elect_lane();
         const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n_pad >> 3) << 17) |
                                (static_cast<uint32_t>(128 >> 4) << 24);
-        const uint64_t a_desc = sw128_desc(smem_addr(smem + kWOffStages));
+        const uint64_t a_desc = sw128_desc(smem_addr(smem + M::kStagesAt));
         const uint64_t q_desc = sw128_desc(smem_addr(smem));
         const uint32_t a_lo = static_cast<uint32_t>(a_desc), q_lo = static_cast<uint32_t>(q_desc);
         const uint32_t q_block = static_cast<uint32_t>(n_pad) * kRowBytes;   // 64 dims of the query
-        Ring<kWStages> st;
+        Ring<M::kStages> st;
         uint32_t loads = 0;
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
@@ -1078,7 +1087,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         }
     } else {
         // ------------------------------------------------------------- sums
-        float* const lse = reinterpret_cast<float*>(smem + kWOffLse);
+        float* const lse = reinterpret_cast<float*>(smem + M::kLseAt);
         const float scale = __fmul_rn(p.sm_scale, kLog2e);
         const uint64_t scale2 = f32x2(scale, scale);
         const int key = warp * 32 + lane;
@@ -1087,15 +1096,17 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
             if (j == 0 || ti == 0) {
                 group_sync(kSoftmaxBar, kWSoftWarps * 32);   // the query before is read
                 const int h = threadIdx.x;                   // 0 .. 127
-                lse[h] = h < p.num_heads
-                             ? __fmul_rn(-kLog2e, p.lse[qi * p.num_heads + h])
-                             : -INFINITY;                    // no head: exp2(-inf) = 0
+                if (h < kHeads)
+                    lse[h] = h < p.num_heads
+                                 ? __fmul_rn(-kLog2e, p.lse[qi * p.num_heads + h])
+                                 : -INFINITY;                // no head: exp2(-inf) = 0
                 group_sync(kSoftmaxBar, kWSoftWarps * 32);
             }
             wait_quiet(smem_addr(&bars->acc_full[j & 1]), (j >> 1) & 1, ok);
             __syncwarp();
             tc_fence_after_sync();
-            const bool live = (smem[kWOffLive + (j & 7) * 32 + (key >> 2)] >> (key & 3) & 1) != 0;
+            const uint32_t bits = *reinterpret_cast<const uint32_t*>(smem + M::kLiveAt + (j & 7) * 16 + 4 * warp);
+            const bool live = (bits >> lane & 1u) != 0u;
             uint64_t sum2 = f32x2(0.0f, 0.0f);
 #pragma unroll 1
             for (int c = 0; c < n_pad; c += 16) {
@@ -1291,14 +1302,15 @@ cudaError_t launch_sparse_attention(const AttentionParams& p, cudaStream_t strea
     const int n_pad = (p.num_heads + 15) / 16 * 16;   // columns of the product
     e = q_tensor_map(p, n_pad, &q_map);
     if (e != cudaSuccess) return e;
+    const auto kernel = p.num_heads <= 64 ? weight_kernel<64> : weight_kernel<128>;
+    const size_t smem = p.num_heads <= 64 ? WeightSmem<64>::kBytes : WeightSmem<128>::kBytes;
     int64_t warps = 0;
-    e = resident_warps(reinterpret_cast<const void*>(weight_kernel), kWeightThreads, kWeightSmem, &warps);
+    e = resident_warps(reinterpret_cast<const void*>(kernel), kWeightThreads, smem, &warps);
     if (e != cudaSuccess) return e;
     const int64_t ctas = warps / (kWeightThreads / 32);
     const int64_t tiles = (p.topk + kTileKeys - 1) / kTileKeys;
     const int64_t blocks = p.num_queries * tiles < ctas ? p.num_queries * tiles : ctas;
-    return launch_kernel(weight_kernel, blocks, kWeightThreads, kWeightSmem, stream, p.pdl, p, tiles,
-                         n_pad, q_map, cache_map);
+    return launch_kernel(kernel, blocks, kWeightThreads, smem, stream, p.pdl, p, tiles, n_pad, q_map);
 }
 
 }  // namespace gkr
