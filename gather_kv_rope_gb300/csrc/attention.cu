@@ -751,12 +751,15 @@ struct Cuts {
 };
 
 // Joins the pieces of each cut query: out = sum_i exp2(lse_i - lse) rows_i.  A block takes one
-// head of one query, four dims a thread; with many pieces, four groups of 128 threads take
-// every fourth piece and add up in shared memory.
-template <int kGroups>
-__global__ void __launch_bounds__(128 * kGroups)
+// head of one query, four dims a thread; four groups of 128 threads take every fourth piece and
+// add up in shared memory.  All of it is latency: for 32 pieces of 128 heads one group took
+// 13.2 us, four 7.0, and four whose first loads do not wait for the log-sum-exps 6.2 (38 pieces
+// of two queries of 64 heads 15.6, 8.5 and 7.2; the two to five pieces of 592 heads, more blocks
+// than fit at once, 5.6, 5.4 and 6.9).
+constexpr int kJoinGroups = 4, kJoinFirst = 4;
+__global__ void __launch_bounds__(128 * kJoinGroups)
     join_kernel(const AttentionParams p, const int32_t pairs, const __grid_constant__ Cuts cuts) {
-    __shared__ float4 part[kGroups > 1 ? kGroups : 1][kGroups > 1 ? 128 : 1];
+    __shared__ float4 part[kJoinGroups][128];
     const int32_t c = blockIdx.x / p.num_heads;
     const int32_t head = blockIdx.x - c * p.num_heads;
     const int g0 = cuts.first[c], n = cuts.pairs[c];
@@ -767,6 +770,16 @@ __global__ void __launch_bounds__(128 * kGroups)
     const float* const lses = rows + 2 * static_cast<int64_t>(pairs) * p.num_heads * 512 + head;
     // the first piece ends its pair's run (slot 1), the others begin theirs (slot 0)
     auto slot = [&](int i) -> int32_t { return (2 * (g0 + i) + (i == 0 ? 1 : 0)) * p.num_heads; };
+    auto load = [&](int i) -> float4 {
+        return *reinterpret_cast<const float4*>(rows + (static_cast<int64_t>(slot(i)) + head) * 512 + 4 * d);
+    };
+    // this thread's first pieces are on their way while the log-sum-exps are read
+    float4 first[kJoinFirst];
+#pragma unroll
+    for (int u = 0; u < kJoinFirst; ++u) {
+        const int i = group + u * kJoinGroups;
+        first[u] = i < n ? load(i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
     // the pieces' log-sum-exps, one a lane
     const int lane = threadIdx.x & 31;
     float m = -INFINITY;
@@ -778,28 +791,28 @@ __global__ void __launch_bounds__(128 * kGroups)
     for (int i = lane; i < n; i += 32) sum = __fadd_rn(sum, exp2_approx(__fsub_rn(lses[slot(i)], ref)));
     sum = warp_sum(sum);
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int i = group; i < n; i += kGroups) {
+    auto add = [&](int i, const float4& t) {
         const float w = exp2_approx(__fsub_rn(lses[slot(i)], ref));
-        const float4 t = *reinterpret_cast<const float4*>(
-            rows + (static_cast<int64_t>(slot(i)) + head) * 512 + 4 * d);
         acc.x = __fmaf_rn(w, t.x, acc.x);
         acc.y = __fmaf_rn(w, t.y, acc.y);
         acc.z = __fmaf_rn(w, t.z, acc.z);
         acc.w = __fmaf_rn(w, t.w, acc.w);
-    }
-    if constexpr (kGroups > 1) {
-        part[group][d] = acc;
-        __syncthreads();
-        if (group != 0) return;
+    };
 #pragma unroll
-        for (int i = 1; i < kGroups; ++i) {
-            const float4 t = part[i][d];
-            acc.x = __fadd_rn(acc.x, t.x);
-            acc.y = __fadd_rn(acc.y, t.y);
-            acc.z = __fadd_rn(acc.z, t.z);
-            acc.w = __fadd_rn(acc.w, t.w);
-        }
+    for (int u = 0; u < kJoinFirst; ++u)
+        if (group + u * kJoinGroups < n) add(group + u * kJoinGroups, first[u]);
+#pragma unroll 4
+    for (int i = group + kJoinFirst * kJoinGroups; i < n; i += kJoinGroups) add(i, load(i));
+    part[group][d] = acc;
+    __syncthreads();
+    if (group != 0) return;
+#pragma unroll
+    for (int i = 1; i < kJoinGroups; ++i) {
+        const float4 t = part[i][d];
+        acc.x = __fadd_rn(acc.x, t.x);
+        acc.y = __fadd_rn(acc.y, t.y);
+        acc.z = __fadd_rn(acc.z, t.z);
+        acc.w = __fadd_rn(acc.w, t.w);
     }
     const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
     const uint2 v = make_uint2(pack_bf16x2_rn(__fmul_rn(acc.x, inv), __fmul_rn(acc.y, inv)),
@@ -1216,9 +1229,8 @@ bool has_pieces(const Cut& cut) {
 }
 
 // The queries that pairs' runs begin inside of.
-void find_cuts(const Cut& cut, Cuts* cuts, int* most) {
+void find_cuts(const Cut& cut, Cuts* cuts) {
     cuts->n = 0;
-    *most = 0;
     for (int32_t g = 1; g < cut.pairs; ++g) {
         const int64_t begin = cut.begin(g), q = begin / cut.per_query;
         if (begin - q * cut.per_query == 0) continue;
@@ -1227,7 +1239,7 @@ void find_cuts(const Cut& cut, Cuts* cuts, int* most) {
             cuts->first[cuts->n] = static_cast<int16_t>(g - 1);
             cuts->pairs[cuts->n++] = 1;
         }
-        if (++cuts->pairs[cuts->n - 1] > *most) *most = cuts->pairs[cuts->n - 1];
+        ++cuts->pairs[cuts->n - 1];
     }
 }
 
@@ -1289,13 +1301,10 @@ cudaError_t launch_sparse_attention(const AttentionParams& p, cudaStream_t strea
                       stream, p.pdl, p, cut, q_map, cache_map);
     if (e != cudaSuccess) return e;
     Cuts cuts;
-    int most = 0;
-    find_cuts(cut, &cuts, &most);
+    find_cuts(cut, &cuts);
     if (cuts.n > 0) {
         const int64_t blocks = static_cast<int64_t>(cuts.n) * p.num_heads;
-        // four groups from eight pieces on: measured at 128 heads, ...
-        e = most >= 8 ? launch_kernel(join_kernel<4>, blocks, 512, 0, stream, p.pdl, p, cut.pairs, cuts)
-                      : launch_kernel(join_kernel<1>, blocks, 128, 0, stream, p.pdl, p, cut.pairs, cuts);
+        e = launch_kernel(join_kernel, blocks, 128 * kJoinGroups, 0, stream, p.pdl, p, cut.pairs, cuts);
         if (e != cudaSuccess) return e;
     }
     if (p.weights == nullptr || p.topk == 0) return e;
