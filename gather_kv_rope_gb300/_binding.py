@@ -264,9 +264,8 @@ def alloc_cache(num_pages: int, block_size: int, record: int, device="cuda",
                 page_stride_bytes: int | None = None, fill: int | None = None) -> torch.Tensor:
     """Allocate a paged cache whose stride(0) is the page stride (padded to the
     record's alignment): uint8 [num_pages, block_size, record] for the packed records 528,
-    584 and 272
-    (inside a page the bytes are a data region then a scale region, not row by row),
-    float8_e4m3fn [num_pages, block_size, 512] for record 512, bfloat16
+    584 and 272 (inside a page the bytes are a data region then a scale region, not row by
+    row), float8_e4m3fn [num_pages, block_size, 512] for record 512, bfloat16
     [num_pages, block_size, 512] for record 1024.  `fill` sets every byte."""
     ps = page_stride(record, block_size) if page_stride_bytes is None else int(page_stride_bytes)
     if ps <= 0:
