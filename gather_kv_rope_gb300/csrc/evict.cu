@@ -8,18 +8,22 @@
 // every number, -0 with 0.
 //
 // The weight of the last entry to be kept is found by its bits: a weight's 32 bits map to an
-// unsigned key in the order of the values, and four passes, each counting the keys that share
-// the bits found so far by their next 8 bits, fix those.  (Weights are few powers of two apart:
-// eight copies of the counters, taken by the lane, keep most additions off each other's.)  Then each entry's fate is
-// known -- kept if newer, or above that key, or equal to it and among the first `ties` such --
-// and its place is a count of bits: entries are handled as words of 32 bits (live, competing,
-// kept), one ballot each, and prefix sums run over the words.  Counts are whole numbers, so the
-// result does not depend on the order of threads.
+// unsigned key in the order of the values, and up to four passes, each counting the keys that
+// share the bits found so far by their next 8 bits, fix those, until all keys that share them
+// stay.  (Weights are few powers of two apart: eight copies of the counters, taken by the lane,
+// keep most additions off each other's.)  Then each entry's fate is known -- kept if newer, or
+// above that key, or equal to it and among the first `ties` such -- and its place is a count of
+// bits: entries are handled as words of 32 bits (live, competing, kept), and prefix sums run over
+// the words.  Counts are whole numbers, so the result does not depend on the order of threads.
 //
-// A row is read once (8 bytes an entry; the kept and evicted slots a second time, from the
-// caches): its keys stay in shared memory.  Long rows are split over a cluster of up to eight
-// CTAs, which read each other's counts through distributed shared memory.  The work is a few
-// microseconds of dependent steps, so latency bounds it, not memory.
+// A row is read once (8 bytes an entry; the kept weights a second time): its keys and slots stay
+// in shared memory.  Long rows are split over a cluster of up to eight CTAs, which read each
+// other's counts through distributed shared memory.  The work is a few dependent steps on little
+// data, so their latency and the instructions of a few CTAs bound it, not memory: with one entry a
+// lane and instruction a step over 16384 entries of a CTA took 3600 cycles (25 instructions for
+// 32 entries), so a lane takes four at a time where it can.  Measured in a graph, keeping 4096 of
+// 4 x 131071 entries 24 us (one entry a lane 26), 2048 of 128 x 2049 7.2 us (9.6), 65536 of
+// 16 x 1000000 320 us (480).
 #include "device.cuh"
 #include "launch.h"
 #include "tensor.cuh"
@@ -29,14 +33,17 @@ namespace gkr {
 namespace {
 
 constexpr int kBins = 256, kCopies = 8;
-// Keys kept in shared memory up to this many entries a CTA; longer parts read the weights again
-// for each pass.
-constexpr int kCachedKeys = 36864;
+// Keys, and slots, kept in shared memory up to this many entries a CTA; longer parts read the
+// weights again for each pass, and the slots when they leave.
+constexpr int kCachedKeys = 36864, kCachedSlots = 20480;
+constexpr size_t kMostWords = kCachedSlots / 32 * (16 + 256);   // bytes
+static_assert(kCachedKeys / 32 * (16 + 128) <= kMostWords, "fits where keys and slots do");
 constexpr int kMaxCluster = 8;
 
-// A weight's key: unsigned order = order of the values; NaN 0 (below -inf), -0 as 0.
+// A weight's key: unsigned order = order of the values; NaN 1 (below -inf, 2^23 - 1), -0 as 0.
+// What does not compete has key 0.
 __device__ __forceinline__ uint32_t weight_key(float w) {
-    if (w != w) return 0u;
+    if (w != w) return 1u;
     const uint32_t b = __float_as_uint(__fadd_rn(w, 0.0f));
     return (b & 0x80000000u) != 0u ? ~b : (b | 0x80000000u);
 }
@@ -59,29 +66,64 @@ __device__ __forceinline__ int32_t block_prefix(int32_t v, int32_t* shared, int 
     return x - v + __reduce_add_sync(kFull, lane < warp ? w : 0);
 }
 
-// Exclusive prefix sums of the popcounts of bits[0 .. n) into out; returns their total.
+// A word of 32 entries: which are live; which compete, then tie, then are kept; and how many
+// live, and kept, ones come before it.
+struct alignas(16) Word {
+    uint32_t live, some;
+    int32_t live_before, some_before;
+};
+
+// Exclusive prefix sums of the popcounts of a field of word[0 .. n) into another; returns their
+// total.
 template <int kThreads>
-__device__ __forceinline__ int32_t scan_words(const uint32_t* bits, int32_t* out, int n,
+__device__ __forceinline__ int32_t scan_words(Word* word, uint32_t Word::* bits, int32_t Word::* out, int n,
                                               int32_t* shared, int warp, int lane) {
     const int per = (n + kThreads - 1) / kThreads;
     const int a = threadIdx.x * per, b = a + per < n ? a + per : n;
     int32_t sum = 0;
-    for (int i = a; i < b; ++i) sum += __popc(bits[i]);
+    for (int i = a; i < b; ++i) sum += __popc(word[i].*bits);
     int32_t total;
     int32_t x = block_prefix<kThreads>(sum, shared, warp, lane, &total);
     for (int i = a; i < b; ++i) {
-        out[i] = x;
-        x += __popc(bits[i]);
+        word[i].*out = x;
+        x += __popc(word[i].*bits);
     }
     __syncthreads();
     return total;
+}
+
+// Four bits of each lane as the words of eight lanes each: all eight get theirs.
+__device__ __forceinline__ uint32_t word_of_nibbles(uint32_t nibble, int lane) {
+    uint32_t x = nibble << (4 * (lane & 7));
+#pragma unroll
+    for (int d = 1; d < 8; d <<= 1) x |= __shfl_xor_sync(kFull, x, d);
+    return x;
+}
+
+// Entries i .. i + 3 of a row, `none` past its end.
+template <typename V4, typename T>
+__device__ __forceinline__ V4 load4(const T* row, int32_t i, int32_t len, bool aligned, T none) {
+    V4 v;
+    if (aligned && i + 4 <= len) {
+        v = __ldg(reinterpret_cast<const V4*>(row + i));
+    } else {
+        v.x = i < len ? __ldg(row + i) : none;
+        v.y = i + 1 < len ? __ldg(row + i + 1) : none;
+        v.z = i + 2 < len ? __ldg(row + i + 2) : none;
+        v.w = i + 3 < len ? __ldg(row + i + 3) : none;
+    }
+    return v;
 }
 
 // The lowest n set bits of x.
 __device__ __forceinline__ uint32_t lowest_bits(uint32_t x, int32_t n) {
     if (n <= 0) return 0u;
     if (n >= __popc(x)) return x;
-    return x & ((2u << __fns(x, 0, n)) - 1u);
+    int p = 0;   // the highest place with at most n bits below it
+#pragma unroll
+    for (int step = 16; step >= 1; step >>= 1)
+        if (__popc(x & ((1u << (p + step)) - 1u)) <= n) p += step;
+    return x & ((1u << p) - 1u);
 }
 
 __device__ __forceinline__ int32_t read_peer(const int32_t* p, uint32_t rank) {
@@ -90,41 +132,27 @@ __device__ __forceinline__ int32_t read_peer(const int32_t* p, uint32_t rank) {
     return v;
 }
 
-// Entries of words w0, w0 + step, ...: their slots (-1 past the part's end) and weights, all loads on
-// their way before the first is used.
-constexpr int kBatch = 8;
-__device__ __forceinline__ void load_batch(const int32_t* idx, const float* wts, int w0, int step,
-                                           int n, int32_t len, int lane, int32_t (&s)[kBatch],
-                                           float (&x)[kBatch]) {
-#pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
-        const int32_t i = 32 * (w0 + step * u) + lane;
-        const bool is = w0 + step * u < n && i < len;
-        s[u] = is ? __ldg(idx + i) : -1;
-        x[u] = is ? __ldg(wts + i) : 0.0f;
-    }
-}
+constexpr int kBatch = 4;   // groups of four words (at the end: words) of a warp in flight
 
 struct alignas(16) EvictShared {
     int32_t scan[32];
     int32_t live, strict, tied;          // this CTA's counts, read by the others
-    int32_t found[2];
+    int32_t found[3];
     int32_t sum[4][kBins];               // counts, one array a pass: the others read it at their own time
     alignas(16) int32_t hist[kBins][kCopies];
 };
 
 // words: words of 32 entries of a CTA's part (the same for all CTAs of a row; the last may have
-// less to do); cached: its keys lie in shared memory.
+// less to do); its keys, and its slots, lie in shared memory where they are `cached`.
 template <int kThreads>
 __global__ void __launch_bounds__(kThreads, 1)
-    evict_kernel(const EvictParams p, const int32_t words, const int32_t cluster, const bool cached) {
+    evict_kernel(const EvictParams p, const int32_t words, const int32_t cluster,
+                 const bool keys_cached, const bool slots_cached) {
     extern __shared__ __align__(16) uint8_t dynamic[];
     EvictShared& sh = *reinterpret_cast<EvictShared*>(dynamic);
-    uint32_t* const live = reinterpret_cast<uint32_t*>(dynamic + sizeof(EvictShared));
-    uint32_t* const some = live + words;                 // competing, then tied, then kept
-    int32_t* const live_before = reinterpret_cast<int32_t*>(some + words);
-    int32_t* const some_before = live_before + words;
-    uint32_t* const keys = reinterpret_cast<uint32_t*>(some_before + words);
+    Word* const word = reinterpret_cast<Word*>(dynamic + sizeof(EvictShared));
+    uint32_t* const keys = reinterpret_cast<uint32_t*>(word + words);
+    int32_t* const slots = reinterpret_cast<int32_t*>(keys + 32 * words);
     constexpr int kWarps = kThreads / 32;
     const int lane = threadIdx.x & 31;
     const int warp = threadIdx.x >> 5;
@@ -132,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int64_t r = blockIdx.x / cluster;
     const int32_t e0 = static_cast<int32_t>(rank) * words * 32;
     const int32_t len = p.length - e0 < 0 ? 0 : p.length - e0 < words * 32 ? p.length - e0 : words * 32;
-    const int32_t n = (len + 31) / 32;                   // words of this part
+    const int32_t n = (len + 127) / 128 * 4;             // words of this part
     pdl_wait_previous();
     pdl_release_next();
     const int32_t* const idx = p.indices + r * p.index_stride + e0;
@@ -152,22 +180,44 @@ __global__ void __launch_bounds__(kThreads, 1)
         return __reduce_add_sync(kFull, v);
     };
 
-    for (int w0 = warp; w0 < n; w0 += kWarps * kBatch) {
-        int32_t s[kBatch];
-        float x[kBatch];
-        load_batch(idx, wts, w0, kWarps, n, len, lane, s, x);
+    const bool aligned = ((reinterpret_cast<uintptr_t>(idx) | reinterpret_cast<uintptr_t>(wts)) & 15) == 0;
+    // The keys of words w .. w + 3, four a lane.
+    auto load_keys = [&](int w) -> uint4 {
+        const int32_t i = 32 * w + 4 * lane;
+        if (keys_cached) return lds16(keys + i);
+        const uint32_t c = word[w + (lane >> 3)].some >> (4 * (lane & 7));
+        const float4 x = load4<float4, float>(wts, i, len, aligned, 0.0f);
+        return make_uint4((c & 1u) != 0u ? weight_key(x.x) : 0u, (c & 2u) != 0u ? weight_key(x.y) : 0u,
+                          (c & 4u) != 0u ? weight_key(x.z) : 0u, (c & 8u) != 0u ? weight_key(x.w) : 0u);
+    };
+
+    for (int w0 = 4 * warp; w0 < n; w0 += 4 * kWarps * kBatch) {
+        int4 s[kBatch];
+        float4 x[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const int w = w0 + kWarps * u;
-            const uint32_t b = __ballot_sync(kFull, s[u] >= 0);
+            const int32_t i = 32 * (w0 + 4 * kWarps * u) + 4 * lane;
+            s[u] = load4<int4, int32_t>(idx, i, len, aligned, -1);
+            if (keys_cached) x[u] = load4<float4, float>(wts, i, len, aligned, 0.0f);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int w = w0 + 4 * kWarps * u;
             if (w < n) {                                 // warp-uniform
-                if (cached) keys[32 * w + lane] = s[u] >= 0 ? weight_key(x[u]) : 0u;
-                if (lane == 0) live[w] = b;
+                const bool a = s[u].x >= 0, b = s[u].y >= 0, c = s[u].z >= 0, d = s[u].w >= 0;
+                const int32_t i = 32 * w + 4 * lane;
+                if (keys_cached)
+                    *reinterpret_cast<uint4*>(keys + i) =
+                        make_uint4(a ? weight_key(x[u].x) : 0u, b ? weight_key(x[u].y) : 0u,
+                                   c ? weight_key(x[u].z) : 0u, d ? weight_key(x[u].w) : 0u);
+                if (slots_cached) *reinterpret_cast<int4*>(slots + i) = s[u];
+                const uint32_t bits = word_of_nibbles((a ? 1u : 0u) | (b ? 2u : 0u) | (c ? 4u : 0u) | (d ? 8u : 0u), lane);
+                if ((lane & 7) == 0) word[w + (lane >> 3)].live = bits;
             }
         }
     }
     __syncthreads();
-    int32_t mine = scan_words<kThreads>(live, live_before, n, sh.scan, warp, lane);
+    int32_t mine = scan_words<kThreads>(word, &Word::live, &Word::live_before, n, sh.scan, warp, lane);
     if (threadIdx.x == 0) sh.live = mine;
     sync();
     int32_t live0;                                       // live entries before this part
@@ -175,9 +225,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int32_t fresh = p.recent < all ? p.recent : all;   // protected entries
     const int32_t old = all - fresh;                         // the first `old` live ones compete
     const int32_t room = p.keep - fresh < old ? p.keep - fresh : old;
-    for (int w = threadIdx.x; w < n; w += kThreads)
-        some[w] = lowest_bits(live[w], old - live0 - live_before[w]);
+    for (int w = threadIdx.x; w < n; w += kThreads) {
+        const uint32_t l = word[w].live, c = lowest_bits(l, old - live0 - word[w].live_before);
+        word[w].some = c;
+    }
     __syncthreads();
+    if (keys_cached && live0 + mine > old) {             // protected entries do not compete
+        for (int w = warp; w < n; w += kWarps)
+            if (((word[w].live & ~word[w].some) >> lane & 1u) != 0u) keys[32 * w + lane] = 0u;
+    }
 
     // the key of the last competing entry kept, and how many of its equals stay
     uint32_t key = 0, mask = 0;
@@ -187,12 +243,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int shift = 24 - 8 * pass;
             for (int i = threadIdx.x; i < kBins * kCopies; i += kThreads) sh.hist[0][i] = 0;
             __syncthreads();
-            for (int w = warp; w < n; w += kWarps) {
-                if ((some[w] >> lane & 1u) != 0u) {
-                    const int32_t i = 32 * w + lane;
-                    const uint32_t k = cached ? keys[i] : weight_key(__ldg(wts + i));
-                    if ((k & mask) == key) atomicAdd(&sh.hist[k >> shift & 255u][lane & (kCopies - 1)], 1);
-                }
+            auto count = [&](uint32_t k) {
+                if ((k & mask) == key) atomicAdd(&sh.hist[k >> shift & 255u][lane & (kCopies - 1)], 1);
+            };
+#pragma unroll 2
+            for (int w = 4 * warp; w < n; w += 4 * kWarps) {
+                const uint4 k = load_keys(w);
+                count(k.x);
+                count(k.y);
+                count(k.z);
+                count(k.w);
             }
             __syncthreads();
             // bins from the top: thread t < 256 has bin 255 - t
@@ -223,35 +283,47 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (above < want && above + h >= want) {
                 sh.found[0] = bin;
                 sh.found[1] = ties - above;
+                sh.found[2] = h;
             }
             __syncthreads();
             key |= static_cast<uint32_t>(sh.found[0]) << shift;
             mask |= 255u << shift;
             ties = sh.found[1];
-            __syncthreads();
+            const bool whole = sh.found[2] == ties;      // every key that begins like this one stays:
+            __syncthreads();                             // its other bits do not matter
+            if (whole) break;
         }
     }
 
-    // competing entries above the key, and those equal to it
+    // competing entries above the key, and those equal to it, in the bits that were fixed
     int32_t strict = 0, tied = 0;
     if (room < old) {
-        for (int w = warp; w < n; w += kWarps) {
-            const uint32_t c = some[w];
-            const int32_t i = 32 * w + lane;
-            const bool is = (c >> lane & 1u) != 0u;
-            const uint32_t k = !is ? 0u : cached ? keys[i] : weight_key(__ldg(wts + i));
-            const uint32_t above = __ballot_sync(kFull, is && k > key);
-            const uint32_t equal = __ballot_sync(kFull, is && k == key);
-            __syncwarp();
-            if (lane == 0) {
-                some[w] = equal;
-                some_before[w] = static_cast<int32_t>(above | (live[w] & ~c));   // bits kept in any case
+#pragma unroll 2
+        for (int w0 = 4 * warp; w0 < n; w0 += 4 * kWarps) {
+            const uint4 k4 = load_keys(w0);
+            const uint32_t k[4] = {k4.x & mask, k4.y & mask, k4.z & mask, k4.w & mask};
+            uint32_t above = 0u, equal = 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                above |= k[i] > key ? 1u << i : 0u;
+                equal |= k[i] == key ? 1u << i : 0u;
             }
-            strict += __popc(above | (live[w] & ~c));
-            tied += __popc(equal);
+            above = word_of_nibbles(above, lane);
+            equal = word_of_nibbles(equal, lane);
+            if ((lane & 7) == 0) {
+                Word& w = word[w0 + (lane >> 3)];
+                const uint32_t c = w.some, stay = (above & c) | (w.live & ~c);   // kept in any case
+                equal &= c;
+                w.some = equal;
+                w.some_before = static_cast<int32_t>(stay);
+                strict += __popc(stay);
+                tied += __popc(equal);
+            }
         }
     }
-    // totals of this CTA (each word was counted by all lanes of one warp)
+    // totals of this CTA
+    strict = __reduce_add_sync(kFull, strict);
+    tied = __reduce_add_sync(kFull, tied);
     __syncthreads();
     if (threadIdx.x == 0) {
         sh.strict = 0;
@@ -278,39 +350,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         int32_t run = tied0;
         for (int w0 = 0; w0 < n; w0 += kThreads) {
             const int w = w0 + threadIdx.x;
-            const uint32_t equal = w < n ? some[w] : 0u;
+            const uint32_t equal = w < n ? word[w].some : 0u;
             int32_t total;
             const int32_t x = run + block_prefix<kThreads>(__popc(equal), sh.scan, warp, lane, &total);
             run += total;
-            if (w < n) some[w] = static_cast<uint32_t>(some_before[w]) | lowest_bits(equal, ties - x);
+            if (w < n) word[w].some = static_cast<uint32_t>(word[w].some_before) | lowest_bits(equal, ties - x);
         }
         __syncthreads();
     } else {                                             // every live entry stays
-        for (int w = threadIdx.x; w < n; w += kThreads) some[w] = live[w];
+        for (int w = threadIdx.x; w < n; w += kThreads) word[w].some = word[w].live;
         kept0 = live0;
         __syncthreads();
     }
-    scan_words<kThreads>(some, some_before, n, sh.scan, warp, lane);
+    scan_words<kThreads>(word, &Word::some, &Word::some_before, n, sh.scan, warp, lane);
 
     int32_t* const kept = p.kept + r * p.keep;
     float* const kept_w = p.kept_weights + r * p.keep;
     int64_t* const gone = p.evicted + r * (p.length - p.keep);
+    const uint32_t below = (1u << lane) - 1u;
     for (int w0 = warp; w0 < n; w0 += kWarps * kBatch) {
+        uint4 x[kBatch];
         int32_t s[kBatch];
-        float x[kBatch];
-        load_batch(idx, wts, w0, kWarps, n, len, lane, s, x);
+        float weight[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const int w = w0 + kWarps * u;
-            if (w < n && s[u] >= 0) {
-                const uint32_t l = live[w], k = some[w], below = (1u << lane) - 1u;
-                const int32_t a = kept0 + some_before[w] + __popc(k & below);
-                if ((k >> lane & 1u) != 0u) {
-                    kept[a] = s[u];
-                    kept_w[a] = x[u];
-                } else {
-                    gone[live0 + live_before[w] + __popc(l & below) - a] = s[u];
-                }
+            const int32_t i = 32 * w + lane;
+            x[u] = w < n ? lds16(word + w) : make_uint4(0u, 0u, 0u, 0u);
+            const bool is = (x[u].x >> lane & 1u) != 0u;
+            s[u] = !is ? -1 : slots_cached ? slots[i] : __ldg(idx + i);
+            weight[u] = (x[u].y >> lane & 1u) != 0u ? __ldg(wts + i) : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const int32_t before = kept0 + static_cast<int32_t>(x[u].w) + __popc(x[u].y & below);
+            if ((x[u].y >> lane & 1u) != 0u) {
+                kept[before] = s[u];
+                kept_w[before] = weight[u];
+            } else if (s[u] >= 0) {
+                gone[live0 + static_cast<int32_t>(x[u].z) + __popc(x[u].x & below) - before] = s[u];
             }
         }
     }
@@ -328,13 +406,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int kThreads>
 cudaError_t launch(const EvictParams& p, int32_t cluster, cudaStream_t stream) {
-    const int32_t words = (p.length + 32 * cluster - 1) / (32 * cluster);
-    const bool cached = words * 32 <= kCachedKeys;
-    const size_t smem = sizeof(EvictShared) + static_cast<size_t>(words) * (cached ? 16 + 128 : 16);
+    const int32_t words = (p.length + 128 * cluster - 1) / (128 * cluster) * 4;
+    const bool keys_cached = words * 32 <= kCachedKeys, slots_cached = words * 32 <= kCachedSlots;
+    const size_t smem = sizeof(EvictShared) +
+                        static_cast<size_t>(words) * (16 + (keys_cached ? 128 : 0) + (slots_cached ? 128 : 0));
     // raises the kernel's limit once per device
     int64_t warps = 0;
     const cudaError_t e = resident_warps(reinterpret_cast<const void*>(evict_kernel<kThreads>), kThreads,
-                                         sizeof(EvictShared) + kCachedKeys / 32 * 144, &warps);
+                                         sizeof(EvictShared) + kMostWords, &warps);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(p.rows * cluster));
@@ -350,7 +429,8 @@ cudaError_t launch(const EvictParams& p, int32_t cluster, cudaStream_t stream) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, evict_kernel<kThreads>, p, words, cluster, cached);
+    return cudaLaunchKernelEx(&cfg, evict_kernel<kThreads>, p, words, cluster, keys_cached,
+                              slots_cached);
 }
 
 }  // namespace
