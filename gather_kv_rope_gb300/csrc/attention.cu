@@ -11,12 +11,16 @@
 //
 // One pass over the records with a running maximum and sum, the tensor cores of two SMs on one
 // query.  Per record and 128 heads both products are 2 x 128 x 512 multiply-adds, 16 cycles of
-// two SMs' tensor cores, against 272 bytes of memory: with many heads the products bound
-// the kernel, so everything else is arranged to stay below those 16 cycles.
+// two SMs' tensor cores, against 272 bytes of memory: with many heads the products are the
+// floor, so everything else is arranged to run beside them.
 //   * The accumulator of a query, 128 heads x 512 dims fp32, is all of an SM's tensor memory.  A
 //     pair of CTAs (cta_group::2, M = 128) splits it: each holds its 64 heads' rows, 256 columns
-//     on 128 lanes, and has room for the logits.
-//   * Records are dequantised once to bf16 in shared memory and are there both operands: rows
+//     on 128 lanes, and has room for two chunks' logits and for three quarters of the query,
+//     which so need not be read from shared memory by every product.
+//   * Records come by four-row gathers of the copy engine (one copy a record took 33 cycles
+//     of issue, a warp's loads more registers than there are), their slots six chunks
+//     ahead: a chunk takes about 2100 cycles, a load from memory up to 4000.
+//   * They are dequantised once to bf16 in shared memory and are there both operands: rows
 //     of 128 bytes (64 dims) in 8-row swizzle groups read K-major for q . K (reduction over
 //     dims) and MN-major for p . K (reduction over records).  A product of the pair takes half
 //     of its columns from each CTA, so for q . K a CTA needs 32 of a chunk's 64 records in
@@ -25,14 +29,22 @@
 //     first with the CTA's 32 records; once q . K has read them, the half of the dims that
 //     the other CTA multiplies is replaced by the other 32 records' dims of its own half.  While
 //     that happens the softmax of the chunk runs.
-//   * Work: the chunks of all queries in a row, cut evenly over the pairs.  A query that lies
-//     inside one pair's run is finished there; the pieces of a cut one go to the workspace
-//     (fp32 rows and their log-sum-exp) and a second kernel joins them.
+//   * Work: the chunks of all queries in a row, cut evenly over the pairs, or whole queries
+//     where that costs no more (make_cut).  A query that lies inside one pair's run is
+//     finished there; the pieces of a cut one go to the workspace (fp32 rows and their
+//     log-sum-exp) and a second kernel joins them.
+// Measured: 128 queries x 128 heads x 2048 entries 76 us, 900 TFLOP/s, 46 % of the measured
+// matrix rate.  A chunk of 64 records takes 2100 cycles, its products alone 1165 (64 columns a
+// product run at 63 % of the rate of 256).  What is left is one stage's way: dequantised (1200),
+// multiplied, its softmax taken and half of it replaced (1300), multiplied again, three stages
+// at a time being all that shared memory holds; issue slots are 74 % taken meanwhile.  Tried and
+// slower: a warp for each product (84 us: 72 registers), eight warps that replace (82), the
+// dequantisation's warps on alternate chunks (79); as fast: 32 rows of each CTA for up to 64
+// heads, which leaves every second softmax warp idle.
 #include <cmath>
 #include <mutex>
 #include <vector>
 
-#include "decode.cuh"
 #include "device.cuh"
 #include "launch.h"
 #include "tensor.cuh"

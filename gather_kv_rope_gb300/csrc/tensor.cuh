@@ -119,7 +119,7 @@ __device__ __forceinline__ void tmem_st_wait() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// Shared-memory matrix descriptor of the K-major B operand with the 128-byte swizzle: start
+// Shared-memory matrix descriptor of a K-major operand with the 128-byte swizzle: start
 // address >> 4 (bits 0-13), leading offset (unused by this layout; 1) at bits 16-29,
 // stride between 8-row groups (1024 bytes) >> 4 at bits 32-45, descriptor version 1 at
 // bits 46-47, swizzle mode 128B (2) at bits 61-63.  The operand's rows are 128 bytes (64
@@ -154,10 +154,9 @@ __device__ __forceinline__ void warp_wait_or_flag(uint32_t bar, uint32_t parity,
 
 // wait_or_flag for kernels whose warps run different code and wait at the same time: a poll is
 // a few instructions, because the polls of waiting warps compete for issue slots and
-// instruction fetches with the warps that work, and the limit is counted in SM clocks
-// (40 million: 20 ms at 2 GHz): reading %globaltimer takes 5 us and holds up the SM's global
-// loads behind it.
-constexpr int64_t kWaitClocks = 40000000;
+// instruction fetches with the warps that work, and the limit is counted in SM clocks (4
+// billion: 2 s at 2 GHz), which are read in a few cycles.
+constexpr int64_t kWaitClocks = INT64_C(4000000000);
 __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity) {
     const int64_t t0 = clock64();
     do {

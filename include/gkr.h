@@ -82,8 +82,9 @@ typedef enum gkr_status {
 #define GKR_ERR_INDEX 4  /* gather: index < -1 or >= num_pages * block_size (row zeroed) */
 #define GKR_ERR_SCALE 8  /* fp8 cache: *fp8_scale not a positive finite number (nothing
                             written by the insert; every gathered row zeroed)           */
-#define GKR_ERR_TIMEOUT 16 /* sparse logits: a bounded wait for the tensor cores gave up
-                              (the launch's logits are not written); not expected      */
+#define GKR_ERR_TIMEOUT 16 /* sparse logits and attention: a bounded wait for the tensor
+                              cores gave up (results that depend on it are not written);
+                              not expected                                              */
 
 /*
  * Paged cache geometry.  The cache is num_pages pages, page p starting at byte
