@@ -680,8 +680,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 const float lse2 =
                     total == 0.0f ? -INFINITY : __fadd_rn(__fsub_rn(m, kLift), log2f(total));
                 // A piece that does not begin its query is its pair's first: slot 0.  Rows leave
-                // through the warp's eighth of the probabilities' buffers, free now, so that
-                // four lanes write 64 bytes of one row.
+                // through a part of the probabilities' buffers, free now, so that four lanes write
+                // 64 bytes of one row: an eighth for each warp, in the rows of its own heads,
+                // which their other warps do not write before it is done (head_any); those of
+                // the other heads may be at the next query already.
                 const int64_t slot = 2 * pair + (seg == 0 ? 1 : 0);
                 float* const pieces = static_cast<float*>(p.workspace);
                 const int64_t at = (whole ? qi : slot) * p.num_heads;
@@ -689,7 +691,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 uint8_t* const dst = (whole ? static_cast<uint8_t*>(p.out)
                                             : reinterpret_cast<uint8_t*>(pieces)) +
                                      at * dst_row + (2 * half + part) * (dst_row >> 2);
-                const uint32_t st = smem_addr(smem + kOffP) + warp * 2048;
+                const uint32_t st = smem_addr(smem + kOffP) + (warp >> 2) * kPBytes + (warp & 1) * (kPBytes / 2) +
+                                    (warp >> 1 & 1) * (kPBytes / 4);
                 const uint32_t mine = st + lane * 64 + (((lane >> 1) & 3) << 4);
                 const int head0 = static_cast<int>(rank) * kPairHeads + (warp & 1) * 32;
                 const int step = whole ? 32 : 16;

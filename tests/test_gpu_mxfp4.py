@@ -429,3 +429,20 @@ def test_evict_ties_across_parts(gkr, L):
     w[2] = 1.0
     for keep, recent in [(L // 2, 0), (L // 3, L // 4), (L - 1, 7), (5, 5)]:
         evict_check(gkr, idx, w, keep, recent)
+
+
+@pytest.mark.parametrize("Q,H,K,holes", [(64, 128, 700, 0.3), (200, 128, 130, 0.0), (160, 32, 130, 0.5),
+                                         (5, 64, 3000, 0.6)])
+def test_attention_again_and_again(gkr, Q, H, K, holes):
+    """Masks that differ from chunk to chunk, and queries that follow one another on an SM: the
+    first results are right, and the same bits come every time, whatever ran before."""
+    c = Case(gkr, Q, H, K, holes=holes, seed=Q, pages=40)
+    out, lse = c.check(gkr)
+    w = c.weights.clone()
+    for i in range(60):
+        if i % 3 == 0:   # other work between, so that timing differs
+            torch.full((1 << (18 + i % 8),), float("nan"), device=DEV)
+        c.weights.copy_(torch.from_numpy(c.w0))
+        o, l = gkr.sparse_attention(c.q, c.cache, c.indices, c.sm, weights=c.weights)
+        assert torch.equal(o.view(torch.int16), out.view(torch.int16)), i
+        assert torch.equal(l, lse) and torch.equal(c.weights, w), i
