@@ -156,6 +156,7 @@ struct alignas(8) PairBarriers {
     uint64_t s_full[2];          // products: the logits of a chunk are complete
     uint64_t stage_empty[kStages];   // products: p . K has read the stage
     uint64_t o_done[2];          // products: p . K of a chunk is complete
+    uint64_t live[kIndexRing];   // gather warps: both masks of a chunk's entries are written
     uint32_t tmem_base;
     int32_t timed_out;
 };
@@ -294,6 +295,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
             mbar_init(smem_addr(&bars->s_full[b]), 1);
             mbar_init(smem_addr(&bars->o_done[b]), 1);
         }
+        for (int i = 0; i < kIndexRing; ++i) mbar_init(smem_addr(&bars->live[i]), 2);
         mbar_init(smem_addr(&bars->q_full), 2 * kSoftmaxWarps);
         mbar_init(smem_addr(&bars->q_next), 1);
         mbar_init(smem_addr(&bars->q_live), 1);
@@ -426,8 +428,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
             __syncwarp();
             const uint32_t raw = raw0 + rw.s * kRawBytes, bar = full + 8 * rw.s;
             if (g != 1) {
-                if (lane == 0)
+                if (lane == 0) {
                     reinterpret_cast<uint32_t*>(smem + kOffLive)[(j & (kIndexRing - 1)) * 2 + cta] = live;
+                    mbar_arrive(smem_addr(&bars->live[j & (kIndexRing - 1)]));
+                }
                 cp_async16_or_zeros(raw + scale_dst,
                                     p.cache + at + static_cast<int64_t>(p.block_size) * 256 + r * 16u, is);
                 cp_async_arrive(bar);
@@ -591,6 +595,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
             const bool last = j + 1 == n || ci + 1 == cut.per_query;   // of this segment
+            // the other CTA's records are not part of what q . K waits for, so their mask has a
+            // barrier of its own (the ring's next round comes after this chunk's probabilities)
+            wait_quiet(smem_addr(&bars->live[j & (kIndexRing - 1)]), (j / kIndexRing) & 1, ok);
             const uint32_t live =
                 (reinterpret_cast<const uint32_t*>(smem + kOffLive)[(j & (kIndexRing - 1)) * 2 + half] >>
                  (16 * part)) & 0xFFFFu;

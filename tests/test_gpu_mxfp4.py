@@ -446,3 +446,21 @@ def test_attention_again_and_again(gkr, Q, H, K, holes):
         o, l = gkr.sparse_attention(c.q, c.cache, c.indices, c.sm, weights=c.weights)
         assert torch.equal(o.view(torch.int16), out.view(torch.int16)), i
         assert torch.equal(l, lse) and torch.equal(c.weights, w), i
+
+
+@pytest.mark.parametrize("Q,H,K", [(64, 8, 2049), (76, 128, 640)])
+def test_attention_ragged_again_and_again(gkr, Q, H, K):
+    """The same for lists of many lengths in a cache that is not in the L2 cache when they start."""
+    c = Case(gkr, Q, H, K, seed=K, pages=1500, holes=0.05)
+    rng = np.random.default_rng(Q)
+    for i, n in enumerate(rng.integers(0, K + 1, Q)):
+        c.idx[i, n:] = -1
+    c.indices.copy_(torch.from_numpy(c.idx))
+    out, lse = c.check(gkr)
+    w = c.weights.clone()
+    for i in range(60):
+        torch.full((1 << 26,), float("nan"), device=DEV)   # 256 MB
+        c.weights.copy_(torch.from_numpy(c.w0))
+        o, l = gkr.sparse_attention(c.q, c.cache, c.indices, c.sm, weights=c.weights)
+        assert torch.equal(o.view(torch.int16), out.view(torch.int16)), i
+        assert torch.equal(l, lse) and torch.equal(c.weights, w), i
