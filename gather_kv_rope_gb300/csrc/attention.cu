@@ -17,9 +17,9 @@
 //     pair of CTAs (cta_group::2, M = 128) splits it: each holds its 64 heads' rows, 256 columns
 //     on 128 lanes, and has room for two chunks' logits and for three quarters of the query,
 //     which so need not be read from shared memory by every product.
-//   * Records come by four-row gathers of the copy engine (one copy a record took 33 cycles
-//     of issue, a warp's loads more registers than there are), their slots six chunks
-//     ahead: a chunk takes about 2100 cycles, a load from memory up to 4000.
+//   * Records come by 16-byte asynchronous copies of three warps, their slots six chunks ahead: a
+//     chunk takes about 2000 cycles, a load from memory up to 4000.  (By the copy engine's
+//     four-row gathers, 90 cycles each, they came too slowly: 79 us where this takes 75.5.)
 //   * They are dequantised once to bf16 in shared memory and are there both operands: rows
 //     of 128 bytes (64 dims) in 8-row swizzle groups read K-major for q . K (reduction over
 //     dims) and MN-major for p . K (reduction over records).  A product of the pair takes half
@@ -33,14 +33,15 @@
 //     where that costs no more (make_cut).  A query that lies inside one pair's run is
 //     finished there; the pieces of a cut one go to the workspace (fp32 rows and their
 //     log-sum-exp) and a second kernel joins them.
-// Measured: 128 queries x 128 heads x 2048 entries 76 us, 900 TFLOP/s, 46 % of the measured
-// matrix rate.  A chunk of 64 records takes 2100 cycles, its products alone 1165 (64 columns a
-// product run at 63 % of the rate of 256).  What is left is one stage's way: dequantised (1200),
-// multiplied, its softmax taken and half of it replaced (1300), multiplied again, three stages
-// at a time being all that shared memory holds; issue slots are 74 % taken meanwhile.  Tried and
-// slower: a warp for each product (84 us: 72 registers), eight warps that replace (82), the
-// dequantisation's warps on alternate chunks (79); as fast: 32 rows of each CTA for up to 64
-// heads, which leaves every second softmax warp idle.
+// Measured: 128 queries x 128 heads x 2048 entries 75.5 us, 910 TFLOP/s, 46 % of the measured
+// matrix rate.  A chunk of 64 records takes 2000 cycles, its products alone 1165 (64 columns a
+// product run at 63 % of the rate of 256).  What is left is shared out: issue slots are 70 %
+// taken, the warp that issues the products, the warps that dequantise and those that gather each
+// spend nearly all of a chunk's time on it, and speeding up one of them alone moves little.
+// Tried: a warp for each product (slower by itself, 72 registers; as fast with two gathering
+// warps); eight warps that replace (82 us); the dequantisation's warps on alternate chunks
+// (78.5), with a fourth stage in the place of the next query's blocks 73, but 4 to 7 % slower for
+// short lists; 32 rows of each CTA for up to 64 heads, every second softmax warp idle: as fast.
 #include <cmath>
 #include <mutex>
 #include <vector>
@@ -145,8 +146,8 @@ static_assert(kRawStages + kStages + 1 < kIndexRing && kIndexAhead < kIndexRing,
 struct alignas(8) PairBarriers {
     // in the leader: arrivals of both CTAs
     uint64_t full_k[kStages];    // own warps: the chunk's records are in place for q . K
-    uint64_t full_v[kStages];    // refill warps: ... and for p . K
-    uint64_t p_full[2];          // softmax: the logits are read, the probabilities written
+    uint64_t p_full[2];          // refill warps: ... and for p . K; softmax: the logits are read,
+                                 // the probabilities written
     uint64_t q_full;             // softmax: a query is in place for q . K
     // in each CTA
     uint64_t q_next;             // the next query's first blocks are in shared memory
@@ -154,8 +155,7 @@ struct alignas(8) PairBarriers {
     uint64_t raw_own[kRawStages], raw_own_empty[kRawStages];   // raw records: landed, read
     uint64_t raw_oth[kRawStages], raw_oth_empty[kRawStages];
     uint64_t s_full[2];          // products: the logits of a chunk are complete
-    uint64_t stage_empty[kStages];   // products: p . K has read the stage
-    uint64_t o_done[2];          // products: p . K of a chunk is complete
+    uint64_t stage_empty[kStages];   // products: p . K of a chunk is complete, its stage read
     uint64_t live[kIndexRing];   // gather warps: both masks of a chunk's entries are written
     uint32_t tmem_base;
     int32_t timed_out;
@@ -261,8 +261,7 @@ __device__ __forceinline__ void query_to_tmem(uint32_t tile, int row, int first,
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
-    attend_kernel(const AttentionParams p, const Cut cut, const __grid_constant__ CUtensorMap q_map,
-                  const __grid_constant__ CUtensorMap cache_map) {
+    attend_kernel(const AttentionParams p, const Cut cut, const __grid_constant__ CUtensorMap q_map) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -281,19 +280,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(smem_addr(&bars->full_k[s]), 2 * kOwnWarps);
-            mbar_init(smem_addr(&bars->full_v[s]), 2 * kRefillWarps);
             mbar_init(smem_addr(&bars->stage_empty[s]), 1);
         }
         for (int s = 0; s < kRawStages; ++s) {
-            mbar_init(smem_addr(&bars->raw_own[s]), 2 + 32);   // two halves, the scales' copies
-            mbar_init(smem_addr(&bars->raw_oth[s]), 1 + 32);
+            mbar_init(smem_addr(&bars->raw_own[s]), 2 * 32);   // lanes of two warps
+            mbar_init(smem_addr(&bars->raw_oth[s]), 32);
             mbar_init(smem_addr(&bars->raw_own_empty[s]), kOwnWarps);
             mbar_init(smem_addr(&bars->raw_oth_empty[s]), kRefillWarps);
         }
         for (int b = 0; b < 2; ++b) {
-            mbar_init(smem_addr(&bars->p_full[b]), 2 * kSoftmaxWarps);
+            mbar_init(smem_addr(&bars->p_full[b]), 2 * (kSoftmaxWarps + kRefillWarps));
             mbar_init(smem_addr(&bars->s_full[b]), 1);
-            mbar_init(smem_addr(&bars->o_done[b]), 1);
         }
         for (int i = 0; i < kIndexRing; ++i) mbar_init(smem_addr(&bars->live[i]), 2);
         mbar_init(smem_addr(&bars->q_full), 2 * kSoftmaxWarps);
@@ -302,7 +299,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         bars->timed_out = 0;
         mbar_init_fence();
     }
-    if (threadIdx.x == kFirstGather * 32) prefetch_map(&cache_map);
     if (threadIdx.x == kPollThread) prefetch_map(&q_map);
     pdl_wait_previous();
     pdl_release_next();
@@ -335,7 +331,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         const uint32_t src_s = (own ? kRawOwnScales : kRawOthScales + rank * 8) + r * 16 + u;
         const uint32_t dst = kOffStages + (own || rank != 0 ? 0u : kHalfBytes) +
                              (u >> 1) * kBlockBytes + r * kRowBytes + (((u & 1) * 4 ^ (r & 7)) << 4);
-        const uint32_t full = map_rank(smem_addr(own ? &bars->full_k[0] : &bars->full_v[0]), 0);
+        const uint32_t full = map_rank(smem_addr(own ? &bars->full_k[0] : &bars->p_full[0]), 0);
         const uint32_t raw_full = smem_addr(own ? &bars->raw_own[0] : &bars->raw_oth[0]);
         const uint32_t raw_empty = smem_addr(own ? &bars->raw_own_empty[0] : &bars->raw_oth_empty[0]);
         const uint32_t raw0 = smem_addr(smem + kOffRaw);
@@ -345,12 +341,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         Ring<kRawStages> rw;
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
-            if (w == (own ? 2 : 3) && lane == 0) {
+            // two threads wait, each for one thing: one after the other takes 200 cycles more
+            if (w == 2 && lane == 0) {
                 wait_quiet(raw_full + 8 * rw.s, rw.parity, ok);
+            } else if (w == 3 && lane == 0 && (!own || j >= kStages)) {
                 // the stage is free; q . K has read what is replaced
-                if (!own || j >= kStages)
-                    wait_quiet(own ? smem_addr(&bars->stage_empty[st.s]) : smem_addr(&bars->s_full[j & 1]),
-                               own ? st.parity ^ 1u : (j >> 1) & 1, ok);
+                wait_quiet(own ? smem_addr(&bars->stage_empty[st.s]) : smem_addr(&bars->s_full[j & 1]),
+                           own ? st.parity ^ 1u : (j >> 1) & 1, ok);
             }
             group_sync(bar, threads);
             const uint32_t raw = raw0 + rw.s * kRawBytes, out = out0 + st.s * kStageBytes;
@@ -361,7 +358,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(raw_empty + 8 * rw.s);
-                mbar_arrive_cluster(full + 8 * st.s);
+                mbar_arrive_cluster(full + 8 * (own ? st.s : j & 1));
             }
             st.next();
             rw.next();
@@ -371,11 +368,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         // Three warps run this: one for each half of the own records' dims, one for this CTA's
         // half of the others'.  The indices come into a ring in shared memory six chunks ahead
         // (a global load takes more than a chunk's time), lane i decodes record i of the
-        // chunk's 32, eight lanes have the copy engine gather four half-rows each, and every
-        // lane copies its record's 16 scale bytes.  An entry that is none gets scale bytes 0
-        // and whatever codes are there -- the first record's of its four, or, where none of the
-        // four is one, those of an earlier chunk: finite values, which the softmax masks.  (One
-        // slot read in their place by every SM takes 4 us a chunk to answer.)
+        // chunk's 32, eight lanes copy a half-row of 128 bytes, and every lane its record's 16
+        // scale bytes; zeros for an entry that is none.  (The copy engine's four-row gathers take
+        // 90 cycles each, 24 of them a chunk: at 2150 cycles they set the pace.)
         const int g = warp - kFirstGather;
         const bool own = g < 2;
         const uint32_t cta = own ? rank : 1u - rank;        // whose records
@@ -383,8 +378,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         const uint32_t full = smem_addr(own ? &bars->raw_own[0] : &bars->raw_oth[0]);
         const uint32_t empty = smem_addr(own ? &bars->raw_own_empty[0] : &bars->raw_oth_empty[0]);
         const uint32_t raw0 = smem_addr(smem + kOffRaw);
-        const int32_t x = static_cast<int32_t>(own ? g : rank) * 128;
-        const uint32_t dst = g * kRawBlock + lane * 512;    // lane < 8: rows 4 lane .. + 3
+        const int sub = lane >> 3, piece = lane & 7;        // row 4 i + sub, 16 bytes of it
+        const uint8_t* const src = p.cache + (own ? g : rank) * 128 + 16 * piece;
+        // rows 4 i + sub and 8 bytes of a swizzle group: i flips bit 2 of the row
+        const uint32_t dst = g * kRawBlock + sub * 128 + ((piece ^ sub) << 4);
         const uint32_t scale_dst = (own ? kRawOwnScales : kRawOthScales) + 16 * lane;
         const uint32_t ring = smem_addr(smem + kOffIndex) + g * kIndexRing * 128 + 4 * lane;
         int ahead = 0;                                      // the next chunk to fetch indices of
@@ -417,15 +414,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
             uint32_t page, r;
             page_row(is ? static_cast<uint32_t>(idx) : 0u, static_cast<uint32_t>(p.block_size), page, r);
             const int64_t at = static_cast<int64_t>(page) * p.page_stride;
-            const int32_t row = static_cast<int32_t>(at >> 8) + static_cast<int32_t>(r);
-            const uint32_t four = lane < 8 ? live >> (4 * lane) & 15u : 0u;   // this lane's rows
-            int32_t r4[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                r4[i] = __shfl_sync(kFull, row, (4 * lane + ((four >> i & 1u) != 0u ? i : __ffs(four) - 1)) & 31);
-            const uint32_t bytes = __popc(__ballot_sync(kFull, four != 0u)) * 512u;
-            if (lane == 0 && j >= kRawStages) wait_quiet(empty + 8 * rw.s, rw.parity ^ 1u, ok);
-            __syncwarp();
+            const int32_t row = is ? static_cast<int32_t>(at >> 8) + static_cast<int32_t>(r) : -1;   // of 256 bytes
+            if (j >= kRawStages) wait_quiet(empty + 8 * rw.s, rw.parity ^ 1u, ok);
             const uint32_t raw = raw0 + rw.s * kRawBytes, bar = full + 8 * rw.s;
             if (g != 1) {
                 if (lane == 0) {
@@ -434,21 +424,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 }
                 cp_async16_or_zeros(raw + scale_dst,
                                     p.cache + at + static_cast<int64_t>(p.block_size) * 256 + r * 16u, is);
-                cp_async_arrive(bar);
             }
-            if (lane == 0) mbar_expect_tx(bar, bytes);
-            __syncwarp();
-            if (four != 0u) tma_gather4(raw + dst, &cache_map, bar, x, r4[0], r4[1], r4[2], r4[3]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int32_t from = __shfl_sync(kFull, row, 4 * i + sub);
+                cp_async16_or_zeros(raw + (dst ^ ((i & 1) << 6)) + i * 512,
+                                    src + static_cast<int64_t>(from < 0 ? 0 : from) * 256, from >= 0);
+            }
+            cp_async_arrive(bar);
             fetch();
             rw.next();
         }
         if (g != 1 && rank == 0 && __any_sync(kFull, bad) && lane == 0) report(p.err, kErrIndex);
-        // the copies in flight land before the CTA leaves: the dequantising warps wait for them,
-        // and where they have given up, this does
-        cp_async_wait<0>();
-        for (int j = n > kRawStages ? n - kRawStages : 0; j < n; ++j)
-            if (lane == 0) wait_quiet(full + 8 * (j % kRawStages), (j / kRawStages) & 1, ok);
-        __syncwarp();
+        cp_async_wait<0>();   // the copies in flight land before the CTA leaves
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------- products
         // The whole warp runs this, one lane issues (elect_lane).
@@ -499,7 +487,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                     sk.next();
                     ++jq;
                 } else {
-                    wait_quiet(smem_addr(&bars->full_v[sv.s]), sv.parity, ok);
                     wait_quiet(smem_addr(&bars->p_full[jo & 1]), (jo >> 1) & 1, ok);
                     __syncwarp();
                     tc_fence_after_sync();
@@ -518,7 +505,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                     }
                     __syncwarp();
                     mma_commit_pair(smem_addr(&bars->stage_empty[sv.s]), elected);
-                    mma_commit_pair(smem_addr(&bars->o_done[jo & 1]), elected);
                     sv.next();
                     ++jo;
                     fresh = false;
@@ -633,7 +619,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 l = __fmul_rn(l, fix);
                 if (!fresh) {
                     // the products of the chunk before are in the accumulator
-                    wait_quiet(smem_addr(&bars->o_done[(j - 1) & 1]), ((j - 1) >> 1) & 1, ok);
+                    wait_quiet(smem_addr(&bars->stage_empty[(j - 1) % kStages]), ((j - 1) / kStages) & 1, ok);
                     __syncwarp();
                     tc_fence_after_sync();
 #pragma unroll 1
@@ -679,7 +665,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 head_sync();
                 const float total = __fadd_rn(__fadd_rn(sums[0], sums[64]), __fadd_rn(sums[128], sums[192]));
                 head_sync();   // read before the next segment's sums
-                if (lane == 0) wait_quiet(smem_addr(&bars->o_done[j & 1]), (j >> 1) & 1, ok);
+                if (lane == 0) wait_quiet(smem_addr(&bars->stage_empty[j % kStages]), (j / kStages) & 1, ok);
                 ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
                 tc_fence_after_sync();
                 const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
@@ -1282,23 +1268,6 @@ cudaError_t q_tensor_map(const AttentionParams& p, int heads, CUtensorMap* map) 
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// The cache as rows of 256 bytes (every data row is one: pages start at multiples of 512), read
-// in half-rows with the 128-byte swizzle; a box is one row high, as four-row gathers want it.
-cudaError_t cache_tensor_map(const AttentionParams& p, CUtensorMap* map) {
-    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
-    if (encode == nullptr) return cudaErrorNotSupported;
-    const int64_t pages = p.num_slots / p.block_size;
-    const cuuint64_t dims[2] = {256, static_cast<cuuint64_t>(pages * (p.page_stride >> 8))};
-    const cuuint64_t strides[1] = {256};
-    const cuuint32_t box[2] = {128, 1};
-    const cuuint32_t step[2] = {1, 1};
-    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(p.cache),
-                              dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 }  // namespace
 
 cudaError_t attention_workspace(int32_t num_heads, int64_t num_queries, int64_t topk,
@@ -1315,12 +1284,11 @@ cudaError_t launch_sparse_attention(const AttentionParams& p, cudaStream_t strea
     Cut cut;
     cudaError_t e = make_cut(p.num_queries, p.topk, &cut);
     if (e != cudaSuccess) return e;
-    CUtensorMap q_map, cache_map;
+    CUtensorMap q_map;
     e = q_tensor_map(p, kPairHeads, &q_map);
-    if (e == cudaSuccess) e = cache_tensor_map(p, &cache_map);
     if (e != cudaSuccess) return e;
     e = launch_kernel(attend_kernel, 2 * static_cast<int64_t>(cut.pairs), kAttendThreads, kAttendSmem,
-                      stream, p.pdl, p, cut, q_map, cache_map);
+                      stream, p.pdl, p, cut, q_map);
     if (e != cudaSuccess) return e;
     Cuts cuts;
     find_cuts(cut, &cuts);
