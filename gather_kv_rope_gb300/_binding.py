@@ -620,14 +620,15 @@ def sparse_attention(q: torch.Tensor, k_cache: torch.Tensor, indices: torch.Tens
     _check_err_flag(err_flag)
     dev = _same_cuda_device(q, k_cache, indices, out, lse, weights, err_flag, workspace)
     if workspace is None:
-        workspace = torch.empty(_attention_workspace(H, Q, K, dev.index), dtype=torch.uint8,
-                                device=dev)
+        size = _attention_workspace(H, Q, K, dev.index)
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
     elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
     _call(dev, lib().gkr_sparse_attention, q.data_ptr(), H, k_cache.data_ptr(), ctypes.byref(desc),
           indices.data_ptr(), istride, Q, K, float(sm_scale), out.data_ptr(), lse.data_ptr(),
-          _ptr(weights), wstride, workspace.data_ptr(), workspace.numel(), _ptr(err_flag),
-          _opts(launch_opts))
+          _ptr(weights), wstride, _ptr(workspace), 0 if workspace is None else workspace.numel(),
+          _ptr(err_flag), _opts(launch_opts))
     return out, lse
 
 

@@ -751,7 +751,10 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // The queries that the cut runs through: query, its first pair and how many work on it.
 constexpr int kMaxPairs = 128;
-constexpr int64_t kCutChunks = 11;
+// Four groups from this many pieces of a query on: 32 pieces (a query, 128 heads) 14.2 us a call with
+// one group, 13.2 with four; ten (8 queries, 32 heads) 25.2 and 22.9; two or three (128 queries,
+// cut, 128 heads, 9600 blocks) 86 and 135.
+constexpr int kManyPieces = 8;
 struct Cuts {
     int32_t n;
     int32_t query[kMaxPairs - 1];
@@ -759,15 +762,14 @@ struct Cuts {
 };
 
 // Joins the pieces of each cut query: out = sum_i exp2(lse_i - lse) rows_i.  A block takes one
-// head of one query, four dims a thread; four groups of 128 threads take every fourth piece and
-// add up in shared memory.  All of it is latency: for 32 pieces of 128 heads one group took
-// 13.2 us, four 7.0, and four whose first loads do not wait for the log-sum-exps 6.2 (38 pieces
-// of two queries of 64 heads 15.6, 8.5 and 7.2; the two to five pieces of 592 heads, more blocks
-// than fit at once, 5.6, 5.4 and 6.9).
-constexpr int kJoinGroups = 4, kJoinFirst = 4;
-__global__ void __launch_bounds__(128 * kJoinGroups)
+// head of one query, four dims a thread; for many pieces, four groups of 128 threads take every
+// fourth piece and add up in shared memory.  A few pieces are a matter of throughput, many of
+// latency, so the first loads do not wait for the log-sum-exps.
+constexpr int kJoinFirst = 4;
+template <int kGroups>
+__global__ void __launch_bounds__(128 * kGroups)
     join_kernel(const AttentionParams p, const int32_t pairs, const __grid_constant__ Cuts cuts) {
-    __shared__ float4 part[kJoinGroups][128];
+    __shared__ float4 part[kGroups][kGroups > 1 ? 128 : 1];
     const int32_t c = blockIdx.x / p.num_heads;
     const int32_t head = blockIdx.x - c * p.num_heads;
     const int g0 = cuts.first[c], n = cuts.pairs[c];
@@ -785,7 +787,7 @@ __global__ void __launch_bounds__(128 * kJoinGroups)
     float4 first[kJoinFirst];
 #pragma unroll
     for (int u = 0; u < kJoinFirst; ++u) {
-        const int i = group + u * kJoinGroups;
+        const int i = group + u * kGroups;
         first[u] = i < n ? load(i) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
     // the pieces' log-sum-exps, one a lane
@@ -808,19 +810,21 @@ __global__ void __launch_bounds__(128 * kJoinGroups)
     };
 #pragma unroll
     for (int u = 0; u < kJoinFirst; ++u)
-        if (group + u * kJoinGroups < n) add(group + u * kJoinGroups, first[u]);
+        if (group + u * kGroups < n) add(group + u * kGroups, first[u]);
 #pragma unroll 4
-    for (int i = group + kJoinFirst * kJoinGroups; i < n; i += kJoinGroups) add(i, load(i));
-    part[group][d] = acc;
-    __syncthreads();
-    if (group != 0) return;
+    for (int i = group + kJoinFirst * kGroups; i < n; i += kGroups) add(i, load(i));
+    if constexpr (kGroups > 1) {
+        part[group][d] = acc;
+        __syncthreads();
+        if (group != 0) return;
 #pragma unroll
-    for (int i = 1; i < kJoinGroups; ++i) {
-        const float4 t = part[i][d];
-        acc.x = __fadd_rn(acc.x, t.x);
-        acc.y = __fadd_rn(acc.y, t.y);
-        acc.z = __fadd_rn(acc.z, t.z);
-        acc.w = __fadd_rn(acc.w, t.w);
+        for (int i = 1; i < kGroups; ++i) {
+            const float4 t = part[i][d];
+            acc.x = __fadd_rn(acc.x, t.x);
+            acc.y = __fadd_rn(acc.y, t.y);
+            acc.z = __fadd_rn(acc.z, t.z);
+            acc.w = __fadd_rn(acc.w, t.w);
+        }
     }
     const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
     const uint2 v = make_uint2(pack_bf16x2_rn(__fmul_rn(acc.x, inv), __fmul_rn(acc.y, inv)),
@@ -1207,7 +1211,7 @@ cudaError_t resident_pairs(int32_t* pairs) {
     return cudaSuccess;
 }
 
-cudaError_t make_cut(int64_t num_queries, int64_t topk, Cut* cut) {
+cudaError_t make_cut(int64_t num_queries, int64_t topk, int32_t num_heads, Cut* cut) {
     int32_t pairs = 0;
     const cudaError_t e = resident_pairs(&pairs);
     if (e != cudaSuccess) return e;
@@ -1216,13 +1220,14 @@ cudaError_t make_cut(int64_t num_queries, int64_t topk, Cut* cut) {
     if (pairs > kMaxPairs) pairs = kMaxPairs;
     cut->pairs = static_cast<int32_t>(cut->total < pairs ? cut->total : pairs);
     cut->each = 0;
-    // Whole queries, as many for each pair, where that leaves the longest run at most kCutChunks
-    // longer than the even cut: about what the pieces' fp32 rows and the kernel that joins them
-    // cost.  128 heads x 128 queries x 2048 entries on 76 pairs: runs of 64 chunks whole 77 us a
-    // call, of 54 cut 88 us; 64 queries x 2049: 33 whole 82, 28 cut 96 (with weights); 37 x 1531
-    // entries, 16 heads: 24 whole 31, 12 cut 27.
+    // Whole queries, as many for each pair, where the longest run is then no longer than the even
+    // cut's and what the pieces' fp32 rows and the kernel that joins them cost, in chunks: five
+    // and one for nine heads.  Measured, us a call whole and cut: 128 queries x 2048 entries x 128
+    // heads (64 chunks, 54) 75 and 86; 120 x 1088 x 128 (34, 27) 45 and 57; 90 x 1600 (50, 30)
+    // x 128 heads 60.4 and 60.0, x 64 60 and 53, x 16 59 and 46; 100 x 1024 (32, 22) x 64 42 and
+    // 44, x 32 41 and 39; 40 x 640 x 16 (10, 6) 16 and 20; 37 x 1531 x 16 (24, 12) 30 and 25.5.
     const int64_t each = (num_queries + pairs - 1) / pairs;
-    if (each * cut->per_query <= (cut->total + pairs - 1) / pairs + kCutChunks) {
+    if (each * cut->per_query <= (cut->total + pairs - 1) / pairs + 5 + num_heads / 9) {
         cut->each = each;
         cut->pairs = static_cast<int32_t>((num_queries + each - 1) / each);
     }
@@ -1237,8 +1242,9 @@ bool has_pieces(const Cut& cut) {
 }
 
 // The queries that pairs' runs begin inside of.
-void find_cuts(const Cut& cut, Cuts* cuts) {
+int find_cuts(const Cut& cut, Cuts* cuts) {   // returns the most pieces of a query
     cuts->n = 0;
+    int most = 0;
     for (int32_t g = 1; g < cut.pairs; ++g) {
         const int64_t begin = cut.begin(g), q = begin / cut.per_query;
         if (begin - q * cut.per_query == 0) continue;
@@ -1247,8 +1253,9 @@ void find_cuts(const Cut& cut, Cuts* cuts) {
             cuts->first[cuts->n] = static_cast<int16_t>(g - 1);
             cuts->pairs[cuts->n++] = 1;
         }
-        ++cuts->pairs[cuts->n - 1];
+        if (++cuts->pairs[cuts->n - 1] > most) most = cuts->pairs[cuts->n - 1];
     }
+    return most;
 }
 
 // The queries [num_queries, num_heads, 512] as a 3-D tensor map with boxes of 64 dims x `heads`
@@ -1273,7 +1280,7 @@ cudaError_t q_tensor_map(const AttentionParams& p, int heads, CUtensorMap* map) 
 cudaError_t attention_workspace(int32_t num_heads, int64_t num_queries, int64_t topk,
                                 int64_t* bytes) {
     Cut cut;
-    const cudaError_t e = make_cut(num_queries, topk, &cut);
+    const cudaError_t e = make_cut(num_queries, topk, num_heads, &cut);
     if (e != cudaSuccess) return e;
     // two pieces a pair: a row and a log-sum-exp for each head
     *bytes = has_pieces(cut) ? 2 * static_cast<int64_t>(cut.pairs) * num_heads * (512 + 1) * 4 : 0;
@@ -1282,7 +1289,7 @@ cudaError_t attention_workspace(int32_t num_heads, int64_t num_queries, int64_t 
 
 cudaError_t launch_sparse_attention(const AttentionParams& p, cudaStream_t stream) {
     Cut cut;
-    cudaError_t e = make_cut(p.num_queries, p.topk, &cut);
+    cudaError_t e = make_cut(p.num_queries, p.topk, p.num_heads, &cut);
     if (e != cudaSuccess) return e;
     CUtensorMap q_map;
     e = q_tensor_map(p, kPairHeads, &q_map);
@@ -1291,10 +1298,11 @@ cudaError_t launch_sparse_attention(const AttentionParams& p, cudaStream_t strea
                       stream, p.pdl, p, cut, q_map);
     if (e != cudaSuccess) return e;
     Cuts cuts;
-    find_cuts(cut, &cuts);
+    const int most = find_cuts(cut, &cuts);
     if (cuts.n > 0) {
         const int64_t blocks = static_cast<int64_t>(cuts.n) * p.num_heads;
-        e = launch_kernel(join_kernel, blocks, 128 * kJoinGroups, 0, stream, p.pdl, p, cut.pairs, cuts);
+        e = most >= kManyPieces ? launch_kernel(join_kernel<4>, blocks, 512, 0, stream, p.pdl, p, cut.pairs, cuts)
+                                : launch_kernel(join_kernel<1>, blocks, 128, 0, stream, p.pdl, p, cut.pairs, cuts);
         if (e != cudaSuccess) return e;
     }
     if (p.weights == nullptr || p.topk == 0) return e;
