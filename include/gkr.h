@@ -359,7 +359,8 @@ GKR_API gkr_status gkr_sparse_logits(const void *q, int32_t num_heads, const voi
  * GKR_ERR_INDEX.  A query without a valid entry gets zeros and lse -inf; weights of
  * invalid entries are not touched.  Entries may repeat; each counts.
  * Arithmetic: bf16 products with fp32 sums, fp32 softmax statistics; the probabilities are
- * rounded to bf16 (relative to a running maximum) for the value product.  Results do not
+ * rounded to bf16 (relative to a running maximum) for the value product.  Records' values below
+ * 2^55 cannot overflow the accumulator, however many are listed.  Results do not
  * depend on the order of execution: every sum has a fixed order.
  *
  * q               device, bf16 [num_queries, num_heads, 512] row-major, 16-byte aligned.
