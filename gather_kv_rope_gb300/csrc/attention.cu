@@ -216,7 +216,7 @@ __device__ __forceinline__ void store_unit(uint32_t codes, uint32_t scale, uint3
     sts16(out ^ 48u, dequant8_e2m1(c.w, f));
 }
 
-// Named barriers of the warps of one role: one thread waits on the mbarriers, the others here,
+// Named barriers of the warps of one role: one or two threads wait on the mbarriers, the others here,
 // where a waiting warp takes no issue slots.  Instruction supply bounds a kernel of so many roles
 // before anything else does: with every warp polling for itself and each role's loop unrolled
 // in full, the warps ran 11200 instructions a chunk and missed the instruction cache on 17 % of

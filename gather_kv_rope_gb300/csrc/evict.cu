@@ -22,7 +22,7 @@
 // data, so their latency and the instructions of a few CTAs bound it, not memory: with one entry a
 // lane and instruction a step over 16384 entries of a CTA took 3600 cycles (25 instructions for
 // 32 entries), so a lane takes four at a time where it can.  Measured in a graph, keeping 4096 of
-// 4 x 131071 entries 24 us (one entry a lane 26), 2048 of 128 x 2049 7.2 us (9.6), 65536 of
+// 4 x 131071 entries 23 us (one entry a lane 26), 2048 of 128 x 2049 7.2 us (9.6), 65536 of
 // 16 x 1000000 320 us (480).
 #include "device.cuh"
 #include "launch.h"
@@ -38,7 +38,7 @@ constexpr int kBins = 256, kCopies = 8;
 constexpr int kCachedKeys = 36864, kCachedSlots = 20480;
 constexpr size_t kMostWords = kCachedSlots / 32 * (16 + 256);   // bytes
 static_assert(kCachedKeys / 32 * (16 + 128) <= kMostWords, "fits where keys and slots do");
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 8, kFewEntries = 2560;
 
 // A weight's key: unsigned order = order of the values; NaN 1 (below -inf, 2^23 - 1), -0 as 0.
 // What does not compete has key 0.
@@ -436,11 +436,19 @@ cudaError_t launch(const EvictParams& p, int32_t cluster, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
-    // CTAs a row: one for each 8192 entries, at most eight; few threads wait less for each other
-    // where the entries are few
+    // CTAs a row: as many as it takes to keep a part's keys in shared memory, then more, down to 4096
+    // entries each, while all rows' CTAs run at once (128 of the 152 SMs: whole clusters have
+    // to fit).  Measured, us in a graph: 4 rows x 16384 entries 16.3 with one CTA a row, 14.6 with
+    // two, 12.0 with four; 4 x 32768 19.3 with two, 14.9 with four, 13.7 with eight; 64 x 32768
+    // 21.5, 32 and 70; 64 x 16384 17.6 with one, 15.9 with two, 26 with four; 64 x 65536 33 with two, 42 with
+    // four, 84 with eight.
     int32_t cluster = 1;
-    while (cluster < kMaxCluster && p.length > 8192 * cluster) cluster *= 2;
-    return p.length <= 4096 ? launch<256>(p, 1, stream) : launch<1024>(p, cluster, stream);
+    while (cluster < kMaxCluster &&
+           (p.length > kCachedKeys * cluster || (p.length > 4096 * cluster && p.rows * cluster * 2 <= 128)))
+        cluster *= 2;
+    // few threads wait less for each other where the entries are few: 128 rows x 1024 entries 5.8 us
+    // with 256 threads and 7.8 with 1024, x 2049 8.2 and 8.5, x 4096 10.0 and 9.2
+    return p.length <= kFewEntries ? launch<256>(p, 1, stream) : launch<1024>(p, cluster, stream);
 }
 
 }  // namespace gkr
