@@ -440,8 +440,8 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
     // entries each, while all rows' CTAs run at once (128 of the 152 SMs: whole clusters have
     // to fit).  Measured, us in a graph: 4 rows x 16384 entries 16.3 with one CTA a row, 14.6 with
     // two, 12.0 with four; 4 x 32768 19.3 with two, 14.9 with four, 13.7 with eight; 64 x 32768
-    // 21.5, 32 and 70; 64 x 16384 17.6 with one, 15.9 with two, 26 with four; 64 x 65536 33 with two, 42 with
-    // four, 84 with eight.
+    // 21.5, 32 and 70; 64 x 16384 17.6 with one, 15.9 with two, 26 with four; 64 x 65536 33 with
+    // two, 42 with four, 84 with eight.
     int32_t cluster = 1;
     while (cluster < kMaxCluster &&
            (p.length > kCachedKeys * cluster || (p.length > 4096 * cluster && p.rows * cluster * 2 <= 128)))
