@@ -666,6 +666,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 const float total = __fadd_rn(__fadd_rn(sums[0], sums[64]), __fadd_rn(sums[128], sums[192]));
                 head_sync();   // read before the next segment's sums
                 if (lane == 0) wait_quiet(smem_addr(&bars->stage_empty[j % kStages]), (j / kStages) & 1, ok);
+                __syncwarp();   // orders the other lanes' accesses after lane 0's wait
                 ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
                 tc_fence_after_sync();
                 const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
