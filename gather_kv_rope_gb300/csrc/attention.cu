@@ -33,7 +33,7 @@
 //     where that costs no more (make_cut).  A query that lies inside one pair's run is
 //     finished there; the pieces of a cut one go to the workspace (fp32 rows and their
 //     log-sum-exp) and a second kernel joins them.
-// Measured: 128 queries x 128 heads x 2048 entries 75.5 us, 910 TFLOP/s, 46 % of the measured
+// Measured: 128 queries x 128 heads x 2048 entries 76.8 us, 895 TFLOP/s, 46 % of the measured
 // matrix rate.  A chunk of 64 records takes 2000 cycles, its products alone 1165 (64 columns a
 // product run at 63 % of the rate of 256).  What is left is shared out: issue slots are 70 %
 // taken, the warp that issues the products, the warps that dequantise and those that gather each
@@ -157,11 +157,19 @@ struct alignas(8) PairBarriers {
     uint64_t s_full[2];          // products: the logits of a chunk are complete
     uint64_t stage_empty[kStages];   // products: p . K of a chunk is complete, its stage read
     uint64_t live[kIndexRing];   // gather warps: both masks of a chunk's entries are written
+    uint64_t drained;            // products: every one that was issued is complete
+    uint32_t next_loads, live_loads;   // of the query, issued so far (q_next, q_live)
     uint32_t tmem_base;
-    int32_t timed_out;
+    volatile int32_t timed_out;  // a wait of this CTA gave up
 };
 constexpr size_t kAttendSmem = 1024 + kOffBars + sizeof(PairBarriers);
 static_assert(kAttendSmem <= 227 * 1024, "a CTA's shared memory");
+
+// The lse of a query, or of a piece, whose results are not written because a wait gave up
+// (kErrTimeout): a NaN that no instruction produces, so that the kernels that follow can tell it
+// from the NaN of a record.
+constexpr uint32_t kUnwritten = 0x7FC0B0B0u;
+__device__ __forceinline__ bool is_unwritten(float lse) { return __float_as_uint(lse) == kUnwritten; }
 
 // 2^x within 2^-22; results below 2^-126 kept (factors that rescale what may be large) ...
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -227,6 +235,30 @@ constexpr int kPollThread = 32;   // of the softmax warps
 constexpr int kOwnBar = 1, kRefillBar = 2, kSoftmaxBar = 3, kHeadsBar = 4;   // and 5
 __device__ __forceinline__ void group_sync(int bar, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
+}
+
+// The same, and whether any of the threads says so.
+__device__ __forceinline__ bool group_any(int bar, int threads, bool mine) {
+    uint32_t any;
+    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %1, 0;\n barrier.red.or.pred p, %2, %3, p;\n"
+                 " selp.u32 %0, 1, 0, p;\n}" : "=r"(any)
+                 : "r"(mine ? 1u : 0u), "r"(bar), "r"(threads) : "memory");
+    return any != 0u;
+}
+
+// The wait of a thread that polls for a group of dequantising warps.  Should it give up, it keeps the
+// group at its named barrier until the warp that issues the products has left (`drained`; it
+// misses the group's arrivals and gives up in turn): only then may stages be overwritten and
+// barriers be arrived at out of turn.  (To tell the group, so that it does neither, took 3 % more
+// time for every call, by a flag or by the barrier.)
+__device__ __noinline__ bool wait_slow_or_hold(uint32_t bar, uint32_t parity, uint32_t drained) {
+    if (mbar_wait_slow(bar, parity, kWaitClocks)) return true;
+    for (int i = 0; i < 3; ++i)   // its wait may have begun later, and then it drains
+        if (wait_landed(drained, 0)) break;
+    return false;
+}
+__device__ __forceinline__ void wait_or_hold(uint32_t bar, uint32_t parity, uint32_t drained, bool& ok) {
+    if (ok && !mbar_try_wait(bar, parity)) ok = wait_slow_or_hold(bar, parity, drained);
 }
 
 // Eight fp32 values as bf16, and scaled.
@@ -296,6 +328,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         mbar_init(smem_addr(&bars->q_full), 2 * kSoftmaxWarps);
         mbar_init(smem_addr(&bars->q_next), 1);
         mbar_init(smem_addr(&bars->q_live), 1);
+        mbar_init(smem_addr(&bars->drained), 1);
+        bars->next_loads = 0;
+        bars->live_loads = 0;
         bars->timed_out = 0;
         mbar_init_fence();
     }
@@ -343,11 +378,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         for (int j = 0; j < n; ++j) {
             // two threads wait, each for one thing: one after the other takes 200 cycles more
             if (w == 2 && lane == 0) {
-                wait_quiet(raw_full + 8 * rw.s, rw.parity, ok);
+                wait_or_hold(raw_full + 8 * rw.s, rw.parity, smem_addr(&bars->drained), ok);
             } else if (w == 3 && lane == 0 && (!own || j >= kStages)) {
                 // the stage is free; q . K has read what is replaced
-                wait_quiet(own ? smem_addr(&bars->stage_empty[st.s]) : smem_addr(&bars->s_full[j & 1]),
-                           own ? st.parity ^ 1u : (j >> 1) & 1, ok);
+                wait_or_hold(own ? smem_addr(&bars->stage_empty[st.s]) : smem_addr(&bars->s_full[j & 1]),
+                             own ? st.parity ^ 1u : (j >> 1) & 1, smem_addr(&bars->drained), ok);
             }
             group_sync(bar, threads);
             const uint32_t raw = raw0 + rw.s * kRawBytes, out = out0 + st.s * kStageBytes;
@@ -415,7 +450,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
             page_row(is ? static_cast<uint32_t>(idx) : 0u, static_cast<uint32_t>(p.block_size), page, r);
             const int64_t at = static_cast<int64_t>(page) * p.page_stride;
             const int32_t row = is ? static_cast<int32_t>(at >> 8) + static_cast<int32_t>(r) : -1;   // of 256 bytes
-            if (j >= kRawStages) wait_quiet(empty + 8 * rw.s, rw.parity ^ 1u, ok);
+            if (j >= kRawStages && !warp_wait(empty + 8 * rw.s, rw.parity ^ 1u, ok)) break;
             const uint32_t raw = raw0 + rw.s * kRawBytes, bar = full + 8 * rw.s;
             if (g != 1) {
                 if (lane == 0) {
@@ -460,11 +495,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 const bool opens = jq == 0 || ci == 0;
                 if (jq < n && jq - jo < 2 && !(opens && jo < jq)) {
                     if (opens) {
-                        wait_quiet(smem_addr(&bars->q_full), loads & 1, ok);
+                        if (!warp_wait(smem_addr(&bars->q_full), loads & 1, ok)) break;
                         ++loads;
                     }
-                    wait_quiet(smem_addr(&bars->full_k[sk.s]), sk.parity, ok);
-                    __syncwarp();
+                    if (!warp_wait(smem_addr(&bars->full_k[sk.s]), sk.parity, ok)) break;
                     tc_fence_after_sync();
                     const uint32_t d = tmem + kSCol + 32 * (jq & 1);
                     // one addition a product: the lower half of the descriptor (start addresses
@@ -487,8 +521,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                     sk.next();
                     ++jq;
                 } else {
-                    wait_quiet(smem_addr(&bars->p_full[jo & 1]), (jo >> 1) & 1, ok);
-                    __syncwarp();
+                    if (!warp_wait(smem_addr(&bars->p_full[jo & 1]), (jo >> 1) & 1, ok)) break;
                     tc_fence_after_sync();
                     const uint32_t a = p_lo + (jo & 1) * (kPBytes >> 4);
                     const uint32_t b = v_lo + sv.s * (kStageBytes >> 4);
@@ -514,6 +547,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                     }
                 }
             }
+            // whatever ended the loop, no product is under way when the pair leaves
+            mma_commit_pair(smem_addr(&bars->drained), elected);
+            if (!wait_landed(smem_addr(&bars->drained), 0)) ok = false;
+            __syncwarp();
         }
     } else {
         // ------------------------------------------------------------- softmax, epilogue
@@ -530,20 +567,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         const int self = (part * 2 + half) * 64;
         const uint32_t p_full = map_rank(smem_addr(&bars->p_full[0]), 0);
         const float scale = __fmul_rn(p.sm_scale, kLog2e);   // logits in powers of two
-        auto head_any = [&](bool mine) -> bool {             // whether any of them says so
-            uint32_t any;
-            asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %1, 0;\n barrier.red.or.pred p, %2, 128, p;\n"
-                         " selp.u32 %0, 1, 0, p;\n}" : "=r"(any)
-                         : "r"(mine ? 1u : 0u), "r"(kHeadsBar + (warp & 1)) : "memory");
-            return any != 0u;
-        };
-        auto head_sync = [&]() { group_sync(kHeadsBar + (warp & 1), 128); };   // the warps of a head
+        // the warps of a head; whether any of their threads says so
+        auto head_sync = [&]() { group_sync(kHeadsBar + (warp & 1), 128); };
+        auto head_any = [&](bool mine) -> bool { return group_any(kHeadsBar + (warp & 1), 128, mine); };
         const uint32_t q_full = map_rank(smem_addr(&bars->q_full), 0);
         // A query's first 384 dims wait in shared memory since the query before was moved, and go
         // to tensor memory; the last 128 come straight to where q . K reads them.
         const int64_t q_last = (c0 + n - 1) / cut.per_query;
         uint32_t q_parity = 0;
         auto fetch_next = [&](int64_t q) {   // one thread
+            ++bars->next_loads;
             mbar_expect_tx(smem_addr(&bars->q_next), kQTmemBlocks * kQBlockBytes);
 #pragma unroll 1
             for (int b = 0; b < kQTmemBlocks; ++b)
@@ -552,7 +585,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                             static_cast<int32_t>(q));
         };
         auto query = [&](int64_t q) {
-            if (threadIdx.x == kPollThread) {
+            if (threadIdx.x == kPollThread && ok) {
+                ++bars->live_loads;
                 mbar_expect_tx(smem_addr(&bars->q_live), kQBytes);
 #pragma unroll 1
                 for (int b = kQTmemBlocks; b < 8; ++b)
@@ -566,14 +600,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
             fence_async_smem();   // what was read is read, before the copy engine writes there
             tc_fence_before_sync();
             group_sync(kSoftmaxBar, kSoftmaxWarps * 32);
-            if (threadIdx.x == kPollThread) {
+            if (threadIdx.x == kPollThread && ok) {
                 if (q < q_last) fetch_next(q + 1);
                 wait_quiet(smem_addr(&bars->q_live), q_parity, ok);
             }
-            if (lane == 0) mbar_arrive_cluster(q_full);
+            ok = __all_sync(kFull, ok) != 0;   // one outcome a warp, the polling thread's with it
+            if (lane == 0 && ok) mbar_arrive_cluster(q_full);
             q_parity ^= 1u;
         };
-        if (threadIdx.x == kPollThread) fetch_next(qi);
+        if (threadIdx.x == kPollThread && ok) fetch_next(qi);
         query(qi);
         float m = -INFINITY, l = 0.0f;
         bool fresh = true;         // no chunk of this query is in the accumulator
@@ -583,14 +618,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
             const bool last = j + 1 == n || ci + 1 == cut.per_query;   // of this segment
             // the other CTA's records are not part of what q . K waits for, so their mask has a
             // barrier of its own (the ring's next round comes after this chunk's probabilities)
-            wait_quiet(smem_addr(&bars->live[j & (kIndexRing - 1)]), (j / kIndexRing) & 1, ok);
+            if (ok) warp_wait(smem_addr(&bars->live[j & (kIndexRing - 1)]), (j / kIndexRing) & 1, ok);
             const uint32_t live =
                 (reinterpret_cast<const uint32_t*>(smem + kOffLive)[(j & (kIndexRing - 1)) * 2 + half] >>
                  (16 * part)) & 0xFFFFu;
             // q . K of this chunk is complete, and with it, issued before, p . K of chunk j - 2:
             // the probabilities' buffer is free
-            wait_quiet(smem_addr(&bars->s_full[j & 1]), (j >> 1) & 1, ok);
-            __syncwarp();
+            if (ok) warp_wait(smem_addr(&bars->s_full[j & 1]), (j >> 1) & 1, ok);
             tc_fence_after_sync();
             float v[16];
             tmem_ld16(tmem + lanes + kSCol + 32 * (j & 1) + 16 * part, v);
@@ -619,8 +653,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 l = __fmul_rn(l, fix);
                 if (!fresh) {
                     // the products of the chunk before are in the accumulator
-                    wait_quiet(smem_addr(&bars->stage_empty[(j - 1) % kStages]), ((j - 1) / kStages) & 1, ok);
-                    __syncwarp();
+                    if (ok) warp_wait(smem_addr(&bars->stage_empty[(j - 1) % kStages]), ((j - 1) / kStages) & 1, ok);
                     tc_fence_after_sync();
 #pragma unroll 1
                     for (int c = 128 * part; c < 128 * part + 128; c += 32) {
@@ -655,7 +688,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
             fence_async_smem();
             tc_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(p_full + 8 * (j & 1));
+            if (lane == 0 && ok) mbar_arrive_cluster(p_full + 8 * (j & 1));
             fresh = false;
             if (last) {
                 // q . K of this query is complete: the next one may take its place, and is
@@ -664,10 +697,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 sums[self] = l;
                 head_sync();
                 const float total = __fadd_rn(__fadd_rn(sums[0], sums[64]), __fadd_rn(sums[128], sums[192]));
-                head_sync();   // read before the next segment's sums
+                // The last value product implies everything before it: each of its chunks passed
+                // only arrivals of warps that had all they waited for.  A head's warps agree on
+                // it, so that its row is written in full or not at all.  (The barrier also puts
+                // the other lanes' accesses behind lane 0's wait, and the next segment's sums
+                // behind the reads of these.)
                 if (lane == 0) wait_quiet(smem_addr(&bars->stage_empty[j % kStages]), (j / kStages) & 1, ok);
-                __syncwarp();   // orders the other lanes' accesses after lane 0's wait
-                ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
+                ok = !head_any(!ok);
                 tc_fence_after_sync();
                 const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
                 const bool whole = seg == 0 && ci + 1 == cut.per_query;
@@ -719,10 +755,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                     }
                     __syncwarp();
                 }
-                if (half == 0 && part == 0 && head < p.num_heads && ok) {
-                    if (whole) p.lse[at + head] = __fmul_rn(lse2, kLn2);
-                    else
-                        pieces[2 * static_cast<int64_t>(cut.pairs) * p.num_heads * 512 + at + head] = lse2;
+                if (half == 0 && part == 0 && head < p.num_heads) {
+                    float* const to = whole ? p.lse : pieces + 2 * static_cast<int64_t>(cut.pairs) * p.num_heads * 512;
+                    to[at + head] = !ok ? __uint_as_float(kUnwritten) : whole ? __fmul_rn(lse2, kLn2) : lse2;
                 }
                 tc_fence_before_sync();
                 m = -INFINITY;
@@ -735,13 +770,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 ++qi;
             }
         }
+        // after a wait that gave up, blocks of a query may still be on their way
+        if (threadIdx.x == kPollThread) {
+            if (bars->next_loads > 0 && !wait_landed(smem_addr(&bars->q_next), (bars->next_loads - 1) & 1)) ok = false;
+            if (bars->live_loads > 0 && !wait_landed(smem_addr(&bars->q_live), (bars->live_loads - 1) & 1)) ok = false;
+        }
+        __syncwarp();
     }
-    if (!ok) atomicOr(&bars->timed_out, 1);
+    if (!ok) bars->timed_out = 1;
     tc_fence_before_sync();
     __syncthreads();
     if (threadIdx.x == 0 && bars->timed_out != 0) report(p.err, kErrTimeout);
     cluster_sync();   // no CTA leaves while the other's products or arrivals reach it
-    if (warp == kMmaWarp) tmem_dealloc_pair(tmem, kTmemCols);
+    if (warp == kMmaWarp) {
+        if (rank != 0) wait_landed(smem_addr(&bars->drained), 0);   // the last arrival from the other CTA
+        __syncwarp();
+        tmem_dealloc_pair(tmem, kTmemCols);
+    }
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -794,7 +839,13 @@ __global__ void __launch_bounds__(128 * kGroups)
     // the pieces' log-sum-exps, one a lane
     const int lane = threadIdx.x & 31;
     float m = -INFINITY;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, lses[slot(i)]);
+    bool unwritten = false;
+    for (int i = lane; i < n; i += 32) {
+        const float x = lses[slot(i)];
+        unwritten |= is_unwritten(x);
+        m = fmaxf(m, x);
+    }
+    unwritten = __any_sync(kFull, unwritten) != 0;   // the same in every warp
 #pragma unroll
     for (int x = 16; x >= 1; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
     const float ref = m == -INFINITY ? 0.0f : m;
@@ -831,6 +882,10 @@ __global__ void __launch_bounds__(128 * kGroups)
     const uint2 v = make_uint2(pack_bf16x2_rn(__fmul_rn(acc.x, inv), __fmul_rn(acc.y, inv)),
                                pack_bf16x2_rn(__fmul_rn(acc.z, inv), __fmul_rn(acc.w, inv)));
     const int64_t at = static_cast<int64_t>(cuts.query[c]) * p.num_heads + head;
+    if (unwritten) {
+        if (threadIdx.x == 0) p.lse[at] = __uint_as_float(kUnwritten);
+        return;
+    }
     st8(static_cast<uint8_t*>(p.out) + at * 1024 + 8 * d, v);
     if (threadIdx.x == 0)
         p.lse[at] = sum == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(m, log2f(sum)), kLn2);
@@ -879,6 +934,7 @@ struct WeightSmem {
         uint64_t scales_empty[2];              // a tile's scales are read
         uint64_t a_full[kStages], a_empty[kStages];
         uint64_t acc_full[2], acc_empty[2];
+        uint64_t drained;                      // every product that was issued is complete
         uint32_t tmem_base;
         int32_t timed_out;
     };
@@ -916,6 +972,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     if (threadIdx.x == 0) {
         mbar_init(smem_addr(&bars->q_full), 1);
         mbar_init(smem_addr(&bars->q_free), 1);
+        mbar_init(smem_addr(&bars->drained), 1);
         for (int s = 0; s < M::kRaw; ++s) {
             mbar_init(smem_addr(&bars->raw[s]), kWGatherWarps * (1 + 32));
             mbar_init(smem_addr(&bars->raw_empty[s]), kWDequantWarps);
@@ -958,14 +1015,13 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         int stage = group;                 // every other one of the ring's
         uint32_t turn = 0;                 // of the ring
 #pragma unroll 1
-        for (int j = 0; j < n; ++j) {
+        for (int j = 0; j < n && ok; ++j) {
 #pragma unroll 1
             for (int h = 0; h < 4; ++h) {   // 128 dims: 64 for each group
                 // every warp waits for itself: at a barrier of the warps each stage took as long
                 // as the slowest of them
-                wait_quiet(smem_addr(&bars->raw[rw.s]), rw.parity, ok);
-                if (turn > 0) wait_quiet(smem_addr(&bars->a_empty[stage]), (turn - 1) & 1, ok);
-                __syncwarp();
+                if (!warp_wait(smem_addr(&bars->raw[rw.s]), rw.parity, ok)) break;
+                if (turn > 0 && !warp_wait(smem_addr(&bars->a_empty[stage]), (turn - 1) & 1, ok)) break;
                 const uint4 codes = lds16_at(raw0 + rw.s * kWRawBytes);
                 uint32_t s;
                 asm volatile("ld.shared.u8 %0, [%1];" : "=r"(s)
@@ -1019,7 +1075,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         Ring<M::kRaw> rw;
         int quarters = 0;
 #pragma unroll 1
-        for (int j = 0; j < n; ++j) {
+        for (int j = 0; j < n && ok; ++j) {
             cp_async_wait<kWIndexAhead - 1>();
             int32_t slot;
             asm volatile("ld.shared.b32 %0, [%1];" : "=r"(slot)
@@ -1038,9 +1094,9 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
                           static_cast<int64_t>(__shfl_sync(kFull, rows, 8 * i + (lane >> 2))) * 256;
 #pragma unroll 1
             for (int h = 0; h < 4; ++h) {
-                if (quarters >= M::kRaw) wait_quiet(smem_addr(&bars->raw_empty[rw.s]), rw.parity ^ 1u, ok);
+                if (quarters >= M::kRaw && !warp_wait(smem_addr(&bars->raw_empty[rw.s]), rw.parity ^ 1u, ok)) break;
                 if (h == 0) {
-                    if (j >= 2) wait_quiet(smem_addr(&bars->scales_empty[j & 1]), ((j >> 1) - 1) & 1, ok);
+                    if (j >= 2 && !warp_wait(smem_addr(&bars->scales_empty[j & 1]), ((j >> 1) - 1) & 1, ok)) break;
                     cp_async16_or_zeros(smem_addr(smem + M::kScalesAt) + ((j & 1) * kTileKeys + rec + lane) * 16,
                                         scales, is);
                     if (lane == 0)
@@ -1069,27 +1125,25 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
         const uint32_t a_lo = static_cast<uint32_t>(a_desc), q_lo = static_cast<uint32_t>(q_desc);
         const uint32_t q_block = static_cast<uint32_t>(n_pad) * kRowBytes;   // 64 dims of the query
         Ring<M::kStages> st;
-        uint32_t loads = 0;
+        uint32_t loads = 0;   // of queries, issued
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
             if (j == 0 || ti == 0) {   // the next query, once the last product of the one before is done
-                if (j > 0) wait_quiet(smem_addr(&bars->q_free), (loads - 1) & 1, ok);
-                __syncwarp();
-                if (elected && ok) {
+                if (j > 0 && !warp_wait(smem_addr(&bars->q_free), (loads - 1) & 1, ok)) break;
+                if (elected) {
                     mbar_expect_tx(smem_addr(&bars->q_full), 8 * q_block);
 #pragma unroll 1
                     for (int b = 0; b < 8; ++b)
                         tma_load_3d(smem_addr(smem) + b * q_block, &q_map, smem_addr(&bars->q_full), 64 * b, 0,
                                     static_cast<int32_t>(qi));
                 }
-                wait_quiet(smem_addr(&bars->q_full), loads & 1, ok);
                 ++loads;
+                if (!warp_wait(smem_addr(&bars->q_full), (loads - 1) & 1, ok)) break;
             }
-            if (j >= 2) wait_quiet(smem_addr(&bars->acc_empty[j & 1]), ((j >> 1) - 1) & 1, ok);
+            if (j >= 2 && !warp_wait(smem_addr(&bars->acc_empty[j & 1]), ((j >> 1) - 1) & 1, ok)) break;
 #pragma unroll 1
             for (int h = 0; h < 8; ++h) {
-                wait_quiet(smem_addr(&bars->a_full[st.s]), st.parity, ok);
-                __syncwarp();
+                if (!warp_wait(smem_addr(&bars->a_full[st.s]), st.parity, ok)) break;
                 tc_fence_after_sync();
                 if (elected) {
                     const uint32_t a = a_lo + st.s * (kWStageBytes >> 4);
@@ -1103,6 +1157,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
                 __syncwarp();
                 st.next();
             }
+            if (!ok) break;
             if (elected) mma_commit(smem_addr(&bars->acc_full[j & 1]));
             if (++ti == tiles) {
                 ti = 0;
@@ -1111,25 +1166,33 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
             }
             __syncwarp();
         }
+        // whatever ended the loop, no product and no block of a query is under way when the CTA leaves
+        if (elected) mma_commit(smem_addr(&bars->drained));
+        __syncwarp();
+        if (!wait_landed(smem_addr(&bars->drained), 0)) ok = false;
+        if (loads > 0 && !wait_landed(smem_addr(&bars->q_full), (loads - 1) & 1)) ok = false;
+        __syncwarp();
     } else {
         // ------------------------------------------------------------- sums
         float* const lse = reinterpret_cast<float*>(smem + M::kLseAt);
         const float scale = __fmul_rn(p.sm_scale, kLog2e);
         const uint64_t scale2 = f32x2(scale, scale);
         const int key = warp * 32 + lane;
+        bool known = false;                                  // every head's lse of this query is
 #pragma unroll 1
         for (int j = 0; j < n; ++j) {
             if (j == 0 || ti == 0) {
                 group_sync(kSoftmaxBar, kWSoftWarps * 32);   // the query before is read
                 const int h = threadIdx.x;                   // 0 .. 127
-                if (h < kHeads)
-                    lse[h] = h < p.num_heads
-                                 ? __fmul_rn(-kLog2e, p.lse[qi * p.num_heads + h])
-                                 : -INFINITY;                // no head: exp2(-inf) = 0
-                group_sync(kSoftmaxBar, kWSoftWarps * 32);
+                bool unwritten = false;
+                if (h < kHeads) {
+                    const float x = h < p.num_heads ? p.lse[qi * p.num_heads + h] : INFINITY;
+                    unwritten = is_unwritten(x);
+                    lse[h] = __fmul_rn(-kLog2e, x);          // no head: exp2(-inf) = 0
+                }
+                known = !group_any(kSoftmaxBar, kWSoftWarps * 32, unwritten);
             }
-            wait_quiet(smem_addr(&bars->acc_full[j & 1]), (j >> 1) & 1, ok);
-            __syncwarp();
+            if (ok) warp_wait(smem_addr(&bars->acc_full[j & 1]), (j >> 1) & 1, ok);
             tc_fence_after_sync();
             const uint32_t bits = *reinterpret_cast<const uint32_t*>(smem + M::kLiveAt + (j & 7) * 16 + 4 * warp);
             const bool live = (bits >> lane & 1u) != 0u;
@@ -1149,9 +1212,9 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
                 }
             }
             tc_fence_before_sync();
-            warp_arrive(smem_addr(&bars->acc_empty[j & 1]), lane);
-            ok = __shfl_sync(kFull, ok ? 1 : 0, 0) != 0;
-            if (live && ok) {
+            __syncwarp();
+            if (lane == 0 && ok) mbar_arrive(smem_addr(&bars->acc_empty[j & 1]));
+            if (live && ok && known) {
                 float even, odd;
                 f32x2_split(sum2, even, odd);
                 float* const dst = p.weights + qi * p.weight_stride + ti * kTileKeys + key;

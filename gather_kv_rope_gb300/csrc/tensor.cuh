@@ -24,8 +24,17 @@ __device__ __forceinline__ void mbar_init_fence() {
 // True once the phase with the given parity has completed.  A thread whose phase is not
 // complete is suspended until it completes or kSuspendNs have passed: a waiting warp then
 // takes no issue slots from the warps that work (spinning without the hint cost ~2 % of
-// the sparse logits).
+// the sparse logits).  A build that defines GKR_WAIT_CLOCKS, for the tests of what happens then,
+// has waits that run out: wait_quiet's limit is that many clocks, and a poll does not suspend.
+#ifdef GKR_WAIT_CLOCKS
+constexpr int64_t kWaitClocks = GKR_WAIT_CLOCKS;
+constexpr uint32_t kSuspendNs = 0;
+constexpr int kWaitPolls = 1;
+#else
+constexpr int64_t kWaitClocks = INT64_C(4000000000);   // 2 s at 2 GHz
 constexpr uint32_t kSuspendNs = 20000;
+constexpr int kWaitPolls = 64;
+#endif
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     uint32_t done;
     asm volatile(
@@ -154,20 +163,40 @@ __device__ __forceinline__ void warp_wait_or_flag(uint32_t bar, uint32_t parity,
 
 // wait_or_flag for kernels whose warps run different code and wait at the same time: a poll is
 // a few instructions, because the polls of waiting warps compete for issue slots and
-// instruction fetches with the warps that work, and the limit is counted in SM clocks (4
-// billion: 2 s at 2 GHz), which are read in a few cycles.
-constexpr int64_t kWaitClocks = INT64_C(4000000000);
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity) {
+// instruction fetches with the warps that work, and the limit is counted in SM clocks, which
+// are read in a few cycles.  Who gave up (ok false) must neither arrive, issue, copy nor store
+// on the strength of what it waited for: then nothing downstream completes either, and no result
+// is written from data that did not come.
+__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, int64_t limit) {
     const int64_t t0 = clock64();
     do {
 #pragma unroll 1
-        for (int i = 0; i < 64; ++i)
+        for (int i = 0; i < kWaitPolls; ++i)
             if (mbar_try_wait(bar, parity)) return true;
-    } while (clock64() - t0 <= kWaitClocks);
+    } while (clock64() - t0 <= limit);
     return false;
 }
 __device__ __forceinline__ void wait_quiet(uint32_t bar, uint32_t parity, bool& ok) {
-    if (ok && !mbar_try_wait(bar, parity)) ok = mbar_wait_slow(bar, parity);
+    if (ok && !mbar_try_wait(bar, parity)) ok = mbar_wait_slow(bar, parity, kWaitClocks);
+}
+// The same for a converged warp, with one outcome: every lane waits, a vote decides.
+__device__ __noinline__ bool warp_wait_slow(uint32_t bar, uint32_t parity) {
+    const int64_t t0 = clock64();
+    do {
+#pragma unroll 1
+        for (int i = 0; i < kWaitPolls; ++i)
+            if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
+    } while (__all_sync(kFull, clock64() - t0 <= kWaitClocks));
+    return false;
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, bool& ok) {
+    if (!__all_sync(kFull, mbar_try_wait(bar, parity))) ok = warp_wait_slow(bar, parity);
+    return ok;
+}
+// The wait for copies and products that are under way when a CTA leaves: with the full limit in
+// every build, and whatever gave up before.
+__device__ __forceinline__ bool wait_landed(uint32_t bar, uint32_t parity) {
+    return mbar_try_wait(bar, parity) || mbar_wait_slow(bar, parity, INT64_C(4000000000));
 }
 
 // One arrival for a whole warp: every lane's earlier shared-memory writes (each lane has

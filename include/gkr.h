@@ -362,6 +362,9 @@ GKR_API gkr_status gkr_sparse_logits(const void *q, int32_t num_heads, const voi
  * rounded to bf16 (relative to a running maximum) for the value product.  Records' values below
  * 2^55 cannot overflow the accumulator, however many are listed.  Results do not
  * depend on the order of execution: every sum has a fixed order.
+ * Should a wait give up (GKR_ERR_TIMEOUT), each row of out is either right or not written, and
+ * the lse of one that is not is a NaN; the weights of a query with such a head are left as they
+ * are, and any other entry has its weight added or is left.
  *
  * q               device, bf16 [num_queries, num_heads, 512] row-major, 16-byte aligned.
  * num_heads       1 .. 128.
