@@ -1285,13 +1285,19 @@ cudaError_t make_cut(int64_t num_queries, int64_t topk, int32_t num_heads, Cut* 
     cut->pairs = static_cast<int32_t>(cut->total < pairs ? cut->total : pairs);
     cut->each = 0;
     // Whole queries, as many for each pair, where the longest run is then no longer than the even
-    // cut's and what the pieces' fp32 rows and the kernel that joins them cost, in chunks: five
-    // and one for nine heads.  Measured, us a call whole and cut: 128 queries x 2048 entries x 128
-    // heads (64 chunks, 54) 75 and 86; 120 x 1088 x 128 (34, 27) 45 and 57; 90 x 1600 (50, 30)
-    // x 128 heads 60.4 and 60.0, x 64 60 and 53, x 16 59 and 46; 100 x 1024 (32, 22) x 64 42 and
-    // 44, x 32 41 and 39; 40 x 640 x 16 (10, 6) 16 and 20; 37 x 1531 x 16 (24, 12) 30 and 25.5.
+    // cut's and what the pieces' fp32 rows and the kernel that joins them cost, in chunks of 1 us:
+    // five, and one for 9 heads where every pair writes two pieces; fewer pieces cost less.
+    // Measured, us in a graph whole and cut: 128 queries x 2048 entries x 128 heads (64 chunks,
+    // 54) 75 and 86; 120 x 1088 x 128 (34, 27) 45 and 57; 90 x 1600 (50, 30) x 128 heads 60.4 and
+    // 60.0, x 64 60 and 53, x 16 59 and 46; 100 x 1024 (32, 22) x 64 42 and 44, x 32 41 and 39;
+    // 40 x 640 x 16 (10, 6) 16 and 20; 37 x 1531 x 16 (24, 12) 30 and 25.5.  Few queries: 1 x 1280 x
+    // 128 (20, 1) 26.0 and 12.5; 1 x 256 x 128 (4, 1) 10.0 and 10.8; 4 x 512 x 128 (8, 1) 14.5 and
+    // 14.2; 16 x 1280 x 128 (20, 5) 26.7 and 23.6; 32 x 1280 x 128 (20, 9) 26.9 and 29.5; 2 x 512 x 32
+    // (8, 1) 13.9 and 10.3.  Of 420 sizes of 1 .. 160 queries, 8 .. 128 heads and 128 .. 2048
+    // entries the slower form is taken in four, by 6 to 9 %.
     const int64_t each = (num_queries + pairs - 1) / pairs;
-    if (each * cut->per_query <= (cut->total + pairs - 1) / pairs + 5 + num_heads / 9) {
+    const int64_t pieces = cut->pairs + (cut->total > pairs ? (num_queries < pairs ? num_queries : pairs) : 0);
+    if (each * cut->per_query <= (cut->total + pairs - 1) / pairs + 5 + num_heads * pieces / (18 * pairs)) {
         cut->each = each;
         cut->pairs = static_cast<int32_t>((num_queries + each - 1) / each);
     }
