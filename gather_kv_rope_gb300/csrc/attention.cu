@@ -770,10 +770,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 ++qi;
             }
         }
-        // after a wait that gave up, blocks of a query may still be on their way
-        if (threadIdx.x == kPollThread) {
-            if (bars->next_loads > 0 && !wait_landed(smem_addr(&bars->q_next), (bars->next_loads - 1) & 1)) ok = false;
-            if (bars->live_loads > 0 && !wait_landed(smem_addr(&bars->q_live), (bars->live_loads - 1) & 1)) ok = false;
+        // after a wait that gave up, blocks of a query may still be on their way (otherwise this
+        // thread has waited for all that it asked for)
+        if (threadIdx.x == kPollThread && !ok) {
+            if (bars->next_loads > 0) wait_landed(smem_addr(&bars->q_next), (bars->next_loads - 1) & 1);
+            if (bars->live_loads > 0) wait_landed(smem_addr(&bars->q_live), (bars->live_loads - 1) & 1);
         }
         __syncwarp();
     }
