@@ -166,3 +166,12 @@ def test_binding_refusals(gkr):
                 dict(keep=4, evicted=torch.zeros(2, 4, dtype=torch.int32))):
         with pytest.raises(ValueError):
             gkr.kv_evict(**{"indices": idx, "weights": w, **bad})
+
+
+def test_evict_list_limit(gkr):
+    """2^21 entries of a list at most: the words of a longer one would outgrow shared memory."""
+    n = (1 << 21) + 1
+    assert evict(gkr, length=n, istride=n, wstride=n) == 1
+    assert evict(gkr, length=n, istride=n, wstride=n, keep=n, recent=0) == 1
+    # at the limit the lengths pass, and the pointers are looked at next
+    assert evict(gkr, length=n - 1, istride=n - 1, wstride=n - 1, idx=A + 2) == 4
