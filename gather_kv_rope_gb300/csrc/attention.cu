@@ -19,7 +19,7 @@
 //     which so need not be read from shared memory by every product.
 //   * Records come by 16-byte asynchronous copies of three warps, their slots six chunks ahead: a
 //     chunk takes about 2000 cycles, a load from memory up to 4000.  (By the copy engine's
-//     four-row gathers, 90 cycles each, they came too slowly: 79 us where this takes 75.5.)
+//     four-row gathers, 90 cycles each, they came too slowly: 79 us where this took 75.5.)
 //   * They are dequantised once to bf16 in shared memory and are there both operands: rows
 //     of 128 bytes (64 dims) in 8-row swizzle groups read K-major for q . K (reduction over
 //     dims) and MN-major for p . K (reduction over records).  A product of the pair takes half
@@ -74,7 +74,7 @@ constexpr int kGatherWarps = 3;          // raw records: own in two halves, the 
 constexpr int kFirstGather = kMmaWarp + 1;
 constexpr int kIndexRing = 8;            // chunks of indices (kept as many) a gather warp holds,
 constexpr int kIndexAhead = 6;           // and has on their way
-constexpr int kAttendThreads = (kFirstGather + kGatherWarps) * 32;   // 24 warps: up to 80 registers
+constexpr int kAttendThreads = (kFirstGather + kGatherWarps) * 32;   // 24 warps: up to 80 registers (16 bytes spilled)
 constexpr uint32_t kBlockBytes = kOwnKeys * kRowBytes;      // 64 dims of the stage's 32 rows
 constexpr uint32_t kHalfBytes = 4 * kBlockBytes;            // 256 dims
 constexpr uint32_t kStageBytes = 2 * kHalfBytes;
@@ -83,7 +83,6 @@ constexpr int kQTmemBlocks = 6;          // blocks of 64 dims of the query in te
 constexpr uint32_t kQBytes = (8 - kQTmemBlocks) * kQBlockBytes;   // and in shared memory
 constexpr uint32_t kPBytes = kPairHeads * kRowBytes;        // probabilities of a chunk, bf16
 constexpr uint32_t kTmemCols = 512;
-constexpr int kMaxHeadsTile = 128;
 constexpr uint32_t kSCol = 256;          // logits: two buffers of 32 columns; output at 0
 constexpr uint32_t kQCol = 320;          // the query's first 384 dims, two to a column
 static_assert(kQCol + kQTmemBlocks * 32 <= kTmemCols, "tensor memory");

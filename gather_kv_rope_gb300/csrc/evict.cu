@@ -21,9 +21,10 @@
 // other's counts through distributed shared memory.  The work is a few dependent steps on little
 // data, so their latency and the instructions of a few CTAs bound it, not memory: with one entry a
 // lane and instruction a step over 16384 entries of a CTA took 3600 cycles (25 instructions for
-// 32 entries), so a lane takes four at a time where it can.  Measured in a graph, keeping 4096 of
-// 4 x 131071 entries 23 us (one entry a lane 26), 2048 of 128 x 2049 7.2 us (9.6), 65536 of
-// 16 x 1000000 320 us (480).
+// 32 entries), so a lane takes four at a time where it can.  Measured in a graph (weights of a
+// log-normal distribution, a tenth of them zeros; in brackets uniform ones to the fourth power):
+// keeping 4096 of 4 x 131071 entries 22 us (24), 2048 of 128 x 2049 9.1 us (7.0), 65536 of
+// 16 x 1000000 312 us (317).
 #include "device.cuh"
 #include "launch.h"
 #include "tensor.cuh"
@@ -438,16 +439,16 @@ cudaError_t launch(const EvictParams& p, int32_t cluster, cudaStream_t stream) {
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
     // CTAs a row: as many as it takes to keep a part's keys in shared memory, then more, down to 4096
     // entries each, while all rows' CTAs run at once (128 of the 152 SMs: whole clusters have
-    // to fit).  Measured, us in a graph: 4 rows x 16384 entries 16.3 with one CTA a row, 14.6 with
-    // two, 12.0 with four; 4 x 32768 19.3 with two, 14.9 with four, 13.7 with eight; 64 x 32768
-    // 21.5, 32 and 70; 64 x 16384 17.6 with one, 15.9 with two, 26 with four; 64 x 65536 33 with
-    // two, 42 with four, 84 with eight.
+    // to fit).  Measured, us in a graph, half of the entries kept: 4 rows x 16384 entries 16.2
+    // with one CTA a row, 14.5 with two, 12.3 with four, 12.5 with eight; 4 x 32768 26.9, 19.4, 14.9 and
+    // 13.9; 64 x 16384 17.5 with one, 16.1 with two, 26.7 with four; 64 x 32768 28.9, 21.6 and 31.9;
+    // 64 x 65536 33.4 with two, 42.3 with four, 84.1 with eight.
     int32_t cluster = 1;
     while (cluster < kMaxCluster &&
            (p.length > kCachedKeys * cluster || (p.length > 4096 * cluster && p.rows * cluster * 2 <= 128)))
         cluster *= 2;
-    // few threads wait less for each other where the entries are few: 128 rows x 1024 entries 5.8 us
-    // with 256 threads and 7.8 with 1024, x 2049 8.2 and 8.5, x 4096 10.0 and 9.2
+    // few threads wait less for each other where the entries are few: 128 rows x 1024 entries, half
+    // kept, 5.8 us with 256 threads and 7.8 with 1024, x 2049 8.7 and 9.0, x 4096 10.5 and 9.7
     return p.length <= kFewEntries ? launch<256>(p, 1, stream) : launch<1024>(p, cluster, stream);
 }
 

@@ -286,7 +286,7 @@ template <int kRecord>
 __device__ __forceinline__ uint32_t decode_compressed(const InsertParams& p, int64_t slot,
                                                       int64_t q, int64_t& off, int64_t& soff,
                                                       int32_t& row) {
-    static_assert(Fmt<kRecord>::kPacked, "the compressed insert writes the packed records");
+    static_assert(Fmt<kRecord>::kCompressed, "the compressed insert writes the MXFP8 records");
     constexpr uint32_t D = Fmt<kRecord>::D;
     constexpr uint32_t S = Fmt<kRecord>::S;
     if (slot < 0) return 0u;

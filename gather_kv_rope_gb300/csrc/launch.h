@@ -128,7 +128,7 @@ struct Fmt {
         kRecord == 528 || kRecord == 272 ? 16u : kRecord == 584 ? 8u : 0u;
     // bytes of a row that lane L owns at 8L-dim granularity: 4 e2m1, 8 e4m3 or 16 bf16 bytes
     static constexpr int kLaneBytes = kRecord == 1024 ? 16 : kRecord == 272 ? 4 : 8;
-    static constexpr bool kPacked = kRecord == 528 || kRecord == 584;
+    static constexpr bool kCompressed = kRecord == 528 || kRecord == 584;   // written by the compressed insert
 };
 
 // Launch-shape helpers (api.cu).  `resident_warps` returns how many warps of `func`

@@ -270,7 +270,7 @@ GKR_API gkr_status gkr_rope_quant_insert(const void *kv, int64_t num_tokens, voi
  *                   bf16 q_out.
  * eps               finite, >= 0.
  * apply_q_norm      0 or 1.
- * The other arguments are gkr_kv_insert's, for the KV row (any of the four records).
+ * The other arguments are gkr_kv_insert's, for the KV row (any of the five records).
  */
 GKR_API gkr_status gkr_qnorm_rope_kv_insert(const void *q_in, int32_t num_heads,
                                             int32_t num_heads_padded, void *q_out,
@@ -320,8 +320,8 @@ GKR_API gkr_status gkr_kv_gather(const void *k_cache, const gkr_cache_desc *cach
  * product).  For query i, head h < num_heads and entry k < topk:
  *   out[i, h, k] = fl32(sm_scale * sum_d q[i, h, d] * K[d])
  * where K = the bf16 row gkr_kv_gather returns for indices[i, k] (any record but 272,
- * which gkr_sparse_attention reads: GKR_EUNSUPPORTED_RECORD); indices[i, k] == -1 gives -inf, an index < -1 or past the cache gives -inf
- * and sets GKR_ERR_INDEX; an fp8 cache whose scale is not a positive finite number gives
+ * which gkr_sparse_attention reads: GKR_EUNSUPPORTED_RECORD); indices[i, k] == -1 gives
+ * -inf, an index < -1 or past the cache gives -inf and sets GKR_ERR_INDEX; an fp8 cache whose scale is not a positive finite number gives
  * -inf everywhere and GKR_ERR_SCALE.  The gathered rows stay on chip (shared memory) and
  * the products run on the tensor cores (bf16 x bf16, fp32 accumulation over the 512
  * dims in the hardware's order), so each value is within 2^-13 * |sm_scale| *
