@@ -903,7 +903,7 @@ __global__ void __launch_bounds__(128 * kGroups)
 //   * one thread multiplies them by the query's heads, which lie in shared memory, into one of
 //     two accumulators;
 //   * four warps turn the accumulator into the records' sums and add them to the weights.
-// Measured at 64 queries of 128 heads and 2049 entries: 31 us, against 45 us with one group of
+// Measured at 64 queries of 128 heads and 2049 entries: 30 us, against 45 us with one group of
 // 16 warps a stage, one stage less and whole half-rows.  The products alone are 17 GFLOP
 // (9 us); what is left is the dequantisation's instructions and the latencies between a stage's
 // filling, its product and its next filling: two or three stages are all that shared memory
