@@ -163,6 +163,31 @@ def lib() -> ctypes.CDLL:
                 # kept_weights, evicted, opts, stream
                 L.gkr_kv_evict.argtypes = [vp, i64, vp, i64, i64, i64, i64, i64, vp, vp, vp, opt, vp]
                 L.gkr_kv_evict.restype = ctypes.c_int
+                # past, added, requests, table, stride, width, free, num_free, block_size, tokens,
+                # slots, positions, starts, taken, err, opts, stream
+                L.gkr_kv_allocate.argtypes = [vp, vp, i32, vp, i64, i32, vp, i64, i32, i64, vp, vp,
+                                              vp, vp, vp, opt, vp]
+                L.gkr_kv_allocate.restype = ctypes.c_int
+                # table, stride, width, lengths, first, requests, block_size, width, indices,
+                # starts, err, opts, stream
+                L.gkr_kv_slots.argtypes = [vp, i64, i32, vp, vp, i32, i32, i64, vp, vp, vp, opt, vp]
+                L.gkr_kv_slots.restype = ctypes.c_int
+                # q, H, T, kv, stride, rows, starts, kv_starts, requests, causal, sm_scale, out,
+                # lse, workspace, bytes, err, opts, stream
+                L.gkr_prompt_attention.argtypes = [vp, i32, i64, vp, i64, i64, vp, vp, i32, i32,
+                                                   ctypes.c_float, vp, vp, vp, i64, vp, opt, vp]
+                L.gkr_prompt_attention.restype = ctypes.c_int
+                L.gkr_prompt_attention_workspace.argtypes = [i32, i64, ctypes.POINTER(i64)]
+                L.gkr_prompt_attention_workspace.restype = ctypes.c_int
+                # q, H, k_cache, desc, prefix, length, indices, stride, Q, topk, sm_scale, out,
+                # lse, workspace, bytes, err, opts, stream
+                L.gkr_prefix_attention.argtypes = [vp, i32, vp, ctypes.POINTER(CacheDesc), vp, i64,
+                                                   vp, i64, i64, i64, ctypes.c_float, vp, vp, vp,
+                                                   i64, vp, opt, vp]
+                L.gkr_prefix_attention.restype = ctypes.c_int
+                L.gkr_prefix_attention_workspace.argtypes = [i32, i64, i64, i64,
+                                                             ctypes.POINTER(i64)]
+                L.gkr_prefix_attention_workspace.restype = ctypes.c_int
                 L.gkr_status_string.argtypes, L.gkr_status_string.restype = [ctypes.c_int], \
                     ctypes.c_char_p
                 L.gkr_last_cuda_error.argtypes, L.gkr_last_cuda_error.restype = [], i32
@@ -548,6 +573,8 @@ def _rows(t: torch.Tensor, dtype: torch.dtype, name: str) -> int:
     """Row stride of a 2-D tensor whose rows are contiguous (a slice of wider rows will do)."""
     if t.dtype == dtype and t.dim() == 2:
         rows, cols = t.shape
+        if rows == 0 or cols == 0:
+            return cols                   # strides of an empty tensor say nothing
         stride, step = t.stride()
         if (step == 1 or cols <= 1) and (stride >= cols or rows <= 1):
             return max(stride, cols)
@@ -676,3 +703,252 @@ def kv_evict(indices: torch.Tensor, weights: torch.Tensor, keep: int, recent: in
           keep, recent, kept.data_ptr(), kept_weights.data_ptr(), evicted.data_ptr(),
           _opts(launch_opts))
     return kept, kept_weights, evicted
+
+
+def _vector(t: torch.Tensor, name: str, length: int | None = None, dtype=torch.int32) -> int:
+    """Length of a contiguous 1-D tensor, checked against `length` where that is given."""
+    if t.dtype != dtype or t.dim() != 1 or not t.is_contiguous() \
+            or (length is not None and t.shape[0] != length):
+        n = "" if length is None else f" [{length}]"
+        raise ValueError(f"{name} must be a contiguous 1-D {dtype} tensor{n}".replace("torch.", ""))
+    return t.shape[0]
+
+
+def _out_vector(t, length: int, dtype: torch.dtype, name: str, like: torch.Tensor):
+    """A given 1-D output after its checks, or a new one beside `like`."""
+    if t is None:
+        return torch.empty(length, dtype=dtype, device=like.device)
+    _vector(t, name, length, dtype)
+    return t
+
+
+def kv_allocate(past: torch.Tensor, added: torch.Tensor, block_table: torch.Tensor,
+                free_pages: torch.Tensor, block_size: int, num_tokens: int,
+                slot_mapping: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                starts: torch.Tensor | None = None, taken: torch.Tensor | None = None,
+                err_flag: torch.Tensor | None = None, launch_opts: LaunchOpts | None = None
+                ) -> tuple[torch.Tensor, torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Pages, slots and positions of the tokens that a batch's requests get.
+
+    past         int32 [B]: tokens that each request holds (0: a new one).
+    added        int32 [B]: tokens that it gets now.
+    block_table  int32 [B, W], rows contiguous: each request's pages in order.  The columns from
+                 ceil(past / block_size) on that the new tokens need are written, with
+    free_pages   int32 [F]: pages to take, from the first on, request after request.
+    num_tokens   rows of the outputs, sum(added) or more; those behind get slot -1, position 0.
+
+    Returns (slot_mapping int64 [num_tokens], positions int64 [num_tokens], starts int32
+    [B + 1], taken int32 [1]): what kv_insert takes, the row where each request's tokens begin
+    (as prompt_attention takes it), and how many pages were taken.  A token that gets no page
+    has slot -1, and err_flag ERR_SLOT.  The lengths stay on the GPU; nothing is kept."""
+    B = _vector(past, "past")
+    _vector(added, "added", B)
+    stride = _rows(block_table, torch.int32, "block_table")
+    if block_table.shape[0] != B:
+        raise ValueError("block_table must have a row for each request")
+    F = _vector(free_pages, "free_pages")
+    num_tokens = int(num_tokens)
+    _check(0 <= num_tokens < 1 << 31, "num_tokens must be in [0, 2^31)")
+    slot_mapping = _out_vector(slot_mapping, num_tokens, torch.int64, "slot_mapping", past)
+    positions = _out_vector(positions, num_tokens, torch.int64, "positions", past)
+    starts = _out_vector(starts, B + 1, torch.int32, "starts", past)
+    taken = _out_vector(taken, 1, torch.int32, "taken", past)
+    _check_err_flag(err_flag)
+    dev = _same_cuda_device(past, added, block_table, free_pages, slot_mapping, positions, starts,
+                            taken, err_flag)
+    _call(dev, lib().gkr_kv_allocate, past.data_ptr(), added.data_ptr(), B, block_table.data_ptr(),
+          stride, block_table.shape[1], free_pages.data_ptr(), F, int(block_size), num_tokens,
+          slot_mapping.data_ptr(), positions.data_ptr(), starts.data_ptr(), taken.data_ptr(),
+          _ptr(err_flag), _opts(launch_opts))
+    return slot_mapping, positions, starts, taken
+
+
+def _slots(block_table, lengths, block_size, width, first, indices, starts, err_flag, launch_opts):
+    B = _vector(lengths, "lengths")
+    stride = _rows(block_table, torch.int32, "block_table")
+    if block_table.shape[0] != B:
+        raise ValueError("block_table must have a row for each request")
+    if first is not None:
+        _vector(first, "first", B)
+    _check_err_flag(err_flag)
+    dev = _same_cuda_device(lengths, block_table, first, indices, starts, err_flag)
+    _call(dev, lib().gkr_kv_slots, block_table.data_ptr(), stride, block_table.shape[1],
+          lengths.data_ptr(), _ptr(first), B, int(block_size), width, indices.data_ptr(),
+          _ptr(starts), _ptr(err_flag), _opts(launch_opts))
+
+
+def kv_slots(block_table: torch.Tensor, lengths: torch.Tensor, block_size: int, width: int,
+             first: torch.Tensor | None = None, indices: torch.Tensor | None = None,
+             err_flag: torch.Tensor | None = None, launch_opts: LaunchOpts | None = None
+             ) -> torch.Tensor:
+    """The slots of what requests hold, as sparse_attention takes them: int32 [B, width], row b
+    the slots of positions first[b] (or 0) .. lengths[b] - 1 in order, then -1.
+
+    block_table  int32 [B, W], rows contiguous;  lengths, first  int32 [B].
+    indices      a contiguous int32 [B, width] to write, or None.
+    A position without a page gets -1, and err_flag ERR_INDEX, as where a row is too short."""
+    width = int(width)
+    _check(0 <= width < 1 << 31, "width must be in [0, 2^31)")
+    indices = _buffer(indices, lengths.shape[0] if lengths.dim() == 1 else 0, width, torch.int32,
+                      "indices", lengths)
+    _slots(block_table, lengths, block_size, width, first, indices, None, err_flag, launch_opts)
+    return indices
+
+
+def kv_slots_packed(block_table: torch.Tensor, lengths: torch.Tensor, block_size: int, total: int,
+                    first: torch.Tensor | None = None, indices: torch.Tensor | None = None,
+                    starts: torch.Tensor | None = None, err_flag: torch.Tensor | None = None,
+                    launch_opts: LaunchOpts | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The same one request after another, as kv_gather takes them: (indices int32 [total],
+    starts int32 [B + 1]); entries behind the last request are -1.  The rows that kv_gather
+    returns for them, with these starts, are what prompt_attention takes as kv and kv_starts."""
+    total = int(total)
+    _check(0 <= total < 1 << 31, "total must be in [0, 2^31)")
+    indices = _out_vector(indices, total, torch.int32, "indices", lengths)
+    starts = _out_vector(starts, lengths.shape[0] + 1 if lengths.dim() == 1 else 1, torch.int32,
+                         "starts", lengths)
+    _slots(block_table, lengths, block_size, total, first, indices, starts, err_flag, launch_opts)
+    return indices, starts
+
+
+@functools.lru_cache(maxsize=256)
+def _prompt_workspace(num_heads: int, num_tokens: int, index: int) -> int:
+    n = ctypes.c_int64()
+    with torch.cuda.device(index):
+        _raise(lib().gkr_prompt_attention_workspace(num_heads, num_tokens, ctypes.byref(n)))
+    return int(n.value)
+
+
+@functools.lru_cache(maxsize=256)
+def _prefix_workspace(num_heads: int, num_queries: int, prefix: int, topk: int, index: int) -> int:
+    n = ctypes.c_int64()
+    with torch.cuda.device(index):
+        _raise(lib().gkr_prefix_attention_workspace(num_heads, num_queries, prefix, topk,
+                                                    ctypes.byref(n)))
+    return int(n.value)
+
+
+def _device_index(device) -> int:
+    dev = torch.device("cuda" if device is None else device)
+    return torch.cuda.current_device() if dev.index is None else dev.index
+
+
+def prompt_attention_workspace(num_heads: int, num_tokens: int, device=None) -> int:
+    """Bytes of workspace a prompt_attention call of these sizes needs on a device."""
+    return _prompt_workspace(int(num_heads), int(num_tokens), _device_index(device))
+
+
+def prefix_attention_workspace(num_heads: int, num_queries: int, prefix_length: int, topk: int,
+                               device=None) -> int:
+    """Bytes of workspace a prefix_attention call of these sizes needs on a device."""
+    return _prefix_workspace(int(num_heads), int(num_queries), int(prefix_length), int(topk),
+                             _device_index(device))
+
+
+def _attention_outputs(q, out, lse):
+    """q bf16 [n, H, 512] and the outputs beside it, checked or new."""
+    shape = q.shape
+    if q.dtype != torch.bfloat16 or len(shape) != 3 or shape[2] != HEAD_DIM \
+            or not q.is_contiguous():
+        raise ValueError("q must be a contiguous bf16 tensor [queries, heads, 512]")
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.dtype != torch.bfloat16 or not out.is_contiguous() or out.shape != shape:
+        raise ValueError("out must be a contiguous bf16 tensor of q's shape")
+    if lse is None:
+        lse = torch.empty(shape[0], shape[1], dtype=torch.float32, device=q.device)
+    elif lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != shape[:2]:
+        raise ValueError("lse must be a contiguous fp32 tensor [queries, heads]")
+    return out, lse
+
+
+def _work_buffer(workspace, size: int, dev):
+    if workspace is None:
+        return torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    return workspace
+
+
+def prompt_attention(q: torch.Tensor, kv: torch.Tensor, starts: torch.Tensor, sm_scale: float,
+                     kv_starts: torch.Tensor | None = None, causal: bool = True,
+                     out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                     workspace: torch.Tensor | None = None, err_flag: torch.Tensor | None = None,
+                     launch_opts: LaunchOpts | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Attention of packed requests over packed latent rows, key and value of every head.
+
+    q          bf16 [T, H, 512], contiguous: the queries, one request after another.
+    kv         bf16 [N, 512], rows contiguous (a slice of wider rows will do): the rows, one
+               request after another, e.g. the prompts' own, or what kv_gather returns for
+               kv_slots_packed, whatever the cache's format.
+    starts     int32 [B + 1]: request b has queries starts[b] .. starts[b + 1] - 1 ...
+    kv_starts  int32 [B + 1]: ... and rows kv_starts[b] .. kv_starts[b + 1] - 1 (None: starts).
+    causal     a request's last query sees all of its rows, each one before it one row less
+               (so more rows than queries are what came before them); False: all see all.
+    out, lse   bf16 [T, H, 512], not overlapping q or kv, and fp32 [T, H] (allocated when None).
+    workspace  contiguous uint8 CUDA tensor of prompt_attention_workspace() bytes or more, for
+               this call alone while it runs (allocated when None).
+
+    out[i, h] = softmax over the rows it sees of (sm_scale * q[i, h] . K) times K, lse[i, h] the
+    log of the softmax's sum; zeros and -inf for a query that sees none.  Queries of no
+    request are left as they are.  Returns (out, lse)."""
+    out, lse = _attention_outputs(q, out, lse)
+    T, H, _ = q.shape
+    stride = _rows(kv, torch.bfloat16, "kv")
+    if kv.shape[1] != HEAD_DIM or (stride % 8 and kv.shape[0] > 1):
+        raise ValueError("kv must be bf16 [rows, 512], rows a multiple of 8 elements apart")
+    if stride % 8:
+        stride = HEAD_DIM
+    B = _vector(starts, "starts") - 1
+    _check(B >= 0, "starts must have an element more than there are requests")
+    if kv_starts is None:
+        kv_starts = starts
+    else:
+        _vector(kv_starts, "kv_starts", B + 1)
+    _check_err_flag(err_flag)
+    dev = _same_cuda_device(q, kv, starts, kv_starts, out, lse, err_flag, workspace)
+    if workspace is None and T:
+        workspace = _work_buffer(None, _prompt_workspace(H, T, dev.index), dev)
+    workspace = _work_buffer(workspace, 0, dev)
+    _call(dev, lib().gkr_prompt_attention, q.data_ptr(), H, T, kv.data_ptr(), stride, kv.shape[0],
+          starts.data_ptr(), kv_starts.data_ptr(), B, 1 if causal else 0, float(sm_scale),
+          out.data_ptr(), lse.data_ptr(), _ptr(workspace),
+          0 if workspace is None else workspace.numel(), _ptr(err_flag), _opts(launch_opts))
+    return out, lse
+
+
+def prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, prefix: torch.Tensor,
+                     indices: torch.Tensor, sm_scale: float, out: torch.Tensor | None = None,
+                     lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+                     err_flag: torch.Tensor | None = None,
+                     launch_opts: LaunchOpts | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """sparse_attention for queries that share a prefix: query i attends to the records that
+    `prefix` lists, the same for every query, and to those of its own row of `indices`, in one
+    softmax.  The prefix is read and dequantised once for all queries.
+
+    prefix     int32 [L], contiguous;  indices  int32 [Q, K], rows contiguous.  -1 (or an index
+               outside the cache) is no entry in either; L or K may be 0.
+    workspace  contiguous uint8 CUDA tensor of prefix_attention_workspace() bytes or more, for
+               this call alone while it runs (allocated when None).
+    q, k_cache, sm_scale, out and lse are sparse_attention's.  Returns (out, lse)."""
+    desc = _cache_desc(k_cache)
+    _check(desc.record == MXFP4, "prefix_attention reads the MXFP4 records (272 bytes)")
+    out, lse = _attention_outputs(q, out, lse)
+    Q, H, _ = q.shape
+    L = _vector(prefix, "prefix")
+    istride = _rows(indices, torch.int32, "indices")
+    rows, K = indices.shape
+    if rows != Q:
+        raise ValueError("indices must have a row for each query")
+    if not 1 <= H <= 128:
+        raise ValueError("prefix_attention takes 1 to 128 heads")
+    _check_err_flag(err_flag)
+    dev = _same_cuda_device(q, k_cache, prefix, indices, out, lse, err_flag, workspace)
+    if workspace is None and Q:
+        workspace = _work_buffer(None, _prefix_workspace(H, Q, L, K, dev.index), dev)
+    workspace = _work_buffer(workspace, 0, dev)
+    _call(dev, lib().gkr_prefix_attention, q.data_ptr(), H, k_cache.data_ptr(), ctypes.byref(desc),
+          prefix.data_ptr(), L, indices.data_ptr(), istride, Q, K, float(sm_scale),
+          out.data_ptr(), lse.data_ptr(), _ptr(workspace),
+          0 if workspace is None else workspace.numel(), _ptr(err_flag), _opts(launch_opts))
+    return out, lse

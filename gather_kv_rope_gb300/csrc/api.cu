@@ -17,6 +17,8 @@ constexpr int64_t kDefaultStagedMin = 24576;
 constexpr int64_t kDefaultStreamMin = 131072;
 constexpr int64_t kMaxRows = INT64_C(1) << 24;   // queries, list entries of a call at most
 constexpr int64_t kMaxList = INT64_C(1) << 21;   // entries of an eviction list at most
+constexpr int64_t kMaxIndex = INT64_C(0x7FFFFFFF);
+constexpr int64_t kMaxPromptRows = INT64_C(0x7FFF0000);   // rows of a prompt attention at most
 constexpr int32_t kMaxQHeads = 4096;   // query heads per token (padded) at most
 std::atomic<int64_t> g_staged_min{kDefaultStagedMin};
 std::atomic<int64_t> g_stream_min{kDefaultStreamMin};
@@ -59,6 +61,26 @@ bool compressed(int32_t record) { return record == 528 || record == 584; }
 // plain caches take any block_size >= 1.
 bool block_size_ok(int32_t record, int32_t bs) {
     return bs > 0 && (!packed(record) || bs % 32 == 0);
+}
+
+// Query heads and rows of a prompt attention: tiles of rows are addressed in 32 bits.
+bool prompt_rows_ok(int32_t num_heads, int64_t num_tokens) {
+    return num_heads >= 1 && num_heads <= kMaxQHeads && num_tokens >= 0 &&
+           num_tokens <= kMaxPromptRows / num_heads;
+}
+bool prefix_sizes_ok(int32_t num_heads, int64_t num_queries, int64_t prefix_length, int64_t topk) {
+    return num_heads >= 1 && num_heads <= gkr::kAttentionMaxHeads && num_queries >= 0 &&
+           num_queries <= kMaxRows && prefix_length >= 0 && prefix_length <= kMaxRows && topk >= 0 &&
+           topk <= kMaxRows && prompt_rows_ok(num_heads, num_queries) &&
+           num_queries * ((topk + 63) / 64) <= kMaxIndex;
+}
+
+bool finite(float x) { return x >= -3.40282347e38f && x <= 3.40282347e38f; }
+
+// Whether two ranges of bytes have one in common.
+bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + static_cast<uintptr_t>(b_bytes) && y < x + static_cast<uintptr_t>(a_bytes);
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
@@ -503,6 +525,213 @@ GKR_API gkr_status gkr_kv_evict(const int32_t* indices, int64_t index_stride,
     p.evicted = evicted;
     p.pdl = pol.pdl;
     return cuda_status(gkr::launch_evict(p, stream));
+}
+
+GKR_API gkr_status gkr_kv_allocate(const int32_t* past, const int32_t* added,
+                                   int32_t num_requests, int32_t* block_table,
+                                   int64_t table_stride, int32_t table_width,
+                                   const int32_t* free_pages, int64_t num_free,
+                                   int32_t block_size, int64_t num_tokens, int64_t* slot_mapping,
+                                   int64_t* positions, int32_t* starts, int32_t* taken,
+                                   int32_t* err_flag, const gkr_launch_opts* opts,
+                                   cudaStream_t stream) {
+    Policy pol;
+    const gkr_status st = resolve_policy(opts, &pol);
+    if (st != GKR_OK) return st;
+    if (num_requests < 0 || num_requests > gkr::kPlanMaxRequests || table_width < 0 ||
+        table_stride < table_width || num_free < 0 || num_free > kMaxIndex || block_size < 1 ||
+        num_tokens < 0 || num_tokens > kMaxIndex)
+        return GKR_EINVAL;
+    if ((num_requests > 0 && (!past || !added || (table_width > 0 && !block_table))) ||
+        (num_free > 0 && !free_pages) || (num_tokens > 0 && (!slot_mapping || !positions)) ||
+        !starts || !taken)
+        return GKR_EINVAL;
+    if (!aligned(past, 4) || !aligned(added, 4) || !aligned(block_table, 4) ||
+        !aligned(free_pages, 4) || !aligned(slot_mapping, 8) || !aligned(positions, 8) ||
+        !aligned(starts, 4) || !aligned(taken, 4) || !aligned(err_flag, 4))
+        return GKR_EALIGN;
+    gkr::AllocateParams p;
+    p.past = past;
+    p.added = added;
+    p.num_requests = num_requests;
+    p.table = block_table;
+    p.table_stride = table_stride;
+    p.table_width = table_width;
+    p.free_pages = free_pages;
+    p.num_free = num_free;
+    p.block_size = block_size;
+    p.num_tokens = num_tokens;
+    p.slots = slot_mapping;
+    p.positions = positions;
+    p.starts = starts;
+    p.taken = taken;
+    p.err = err_flag;
+    p.pdl = pol.pdl;
+    return cuda_status(gkr::launch_allocate(p, stream));
+}
+
+GKR_API gkr_status gkr_kv_slots(const int32_t* block_table, int64_t table_stride,
+                                int32_t table_width, const int32_t* lengths,
+                                const int32_t* first, int32_t num_requests, int32_t block_size,
+                                int64_t width, int32_t* indices, int32_t* starts,
+                                int32_t* err_flag, const gkr_launch_opts* opts,
+                                cudaStream_t stream) {
+    Policy pol;
+    const gkr_status st = resolve_policy(opts, &pol);
+    if (st != GKR_OK) return st;
+    const bool packed_rows = starts != nullptr;
+    if (num_requests < 0 || table_width < 0 || table_stride < table_width || block_size < 1 ||
+        width < 0 || width > kMaxIndex || (packed_rows && num_requests > gkr::kPlanMaxRequests))
+        return GKR_EINVAL;
+    // blocks of a launch
+    if (!packed_rows && width > 0 && num_requests > kMaxIndex / ((width + 2047) / 2048))
+        return GKR_EINVAL;
+    if (!packed_rows && (num_requests == 0 || width == 0)) return GKR_OK;
+    if ((num_requests > 0 && (!lengths || (table_width > 0 && !block_table))) ||
+        (width > 0 && !indices))
+        return GKR_EINVAL;
+    if (!aligned(block_table, 4) || !aligned(lengths, 4) || !aligned(first, 4) ||
+        !aligned(indices, 4) || !aligned(starts, 4) || !aligned(err_flag, 4))
+        return GKR_EALIGN;
+    gkr::SlotsParams p;
+    p.table = block_table;
+    p.table_stride = table_stride;
+    p.table_width = table_width;
+    p.lengths = lengths;
+    p.first = first;
+    p.num_requests = num_requests;
+    p.block_size = block_size;
+    p.indices = indices;
+    p.width = width;
+    p.starts = starts;
+    p.err = err_flag;
+    p.pdl = pol.pdl;
+    return cuda_status(gkr::launch_slots(p, stream));
+}
+
+GKR_API gkr_status gkr_prompt_attention_workspace(int32_t num_heads, int64_t num_tokens,
+                                                  int64_t* bytes) {
+    if (bytes == nullptr || !prompt_rows_ok(num_heads, num_tokens)) return GKR_EINVAL;
+    *bytes = 0;
+    if (num_tokens == 0) return GKR_OK;
+    return cuda_status(gkr::prompt_workspace(num_heads, num_tokens, bytes));
+}
+
+GKR_API gkr_status gkr_prompt_attention(const void* q, int32_t num_heads, int64_t num_tokens,
+                                        const void* kv, int64_t kv_stride, int64_t num_rows,
+                                        const int32_t* starts, const int32_t* kv_starts,
+                                        int32_t num_requests, int32_t causal, float sm_scale,
+                                        void* out, float* lse, void* workspace,
+                                        int64_t workspace_bytes, int32_t* err_flag,
+                                        const gkr_launch_opts* opts, cudaStream_t stream) {
+    Policy pol;
+    const gkr_status st = resolve_policy(opts, &pol);
+    if (st != GKR_OK) return st;
+    if (!prompt_rows_ok(num_heads, num_tokens) || num_rows < 0 || num_rows > kMaxPromptRows ||
+        kv_stride < 512 || kv_stride > (INT64_C(1) << 34) || kv_stride % 8 != 0 ||
+        num_requests < 0 || num_requests > gkr::kPlanMaxRequests || causal < 0 || causal > 1 ||
+        !finite(sm_scale))
+        return GKR_EINVAL;
+    if (num_tokens == 0 || num_requests == 0) return GKR_OK;
+    if (!q || (num_rows > 0 && !kv) || !starts || !kv_starts || !out || !lse) return GKR_EINVAL;
+    if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(starts, 4) || !aligned(kv_starts, 4) ||
+        !aligned(out, 16) || !aligned(lse, 4) || !aligned(err_flag, 4))
+        return GKR_EALIGN;
+    const int64_t out_bytes = num_tokens * num_heads * 1024;
+    if (overlap(out, out_bytes, q, out_bytes) ||
+        (num_rows > 0 && overlap(out, out_bytes, kv, ((num_rows - 1) * kv_stride + 512) * 2)))
+        return GKR_EINVAL;
+    int64_t need = 0;
+    const cudaError_t e = gkr::prompt_workspace(num_heads, num_tokens, &need);
+    if (e != cudaSuccess) return cuda_status(e);
+    if (workspace_bytes < need || (need > 0 && !workspace)) return GKR_EINVAL;
+    if (need > 0 && !aligned(workspace, 16)) return GKR_EALIGN;
+    gkr::PromptParams p;
+    p.q = q;
+    p.num_heads = num_heads;
+    p.num_tokens = num_tokens;
+    p.kv = kv;
+    p.kv_stride = kv_stride;
+    p.num_rows = num_rows;
+    p.starts = starts;
+    p.kv_starts = kv_starts;
+    p.num_requests = num_requests;
+    p.causal = causal;
+    p.sm_scale = sm_scale;
+    p.out = out;
+    p.lse = lse;
+    p.workspace = workspace;
+    p.err = err_flag;
+    p.pdl = pol.pdl;
+    return cuda_status(gkr::launch_prompt_attention(p, stream));
+}
+
+GKR_API gkr_status gkr_prefix_attention_workspace(int32_t num_heads, int64_t num_queries,
+                                                  int64_t prefix_length, int64_t topk,
+                                                  int64_t* bytes) {
+    if (bytes == nullptr || !prefix_sizes_ok(num_heads, num_queries, prefix_length, topk))
+        return GKR_EINVAL;
+    *bytes = 0;
+    if (num_queries == 0) return GKR_OK;
+    return cuda_status(gkr::prefix_workspace(num_heads, num_queries, prefix_length, topk, bytes));
+}
+
+GKR_API gkr_status gkr_prefix_attention(const void* q, int32_t num_heads, const void* k_cache,
+                                        const gkr_cache_desc* cache, const int32_t* prefix,
+                                        int64_t prefix_length, const int32_t* indices,
+                                        int64_t index_stride, int64_t num_queries, int64_t topk,
+                                        float sm_scale, void* out, float* lse, void* workspace,
+                                        int64_t workspace_bytes, int32_t* err_flag,
+                                        const gkr_launch_opts* opts, cudaStream_t stream) {
+    RecordRows rows;
+    gkr_status st = check_cache(cache, &rows);
+    if (st != GKR_OK) return st;
+    if (cache->record != 272) return GKR_EUNSUPPORTED_RECORD;
+    // rows of 256 bytes are counted in 32 bits
+    if ((cache->page_stride >> 8) > INT64_C(0x7FFFFFFF) / cache->num_pages)
+        return GKR_EBAD_PAGE_GEOMETRY;
+    Policy pol;
+    st = resolve_policy(opts, &pol);
+    if (st != GKR_OK) return st;
+    if (!prefix_sizes_ok(num_heads, num_queries, prefix_length, topk) || index_stride < topk ||
+        !finite(sm_scale))
+        return GKR_EINVAL;
+    if (num_queries == 0) return GKR_OK;
+    if (!q || !k_cache || !out || !lse || (prefix_length > 0 && !prefix) || (topk > 0 && !indices))
+        return GKR_EINVAL;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(out, 16) || !aligned(prefix, 4) ||
+        !aligned(indices, 4) || !aligned(lse, 4) || !aligned(err_flag, 4))
+        return GKR_EALIGN;
+    const int64_t out_bytes = num_queries * num_heads * 1024;
+    if (overlap(out, out_bytes, q, out_bytes)) return GKR_EINVAL;
+    int64_t need = 0;
+    const cudaError_t e =
+        gkr::prefix_workspace(num_heads, num_queries, prefix_length, topk, &need);
+    if (e != cudaSuccess) return cuda_status(e);
+    if (workspace_bytes < need || (need > 0 && !workspace)) return GKR_EINVAL;
+    if (need > 0 && !aligned(workspace, 16)) return GKR_EALIGN;
+    gkr::PrefixParams p;
+    p.own.q = q;
+    p.own.num_heads = num_heads;
+    p.own.cache = static_cast<const uint8_t*>(k_cache);
+    p.own.page_stride = cache->page_stride;
+    p.own.block_size = cache->block_size;
+    p.own.num_slots = static_cast<int32_t>(cache->num_pages * cache->block_size);
+    p.own.indices = indices;
+    p.own.index_stride = index_stride;
+    p.own.num_queries = num_queries;
+    p.own.topk = topk;
+    p.own.sm_scale = sm_scale;
+    p.own.out = out;
+    p.own.lse = lse;
+    p.own.weights = nullptr;
+    p.own.weight_stride = 0;
+    p.own.workspace = workspace;
+    p.own.err = err_flag;
+    p.own.pdl = pol.pdl;
+    p.prefix = prefix;
+    p.prefix_length = prefix_length;
+    return cuda_status(gkr::launch_prefix_attention(p, stream));
 }
 
 GKR_API const char* gkr_status_string(gkr_status status) {

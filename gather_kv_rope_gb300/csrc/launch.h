@@ -111,6 +111,71 @@ struct EvictParams {
     int32_t pdl;
 };
 
+// Validated arguments of one page allocation (kv_allocate).
+struct AllocateParams {
+    const int32_t* past;       // [num_requests] tokens that the requests hold
+    const int32_t* added;      // [num_requests] tokens that they get
+    int32_t num_requests;      // 0 .. kPlanMaxRequests
+    int32_t* table;            // row b at table + b * table_stride, table_width pages
+    int64_t table_stride;
+    int32_t table_width;
+    const int32_t* free_pages;
+    int64_t num_free;
+    int32_t block_size;
+    int64_t num_tokens;        // rows of slots and positions, < 2^31
+    int64_t* slots;
+    int64_t* positions;
+    int32_t* starts;           // [num_requests + 1]
+    int32_t* taken;            // [1]
+    int32_t* err;              // nullable
+    int32_t pdl;
+};
+
+// Validated arguments of one list of slots, padded rows or (starts not null) packed.
+struct SlotsParams {
+    const int32_t* table;      // row b at table + b * table_stride, table_width pages
+    int64_t table_stride;
+    int32_t table_width;
+    const int32_t* lengths;    // [num_requests] tokens that the requests hold
+    const int32_t* first;      // [num_requests] the first position listed, or null: 0
+    int32_t num_requests;
+    int32_t block_size;
+    int32_t* indices;          // [num_requests, width], or packed [width]
+    int64_t width;
+    int32_t* starts;           // packed: [num_requests + 1]; else null
+    int32_t* err;              // nullable
+    int32_t pdl;
+};
+constexpr int32_t kPlanMaxRequests = 16384;
+
+// Validated arguments of one attention of packed requests over packed rows.
+struct PromptParams {
+    const void* q;             // bf16 [num_tokens, num_heads, 512]
+    int32_t num_heads;
+    int64_t num_tokens;        // num_tokens * num_heads < 2^31 - 2^16
+    const void* kv;            // bf16 [num_rows, 512], rows at kv_stride elements
+    int64_t kv_stride;
+    int64_t num_rows;
+    const int32_t* starts;     // [num_requests + 1] of the queries
+    const int32_t* kv_starts;  // [num_requests + 1] of the rows
+    int32_t num_requests;      // 1 .. kPlanMaxRequests
+    int32_t causal;
+    float sm_scale;
+    void* out;                 // bf16 [num_tokens, num_heads, 512]
+    float* lse;                // fp32 [num_tokens, num_heads]
+    void* workspace;
+    int32_t* err;              // nullable
+    int32_t pdl;
+};
+
+// Validated arguments of one decode attention behind a shared prefix: `own` has the queries,
+// the cache, each query's own list and the outputs.
+struct PrefixParams {
+    AttentionParams own;
+    const int32_t* prefix;     // [prefix_length]
+    int64_t prefix_length;
+};
+
 // Row geometry of the five cache formats ("record" = bytes a token occupies):
 //   272  MXFP4 record: 256 B e2m1 data row + 16 B scale row;
 //   528  V4.1 MXFP8 record: 512 B e4m3 data row + 16 B scale row;
@@ -238,6 +303,16 @@ cudaError_t attention_workspace(int32_t num_heads, int64_t num_queries, int64_t 
 constexpr int32_t kAttentionMaxHeads = 128;
 // The records each row keeps by weight, and the slots it frees.
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);
+// Pages, slots and positions of a step; the slots of what requests hold.
+cudaError_t launch_allocate(const AllocateParams& p, cudaStream_t stream);
+cudaError_t launch_slots(const SlotsParams& p, cudaStream_t stream);
+// Attention of packed prompts, decode attention behind a shared prefix, and the bytes of
+// workspace that they need on the current device.
+cudaError_t launch_prompt_attention(const PromptParams& p, cudaStream_t stream);
+cudaError_t prompt_workspace(int32_t num_heads, int64_t num_tokens, int64_t* bytes);
+cudaError_t launch_prefix_attention(const PrefixParams& p, cudaStream_t stream);
+cudaError_t prefix_workspace(int32_t num_heads, int64_t num_queries, int64_t prefix_length,
+                             int64_t topk, int64_t* bytes);
 cudaError_t launch_gather_v41(const GatherParams& p, cudaStream_t stream);
 cudaError_t launch_gather_v4(const GatherParams& p, cudaStream_t stream);
 cudaError_t launch_gather_mxfp4(const GatherParams& p, cudaStream_t stream);

@@ -16,7 +16,12 @@
  *   gkr_sparse_attention: the whole of sparse decode attention over 4-bit (MXFP4)
  *                  records: logits, softmax, value product, and on request the attention
  *                  each record received;
- *   gkr_kv_evict:  the records a budget keeps by that attention, and the slots it frees.
+ *   gkr_kv_evict:  the records a budget keeps by that attention, and the slots it frees;
+ *   gkr_kv_allocate, gkr_kv_slots: the pages, slots and positions of a batch's new tokens, and
+ *                  the slots of what its requests hold, from their lengths;
+ *   gkr_prompt_attention: causal attention of packed prompts over their latent rows;
+ *   gkr_prefix_attention: decode attention of a batch over the 4-bit records of a prefix that
+ *                  all queries share and of each query's own list.
  *
  * Operations follow these passages (page title, section):
  *   "PR #56893 [DSv4.1] Store the whole KV in MXFP8 (FlashMLA V4.1 record)",
@@ -425,6 +430,130 @@ GKR_API gkr_status gkr_kv_evict(const int32_t *indices, int64_t index_stride,
                                 const gkr_launch_opts *opts, cudaStream_t stream);
 
 /*
+ * kv_allocate: the pages, slots and positions of the tokens that a batch's requests get (an
+ * extension of the library; the slot_mapping and positions that gkr_kv_insert takes).  With
+ * bs = block_size and W = table_width, request b holds past[b] tokens and gets added[b]:
+ *   held = min(ceil(past[b] / bs), W), end = min(ceil((past[b] + added[b]) / bs), W);
+ *   its columns held .. end - 1 of the block table take the next end - held pages of the free
+ *   list, request after request, each in the list's order;
+ *   starts[b] = the sum of added over the requests before b; row starts[b] + i is its token i:
+ *   positions = past[b] + i, slot_mapping = page * bs + position % bs, page the table's entry
+ *   of column position / bs.
+ * starts[num_requests] is the number of tokens, and the rows behind it get slot -1 (which
+ * inserts skip) and position 0.  *taken: pages taken from the list (the caller moves on by as
+ * many).  A token without a page (its table entry is negative or past the table's width, or
+ * the list was too short: the columns without a page are left as they are) gets slot -1,
+ * as do those that num_tokens has no row for; GKR_ERR_SLOT.  A negative length counts as 0;
+ * GKR_ERR_POS.  The same call repeated gives the same result.
+ *
+ * past, added      device, int32 [num_requests].
+ * num_requests     0 .. 16384.
+ * block_table      device, int32, row b at block_table + b * table_stride, table_width columns
+ *                  (table_stride >= table_width); the new pages' columns are written.
+ * free_pages       device, int32 [num_free], num_free < 2^31.
+ * block_size       >= 1.
+ * num_tokens       rows of slot_mapping and positions, 0 .. 2^31 - 1.
+ * slot_mapping, positions   device, int64 [num_tokens].
+ * starts           device, int32 [num_requests + 1] (the sums end at 2^31 - 1; GKR_ERR_SLOT).
+ * taken            device, int32 [1].
+ * No output overlaps an input or another output.
+ */
+GKR_API gkr_status gkr_kv_allocate(const int32_t *past, const int32_t *added,
+                                   int32_t num_requests, int32_t *block_table,
+                                   int64_t table_stride, int32_t table_width,
+                                   const int32_t *free_pages, int64_t num_free,
+                                   int32_t block_size, int64_t num_tokens, int64_t *slot_mapping,
+                                   int64_t *positions, int32_t *starts, int32_t *taken,
+                                   int32_t *err_flag, const gkr_launch_opts *opts,
+                                   cudaStream_t stream);
+
+/*
+ * kv_slots: the slots of what requests hold (an extension of the library; the index lists that
+ * gkr_kv_gather and gkr_sparse_attention take).  Request b lists its positions first[b] ..
+ * lengths[b] - 1 (first NULL: from 0), slot = page * block_size + position % block_size.
+ *   starts NULL: indices is [num_requests, width], each row padded with -1;
+ *   else packed: indices is [width], one request after another, then -1, and starts
+ *   [num_requests + 1] says where each begins (num_requests <= 16384).
+ * A position without a page, or whose slot is no int32, gets -1; positions that `width` has no
+ * room for are left out; negative lengths and firsts count as 0; GKR_ERR_INDEX for each.
+ * width 0 .. 2^31 - 1.  The other arguments are gkr_kv_allocate's.
+ */
+GKR_API gkr_status gkr_kv_slots(const int32_t *block_table, int64_t table_stride,
+                                int32_t table_width, const int32_t *lengths,
+                                const int32_t *first, int32_t num_requests, int32_t block_size,
+                                int64_t width, int32_t *indices, int32_t *starts,
+                                int32_t *err_flag, const gkr_launch_opts *opts,
+                                cudaStream_t stream);
+
+/*
+ * prompt_attention: attention of packed requests over packed bf16 latent rows (an extension of
+ * the library; the latent row is key and value of every head, as in gkr_sparse_attention; the
+ * rows are a prompt's own or what gkr_kv_gather returns for any record).  Request b has the n
+ * queries starts[b] .. starts[b + 1] - 1 and the m rows K from kv_starts[b] on.  For its query
+ * i and head h:
+ *   rows = K[0 .. m - n + i] if causal (its last query sees all rows; none where that is
+ *   negative), else K[0 .. m - 1];
+ *   s[k] = sm_scale * q[i, h] . K[k],  lse = log(sum exp(s[k])),
+ *   out = bf16(sum exp(s[k] - lse) K[k]).
+ * A query without rows gets zeros and lse -inf.  Queries of no request are left as they are.
+ * Arithmetic as for gkr_sparse_attention; a row that a query does not see (another request's, a
+ * later one, one behind the last) has no influence on it, whatever it holds.  A row with an
+ * infinity or a NaN makes the queries that see it NaN (where their logit for it is -inf, NaN or
+ * what they would be without it).
+ *
+ * q              device, bf16 [num_tokens, num_heads, 512], 16-byte aligned.
+ * num_heads      1 .. 4096; num_tokens >= 0, num_heads * num_tokens <= 2147418112.
+ * kv             device, bf16 [num_rows, 512], 16-byte aligned, row r at kv + r * kv_stride
+ *                elements (kv_stride >= 512, a multiple of 8); num_rows 0 .. 2147418112.
+ * starts, kv_starts   device, int32 [num_requests + 1], not descending, within the tensors
+ *                (values out of range are taken as the nearest in range; GKR_ERR_INDEX).
+ * num_requests   0 .. 16384 (0, like no tokens, enqueues nothing).
+ * causal         0 or 1.
+ * out            device, bf16 [num_tokens, num_heads, 512], 16-byte aligned, not overlapping q
+ *                or kv (GKR_EINVAL).
+ * lse            device, fp32 [num_tokens, num_heads].
+ * workspace      device, at least gkr_prompt_attention_workspace() bytes, 16-byte aligned; as
+ *                for gkr_sparse_attention.
+ * err_flag       device int32 or NULL; GKR_ERR_INDEX / GKR_ERR_TIMEOUT.
+ */
+GKR_API gkr_status gkr_prompt_attention(const void *q, int32_t num_heads, int64_t num_tokens,
+                                        const void *kv, int64_t kv_stride, int64_t num_rows,
+                                        const int32_t *starts, const int32_t *kv_starts,
+                                        int32_t num_requests, int32_t causal, float sm_scale,
+                                        void *out, float *lse, void *workspace,
+                                        int64_t workspace_bytes, int32_t *err_flag,
+                                        const gkr_launch_opts *opts, cudaStream_t stream);
+
+/* Workspace of a gkr_prompt_attention call of these sizes on the current device. */
+GKR_API gkr_status gkr_prompt_attention_workspace(int32_t num_heads, int64_t num_tokens,
+                                                  int64_t *bytes);
+
+/*
+ * prefix_attention: gkr_sparse_attention for queries that share a prefix (an extension of the
+ * library): query i attends to the records prefix[0 .. prefix_length - 1], the same for every
+ * query, and to those that its row of indices lists, in one softmax.  The prefix's records are
+ * read and dequantised for all queries at once.  -1 and invalid indices as there, in
+ * both lists; either may be empty.
+ *
+ * prefix         device, int32 [prefix_length]; prefix_length 0 .. 2^24.
+ * out            not overlapping q (GKR_EINVAL) or any other input.
+ * workspace      device, at least gkr_prefix_attention_workspace() bytes, 16-byte aligned.
+ * The other arguments are gkr_sparse_attention's.
+ */
+GKR_API gkr_status gkr_prefix_attention(const void *q, int32_t num_heads, const void *k_cache,
+                                        const gkr_cache_desc *cache, const int32_t *prefix,
+                                        int64_t prefix_length, const int32_t *indices,
+                                        int64_t index_stride, int64_t num_queries, int64_t topk,
+                                        float sm_scale, void *out, float *lse, void *workspace,
+                                        int64_t workspace_bytes, int32_t *err_flag,
+                                        const gkr_launch_opts *opts, cudaStream_t stream);
+
+/* Workspace of a gkr_prefix_attention call of these sizes on the current device. */
+GKR_API gkr_status gkr_prefix_attention_workspace(int32_t num_heads, int64_t num_queries,
+                                                  int64_t prefix_length, int64_t topk,
+                                                  int64_t *bytes);
+
+/*
  * Process-wide defaults of the launch options (gkr_launch_opts fields left at -1 take
  * them).  Setting them while another thread launches is safe (atomics) but changes that
  * thread's later calls too; per-call options do not.
@@ -485,7 +614,8 @@ GKR_API int32_t gkr_last_cuda_error(void);
  * takes a gkr_launch_opts pointer before the stream; gkr_qnorm_rope_kv_insert.
  * 3.1.0: gkr_sparse_logits.  3.2.0: gkr_qnorm_rope_kv_insert takes q_scale (an e4m3
  * query output).  Record 272, gkr_sparse_attention and gkr_kv_evict were added to 3.2.0
- * without a change to any call it had; their symbols tell a library that has them. */
+ * without a change to any call it had, and so were gkr_kv_allocate, gkr_kv_slots,
+ * gkr_prompt_attention and gkr_prefix_attention; their symbols tell a library that has them. */
 GKR_API int32_t gkr_version(void);
 
 #ifdef __cplusplus
