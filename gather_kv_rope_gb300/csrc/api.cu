@@ -33,6 +33,13 @@ struct OccEntry {
 std::mutex g_occ_mutex;
 std::vector<OccEntry> g_occ;
 
+struct PairEntry {
+    int device;
+    const void* func;
+    int32_t pairs;
+};
+std::vector<PairEntry> g_pairs;
+
 struct RecordRows {
     int32_t data, scale, align;
 };
@@ -157,6 +164,39 @@ cudaError_t resident_warps(const void* func, int threads, size_t smem, int64_t* 
     const int64_t w = static_cast<int64_t>(sms) * per_sm * (threads / 32);
     g_occ.push_back({dev, func, smem, threads, w});
     *warps = w;
+    return cudaSuccess;
+}
+
+cudaError_t resident_pairs(const void* func, int threads, size_t smem, int32_t* pairs) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(g_occ_mutex);
+    for (const PairEntry& o : g_pairs) {
+        if (o.device == dev && o.func == func) {
+            *pairs = o.pairs;
+            return cudaSuccess;
+        }
+    }
+    e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    e = cudaOccupancyMaxActiveClusters(&n, func, &cfg);
+    if (e != cudaSuccess) return e;
+    if (n < 1) return cudaErrorInvalidConfiguration;
+    g_pairs.push_back({dev, func, n});
+    *pairs = n;
     return cudaSuccess;
 }
 

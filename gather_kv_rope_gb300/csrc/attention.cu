@@ -43,9 +43,8 @@
 // (78.5), with a fourth stage in the place of the next query's blocks 73, but 4 to 7 % slower for
 // short lists; 32 rows of each CTA for up to 64 heads, every second softmax warp idle: as fast.
 #include <cmath>
-#include <mutex>
-#include <vector>
 
+#include "attend.cuh"
 #include "device.cuh"
 #include "launch.h"
 #include "tensor.cuh"
@@ -53,10 +52,6 @@
 namespace gkr {
 
 namespace {
-
-constexpr int32_t kErrIndex = 4;
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
 
 constexpr int kPairHeads = 64;           // heads (rows) of each CTA of the pair
 constexpr int kChunkKeys = 64;           // records per chunk
@@ -86,18 +81,6 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kSCol = 256;          // logits: two buffers of 32 columns; output at 0
 constexpr uint32_t kQCol = 320;          // the query's first 384 dims, two to a column
 static_assert(kQCol + kQTmemBlocks * 32 <= kTmemCols, "tensor memory");
-// A new maximum replaces the running one only when it is this much larger (in powers of two), for
-// any of the 32 heads of a warp: rescaling the accumulator takes longer than a chunk's softmax
-// (1400 cycles), and at 8, with the logits of heavy-tailed latents, every second chunk had some
-// head that rose.  The reference does not touch the precision of floating-point terms, only
-// their range: probabilities stay below 2^(kLag + kLift) = 2^48, and an output of fewer than
-// 2^24 records below 2^55 each cannot overflow.
-constexpr float kLag = 32.0f;
-// Probabilities are taken as exp2(s - m + kLift): bf16 ends at 2^-133, and without the lift terms
-// that the output still shows (it ends there too) would be rounded away before they are
-// multiplied by a record's values and summed.
-constexpr float kLift = 16.0f;
-
 // kind::f16 over the pair, M = 128, fp32 accumulator, bf16 A and B (fields as in logits.cu):
 // logits N = 64, both K-major; output N = 256, B MN-major (bit 16).
 constexpr uint32_t idesc(int n, bool b_mn) {
@@ -164,51 +147,6 @@ struct alignas(8) PairBarriers {
 constexpr size_t kAttendSmem = 1024 + kOffBars + sizeof(PairBarriers);
 static_assert(kAttendSmem <= 227 * 1024, "a CTA's shared memory");
 
-// The lse of a query, or of a piece, whose results are not written because a wait gave up
-// (kErrTimeout): a NaN that no instruction produces, so that the kernels that follow can tell it
-// from the NaN of a record.
-constexpr uint32_t kUnwritten = 0x7FC0B0B0u;
-__device__ __forceinline__ bool is_unwritten(float lse) { return __float_as_uint(lse) == kUnwritten; }
-
-// 2^x within 2^-22; results below 2^-126 kept (factors that rescale what may be large) ...
-__device__ __forceinline__ float exp2_approx(float x) {
-    float y;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// ... or, in one instruction, flushed to zero (a probability: kLift puts those below 2^-142).
-__device__ __forceinline__ float exp2_flush(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
-                 "r"(v.w)
-                 : "memory");
-}
-
-__device__ __forceinline__ uint4 lds16_at(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
-    return v;
-}
-
-// A stage of a ring and the parity of its current round.
-template <int N>
-struct Ring {
-    int s = 0;
-    uint32_t parity = 0;
-    __device__ __forceinline__ void next() {
-        if (++s == N) {
-            s = 0;
-            parity ^= 1u;
-        }
-    }
-};
-
 // A unit's 32 dims (16 bytes of codes, a scale byte) as bf16 into four 16-byte pieces of a
 // swizzled row: piece j of the unit lies at the first one's address with j in bits 4 and 5
 // flipped.
@@ -232,19 +170,6 @@ __device__ __forceinline__ void store_unit(uint32_t codes, uint32_t scale, uint3
 // issues the products.
 constexpr int kPollThread = 32;   // of the softmax warps
 constexpr int kOwnBar = 1, kRefillBar = 2, kSoftmaxBar = 3, kHeadsBar = 4;   // and 5
-__device__ __forceinline__ void group_sync(int bar, int threads) {
-    asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(threads) : "memory");
-}
-
-// The same, and whether any of the threads says so.
-__device__ __forceinline__ bool group_any(int bar, int threads, bool mine) {
-    uint32_t any;
-    asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %1, 0;\n barrier.red.or.pred p, %2, %3, p;\n"
-                 " selp.u32 %0, 1, 0, p;\n}" : "=r"(any)
-                 : "r"(mine ? 1u : 0u), "r"(bar), "r"(threads) : "memory");
-    return any != 0u;
-}
-
 // The wait of a thread that polls for a group of dequantising warps.  Should it give up, it keeps the
 // group at its named barrier until the warp that issues the products has left (`drained`; it
 // misses the group's arrivals and gives up in turn): only then may stages be overwritten and
@@ -258,18 +183,6 @@ __device__ __noinline__ bool wait_slow_or_hold(uint32_t bar, uint32_t parity, ui
 }
 __device__ __forceinline__ void wait_or_hold(uint32_t bar, uint32_t parity, uint32_t drained, bool& ok) {
     if (ok && !mbar_try_wait(bar, parity)) ok = wait_slow_or_hold(bar, parity, drained);
-}
-
-// Eight fp32 values as bf16, and scaled.
-__device__ __forceinline__ uint4 pack8(const float* v) {
-    return make_uint4(pack_bf16x2_rn(v[0], v[1]), pack_bf16x2_rn(v[2], v[3]),
-                      pack_bf16x2_rn(v[4], v[5]), pack_bf16x2_rn(v[6], v[7]));
-}
-__device__ __forceinline__ uint4 pack8(const float* v, float f) {
-    return make_uint4(pack_bf16x2_rn(__fmul_rn(v[0], f), __fmul_rn(v[1], f)),
-                      pack_bf16x2_rn(__fmul_rn(v[2], f), __fmul_rn(v[3], f)),
-                      pack_bf16x2_rn(__fmul_rn(v[4], f), __fmul_rn(v[5], f)),
-                      pack_bf16x2_rn(__fmul_rn(v[6], f), __fmul_rn(v[7], f)));
 }
 
 // Row `row` of a query tile (blocks of 64 rows of 64 dims, 128-byte swizzle) into this thread's
@@ -706,6 +619,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 tc_fence_after_sync();
                 const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
                 const bool whole = seg == 0 && ci + 1 == cut.per_query;
+                const bool narrow = whole && p.wide == 0;
                 const float lse2 =
                     total == 0.0f ? -INFINITY : __fadd_rn(__fsub_rn(m, kLift), log2f(total));
                 // A piece that does not begin its query is its pair's first: slot 0.  Rows leave
@@ -716,7 +630,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 const int64_t slot = 2 * pair + (seg == 0 ? 1 : 0);
                 float* const pieces = static_cast<float*>(p.workspace);
                 const int64_t at = (whole ? qi : slot) * p.num_heads;
-                const int64_t dst_row = whole ? 1024 : 2048;
+                const int64_t dst_row = narrow ? 1024 : 2048;
                 uint8_t* const dst = (whole ? static_cast<uint8_t*>(p.out)
                                             : reinterpret_cast<uint8_t*>(pieces)) +
                                      at * dst_row + (2 * half + part) * (dst_row >> 2);
@@ -724,12 +638,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                                     (warp >> 1 & 1) * (kPBytes / 4);
                 const uint32_t mine = st + lane * 64 + (((lane >> 1) & 3) << 4);
                 const int head0 = static_cast<int>(rank) * kPairHeads + (warp & 1) * 32;
-                const int step = whole ? 32 : 16;
+                const int step = narrow ? 32 : 16;
 #pragma unroll 1
                 for (int c = 0; c < 128; c += step) {           // 64 bytes of each row
                     float t[16];
                     tmem_ld16(tmem + lanes + 128 * part + c, t);
-                    if (whole) {
+                    if (narrow) {
                         sts16(mine, pack8(t, inv));
                         sts16(mine ^ 16u, pack8(t + 8, inv));
                         tmem_ld16(tmem + lanes + 128 * part + c + 16, t);
@@ -745,7 +659,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                                              __float_as_uint(__fmul_rn(t[4 * i + 3], inv))));
                     }
                     __syncwarp();
-                    uint8_t* const to = dst + c * (whole ? 2 : 4) + (lane & 3) * 16;
+                    uint8_t* const to = dst + c * (narrow ? 2 : 4) + (lane & 3) * 16;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int r = 8 * i + (lane >> 2);
@@ -756,7 +670,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 }
                 if (half == 0 && part == 0 && head < p.num_heads) {
                     float* const to = whole ? p.lse : pieces + 2 * static_cast<int64_t>(cut.pairs) * p.num_heads * 512;
-                    to[at + head] = !ok ? __uint_as_float(kUnwritten) : whole ? __fmul_rn(lse2, kLn2) : lse2;
+                    to[at + head] = !ok ? __uint_as_float(kUnwritten) : narrow ? __fmul_rn(lse2, kLn2) : lse2;
                 }
                 tc_fence_before_sync();
                 m = -INFINITY;
@@ -879,6 +793,7 @@ __global__ void __launch_bounds__(128 * kGroups)
         }
     }
     const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+    const float lse2 = sum == 0.0f ? -INFINITY : __fadd_rn(m, log2f(sum));
     const uint2 v = make_uint2(pack_bf16x2_rn(__fmul_rn(acc.x, inv), __fmul_rn(acc.y, inv)),
                                pack_bf16x2_rn(__fmul_rn(acc.z, inv), __fmul_rn(acc.w, inv)));
     const int64_t at = static_cast<int64_t>(cuts.query[c]) * p.num_heads + head;
@@ -886,9 +801,14 @@ __global__ void __launch_bounds__(128 * kGroups)
         if (threadIdx.x == 0) p.lse[at] = __uint_as_float(kUnwritten);
         return;
     }
+    if (p.wide != 0) {
+        *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * 512 + 4 * d) =
+            make_float4(__fmul_rn(acc.x, inv), __fmul_rn(acc.y, inv), __fmul_rn(acc.z, inv), __fmul_rn(acc.w, inv));
+        if (threadIdx.x == 0) p.lse[at] = lse2;
+        return;
+    }
     st8(static_cast<uint8_t*>(p.out) + at * 1024 + 8 * d, v);
-    if (threadIdx.x == 0)
-        p.lse[at] = sum == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(m, log2f(sum)), kLn2);
+    if (threadIdx.x == 0) p.lse[at] = __fmul_rn(lse2, kLn2);
 }
 
 // ---------------------------------------------------------------- weights
@@ -1233,51 +1153,9 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
     if (warp == kWMmaWarp) tmem_dealloc(tmem, 256);
 }
 
-// The pairs of CTAs that the current device holds at once (cached per device).
-struct PairCount {
-    int device;
-    int32_t pairs;
-};
-std::mutex g_pairs_mutex;
-std::vector<PairCount> g_pairs;
-
-cudaError_t resident_pairs(int32_t* pairs) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    std::lock_guard<std::mutex> lock(g_pairs_mutex);
-    for (const PairCount& c : g_pairs) {
-        if (c.device == dev) {
-            *pairs = c.pairs;
-            return cudaSuccess;
-        }
-    }
-    e = cudaFuncSetAttribute(attend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(kAttendSmem));
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(2);
-    cfg.blockDim = dim3(kAttendThreads);
-    cfg.dynamicSmemBytes = kAttendSmem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, attend_kernel, &cfg);
-    if (e != cudaSuccess) return e;
-    if (n < 1) return cudaErrorInvalidConfiguration;
-    g_pairs.push_back({dev, n});
-    *pairs = n;
-    return cudaSuccess;
-}
-
 cudaError_t make_cut(int64_t num_queries, int64_t topk, int32_t num_heads, Cut* cut) {
     int32_t pairs = 0;
-    const cudaError_t e = resident_pairs(&pairs);
+    const cudaError_t e = resident_pairs(reinterpret_cast<const void*>(attend_kernel), kAttendThreads, kAttendSmem, &pairs);
     if (e != cudaSuccess) return e;
     cut->per_query = topk == 0 ? 1 : (topk + kChunkKeys - 1) / kChunkKeys;
     cut->total = num_queries * cut->per_query;

@@ -93,6 +93,7 @@ struct AttentionParams {
     void* workspace;           // attention_workspace() bytes
     int32_t* err;              // nullable
     int32_t pdl;
+    int32_t wide = 0;          // 1: out has fp32 rows and lse is in powers of two (no weights)
 };
 
 // Validated arguments of one eviction launch.
@@ -203,6 +204,10 @@ struct Fmt {
 // on a device also raises its dynamic shared-memory limit when it needs more than
 // the default 48 KiB.
 cudaError_t resident_warps(const void* func, int threads, size_t smem, int64_t* warps);
+
+// The pairs of CTAs (clusters of two, blocks of `threads` threads and `smem` dynamic shared bytes) of
+// `func` that the current device holds at once; cached as above.
+cudaError_t resident_pairs(const void* func, int threads, size_t smem, int32_t* pairs);
 
 // Launch `kernel`, with the programmatic-dependent-launch attribute when `pdl` is set.
 template <typename... KArgs, typename... Args>

@@ -1,145 +1,1075 @@
-// Attention of packed prompts over packed latent rows, and decode attention behind a shared
-// prefix.  First form: a warp for each query head, one row at a time.
+// Attention of packed requests over packed bf16 latent rows, and decode attention of a batch
+// behind a shared prefix of MXFP4 records.
+//
+// Operation (the latent row is key and value of every head, as in the sparse attention): a
+// query head q that sees the rows K[0 .. see - 1] of its request gets
+//   s[k] = sm_scale * q . K[k],  m = max s,  l = sum exp(s - m),
+//   out = sum exp(s[k] - m) K[k] / l,  lse = m + log l;   see = 0: zeros and -inf.
+// Causal: of a request's n queries and m rows, query i sees m - n + i + 1.
+//
+// A request's query heads are rows of one matrix, query after query, and a tile is 128 of them,
+// whatever the number of heads: 128 heads of one query or 16 of eight.  A pair of CTAs
+// (cta_group::2, M = 128) multiplies a tile by chunks of 128 rows of K, both products, 2 x 128 x
+// 128 x 512 multiply-adds: 2048 cycles of the two SMs' tensor cores.  They are the floor of
+// every larger call, so everything else runs beside them:
+//   * The accumulator, 128 x 512 fp32, takes half of the two SMs' tensor memory, a chunk's logits
+//     an eighth (64 columns), three quarters of the query tile the rest (192 columns).
+//   * Rows come by TMA into a ring of three stages of 64 KB: a CTA's own 64 rows of the chunk for
+//     q . K; once that is done, the half of the dims that the other CTA multiplies is replaced
+//     by the other 64 rows' half of this CTA's dims for p . K (a product of the pair takes half
+//     of its columns from each CTA, at the same address in both).  The next query tile passes
+//     through the ring like a chunk.
+//   * q . K of the next chunk is issued before p . K of this one, so that the softmax of a chunk
+//     has the time of two products.  The probabilities have one buffer, and so have the logits.
+//   * Work: a unit for each tile (its loads and its epilogue) and one for each of its chunks, all
+//     tiles in a row, cut evenly over the pairs.  Each CTA finds its cut from the requests'
+//     lengths by itself (closed sums, no plan to launch).  The pieces of a tile that is cut go
+//     to the workspace (fp32 rows and their log-sum-exp) and a second kernel joins them.
+// What a row does not see: columns past its last row are -inf before the softmax.  Their
+// probabilities are 0, but 0 times an infinity or NaN is NaN, so in a chunk with such
+// columns, values that are not finite are cleared before p . K (a row that does see them has NaN
+// from its logit).
 #include <cmath>
+#include <mutex>
+#include <vector>
 
-#include "decode.cuh"
+#include "attend.cuh"
 #include "device.cuh"
 #include "launch.h"
+#include "tensor.cuh"
 
 namespace gkr {
 
 namespace {
 
-constexpr int32_t kErrIndex = 4;
-constexpr int kRowThreads = 256;
+constexpr int kTileRows = 128;           // query heads of a tile, half of them in each CTA
+constexpr int kCtaRows = 64;
+constexpr int kChunk = 128;              // rows of K per chunk, half of them of each CTA
+constexpr int kCtaKeys = 64;
+constexpr int kStages = 3;
+constexpr int kSoftmaxWarps = 8;         // warp w: tensor-memory lanes 32 (w % 4) .., half w / 4 of
+                                         // their columns
+constexpr int kMmaWarp = kSoftmaxWarps;  // products (rank 0); rank 1: tells rank 0 what has landed
+constexpr int kLoadWarp = kMmaWarp + 1;  // query tiles and rows for q . K
+constexpr int kRefillWarp = kLoadWarp + 1;   // rows for p . K
+constexpr int kTileThreads = (kRefillWarp + 1) * 32;
+constexpr uint32_t kBlockBytes = kCtaKeys * kRowBytes;      // 64 dims of 64 rows
+constexpr uint32_t kHalfBytes = 4 * kBlockBytes;            // 256 dims
+constexpr uint32_t kStageBytes = 2 * kHalfBytes;
+constexpr int kQTmemBlocks = 6;          // blocks of 64 dims of the query tile in tensor memory
+constexpr uint32_t kQBytes = (8 - kQTmemBlocks) * kBlockBytes;   // and in shared memory
+constexpr uint32_t kPBytes = 2 * kBlockBytes;               // probabilities of a chunk, bf16
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kSCol = 256;          // logits, 64 columns; output at 0
+constexpr uint32_t kQCol = 320;          // the query's first 384 dims, two to a column
+static_assert(kQCol + kQTmemBlocks * 32 == kTmemCols, "tensor memory");
 
-__device__ __forceinline__ float warp_add(float v) {
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kFull, v, d));
-    return v;
+// kind::f16 over the pair, M = 128, fp32 accumulator, bf16 A and B: logits N = 128, both K-major;
+// output N = 256, B MN-major (bit 16).
+constexpr uint32_t idesc(int n, bool b_mn) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) |
+           (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(128 >> 4) << 24);
 }
+constexpr uint32_t kIdescS = idesc(kChunk, false);
+constexpr uint32_t kIdescO = idesc(256, true);
 
-// A query head's softmax and sum over the rows it is given one after another; lane L has
-// dims [8L, 8L + 8) and [256 + 8L, 256 + 8L + 8).
-struct RowState {
-    float q[16], acc[16], m, l;
-    __device__ void init(const uint8_t* qrow, int lane, float sm_scale) {
-        unpack_bf16x8(*reinterpret_cast<const uint4*>(qrow + 16 * lane), q);
-        unpack_bf16x8(*reinterpret_cast<const uint4*>(qrow + 512 + 16 * lane), q + 8);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = 0.0f;
-        m = -INFINITY;
-        l = 0.0f;
-        scale = sm_scale;
-    }
-    __device__ void add(const uint4 a, const uint4 b) {
-        float k[16], s = 0.0f;
-        unpack_bf16x8(a, k);
-        unpack_bf16x8(b, k + 8);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s = __fmaf_rn(q[i], k[i], s);
-        s = __fmul_rn(warp_add(s), scale);
-        const float top = fmaxf(m, s);
-        const float ref = top == -INFINITY ? 0.0f : top;
-        const float fix = expf(__fsub_rn(m, ref)), p = expf(__fsub_rn(s, ref));
-        m = top;
-        l = __fmaf_rn(l, fix, p);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] = __fmaf_rn(acc[i], fix, __fmul_rn(p, k[i]));
-    }
-    __device__ void write(uint8_t* out, float* lse, int lane) {
-        const float inv = l == 0.0f ? 0.0f : __fdiv_rn(1.0f, l);
-        uint32_t w[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            w[i] = pack_bf16x2_rn(__fmul_rn(acc[2 * i], inv), __fmul_rn(acc[2 * i + 1], inv));
-        st16(out + 16 * lane, make_uint4(w[0], w[1], w[2], w[3]));
-        st16(out + 512 + 16 * lane, make_uint4(w[4], w[5], w[6], w[7]));
-        if (lane == 0) *lse = l == 0.0f ? -INFINITY : __fadd_rn(m, logf(l));
-    }
-    float scale;
+// Shared memory of a CTA, from a 1024-byte boundary.
+constexpr uint32_t kOffP = kQBytes;
+constexpr uint32_t kOffStages = kOffP + kPBytes;
+constexpr uint32_t kOffHeads = kOffStages + kStages * kStageBytes;   // [4][64] maxima, then sums, of a row
+constexpr uint32_t kOffBars = kOffHeads + 256 * 4;
+
+struct alignas(8) TileBarriers {
+    // in the leader: arrivals of both CTAs
+    uint64_t peer_full[kStages];   // rank 1: its rows of the stage have landed, for q . K
+    uint64_t peer_refilled[kStages];   // ... and for p . K
+    uint64_t s_free;               // softmax: the logits are read
+    uint64_t p_full;               // softmax: the probabilities are written
+    uint64_t q_full;               // softmax: a query tile is in place
+    // in each CTA
+    uint64_t full[kStages];        // a query tile or rows for q . K have landed
+    uint64_t refilled[kStages];    // rows for p . K have
+    uint64_t empty[kStages];       // p . K of the chunk is complete; the query tile is moved
+    uint64_t s_full[2];            // the logits of a chunk are complete (even, odd chunks)
+    uint64_t drained;              // every product that was issued is complete
+    // the pair's first unit: request, tile of it, unit of the tile; how many there are
+    int64_t units, at;
+    int64_t sums[kTileThreads / 32];
+    int32_t request, tile, unit;
+    uint32_t tmem_base;
+    volatile int32_t timed_out;
+};
+constexpr size_t kTileSmem = 1024 + kOffBars + sizeof(TileBarriers);
+static_assert(kTileSmem <= 227 * 1024, "a CTA's shared memory");
+
+// Arguments of the tile kernel.
+struct TileArgs {
+    int32_t num_heads;
+    int64_t num_tokens, num_rows;
+    const int32_t* starts;       // null: one request, all queries and rows
+    const int32_t* kv_starts;
+    int32_t num_requests;
+    int32_t causal;
+    const int32_t* live;         // per row, < 0 or >= num_slots: no row; or null (one request only)
+    int32_t num_slots;
+    float sm_scale;
+    void* out;                   // bf16 rows, or fp32 rows if `wide`
+    float* lse;                  // natural, or in powers of two if `wide`
+    int32_t wide;
+    float* pieces;               // [pairs][2][slot_rows][512]
+    float* piece_lse;            // [pairs][2][slot_rows]
+    int4* meta;                  // [pairs] see kTailOpen
+    int32_t slot_rows;           // rows of a piece at most
+    int32_t* err;
+};
+// What a pair left in the workspace: slot 1, the beginning of a tile that the next pairs go on
+// with (x: its first row, y: its rows); slot 0, a tile begun before, which it ended or not.
+constexpr int kTailOpen = 1, kHeadThere = 2, kHeadEnds = 4;
+
+// A unit less than this many for each pair is not worth another piece to join.
+constexpr int64_t kUnitsAPair = 3;
+
+// A request's rows and its tiles' work.
+struct Request {
+    int64_t row0;        // first row of q
+    int64_t k0;          // first row of K
+    int32_t rows, keys, tiles;
+    int64_t past;        // keys - queries
 };
 
-__global__ void __launch_bounds__(kRowThreads) prompt_kernel(const PromptParams p) {
+__device__ __forceinline__ Request request_at(const TileArgs& p, int b, bool& bad) {
+    int64_t q0 = 0, q1 = p.num_tokens, k0 = 0, k1 = p.num_rows;
+    if (p.starts != nullptr) {
+        const int64_t a = p.starts[b], z = p.starts[b + 1], c = p.kv_starts[b], e = p.kv_starts[b + 1];
+        q0 = min(max(a, INT64_C(0)), p.num_tokens);
+        q1 = min(max(z, q0), p.num_tokens);
+        k0 = min(max(c, INT64_C(0)), p.num_rows);
+        k1 = min(max(e, k0), p.num_rows);
+        bad |= a != q0 || z != q1 || c != k0 || e != k1;
+    }
+    Request r;
+    r.row0 = q0 * p.num_heads;
+    r.k0 = k0;
+    r.rows = static_cast<int32_t>((q1 - q0) * p.num_heads);
+    r.keys = static_cast<int32_t>(k1 - k0);
+    r.tiles = (r.rows + kTileRows - 1) / kTileRows;
+    r.past = (k1 - k0) - (q1 - q0);
+    return r;
+}
+
+// How many rows row `row` of a request sees.
+__device__ __forceinline__ int32_t sees(const TileArgs& p, const Request& r, int32_t row) {
+    if (p.causal == 0) return r.keys;
+    const int64_t see = r.past + static_cast<uint32_t>(row) / static_cast<uint32_t>(p.num_heads) + 1;
+    return static_cast<int32_t>(min(max(see, INT64_C(0)), static_cast<int64_t>(r.keys)));
+}
+// Chunks of a tile: what its last row sees.
+__device__ __forceinline__ int32_t chunks_of(const TileArgs& p, const Request& r, int32_t tile) {
+    const int32_t see = tile == r.tiles - 1 ? r.keys : sees(p, r, tile * kTileRows + kTileRows - 1);
+    return static_cast<int32_t>((static_cast<int64_t>(see) + kChunk - 1) / kChunk);
+}
+// Units of the request's first `tile` tiles (tile < tiles).  Causal: tile x, but for the last,
+// has max(0, ceil((past + floor((128 x + 127) / H) + 1) / 128)) chunks, which is
+// max(0, floor((x + c) / H)) with c = floor((127 + (past + 128) H) / 128), as a tile and a chunk
+// are both 128; and the sum of max(0, floor(y / H)) over y < z is H a (a - 1) / 2 + a (z - a H), a =
+// floor(z / H).
+__device__ __forceinline__ int64_t floors_below(int64_t z, int64_t h) {
+    if (z <= 0) return 0;
+    const int64_t a = z / h;
+    return h * (a * (a - 1) / 2) + a * (z - a * h);
+}
+__device__ __forceinline__ int64_t units_before(const TileArgs& p, const Request& r, int64_t tile) {
+    if (p.causal == 0) return tile * (1 + (static_cast<int64_t>(r.keys) + kChunk - 1) / kChunk);
+    const int64_t h = p.num_heads;
+    const int64_t c = (kTileRows - 1 + (r.past + kChunk) * h) >> 7;
+    return tile + floors_below(tile + c, h) - floors_below(c, h);
+}
+__device__ __forceinline__ int64_t units_of(const TileArgs& p, const Request& r) {
+    if (r.tiles == 0) return 0;
+    return units_before(p, r, r.tiles - 1) + 1 + (static_cast<int64_t>(r.keys) + kChunk - 1) / kChunk;
+}
+
+// A pair's part of one tile.
+struct Segment {
+    Request r;
+    int32_t row0;            // of the request
+    int32_t rows;            // of the tile
+    int32_t chunks;          // of the tile
+    int32_t begin, end;      // of them, this pair's
+};
+
+// A pair's segments, one after another; every role walks through them for itself.
+struct Walk {
+    Request r;
+    int64_t left;
+    int32_t b, tile, unit;
+    __device__ void init(const TileArgs& p, const TileBarriers* bars) {
+        b = bars->request;
+        tile = bars->tile;
+        unit = bars->unit;
+        left = bars->units;
+        bool bad = false;
+        if (left > 0) r = request_at(p, b, bad);
+    }
+    __device__ bool next(const TileArgs& p, Segment& s) {
+        while (left > 0) {
+            if (tile >= r.tiles) {
+                if (++b >= p.num_requests) return false;
+                bool bad = false;
+                r = request_at(p, b, bad);
+                tile = 0;
+                unit = 0;
+                continue;
+            }
+            s.r = r;
+            s.row0 = tile * kTileRows;
+            s.rows = min(kTileRows, r.rows - s.row0);
+            s.chunks = chunks_of(p, r, tile);
+            const int64_t take = min(left, static_cast<int64_t>(1 + s.chunks - unit));
+            s.begin = max(unit, 1) - 1;
+            s.end = static_cast<int32_t>(unit + take) - 1;
+            left -= take;
+            unit += static_cast<int32_t>(take);
+            if (unit == 1 + s.chunks) {
+                ++tile;
+                unit = 0;
+            }
+            if (s.chunks == 0 || s.end > s.begin) return true;
+        }
+        return false;
+    }
+};
+
+// The pair's first unit and how many it has, into `bars`: all threads sum up the requests' units
+// and find the request; then (after a barrier) a warp finds the tile.
+__device__ __forceinline__ void find_work(const TileArgs& p, TileBarriers* bars, int64_t pair, int64_t pairs) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int run = (p.num_requests + kTileThreads - 1) / kTileThreads;
+    const int first = min(p.num_requests, static_cast<int>(threadIdx.x) * run);
+    const int last = min(p.num_requests, first + run);
+    int64_t mine = 0;
+    bool bad = false;
+    for (int b = first; b < last; ++b) mine += units_of(p, request_at(p, b, bad));
+    if (bad && blockIdx.x == 0) report(p.err, kErrIndex);
+    int64_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(kFull, upto, d);
+        if (lane >= d) upto += o;
+    }
+    if (lane == 31) bars->sums[warp] = upto;
+    __syncthreads();
+    int64_t before = upto - mine, total = 0;
+    for (int w = 0; w < kTileThreads / 32; ++w) {
+        const int64_t s = bars->sums[w];
+        if (w < warp) before += s;
+        total += s;
+    }
+    const int64_t most = (total + kUnitsAPair - 1) / kUnitsAPair;
+    if (most < pairs) pairs = most;
+    const int64_t x0 = pair < pairs ? total * pair / pairs : 0, x1 = pair < pairs ? total * (pair + 1) / pairs : 0;
+    if (threadIdx.x == 0) bars->units = x1 - x0;
+    if (x1 > x0 && x0 >= before && x0 < before + mine) {   // in this thread's run of requests
+        int64_t at = x0 - before;
+        for (int b = first; b < last; ++b) {
+            const int64_t u = units_of(p, request_at(p, b, bad));
+            if (at < u) {
+                bars->request = b;
+                bars->at = at;
+                break;
+            }
+            at -= u;
+        }
+    }
+}
+__device__ __forceinline__ void find_tile(const TileArgs& p, TileBarriers* bars) {
     const int lane = threadIdx.x & 31;
-    pdl_wait_previous();
-    pdl_release_next();
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
-    const int64_t t = row / p.num_heads;
-    if (t >= p.num_tokens) return;
-    for (int b = 0; b < p.num_requests; ++b) {
-        const int64_t q0 = min(max(static_cast<int64_t>(p.starts[b]), INT64_C(0)), p.num_tokens);
-        const int64_t q1 = min(max(static_cast<int64_t>(p.starts[b + 1]), q0), p.num_tokens);
-        const int64_t k0 = min(max(static_cast<int64_t>(p.kv_starts[b]), INT64_C(0)), p.num_rows);
-        const int64_t k1 = min(max(static_cast<int64_t>(p.kv_starts[b + 1]), k0), p.num_rows);
-        if (lane == 0 && row == 0 &&
-            (q0 != p.starts[b] || q1 != p.starts[b + 1] || k0 != p.kv_starts[b] || k1 != p.kv_starts[b + 1]))
-            report(p.err, kErrIndex);
-        if (t < q0 || t >= q1) continue;
-        const int64_t see = p.causal ? max((k1 - k0) - (q1 - q0) + (t - q0) + 1, INT64_C(0)) : k1 - k0;
-        RowState s;
-        s.init(static_cast<const uint8_t*>(p.q) + row * 1024, lane, p.sm_scale);
-        const uint8_t* k = static_cast<const uint8_t*>(p.kv) + k0 * p.kv_stride * 2 + 16 * lane;
-        for (int64_t i = 0; i < see; ++i, k += p.kv_stride * 2)
-            s.add(*reinterpret_cast<const uint4*>(k), *reinterpret_cast<const uint4*>(k + 512));
-        s.write(static_cast<uint8_t*>(p.out) + row * 1024, p.lse + row, lane);
+    const int64_t at = bars->at;
+    bool bad = false;
+    const Request r = request_at(p, bars->request, bad);
+    int64_t lo = 0, hi = r.tiles;           // units_before(lo) <= at < units_before(hi)
+    while (hi - lo > 1) {
+        const int64_t x = lo + (hi - lo) * lane / 32;
+        const uint32_t below = __ballot_sync(kFull, units_before(p, r, x) <= at);   // lane 0 always
+        const int n = __popc(below);
+        const int64_t l = lo + (hi - lo) * (n - 1) / 32, h = n == 32 ? hi : lo + (hi - lo) * n / 32;
+        lo = l;
+        hi = h > l ? h : l + 1;
+    }
+    if (lane == 0) {
+        bars->tile = static_cast<int32_t>(lo);
+        bars->unit = static_cast<int32_t>(at - units_before(p, r, lo));
     }
 }
 
-__global__ void __launch_bounds__(kRowThreads) prefix_kernel(const PrefixParams p) {
-    const int lane = threadIdx.x & 31;
-    pdl_wait_previous();
-    pdl_release_next();
-    const AttentionParams& a = p.own;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kRowThreads / 32) + (threadIdx.x >> 5);
-    const int64_t i = row / a.num_heads;
-    if (i >= a.num_queries) return;
-    RowState s;
-    s.init(static_cast<const uint8_t*>(a.q) + row * 1024, lane, a.sm_scale);
-    bool bad = false;
-    const auto list = [&](const int32_t* idx, int64_t n) {
-        for (int64_t k = 0; k < n; ++k) {
-            const int32_t slot = idx[k];
-            if (slot < 0 || slot >= a.num_slots) {
-                bad |= slot != -1;
-                continue;
-            }
-            uint32_t page, at;
-            page_row(static_cast<uint32_t>(slot), static_cast<uint32_t>(a.block_size), page, at);
-            const uint8_t* const base = a.cache + page * a.page_stride;
-            const uint8_t* const data = base + at * 256u + 4 * lane;
-            const uint8_t* const scale = base + static_cast<int64_t>(a.block_size) * 256 + at * 16u + (lane >> 2);
-            s.add(dequant8_e2m1(*reinterpret_cast<const uint32_t*>(data), e2m1_factor(scale[0])),
-                  dequant8_e2m1(*reinterpret_cast<const uint32_t*>(data + 128), e2m1_factor(scale[8])));
+// Row `row` of a query tile in a stage: blocks `first` .. `first` + 2 into this thread's lane of
+// tensor memory (both halves of the lanes hold every row: each produces half of the columns), and
+// a quarter of the row's last two blocks to shared memory.
+__device__ __forceinline__ void take_query(uint32_t tile, int row, int part, int half, uint32_t dst, uint32_t q_smem) {
+    const uint32_t src = tile + row * kRowBytes + ((row & 7) << 4);
+#pragma unroll 1
+    for (int b = part * kQTmemBlocks / 2; b < (part + 1) * kQTmemBlocks / 2; ++b) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {   // 32 dims
+            uint4 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = lds16_at((src ^ ((4 * h + i) << 4)) + b * kBlockBytes);
+            tmem_st16(dst + 32 * b + 16 * h, v);
         }
-    };
-    list(p.prefix, p.prefix_length);
-    list(a.indices + i * a.index_stride, a.topk);
-    if (bad && lane == 0) report(a.err, kErrIndex);
-    s.write(static_cast<uint8_t*>(a.out) + row * 1024, a.lse + row, lane);
+    }
+    const uint32_t at = half * kBlockBytes + row * kRowBytes + part * 64;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        sts16(q_smem + at + 16 * i, lds16_at(tile + kQTmemBlocks * kBlockBytes + at + 16 * i));
+    tmem_st_wait();
 }
 
-int64_t row_blocks(int64_t rows) { return (rows + kRowThreads / 32 - 1) / (kRowThreads / 32); }
+// Values of key row `row` in this CTA's half of the dims (four blocks at `half`) that are not
+// finite become 0; a warp.
+__device__ __noinline__ void clear_row(uint32_t half, int row, int lane) {
+    const uint32_t at = half + (lane >> 3) * kBlockBytes + row * kRowBytes + (lane & 7) * 16;
+    uint4 v = lds16_at(at);
+    uint32_t* const w = &v.x;
+    bool found = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t x = w[i];
+        const bool lo = (x & 0x7F80u) == 0x7F80u, hi = (x & 0x7F800000u) == 0x7F800000u;
+        w[i] = (lo ? 0u : x & 0xFFFFu) | (hi ? 0u : x & 0xFFFF0000u);
+        found |= lo || hi;
+    }
+    if (found) sts16(at, v);
+}
+
+// Named barriers of the softmax warps: all of them, and the four warps of a half of the rows.
+constexpr int kSoftmaxBar = 1, kHeadsBar = 2;   // and 3
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
+    tile_kernel(const TileArgs p, const __grid_constant__ CUtensorMap q_map,
+                const __grid_constant__ CUtensorMap k_map) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* const smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    TileBarriers* const bars = reinterpret_cast<TileBarriers*>(smem + kOffBars);
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int64_t pair = blockIdx.x >> 1;
+
+    if (warp == kMmaWarp) {
+        tmem_alloc_pair(smem_addr(&bars->tmem_base), kTmemCols);
+        tmem_relinquish_pair();
+    }
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(smem_addr(&bars->peer_full[s]), 1);
+            mbar_init(smem_addr(&bars->peer_refilled[s]), 1);
+            mbar_init(smem_addr(&bars->full[s]), 1);
+            mbar_init(smem_addr(&bars->refilled[s]), 1);
+            mbar_init(smem_addr(&bars->empty[s]), 1);
+        }
+        mbar_init(smem_addr(&bars->s_full[0]), 1);
+        mbar_init(smem_addr(&bars->s_full[1]), 1);
+        mbar_init(smem_addr(&bars->s_free), 2 * kSoftmaxWarps);
+        mbar_init(smem_addr(&bars->p_full), 2 * kSoftmaxWarps);
+        mbar_init(smem_addr(&bars->q_full), 2 * kSoftmaxWarps);
+        mbar_init(smem_addr(&bars->drained), 1);
+        bars->timed_out = 0;
+        mbar_init_fence();
+    }
+    if (threadIdx.x == kLoadWarp * 32) {
+        prefetch_map(&q_map);
+        prefetch_map(&k_map);
+    }
+    pdl_wait_previous();
+    pdl_release_next();
+    find_work(p, bars, pair, gridDim.x >> 1);
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 0 && bars->units > 0) find_tile(p, bars);
+    __syncthreads();
+    cluster_sync();   // the other CTA's barriers exist
+    tc_fence_after_sync();
+    // All 512 columns are this CTA's, so they begin at address 0.
+    constexpr uint32_t tmem = 0;
+    bool ok = bars->tmem_base == 0;
+    Walk walk;
+    walk.init(p, bars);
+    Segment s;
+    Ring<kStages> ring;
+
+    if (warp == kLoadWarp) {
+        // ------------------------------------------------------------- rows for q . K
+        if (lane == 0) {
+            int loads = 0;
+            // the 64 rows from `row` on, all dims: the next item of the ring
+            auto load = [&](const CUtensorMap* map, int64_t row) {
+                if (loads >= kStages) wait_quiet(smem_addr(&bars->empty[ring.s]), ring.parity ^ 1u, ok);
+                if (!ok) return;
+                const uint32_t full = smem_addr(&bars->full[ring.s]);
+                const uint32_t to = smem_addr(smem) + kOffStages + ring.s * kStageBytes;
+                mbar_expect_tx(full, kStageBytes);
+                tma_load_3d(to, map, full, 0, static_cast<int32_t>(row), 0);
+                tma_load_3d(to + kHalfBytes, map, full, 0, static_cast<int32_t>(row), 4);
+                ring.next();
+                ++loads;
+            };
+            while (ok && walk.next(p, s)) {
+                if (s.chunks == 0) continue;
+                load(&q_map, s.r.row0 + s.row0 + rank * kCtaRows);
+#pragma unroll 1
+                for (int c = s.begin; c < s.end && ok; ++c)
+                    load(&k_map, s.r.k0 + static_cast<int64_t>(c) * kChunk + rank * kCtaKeys);
+            }
+            // what is under way lands before the CTA leaves
+            for (int i = max(0, loads - kStages); i < loads; ++i)
+                if (!wait_landed(smem_addr(&bars->full[i % kStages]), (i / kStages) & 1)) ok = false;
+        }
+        __syncwarp();
+    } else if (warp == kRefillWarp) {
+        // ------------------------------------------------------------- rows for p . K
+        if (lane == 0) {
+            int j = 0, used[kStages] = {0, 0, 0};
+            while (ok && walk.next(p, s)) {
+                if (s.chunks == 0) continue;
+                ring.next();   // the query tile
+#pragma unroll 1
+                for (int c = s.begin; c < s.end; ++c, ++j) {
+                    wait_quiet(smem_addr(&bars->s_full[j & 1]), (j >> 1) & 1, ok);   // q . K has read it
+                    if (!ok) break;
+                    const uint32_t bar = smem_addr(&bars->refilled[ring.s]);
+                    mbar_expect_tx(bar, kHalfBytes);
+                    tma_load_3d(smem_addr(smem) + kOffStages + ring.s * kStageBytes + (1u - rank) * kHalfBytes, &k_map,
+                                bar, 0,
+                                static_cast<int32_t>(s.r.k0 + static_cast<int64_t>(c) * kChunk + (1u - rank) * kCtaKeys),
+                                static_cast<int32_t>(4 * rank));
+#pragma unroll
+                    for (int i = 0; i < kStages; ++i) used[i] += i == ring.s ? 1 : 0;
+                    ring.next();
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kStages; ++i)
+                if (used[i] > 0 && !wait_landed(smem_addr(&bars->refilled[i]), (used[i] - 1) & 1)) ok = false;
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // ------------------------------------------------------------- products
+        // The whole warp runs this, one lane issues (elect_lane).  In rank 1 it passes on, in the
+        // same order, that this CTA's rows have landed.
+        const uint32_t elected = elect_lane();
+        const uint64_t q_desc = sw128_desc(smem_addr(smem));
+        const uint64_t k_desc0 = sw128_desc(smem_addr(smem + kOffStages));
+        const uint64_t v_desc0 = sw128_mn_desc(smem_addr(smem + kOffStages), kBlockBytes);
+        const uint64_t p_desc0 = sw128_desc(smem_addr(smem + kOffP));
+        const uint32_t q_lo = static_cast<uint32_t>(q_desc), k_lo = static_cast<uint32_t>(k_desc0);
+        const uint32_t v_lo = static_cast<uint32_t>(v_desc0), p_lo = static_cast<uint32_t>(p_desc0);
+        uint32_t turns = 0;                   // bit s: parity of the chunks so far in stage s
+        int tiles = 0, jq = 0, jo = 0;        // query tiles; chunks multiplied by q, by p
+        Ring<kStages> rq;                     // the stage of chunk jq; `ring`: of chunk jo
+        auto multiply_q = [&]() {
+            if (!warp_wait(smem_addr(&bars->full[rq.s]), rq.parity, ok)) return;
+            if (rank != 0) {
+                if (lane == 0) mbar_arrive_cluster(map_rank(smem_addr(&bars->peer_full[rq.s]), 0));
+            } else {
+                // (a chunk of the same stage before it has been multiplied by p by now)
+                if (!warp_wait(smem_addr(&bars->peer_full[rq.s]), turns >> rq.s & 1u, ok)) return;
+                if (jq > 0 && !warp_wait(smem_addr(&bars->s_free), (jq - 1) & 1, ok)) return;
+                tc_fence_after_sync();
+                const uint32_t b = k_lo + rq.s * (kStageBytes >> 4);
+                if (elected) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {       // 16 dims
+                        const uint64_t bk = desc_at(k_desc0, b + (((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4));
+                        if (k < 4 * kQTmemBlocks)
+                            mma_bf16_ts_pair(tmem + kSCol, tmem + kQCol + 8 * k, bk, kIdescS, k != 0);
+                        else
+                            mma_bf16_ss_pair(tmem + kSCol,
+                                             desc_at(q_desc, q_lo + ((((k >> 2) - kQTmemBlocks) * kBlockBytes + (k & 3) * 32) >> 4)),
+                                             bk, kIdescS, true);
+                    }
+                }
+                __syncwarp();
+                mma_commit_pair(smem_addr(&bars->s_full[jq & 1]), elected);
+            }
+            rq.next();
+            ++jq;
+        };
+        auto multiply_p = [&](bool fresh) {
+            const uint32_t turn = turns >> ring.s & 1u;
+            if (!warp_wait(smem_addr(&bars->refilled[ring.s]), turn, ok)) return;
+            if (rank != 0) {
+                if (lane == 0) mbar_arrive_cluster(map_rank(smem_addr(&bars->peer_refilled[ring.s]), 0));
+            } else {
+                if (!warp_wait(smem_addr(&bars->peer_refilled[ring.s]), turn, ok)) return;
+                if (!warp_wait(smem_addr(&bars->p_full), jo & 1, ok)) return;
+                tc_fence_after_sync();
+                const uint32_t b = v_lo + ring.s * (kStageBytes >> 4);
+                if (elected) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {            // 16 rows; k / 4: of which CTA
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)          // 128 of each CTA's 256 dims
+                            mma_bf16_ss_pair(tmem + 128 * h, desc_at(p_desc0, p_lo + (((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4)),
+                                             desc_at(v_desc0, b + (((k >> 2) * kHalfBytes + (k & 3) * 2048 + h * 2 * kBlockBytes) >> 4)),
+                                             kIdescO, k != 0 || !fresh);
+                    }
+                }
+                __syncwarp();
+                mma_commit_pair(smem_addr(&bars->empty[ring.s]), elected);
+            }
+            turns ^= 1u << ring.s;
+            ring.next();
+            ++jo;
+        };
+#pragma unroll 1
+        while (ok && walk.next(p, s)) {
+            if (s.chunks == 0) continue;
+            ring.next();   // the query tile
+            rq = ring;
+            if (rank == 0 && !warp_wait(smem_addr(&bars->q_full), tiles & 1, ok)) break;
+            ++tiles;
+            multiply_q();
+#pragma unroll 1
+            for (int c = s.begin; c < s.end && ok; ++c) {
+                if (c + 1 < s.end) multiply_q();
+                if (ok) multiply_p(c == s.begin);
+            }
+        }
+        // whatever ended the loop, no product is under way when the pair leaves
+        if (rank == 0) {
+            mma_commit_pair(smem_addr(&bars->drained), elected);
+            if (!wait_landed(smem_addr(&bars->drained), 0)) ok = false;
+            __syncwarp();
+        }
+    } else {
+        // ------------------------------------------------------------- softmax, epilogue
+        // Tensor-memory lane L: row L % 64 of this CTA; of a chunk the rows of CTA L / 64; of the
+        // output the dims 256 (L / 64) ...  Two warps share a lane, one for each half of its
+        // columns, so four threads have a row; they exchange maxima and sums.
+        const int quarter = warp & 3, part = warp >> 2;
+        const int row = (warp & 1) * 32 + lane;
+        const int half = quarter >> 1;
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        float* const heads = reinterpret_cast<float*>(smem + kOffHeads) + row;
+        const int self = (part * 2 + half) * 64;
+        const uint32_t s_free = map_rank(smem_addr(&bars->s_free), 0);
+        const uint32_t p_full = map_rank(smem_addr(&bars->p_full), 0);
+        const uint32_t q_full = map_rank(smem_addr(&bars->q_full), 0);
+        const float scale = __fmul_rn(p.sm_scale, kLog2e);   // logits in powers of two
+        const uint32_t stages = smem_addr(smem) + kOffStages;
+        // this thread's 64 bytes of the probabilities; those of the warp's rows leave through them
+        const uint32_t p_half = smem_addr(smem) + kOffP + half * kBlockBytes;
+        const uint32_t prow = p_half + row * kRowBytes + ((part * 4 ^ (row & 7)) << 4);
+        auto head_sync = [&]() { group_sync(kHeadsBar + (warp & 1), 128); };
+        auto head_any = [&](bool mine) -> bool { return group_any(kHeadsBar + (warp & 1), 128, mine); };
+        if (threadIdx.x == 0 && rank == 0) p.meta[pair] = make_int4(0, 0, 0, 0);
+
+        // The next segment with chunks; tiles that see no row are written on the way.
+        auto advance = [&](Segment& n) -> bool {
+            while (walk.next(p, n)) {
+                if (n.chunks > 0) return true;
+                const int rows = min(kCtaRows, n.rows - static_cast<int>(rank) * kCtaRows);
+                const int64_t at = n.r.row0 + n.row0 + rank * kCtaRows;
+                const int64_t bytes = p.wide != 0 ? 2048 : 1024;
+                for (int64_t i = threadIdx.x * INT64_C(16); i < rows * bytes; i += kSoftmaxWarps * 32 * 16)
+                    st16(static_cast<uint8_t*>(p.out) + at * bytes + i, make_uint4(0u, 0u, 0u, 0u));
+                if (static_cast<int>(threadIdx.x) < rows) p.lse[at + threadIdx.x] = -INFINITY;
+            }
+            return false;
+        };
+        // The query tile that is the ring's next item to where q . K reads it.
+        auto query = [&]() {
+            if (ok && warp_wait(smem_addr(&bars->full[ring.s]), ring.parity, ok))
+                take_query(stages + ring.s * kStageBytes, row, part, half, tmem + lanes + kQCol, smem_addr(smem));
+            fence_async_smem();   // what was read is read, before TMA writes there
+            tc_fence_before_sync();
+            ok = !group_any(kSoftmaxBar, kSoftmaxWarps * 32, !ok);
+            if (threadIdx.x == 0 && ok) mbar_arrive(smem_addr(&bars->empty[ring.s]));
+            if (lane == 0 && ok) mbar_arrive_cluster(q_full);
+            ring.next();
+        };
+
+        Segment n;
+        bool more = advance(n);
+        if (more) query();
+        int j = 0;
+        uint32_t turns = 0;        // bit s: parity of the chunks so far in stage s
+#pragma unroll 1
+        while (more) {
+            s = n;
+            float m = -INFINITY, l = 0.0f;
+            Ring<kStages> last;        // the stage of the chunk before
+            const int32_t my_row = s.row0 + static_cast<int32_t>(rank) * kCtaRows + row;   // of the request
+            const int32_t see = sees(p, s.r, min(my_row, s.r.rows - 1));
+            const int32_t least = sees(p, s.r, s.row0);   // of the tile's rows
+            const int32_t column = half * kCtaKeys + part * 32;   // of the chunk
+#pragma unroll 1
+            for (int c = s.begin; c < s.end; ++c, ++j) {
+                const bool fresh = c == s.begin;
+                const int64_t key = static_cast<int64_t>(c) * kChunk + column;   // this thread's first
+                uint32_t live = kFull;
+                if (p.live != nullptr) {
+                    const int32_t slot = key + lane < p.num_rows ? p.live[key + lane] : -1;
+                    live = __ballot_sync(kFull, slot >= 0 && slot < p.num_slots);
+                }
+                if (ok) warp_wait(smem_addr(&bars->s_full[j & 1]), (j >> 1) & 1, ok);
+                tc_fence_after_sync();
+                float v[32];
+                tmem_ld32(tmem + lanes + kSCol + 32 * part, v);
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0 && ok) mbar_arrive_cluster(s_free);
+                // columns that some row of the tile does not see
+                if (key + 32 > least) {
+                    const int64_t from = least - key;
+                    uint32_t odd = 0;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (i >= from && !(fabsf(v[i]) <= 3.40282347e38f)) odd |= 1u << i;
+                    odd = __reduce_or_sync(kFull, odd);
+                    // A row of K with an infinity or a NaN makes every logit of its column one or
+                    // the other, in both CTAs; other logits may be, and then nothing is cleared.
+                    if (odd != 0u && ok && warp_wait(smem_addr(&bars->full[ring.s]), ring.parity, ok) &&
+                        warp_wait(smem_addr(&bars->refilled[ring.s]), turns >> ring.s & 1u, ok)) {
+                        for (uint32_t left = odd; left != 0u; left &= left - 1u)
+                            clear_row(stages + ring.s * kStageBytes + half * kHalfBytes, part * 32 + __ffs(left) - 1, lane);
+                    }
+                    const int64_t lim = see - key;
+                    live &= lim >= 32 ? kFull : lim <= 0 ? 0u : (1u << lim) - 1u;
+                }
+                const uint64_t scale2 = f32x2(scale, scale);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2)
+                    f32x2_split(mul_f32x2(f32x2(v[i], v[i + 1]), scale2), v[i], v[i + 1]);
+                if (live != kFull) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (((live >> i) & 1u) == 0u) v[i] = -INFINITY;
+                }
+                float top = fmaxf(v[0], v[1]);
+#pragma unroll
+                for (int i = 2; i < 32; i += 2) top = fmaxf(top, fmaxf(v[i], v[i + 1]));
+                // Rarely a logit is far above its row's reference; the row's four threads learn
+                // of it by the barrier alone, and only then exchange their maxima.
+                if (head_any(top > m + kLag || (m == -INFINITY && top > m))) {
+                    heads[self] = top;
+                    head_sync();
+                    top = fmaxf(fmaxf(heads[0], heads[64]), fmaxf(heads[128], heads[192]));
+                    head_sync();   // read before they are written again
+                    const bool rise = top > m + kLag || (m == -INFINITY && top > m);
+                    const float fix = rise ? exp2_approx(__fsub_rn(m, top)) : 1.0f;
+                    if (rise) m = top;
+                    l = __fmul_rn(l, fix);
+                    if (!fresh) {
+                        // the products of the chunk before are in the accumulator
+                        if (ok) warp_wait(smem_addr(&bars->empty[last.s]), last.parity, ok);
+                        tc_fence_after_sync();
+#pragma unroll 1
+                        for (int d = 128 * part; d < 128 * part + 128; d += 32) {
+                            float t[32];
+                            tmem_ld32(tmem + lanes + d, t);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) t[i] = __fmul_rn(t[i], fix);
+                            tmem_st32(tmem + lanes + d, t);
+                        }
+                        tmem_st_wait();
+                    }
+                }
+                const float ref = m == -INFINITY ? 0.0f : __fsub_rn(m, kLift);
+                const uint64_t ref2 = f32x2(-ref, -ref);
+#pragma unroll
+                for (int i = 0; i < 32; i += 2) {
+                    f32x2_split(add_f32x2(f32x2(v[i], v[i + 1]), ref2), v[i], v[i + 1]);
+                    v[i] = exp2_flush(v[i]);
+                    v[i + 1] = exp2_flush(v[i + 1]);
+                }
+                uint64_t sum2 = add_f32x2(f32x2(v[0], v[1]), f32x2(v[2], v[3]));
+#pragma unroll
+                for (int i = 4; i < 32; i += 4)
+                    sum2 = add_f32x2(sum2, add_f32x2(f32x2(v[i], v[i + 1]), f32x2(v[i + 2], v[i + 3])));
+                float sum_a, sum_b;
+                f32x2_split(sum2, sum_a, sum_b);
+                l = __fadd_rn(l, __fadd_rn(sum_a, sum_b));
+                // the chunk before is multiplied: its probabilities are read
+                if (!fresh && ok) warp_wait(smem_addr(&bars->empty[last.s]), last.parity, ok);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sts16(prow ^ (i << 4), pack8(v + 8 * i));
+                fence_async_smem();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0 && ok) mbar_arrive_cluster(p_full);
+                last = ring;
+                turns ^= 1u << ring.s;
+                ring.next();
+            }
+            // q . K of this tile is complete: the next query tile may take its place, and is
+            // multiplied while this one's results are written
+            more = advance(n);
+            if (more) query();
+            heads[self] = l;
+            head_sync();
+            const float total = __fadd_rn(__fadd_rn(heads[0], heads[64]), __fadd_rn(heads[128], heads[192]));
+            // The last value product implies everything before it.  A row's warps agree on it, so
+            // that it is written in full or not at all.  (The barrier also puts the other lanes'
+            // accesses behind lane 0's wait, and the next sums behind the reads of these.)
+            if (ok) warp_wait(smem_addr(&bars->empty[last.s]), last.parity, ok);
+            ok = !head_any(!ok);
+            tc_fence_after_sync();
+            const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
+            const bool whole = s.begin == 0 && s.end == s.chunks;
+            const float lse2 = total == 0.0f ? -INFINITY : __fadd_rn(__fsub_rn(m, kLift), log2f(total));
+            const int64_t first_row = s.r.row0 + s.row0;
+            const int slot = s.begin == 0 ? 1 : 0;
+            if (!whole && threadIdx.x == 0 && rank == 0) {
+                int4 mark = p.meta[pair];
+                if (slot == 0) {
+                    mark.z |= kHeadThere | (s.end == s.chunks ? kHeadEnds : 0);
+                } else {
+                    mark.x = static_cast<int32_t>(first_row);
+                    mark.y = s.rows;
+                    mark.z |= kTailOpen;
+                }
+                p.meta[pair] = mark;
+            }
+            const bool narrow = whole && p.wide == 0;
+            const int64_t at = whole ? first_row : (2 * pair + slot) * p.slot_rows;
+            const int64_t dst_row = narrow ? 1024 : 2048;
+            uint8_t* const dst = (whole ? static_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(p.pieces)) +
+                                 at * dst_row + (2 * half + part) * (dst_row >> 2);
+            const int rows = ok ? s.rows : 0;
+            const int row0 = static_cast<int>(rank) * kCtaRows + (warp & 1) * 32;
+            const int step = narrow ? 32 : 16;
+#pragma unroll 1
+            for (int d = 0; d < 128; d += step) {           // 64 bytes of each row
+                float t[16];
+                tmem_ld16(tmem + lanes + 128 * part + d, t);
+                if (narrow) {
+                    sts16(prow, pack8(t, inv));
+                    sts16(prow ^ 16u, pack8(t + 8, inv));
+                    tmem_ld16(tmem + lanes + 128 * part + d + 16, t);
+                    sts16(prow ^ 32u, pack8(t, inv));
+                    sts16(prow ^ 48u, pack8(t + 8, inv));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        sts16(prow ^ (i << 4), make_uint4(__float_as_uint(__fmul_rn(t[4 * i], inv)),
+                                                          __float_as_uint(__fmul_rn(t[4 * i + 1], inv)),
+                                                          __float_as_uint(__fmul_rn(t[4 * i + 2], inv)),
+                                                          __float_as_uint(__fmul_rn(t[4 * i + 3], inv))));
+                }
+                __syncwarp();
+                // four lanes write 64 bytes of one row
+                uint8_t* const to = dst + d * (narrow ? 2 : 4) + (lane & 3) * 16;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 8 * i + (lane >> 2), in_cta = (warp & 1) * 32 + r;
+                    const uint4 x = lds16_at(p_half + in_cta * kRowBytes + (((part * 4 + (lane & 3)) ^ (r & 7)) << 4));
+                    if (row0 + r < rows) st16(to + (row0 + r) * dst_row, x);
+                }
+                __syncwarp();
+            }
+            if (half == 0 && part == 0 && row0 + lane < s.rows) {
+                float* const to = whole ? p.lse : p.piece_lse;
+                to[at + row0 + lane] = !ok ? __uint_as_float(kUnwritten) : narrow ? __fmul_rn(lse2, kLn2) : lse2;
+            }
+            tc_fence_before_sync();
+        }
+    }
+    if (!ok) bars->timed_out = 1;
+    tc_fence_before_sync();
+    __syncthreads();
+    if (threadIdx.x == 0 && bars->timed_out != 0) report(p.err, kErrTimeout);
+    cluster_sync();   // no CTA leaves while the other's products or arrivals reach it
+    if (warp == kMmaWarp) {
+        if (rank != 0) wait_landed(smem_addr(&bars->drained), 0);   // the last arrival from the other CTA
+        __syncwarp();
+        tmem_dealloc_pair(tmem, kTmemCols);
+    }
+}
+
+// ---------------------------------------------------------------- pieces
+
+// 16 dims of a row of fp32: four groups of four, 128 apart.
+struct Dims {
+    float4 d[4];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    __device__ __forceinline__ void add(const float* row, int lane, float w) {
+        float4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(row + 128 * i + 4 * lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            d[i].x = __fmaf_rn(w, x[i].x, d[i].x);
+            d[i].y = __fmaf_rn(w, x[i].y, d[i].y);
+            d[i].z = __fmaf_rn(w, x[i].z, d[i].z);
+            d[i].w = __fmaf_rn(w, x[i].w, d[i].w);
+        }
+    }
+    __device__ __forceinline__ void store(uint8_t* row, int lane, float f, bool wide) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = __fmul_rn(d[i].x, f), b = __fmul_rn(d[i].y, f), c = __fmul_rn(d[i].z, f),
+                        e = __fmul_rn(d[i].w, f);
+            if (wide) *reinterpret_cast<float4*>(row + 512 * i + 16 * lane) = make_float4(a, b, c, e);
+            else st8(row + 256 * i + 8 * lane, make_uint2(pack_bf16x2_rn(a, b), pack_bf16x2_rn(c, e)));
+        }
+    }
+};
+
+// Joins the pieces of each tile that was cut: out = sum_i exp2(lse_i - lse) rows_i.  A warp takes
+// a row; blocks of tiles that were not cut leave at once.
+constexpr int kJoinRows = 8;
+__global__ void __launch_bounds__(kJoinRows * 32) tile_join_kernel(const TileArgs p, const int32_t pairs) {
+    const int parts = (p.slot_rows + kJoinRows - 1) / kJoinRows;
+    const int g = blockIdx.x / parts, lane = threadIdx.x & 31;
+    const int r = (blockIdx.x - g * parts) * kJoinRows + (threadIdx.x >> 5);
+    pdl_wait_previous();
+    pdl_release_next();
+    const int4 mark = p.meta[g];
+    if ((mark.z & kTailOpen) == 0 || r >= mark.y) return;
+    int n = 1;
+    while (g + n < pairs && (p.meta[g + n++].z & kHeadEnds) == 0) {}
+    // the first piece ends its pair's run (slot 1), the others begin theirs (slot 0)
+    auto piece = [&](int i) -> int64_t { return (2 * static_cast<int64_t>(g + i) + (i == 0 ? 1 : 0)) * p.slot_rows + r; };
+    float m = -INFINITY;
+    bool unwritten = false;
+    for (int i = lane; i < n; i += 32) {
+        const float x = p.piece_lse[piece(i)];
+        unwritten |= is_unwritten(x);
+        m = fmaxf(m, x);
+    }
+    unwritten = __any_sync(kFull, unwritten) != 0;
+#pragma unroll
+    for (int x = 16; x >= 1; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
+    const float ref = m == -INFINITY ? 0.0f : m;
+    float sum = 0.0f;
+    Dims acc;
+    acc.zero();
+#pragma unroll 2
+    for (int i = 0; i < n; ++i) {
+        const float w = exp2_approx(__fsub_rn(p.piece_lse[piece(i)], ref));
+        sum = __fadd_rn(sum, w);
+        acc.add(p.pieces + piece(i) * 512, lane, w);
+    }
+    const int64_t row = mark.x + r;
+    if (unwritten) {
+        if (lane == 0) p.lse[row] = __uint_as_float(kUnwritten);
+        return;
+    }
+    const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+    acc.store(static_cast<uint8_t*>(p.out) + row * (p.wide != 0 ? 2048 : 1024), lane, inv, p.wide != 0);
+    if (lane == 0) {
+        const float lse2 = sum == 0.0f ? -INFINITY : __fadd_rn(m, log2f(sum));
+        p.lse[row] = p.wide != 0 ? lse2 : __fmul_rn(lse2, kLn2);
+    }
+}
+
+// Joins two results of every row, fp32 with log-sum-exps in powers of two.
+struct MergeArgs {
+    const float *a, *b, *a_lse, *b_lse;
+    int64_t rows;
+    void* out;
+    float* lse;
+};
+__global__ void __launch_bounds__(kJoinRows * 32) merge_kernel(const MergeArgs p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * kJoinRows + (threadIdx.x >> 5);
+    pdl_wait_previous();
+    pdl_release_next();
+    if (row >= p.rows) return;
+    const float x = p.a_lse[row], y = p.b_lse[row];
+    if (is_unwritten(x) || is_unwritten(y)) {
+        if (lane == 0) p.lse[row] = __uint_as_float(kUnwritten);
+        return;
+    }
+    const float m = fmaxf(x, y), ref = m == -INFINITY ? 0.0f : m;
+    const float u = exp2_approx(__fsub_rn(x, ref)), w = exp2_approx(__fsub_rn(y, ref));
+    const float sum = __fadd_rn(u, w);
+    Dims acc;
+    acc.zero();
+    acc.add(p.a + row * 512, lane, u);
+    acc.add(p.b + row * 512, lane, w);
+    acc.store(static_cast<uint8_t*>(p.out) + row * 1024, lane, sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum), false);
+    if (lane == 0) p.lse[row] = sum == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(m, log2f(sum)), kLn2);
+}
+
+// ---------------------------------------------------------------- host
+
+// `rows` rows of 512 bf16 (`stride` bytes apart) as a 3-D tensor map of 64 dims x rows x 8 blocks of
+// dims, with boxes of 64 rows of four blocks: one load brings half the dims of 64 rows as four
+// operand blocks.  Rows past the last read as zeros.
+cudaError_t rows_tensor_map(const void* base, int64_t rows, int64_t stride, CUtensorMap* map) {
+    const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+    if (encode == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), 8};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(stride), 128};
+    const cuuint32_t box[3] = {64, kCtaRows, 4};
+    const cuuint32_t step[3] = {1, 1, 1};
+    const CUresult r =
+        encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// The workspace of a tile launch: pieces, their log-sum-exps, what each pair left.
+constexpr int64_t up16(int64_t x) { return (x + 15) / 16 * 16; }
+int32_t slot_rows(int64_t rows) { return static_cast<int32_t>(rows < kTileRows ? rows : kTileRows); }
+int64_t tile_bytes(int32_t pairs, int64_t rows) {
+    const int64_t n = 2 * static_cast<int64_t>(pairs) * slot_rows(rows);
+    return n * 2048 + up16(n * 4) + static_cast<int64_t>(pairs) * 16;
+}
+
+cudaError_t tile_pairs(int32_t* pairs) {
+    return resident_pairs(reinterpret_cast<const void*>(tile_kernel), kTileThreads, kTileSmem, pairs);
+}
+
+// Attention of the rows of q; args but for what is in the workspace.
+cudaError_t launch_tiles(TileArgs a, const void* q, const void* kv, int64_t kv_stride, uint8_t* workspace,
+                         int32_t pdl, cudaStream_t stream) {
+    int32_t pairs = 0;
+    cudaError_t e = tile_pairs(&pairs);
+    if (e != cudaSuccess) return e;
+    const int64_t rows = a.num_tokens * a.num_heads;
+    a.slot_rows = slot_rows(rows);
+    const int64_t n = 2 * static_cast<int64_t>(pairs) * a.slot_rows;
+    a.pieces = reinterpret_cast<float*>(workspace);
+    a.piece_lse = reinterpret_cast<float*>(workspace + n * 2048);
+    a.meta = reinterpret_cast<int4*>(workspace + n * 2048 + up16(n * 4));
+    CUtensorMap q_map, k_map;
+    e = rows_tensor_map(q, rows, 1024, &q_map);
+    if (e != cudaSuccess) return e;
+    // no rows: nothing is loaded by the map
+    e = a.num_rows > 0 ? rows_tensor_map(kv, a.num_rows, kv_stride * 2, &k_map) : rows_tensor_map(q, rows, 1024, &k_map);
+    if (e != cudaSuccess) return e;
+    e = launch_kernel(tile_kernel, 2 * static_cast<int64_t>(pairs), kTileThreads, kTileSmem, stream, pdl, a, q_map, k_map);
+    if (e != cudaSuccess) return e;
+    const int64_t blocks = static_cast<int64_t>(pairs) * ((a.slot_rows + kJoinRows - 1) / kJoinRows);
+    return launch_kernel(tile_join_kernel, blocks, kJoinRows * 32, 0, stream, pdl, a, pairs);
+}
+
+// The workspace of a prefix attention: the prefix as bf16 rows, both parts' rows and
+// log-sum-exps, both parts' own workspaces.
+struct PrefixLayout {
+    int64_t rows, shared, shared_lse, own, own_lse, tiles, attend, bytes;
+};
+cudaError_t prefix_layout(int32_t num_heads, int64_t num_queries, int64_t prefix_length, int64_t topk,
+                          PrefixLayout* w) {
+    const int64_t n = num_queries * num_heads;
+    const bool both = prefix_length > 0 && topk > 0;
+    int64_t at = 0, attend = 0;
+    int32_t pairs = 0;
+    cudaError_t e = cudaSuccess;
+    if (prefix_length > 0) e = tile_pairs(&pairs);
+    if (e == cudaSuccess && (topk > 0 || prefix_length == 0))
+        e = attention_workspace(num_heads, num_queries, topk, &attend);
+    if (e != cudaSuccess) return e;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += (bytes + 127) / 128 * 128;
+        return here;
+    };
+    w->rows = take(prefix_length * 1024);
+    w->shared = take(both ? n * 2048 : 0);
+    w->shared_lse = take(both ? n * 4 : 0);
+    w->own = take(both ? n * 2048 : 0);
+    w->own_lse = take(both ? n * 4 : 0);
+    w->tiles = take(prefix_length > 0 ? tile_bytes(pairs, n) : 0);
+    w->attend = take(attend);
+    w->bytes = at;
+    return cudaSuccess;
+}
 
 }  // namespace
 
-cudaError_t prompt_workspace(int32_t, int64_t, int64_t* bytes) {
-    *bytes = 0;
+cudaError_t prompt_workspace(int32_t num_heads, int64_t num_tokens, int64_t* bytes) {
+    int32_t pairs = 0;
+    const cudaError_t e = tile_pairs(&pairs);
+    if (e != cudaSuccess) return e;
+    *bytes = tile_bytes(pairs, num_tokens * num_heads);
     return cudaSuccess;
 }
 
-cudaError_t prefix_workspace(int32_t, int64_t, int64_t, int64_t, int64_t* bytes) {
-    *bytes = 0;
-    return cudaSuccess;
+cudaError_t prefix_workspace(int32_t num_heads, int64_t num_queries, int64_t prefix_length, int64_t topk,
+                             int64_t* bytes) {
+    PrefixLayout w;
+    const cudaError_t e = prefix_layout(num_heads, num_queries, prefix_length, topk, &w);
+    *bytes = e == cudaSuccess ? w.bytes : 0;
+    return e;
 }
 
 cudaError_t launch_prompt_attention(const PromptParams& p, cudaStream_t stream) {
-    return launch_kernel(prompt_kernel, row_blocks(p.num_tokens * p.num_heads), kRowThreads, 0, stream, p.pdl, p);
+    TileArgs a = {};
+    a.num_heads = p.num_heads;
+    a.num_tokens = p.num_tokens;
+    a.num_rows = p.num_rows;
+    a.starts = p.starts;
+    a.kv_starts = p.kv_starts;
+    a.num_requests = p.num_requests;
+    a.causal = p.causal;
+    a.sm_scale = p.sm_scale;
+    a.out = p.out;
+    a.lse = p.lse;
+    a.err = p.err;
+    return launch_tiles(a, p.q, p.kv, p.kv_stride, static_cast<uint8_t*>(p.workspace), p.pdl, stream);
 }
 
 cudaError_t launch_prefix_attention(const PrefixParams& p, cudaStream_t stream) {
-    return launch_kernel(prefix_kernel, row_blocks(p.own.num_queries * p.own.num_heads), kRowThreads, 0, stream,
-                         p.own.pdl, p);
+    const AttentionParams& o = p.own;
+    PrefixLayout w;
+    cudaError_t e = prefix_layout(o.num_heads, o.num_queries, p.prefix_length, o.topk, &w);
+    if (e != cudaSuccess) return e;
+    uint8_t* const base = static_cast<uint8_t*>(o.workspace);
+    const bool both = p.prefix_length > 0 && o.topk > 0;
+    AttentionParams own = o;
+    own.workspace = base + w.attend;
+    if (p.prefix_length == 0) return launch_sparse_attention(own, stream);
+    if (both) {
+        own.out = base + w.own;
+        own.lse = reinterpret_cast<float*>(base + w.own_lse);
+        own.wide = 1;
+        e = launch_sparse_attention(own, stream);
+        if (e != cudaSuccess) return e;
+    }
+    GatherParams g = {};
+    g.cache = o.cache;
+    g.page_stride = o.page_stride;
+    g.block_size = o.block_size;
+    g.num_slots = o.num_slots;
+    g.indices = p.prefix;
+    g.num_indices = p.prefix_length;
+    g.out = base + w.rows;
+    g.err = o.err;
+    g.pdl = o.pdl;
+    e = launch_gather_mxfp4(g, stream);
+    if (e != cudaSuccess) return e;
+    TileArgs a = {};
+    a.num_heads = o.num_heads;
+    a.num_tokens = o.num_queries;
+    a.num_rows = p.prefix_length;
+    a.num_requests = 1;
+    a.live = p.prefix;
+    a.num_slots = o.num_slots;
+    a.sm_scale = o.sm_scale;
+    a.out = both ? static_cast<void*>(base + w.shared) : o.out;
+    a.lse = both ? reinterpret_cast<float*>(base + w.shared_lse) : o.lse;
+    a.wide = both ? 1 : 0;
+    a.err = o.err;
+    e = launch_tiles(a, o.q, base + w.rows, 512, base + w.tiles, o.pdl, stream);
+    if (e != cudaSuccess || !both) return e;
+    MergeArgs m;
+    m.a = reinterpret_cast<const float*>(base + w.shared);
+    m.b = reinterpret_cast<const float*>(base + w.own);
+    m.a_lse = reinterpret_cast<const float*>(base + w.shared_lse);
+    m.b_lse = reinterpret_cast<const float*>(base + w.own_lse);
+    m.rows = o.num_queries * o.num_heads;
+    m.out = o.out;
+    m.lse = o.lse;
+    return launch_kernel(merge_kernel, (m.rows + kJoinRows - 1) / kJoinRows, kJoinRows * 32, 0, stream, o.pdl, m);
 }
 
 }  // namespace gkr
