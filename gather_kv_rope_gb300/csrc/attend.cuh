@@ -68,6 +68,11 @@ struct Ring {
             parity ^= 1u;
         }
     }
+    __device__ __forceinline__ void skip(int n) {
+        const uint32_t at = static_cast<uint32_t>(s) + static_cast<uint32_t>(n);
+        parity ^= at / N & 1u;
+        s = static_cast<int>(at % N);
+    }
 };
 
 // A barrier of the first `threads` threads that come to it.

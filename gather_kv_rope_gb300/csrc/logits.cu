@@ -137,29 +137,6 @@ __device__ __forceinline__ void prefetch_l2_bulk(const void* src, uint32_t bytes
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
 }
 
-// TMA store (async proxy) of a 32 x 32 fp32 box from shared memory to the logits at
-// (entry x, head y, query z), in this thread's bulk group; entries past topk and heads past
-// num_heads are not written.  The tile holds row r (head y + r) at r * 128 bytes, its
-// 16-byte piece c at position c ^ (r % 8) (the map's 128-byte swizzle).
-__device__ __forceinline__ void tma_store_tile(const CUtensorMap* map, const void* tile, int32_t x,
-                                               int32_t y, int32_t z) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
-            reinterpret_cast<uint64_t>(map)),
-        "r"(x), "r"(y), "r"(z), "r"(smem_addr(tile))
-        : "memory");
-}
-__device__ __forceinline__ void bulk_commit() {
-    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-}
-// Wait until none of this thread's bulk groups still reads its shared-memory source.
-__device__ __forceinline__ void bulk_wait_read_all() {
-    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-}
-// Wait until all of this thread's bulk groups have completed.
-__device__ __forceinline__ void bulk_wait_all() {
-    asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-}
 __device__ __forceinline__ void st_shared16(void* p, float4 v) {
     *reinterpret_cast<float4*>(p) = v;
 }
@@ -521,7 +498,7 @@ __global__ void __launch_bounds__(kLogitThreads, 1)
                 fence_async_smem();
                 __syncwarp();
                 if (lane == 0 && ok && stores) {
-                    tma_store_tile(&out_map, tile, static_cast<int32_t>(k0 + c), h0,
+                    tma_store_3d(&out_map, smem_addr(tile), static_cast<int32_t>(k0 + c), h0,
                                    static_cast<int32_t>(qi));
                     bulk_commit();
                 }

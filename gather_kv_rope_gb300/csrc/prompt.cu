@@ -17,8 +17,12 @@
 //   * Rows come by TMA into a ring of three stages of 64 KB: a CTA's own 64 rows of the chunk for
 //     q . K; once that is done, the half of the dims that the other CTA multiplies is replaced
 //     by the other 64 rows' half of this CTA's dims for p . K (a product of the pair takes half
-//     of its columns from each CTA, at the same address in both).  The next query tile passes
-//     through the ring like a chunk.
+//     of its columns from each CTA, at the same address in both).
+//   * The next query tile passes through the ring like a chunk; the tensor cores copy it on to
+//     tensor memory.  Its stage then takes the results of the tile before, which leave by TMA
+//     stores.  So neither passes through registers on the way that every product's operands
+//     take: loads, stores and tensor-memory accesses of the warps share one pipe of 128 bytes a
+//     cycle, which a tile's query and results took for 9000 cycles.
 //   * q . K of the next chunk is issued before p . K of this one, so that the softmax of a chunk
 //     has the time of two products.  The probabilities have one buffer, and so have the logits.
 //   * Work: a unit for each tile (its loads and its epilogue) and one for each of its chunks, all
@@ -49,9 +53,11 @@ constexpr int kCtaKeys = 64;
 constexpr int kStages = 3;
 constexpr int kSoftmaxWarps = 8;         // warp w: tensor-memory lanes 32 (w % 4) .., half w / 4 of
                                          // their columns
-constexpr int kMmaWarp = kSoftmaxWarps;  // products (rank 0); rank 1: tells rank 0 what has landed
-constexpr int kLoadWarp = kMmaWarp + 1;  // query tiles and rows for q . K
-constexpr int kRefillWarp = kLoadWarp + 1;   // rows for p . K
+constexpr int kMoveWarps = 8;            // write results, warp w of them as above
+constexpr int kFirstMove = kSoftmaxWarps;
+constexpr int kMmaWarp = kFirstMove + kMoveWarps;   // products (rank 0); rank 1: tells rank 0 what has landed
+constexpr int kLoadWarp = kMmaWarp + 1;  // query tiles and rows for q . K; the pair's work
+constexpr int kRefillWarp = kLoadWarp + 1;   // rows for p . K, the query's last dims
 constexpr int kTileThreads = (kRefillWarp + 1) * 32;
 constexpr uint32_t kBlockBytes = kCtaKeys * kRowBytes;      // 64 dims of 64 rows
 constexpr uint32_t kHalfBytes = 4 * kBlockBytes;            // 256 dims
@@ -77,20 +83,39 @@ constexpr uint32_t kIdescO = idesc(256, true);
 constexpr uint32_t kOffP = kQBytes;
 constexpr uint32_t kOffStages = kOffP + kPBytes;
 constexpr uint32_t kOffHeads = kOffStages + kStages * kStageBytes;   // [4][64] maxima, then sums, of a row
-constexpr uint32_t kOffBars = kOffHeads + 256 * 4;
+constexpr uint32_t kOffStats = kOffHeads + 256 * 4;         // [2][64] a tile's 1 / sum and log-sum-exp of a row
+constexpr uint32_t kOffBars = kOffStats + 2 * 64 * 8;
+
+// A pair's part of one tile, as its roles need it.
+constexpr int kParts = 4;                // in the ring: the loads are never two tiles ahead
+struct alignas(16) Part {
+    int64_t row0;            // the tile's first row of q
+    int64_t k0;              // the request's first row of K
+    int64_t see;             // rows that the query of the tile's first row sees, not yet clamped
+    int32_t offset;          // that row's head
+    int32_t rows, keys;      // rows of the tile; rows of K
+    int32_t least;           // rows that all of the tile's rows see
+    int32_t chunks;          // of the tile; 0: no more parts
+    int32_t begin, end;      // of them, this pair's
+};
 
 struct alignas(8) TileBarriers {
     // in the leader: arrivals of both CTAs
-    uint64_t peer_full[kStages];   // rank 1: its rows of the stage have landed, for q . K
-    uint64_t peer_refilled[kStages];   // ... and for p . K
+    uint64_t peer_full[kStages];   // rank 1: a query tile or its rows for q . K have landed
+    uint64_t peer_refilled[kStages];   // ... its rows for p . K
+    uint64_t peer_tail;            // ... the query's last dims
     uint64_t s_free;               // softmax: the logits are read
     uint64_t p_full;               // softmax: the probabilities are written
-    uint64_t q_full;               // softmax: a query tile is in place
+    uint64_t o_free;               // movers: a tile's output is read
     // in each CTA
     uint64_t full[kStages];        // a query tile or rows for q . K have landed
     uint64_t refilled[kStages];    // rows for p . K have
-    uint64_t empty[kStages];       // p . K of the chunk is complete; the query tile is moved
+    uint64_t tail;                 // the query's last dims have
+    uint64_t empty[kStages];       // p . K of the chunk is complete; results have left the stage
     uint64_t s_full[2];            // the logits of a chunk are complete (even, odd chunks)
+    uint64_t copied[2];            // a query tile is in tensor memory (even, odd tiles)
+    uint64_t part[kParts];         // a part of the pair's work is described
+    uint64_t stats[2];             // softmax: a tile's sums and log-sum-exps are there
     uint64_t drained;              // every product that was issued is complete
     // the pair's first unit: request, tile of it, unit of the tile; how many there are
     int64_t units, at;
@@ -98,8 +123,9 @@ struct alignas(8) TileBarriers {
     int32_t request, tile, unit;
     uint32_t tmem_base;
     volatile int32_t timed_out;
+    Part parts[kParts];
 };
-constexpr size_t kTileSmem = 1024 + kOffBars + sizeof(TileBarriers);
+constexpr size_t kTileSmem = kOffBars + sizeof(TileBarriers);
 static_assert(kTileSmem <= 227 * 1024, "a CTA's shared memory");
 
 // Arguments of the tile kernel.
@@ -157,11 +183,13 @@ __device__ __forceinline__ Request request_at(const TileArgs& p, int b, bool& ba
     return r;
 }
 
+__device__ __forceinline__ int32_t clamped(int64_t see, int32_t keys) {
+    return static_cast<int32_t>(min(max(see, INT64_C(0)), static_cast<int64_t>(keys)));
+}
 // How many rows row `row` of a request sees.
 __device__ __forceinline__ int32_t sees(const TileArgs& p, const Request& r, int32_t row) {
     if (p.causal == 0) return r.keys;
-    const int64_t see = r.past + static_cast<uint32_t>(row) / static_cast<uint32_t>(p.num_heads) + 1;
-    return static_cast<int32_t>(min(max(see, INT64_C(0)), static_cast<int64_t>(r.keys)));
+    return clamped(r.past + static_cast<uint32_t>(row) / static_cast<uint32_t>(p.num_heads) + 1, r.keys);
 }
 // Chunks of a tile: what its last row sees.
 __device__ __forceinline__ int32_t chunks_of(const TileArgs& p, const Request& r, int32_t tile) {
@@ -189,16 +217,7 @@ __device__ __forceinline__ int64_t units_of(const TileArgs& p, const Request& r)
     return units_before(p, r, r.tiles - 1) + 1 + (static_cast<int64_t>(r.keys) + kChunk - 1) / kChunk;
 }
 
-// A pair's part of one tile.
-struct Segment {
-    Request r;
-    int32_t row0;            // of the request
-    int32_t rows;            // of the tile
-    int32_t chunks;          // of the tile
-    int32_t begin, end;      // of them, this pair's
-};
-
-// A pair's segments, one after another; every role walks through them for itself.
+// A pair's parts, one after another.
 struct Walk {
     Request r;
     int64_t left;
@@ -211,7 +230,8 @@ struct Walk {
         bool bad = false;
         if (left > 0) r = request_at(p, b, bad);
     }
-    __device__ bool next(const TileArgs& p, Segment& s) {
+    // The next one; `chunks` 0 is a tile that sees no row here.
+    __device__ bool next(const TileArgs& p, Part& s) {
         while (left > 0) {
             if (tile >= r.tiles) {
                 if (++b >= p.num_requests) return false;
@@ -221,9 +241,15 @@ struct Walk {
                 unit = 0;
                 continue;
             }
-            s.r = r;
-            s.row0 = tile * kTileRows;
-            s.rows = min(kTileRows, r.rows - s.row0);
+            const int32_t row = tile * kTileRows;
+            s.row0 = r.row0 + row;
+            s.k0 = r.k0;
+            s.rows = min(kTileRows, r.rows - row);
+            s.keys = r.keys;
+            const uint32_t query = static_cast<uint32_t>(row) / static_cast<uint32_t>(p.num_heads);
+            s.offset = row - static_cast<int32_t>(query) * p.num_heads;
+            s.see = p.causal == 0 ? r.keys : r.past + query + 1;
+            s.least = clamped(s.see, r.keys);
             s.chunks = chunks_of(p, r, tile);
             const int64_t take = min(left, static_cast<int64_t>(1 + s.chunks - unit));
             s.begin = max(unit, 1) - 1;
@@ -302,28 +328,6 @@ __device__ __forceinline__ void find_tile(const TileArgs& p, TileBarriers* bars)
     }
 }
 
-// Row `row` of a query tile in a stage: blocks `first` .. `first` + 2 into this thread's lane of
-// tensor memory (both halves of the lanes hold every row: each produces half of the columns), and
-// a quarter of the row's last two blocks to shared memory.
-__device__ __forceinline__ void take_query(uint32_t tile, int row, int part, int half, uint32_t dst, uint32_t q_smem) {
-    const uint32_t src = tile + row * kRowBytes + ((row & 7) << 4);
-#pragma unroll 1
-    for (int b = part * kQTmemBlocks / 2; b < (part + 1) * kQTmemBlocks / 2; ++b) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {   // 32 dims
-            uint4 v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = lds16_at((src ^ ((4 * h + i) << 4)) + b * kBlockBytes);
-            tmem_st16(dst + 32 * b + 16 * h, v);
-        }
-    }
-    const uint32_t at = half * kBlockBytes + row * kRowBytes + part * 64;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        sts16(q_smem + at + 16 * i, lds16_at(tile + kQTmemBlocks * kBlockBytes + at + 16 * i));
-    tmem_st_wait();
-}
-
 // Values of key row `row` in this CTA's half of the dims (four blocks at `half`) that are not
 // finite become 0; a warp.
 __device__ __noinline__ void clear_row(uint32_t half, int row, int lane) {
@@ -341,15 +345,26 @@ __device__ __noinline__ void clear_row(uint32_t half, int row, int lane) {
     if (found) sts16(at, v);
 }
 
-// Named barriers of the softmax warps: all of them, and the four warps of a half of the rows.
-constexpr int kSoftmaxBar = 1, kHeadsBar = 2;   // and 3
+// `rows` rows of 1 KB from a stage (eight swizzled blocks of 128 bytes) to global memory, `stride` bytes
+// apart; eight warps.
+__device__ __forceinline__ void copy_rows(uint32_t stage, uint8_t* dst, int64_t stride, int rows, int warp, int lane) {
+#pragma unroll 2
+    for (int r = warp; r < min(rows, kCtaRows); r += kMoveWarps) {
+        const uint32_t at = stage + (lane >> 3) * kBlockBytes + r * kRowBytes + (((lane ^ r) & 7) << 4);
+        const uint4 a = lds16_at(at), b = lds16_at(at + 4 * kBlockBytes);
+        st16(dst + r * stride + 16 * lane, a);
+        st16(dst + r * stride + 512 + 16 * lane, b);
+    }
+}
+
+// Named barriers: the four softmax warps of each half of the rows; the movers.
+constexpr int kHeadsBar = 1, kMoveBar = 3;
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     tile_kernel(const TileArgs p, const __grid_constant__ CUtensorMap q_map,
-                const __grid_constant__ CUtensorMap k_map) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* const smem = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+                const __grid_constant__ CUtensorMap tail_map, const __grid_constant__ CUtensorMap k_map,
+                const __grid_constant__ CUtensorMap out_map) {
+    extern __shared__ __align__(1024) uint8_t smem[];
     TileBarriers* const bars = reinterpret_cast<TileBarriers*>(smem + kOffBars);
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -368,18 +383,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             mbar_init(smem_addr(&bars->refilled[s]), 1);
             mbar_init(smem_addr(&bars->empty[s]), 1);
         }
-        mbar_init(smem_addr(&bars->s_full[0]), 1);
-        mbar_init(smem_addr(&bars->s_full[1]), 1);
+        for (int s = 0; s < kParts; ++s) mbar_init(smem_addr(&bars->part[s]), 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_addr(&bars->s_full[s]), 1);
+            mbar_init(smem_addr(&bars->copied[s]), 1);
+            mbar_init(smem_addr(&bars->stats[s]), kSoftmaxWarps);
+        }
+        mbar_init(smem_addr(&bars->peer_tail), 1);
+        mbar_init(smem_addr(&bars->tail), 1);
         mbar_init(smem_addr(&bars->s_free), 2 * kSoftmaxWarps);
         mbar_init(smem_addr(&bars->p_full), 2 * kSoftmaxWarps);
-        mbar_init(smem_addr(&bars->q_full), 2 * kSoftmaxWarps);
+        mbar_init(smem_addr(&bars->o_free), 2 * kMoveWarps);
         mbar_init(smem_addr(&bars->drained), 1);
         bars->timed_out = 0;
         mbar_init_fence();
     }
     if (threadIdx.x == kLoadWarp * 32) {
         prefetch_map(&q_map);
+        prefetch_map(&tail_map);
         prefetch_map(&k_map);
+        prefetch_map(&out_map);
     }
     pdl_wait_previous();
     pdl_release_next();
@@ -392,71 +415,109 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     tc_fence_after_sync();
     // All 512 columns are this CTA's, so they begin at address 0.
     constexpr uint32_t tmem = 0;
-    bool ok = bars->tmem_base == 0;
-    Walk walk;
-    walk.init(p, bars);
-    Segment s;
+    bool ok = bars->tmem_base == 0 && (smem_addr(smem) & 1023u) == 0u;
+    // Part `tile` of the pair's work; a warp.  False after the last, or once a wait gave up.
+    auto part_at = [&](int tile, Part& s) -> bool {
+        if (!ok || !warp_wait(smem_addr(&bars->part[tile & (kParts - 1)]), (tile / kParts) & 1, ok)) return false;
+        s = bars->parts[tile & (kParts - 1)];
+        return s.chunks > 0;
+    };
     Ring<kStages> ring;
 
     if (warp == kLoadWarp) {
         // ------------------------------------------------------------- rows for q . K
-        if (lane == 0) {
-            int loads = 0;
-            // the 64 rows from `row` on, all dims: the next item of the ring
-            auto load = [&](const CUtensorMap* map, int64_t row) {
-                if (loads >= kStages) wait_quiet(smem_addr(&bars->empty[ring.s]), ring.parity ^ 1u, ok);
-                if (!ok) return;
+        // The warp walks through the pair's work and describes each part for the other roles; one
+        // lane loads.  A part's description is replaced four parts on; as a tile's results keep
+        // the stage of the next tile's query, the loads are never more than two tiles ahead of
+        // the tile whose results are being written.
+        int loads = 0, tile = 0;
+        // the 64 rows from `row` on, all dims (a query's first 384): the next item of the ring
+        auto load = [&](bool query, int64_t row) {
+            if (loads >= kStages) warp_wait(smem_addr(&bars->empty[ring.s]), ring.parity ^ 1u, ok);
+            if (!ok) return;
+            if (lane == 0) {
                 const uint32_t full = smem_addr(&bars->full[ring.s]);
                 const uint32_t to = smem_addr(smem) + kOffStages + ring.s * kStageBytes;
-                mbar_expect_tx(full, kStageBytes);
-                tma_load_3d(to, map, full, 0, static_cast<int32_t>(row), 0);
-                tma_load_3d(to + kHalfBytes, map, full, 0, static_cast<int32_t>(row), 4);
-                ring.next();
-                ++loads;
-            };
-            while (ok && walk.next(p, s)) {
-                if (s.chunks == 0) continue;
-                load(&q_map, s.r.row0 + s.row0 + rank * kCtaRows);
-#pragma unroll 1
-                for (int c = s.begin; c < s.end && ok; ++c)
-                    load(&k_map, s.r.k0 + static_cast<int64_t>(c) * kChunk + rank * kCtaKeys);
+                mbar_expect_tx(full, query ? kQTmemBlocks * kBlockBytes : kStageBytes);
+                tma_load_3d(to, query ? &q_map : &k_map, full, 0, static_cast<int32_t>(row), 0);
+                tma_load_3d(to + kHalfBytes, query ? &tail_map : &k_map, full, 0, static_cast<int32_t>(row), 4);
             }
-            // what is under way lands before the CTA leaves
-            for (int i = max(0, loads - kStages); i < loads; ++i)
-                if (!wait_landed(smem_addr(&bars->full[i % kStages]), (i / kStages) & 1)) ok = false;
+            __syncwarp();
+            ring.next();
+            ++loads;
+        };
+        Walk walk;
+        walk.init(p, bars);
+        Part s;
+        while (ok) {
+            const bool some = walk.next(p, s);
+            if (some && s.chunks == 0) {   // zeros
+                const int rows = min(kCtaRows, s.rows - static_cast<int>(rank) * kCtaRows);
+                const int64_t at = s.row0 + rank * kCtaRows, bytes = p.wide != 0 ? 2048 : 1024;
+                for (int64_t i = lane * INT64_C(16); i < rows * bytes; i += 512)
+                    st16(static_cast<uint8_t*>(p.out) + at * bytes + i, make_uint4(0u, 0u, 0u, 0u));
+                for (int i = lane; i < rows; i += 32) p.lse[at + i] = -INFINITY;
+                continue;
+            }
+            if (!some) s.chunks = 0;
+            if (lane == 0) {
+                bars->parts[tile & (kParts - 1)] = s;
+                mbar_arrive(smem_addr(&bars->part[tile & (kParts - 1)]));
+            }
+            __syncwarp();
+            if (!some) break;
+            ++tile;
+            load(true, s.row0 + rank * kCtaRows);
+#pragma unroll 1
+            for (int c = s.begin; c < s.end && ok; ++c)
+                load(false, s.k0 + static_cast<int64_t>(c) * kChunk + rank * kCtaKeys);
         }
+        // what is under way lands before the CTA leaves
+        for (int i = max(0, loads - kStages); i < loads; ++i)
+            if (!wait_landed(smem_addr(&bars->full[i % kStages]), (i / kStages) & 1)) ok = false;
         __syncwarp();
     } else if (warp == kRefillWarp) {
         // ------------------------------------------------------------- rows for p . K
-        if (lane == 0) {
-            int j = 0, used[kStages] = {0, 0, 0};
-            while (ok && walk.next(p, s)) {
-                if (s.chunks == 0) continue;
-                ring.next();   // the query tile
+        int j = 0, tile = 0, used[kStages] = {0, 0, 0};
+        Part s;
+        for (; part_at(tile, s); ++tile) {
+            // q . K of the tile before is complete: the query's last dims may be replaced
+            if (lane == 0) {
+                const uint32_t bar = smem_addr(&bars->tail);
+                mbar_expect_tx(bar, kQBytes);
+                tma_load_3d(smem_addr(smem), &tail_map, bar, 0, static_cast<int32_t>(s.row0 + rank * kCtaRows),
+                            kQTmemBlocks);
+            }
+            __syncwarp();
+            ring.next();   // the query tile
 #pragma unroll 1
-                for (int c = s.begin; c < s.end; ++c, ++j) {
-                    wait_quiet(smem_addr(&bars->s_full[j & 1]), (j >> 1) & 1, ok);   // q . K has read it
-                    if (!ok) break;
+            for (int c = s.begin; c < s.end; ++c, ++j) {
+                if (!warp_wait(smem_addr(&bars->s_full[j & 1]), (j >> 1) & 1, ok)) break;   // q . K has read it
+                if (lane == 0) {
                     const uint32_t bar = smem_addr(&bars->refilled[ring.s]);
                     mbar_expect_tx(bar, kHalfBytes);
                     tma_load_3d(smem_addr(smem) + kOffStages + ring.s * kStageBytes + (1u - rank) * kHalfBytes, &k_map,
                                 bar, 0,
-                                static_cast<int32_t>(s.r.k0 + static_cast<int64_t>(c) * kChunk + (1u - rank) * kCtaKeys),
+                                static_cast<int32_t>(s.k0 + static_cast<int64_t>(c) * kChunk + (1u - rank) * kCtaKeys),
                                 static_cast<int32_t>(4 * rank));
-#pragma unroll
-                    for (int i = 0; i < kStages; ++i) used[i] += i == ring.s ? 1 : 0;
-                    ring.next();
                 }
-            }
+                __syncwarp();
 #pragma unroll
-            for (int i = 0; i < kStages; ++i)
-                if (used[i] > 0 && !wait_landed(smem_addr(&bars->refilled[i]), (used[i] - 1) & 1)) ok = false;
+                for (int i = 0; i < kStages; ++i) used[i] += i == ring.s ? 1 : 0;
+                ring.next();
+            }
         }
+#pragma unroll
+        for (int i = 0; i < kStages; ++i)
+            if (used[i] > 0 && !wait_landed(smem_addr(&bars->refilled[i]), (used[i] - 1) & 1)) ok = false;
+        if (tile > 0 && !wait_landed(smem_addr(&bars->tail), (tile - 1) & 1)) ok = false;
         __syncwarp();
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------- products
         // The whole warp runs this, one lane issues (elect_lane).  In rank 1 it passes on, in the
-        // same order, that this CTA's rows have landed.
+        // same order, that this CTA's loads have landed.  q . K is one chunk ahead of p . K within
+        // a tile; between tiles p . K of the last chunk comes first, as it and the writing of the
+        // results take longer than what the next tile needs until its first p . K.
         const uint32_t elected = elect_lane();
         const uint64_t q_desc = sw128_desc(smem_addr(smem));
         const uint64_t k_desc0 = sw128_desc(smem_addr(smem + kOffStages));
@@ -464,76 +525,116 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         const uint64_t p_desc0 = sw128_desc(smem_addr(smem + kOffP));
         const uint32_t q_lo = static_cast<uint32_t>(q_desc), k_lo = static_cast<uint32_t>(k_desc0);
         const uint32_t v_lo = static_cast<uint32_t>(v_desc0), p_lo = static_cast<uint32_t>(p_desc0);
-        uint32_t turns = 0;                   // bit s: parity of the chunks so far in stage s
-        int tiles = 0, jq = 0, jo = 0;        // query tiles; chunks multiplied by q, by p
+        uint32_t turns = 0;                   // bit s: parity of the chunks that p has met in stage s
+        int jq = 0, jo = 0;                   // chunks multiplied by q, by p
+        int tq = 0, to = 0, left_q = 0, left_next = 0, left_o = 0;   // parts begun, and what is left of them
+        bool some = true, opened = false, fresh = true;   // opened: the next part's query is on its way
         Ring<kStages> rq;                     // the stage of chunk jq; `ring`: of chunk jo
-        auto multiply_q = [&]() {
-            if (!warp_wait(smem_addr(&bars->full[rq.s]), rq.parity, ok)) return;
-            if (rank != 0) {
-                if (lane == 0) mbar_arrive_cluster(map_rank(smem_addr(&bars->peer_full[rq.s]), 0));
-            } else {
-                // (a chunk of the same stage before it has been multiplied by p by now)
-                if (!warp_wait(smem_addr(&bars->peer_full[rq.s]), turns >> rq.s & 1u, ok)) return;
-                if (jq > 0 && !warp_wait(smem_addr(&bars->s_free), (jq - 1) & 1, ok)) return;
-                tc_fence_after_sync();
-                const uint32_t b = k_lo + rq.s * (kStageBytes >> 4);
-                if (elected) {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {       // 16 dims
-                        const uint64_t bk = desc_at(k_desc0, b + (((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4));
-                        if (k < 4 * kQTmemBlocks)
-                            mma_bf16_ts_pair(tmem + kSCol, tmem + kQCol + 8 * k, bk, kIdescS, k != 0);
-                        else
-                            mma_bf16_ss_pair(tmem + kSCol,
-                                             desc_at(q_desc, q_lo + ((((k >> 2) - kQTmemBlocks) * kBlockBytes + (k & 3) * 32) >> 4)),
-                                             bk, kIdescS, true);
-                    }
-                }
-                __syncwarp();
-                mma_commit_pair(smem_addr(&bars->s_full[jq & 1]), elected);
-            }
-            rq.next();
-            ++jq;
-        };
-        auto multiply_p = [&](bool fresh) {
-            const uint32_t turn = turns >> ring.s & 1u;
-            if (!warp_wait(smem_addr(&bars->refilled[ring.s]), turn, ok)) return;
-            if (rank != 0) {
-                if (lane == 0) mbar_arrive_cluster(map_rank(smem_addr(&bars->peer_refilled[ring.s]), 0));
-            } else {
-                if (!warp_wait(smem_addr(&bars->peer_refilled[ring.s]), turn, ok)) return;
-                if (!warp_wait(smem_addr(&bars->p_full), jo & 1, ok)) return;
-                tc_fence_after_sync();
-                const uint32_t b = v_lo + ring.s * (kStageBytes >> 4);
-                if (elected) {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {            // 16 rows; k / 4: of which CTA
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)          // 128 of each CTA's 256 dims
-                            mma_bf16_ss_pair(tmem + 128 * h, desc_at(p_desc0, p_lo + (((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4)),
-                                             desc_at(v_desc0, b + (((k >> 2) * kHalfBytes + (k & 3) * 2048 + h * 2 * kBlockBytes) >> 4)),
-                                             kIdescO, k != 0 || !fresh);
-                    }
-                }
-                __syncwarp();
-                mma_commit_pair(smem_addr(&bars->empty[ring.s]), elected);
-            }
-            turns ^= 1u << ring.s;
-            ring.next();
-            ++jo;
-        };
+        Part s;
 #pragma unroll 1
-        while (ok && walk.next(p, s)) {
-            if (s.chunks == 0) continue;
-            ring.next();   // the query tile
-            rq = ring;
-            if (rank == 0 && !warp_wait(smem_addr(&bars->q_full), tiles & 1, ok)) break;
-            ++tiles;
-            multiply_q();
+        while (true) {
+            if (some && left_q == 0 && !opened && jq - jo < 2) {
+                some = part_at(tq, s);
+                if (!ok) break;
+                if (!some) continue;
+                left_next = s.end - s.begin;
+                if (!warp_wait(smem_addr(&bars->full[rq.s]), rq.parity, ok)) break;
+                if (rank != 0) {
+                    if (lane == 0) mbar_arrive_cluster(map_rank(smem_addr(&bars->peer_full[rq.s]), 0));
+                } else {
+                    if (!warp_wait(smem_addr(&bars->peer_full[rq.s]), rq.parity, ok)) break;
+                    // q . K of the tile before has read its query
+                    if (jq > 0 && !warp_wait(smem_addr(&bars->s_full[(jq - 1) & 1]), ((jq - 1) >> 1) & 1, ok)) break;
+                    tc_fence_after_sync();
+                    const uint32_t q = k_lo + rq.s * (kStageBytes >> 4);
+                    if (elected) {
 #pragma unroll 1
-            for (int c = s.begin; c < s.end && ok; ++c) {
-                if (c + 1 < s.end) multiply_q();
-                if (ok) multiply_p(c == s.begin);
+                        for (int b = 0; b < kQTmemBlocks; ++b)
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)   // 8 dims
+                                copy_to_tmem_pair(tmem + kQCol + 32 * b + 4 * i, desc_at(k_desc0, q + b * (kBlockBytes >> 4) + i));
+                    }
+                    __syncwarp();
+                    mma_commit_pair(smem_addr(&bars->copied[tq & 1]), elected);
+                }
+                rq.next();
+                opened = true;
+            } else if (some && jq - jo < 2 && !(opened && jo < jq)) {
+                if (opened) {
+                    if (!warp_wait(smem_addr(&bars->tail), tq & 1, ok)) break;
+                    if (rank != 0) {
+                        if (lane == 0) mbar_arrive_cluster(map_rank(smem_addr(&bars->peer_tail), 0));
+                    } else if (!warp_wait(smem_addr(&bars->peer_tail), tq & 1, ok)) {
+                        break;
+                    }
+                    opened = false;
+                    left_q = left_next;
+                    ++tq;
+                }
+                if (!warp_wait(smem_addr(&bars->full[rq.s]), rq.parity, ok)) break;
+                if (rank != 0) {
+                    if (lane == 0) mbar_arrive_cluster(map_rank(smem_addr(&bars->peer_full[rq.s]), 0));
+                } else {
+                    if (!warp_wait(smem_addr(&bars->peer_full[rq.s]), rq.parity, ok)) break;
+                    if (jq > 0 && !warp_wait(smem_addr(&bars->s_free), (jq - 1) & 1, ok)) break;
+                    tc_fence_after_sync();
+                    const uint32_t b = k_lo + rq.s * (kStageBytes >> 4);
+                    if (elected) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {       // 16 dims
+                            const uint64_t bk = desc_at(k_desc0, b + (((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4));
+                            if (k < 4 * kQTmemBlocks)
+                                mma_bf16_ts_pair(tmem + kSCol, tmem + kQCol + 8 * k, bk, kIdescS, k != 0);
+                            else
+                                mma_bf16_ss_pair(tmem + kSCol,
+                                                 desc_at(q_desc, q_lo + ((((k >> 2) - kQTmemBlocks) * kBlockBytes + (k & 3) * 32) >> 4)),
+                                                 bk, kIdescS, true);
+                        }
+                    }
+                    __syncwarp();
+                    mma_commit_pair(smem_addr(&bars->s_full[jq & 1]), elected);
+                }
+                rq.next();
+                ++jq;
+                --left_q;
+            } else if (jo < jq) {
+                if (left_o == 0) {
+                    if (!part_at(to, s)) break;
+                    left_o = s.end - s.begin;
+                    ring.next();
+                    ++to;
+                    fresh = true;
+                }
+                const uint32_t turn = turns >> ring.s & 1u;
+                if (!warp_wait(smem_addr(&bars->refilled[ring.s]), turn, ok)) break;
+                if (rank != 0) {
+                    if (lane == 0) mbar_arrive_cluster(map_rank(smem_addr(&bars->peer_refilled[ring.s]), 0));
+                } else {
+                    if (!warp_wait(smem_addr(&bars->peer_refilled[ring.s]), turn, ok)) break;
+                    if (!warp_wait(smem_addr(&bars->p_full), jo & 1, ok)) break;
+                    if (fresh && to > 1 && !warp_wait(smem_addr(&bars->o_free), to & 1, ok)) break;   // of part to - 2
+                    tc_fence_after_sync();
+                    const uint32_t b = v_lo + ring.s * (kStageBytes >> 4);
+                    if (elected) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {            // 16 rows; k / 4: of which CTA
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)          // 128 of each CTA's 256 dims
+                                mma_bf16_ss_pair(tmem + 128 * h, desc_at(p_desc0, p_lo + (((k >> 2) * kBlockBytes + (k & 3) * 32) >> 4)),
+                                                 desc_at(v_desc0, b + (((k >> 2) * kHalfBytes + (k & 3) * 2048 + h * 2 * kBlockBytes) >> 4)),
+                                                 kIdescO, k != 0 || !fresh);
+                        }
+                    }
+                    __syncwarp();
+                    mma_commit_pair(smem_addr(&bars->empty[ring.s]), elected);
+                }
+                turns ^= 1u << ring.s;
+                ring.next();
+                ++jo;
+                --left_o;
+                fresh = false;
+            } else {
+                break;
             }
         }
         // whatever ended the loop, no product is under way when the pair leaves
@@ -542,11 +643,150 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             if (!wait_landed(smem_addr(&bars->drained), 0)) ok = false;
             __syncwarp();
         }
+    } else if (warp >= kFirstMove) {
+        // ------------------------------------------------------------- results
+        // Warp w has tensor-memory lanes 32 (w % 4) .. and half w / 4 of what is in them: lane L is
+        // row L % 64 of this CTA and of the output the dims 256 (L / 64) ...  The rows leave
+        // through the stage of the next tile's query, once that is copied to tensor memory.
+        const int quarter = warp & 3, part = (warp - kFirstMove) >> 2, half = quarter >> 1;
+        const int row = (warp & 1) * 32 + lane;
+        const int in_tile = static_cast<int>(rank) * kCtaRows + row;
+        const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t o_free = map_rank(smem_addr(&bars->o_free), 0);
+        const bool first = threadIdx.x == kFirstMove * 32;
+        if (first && rank == 0) p.meta[pair] = make_int4(0, 0, 0, 0);
+        auto all_sync = [&]() { group_sync(kMoveBar, kMoveWarps * 32); };
+        // Where part `s` goes: the results, or a piece (slot 1: it begins its tile).
+        auto slot_of = [&](const Part& s) -> int { return s.begin == 0 ? 1 : 0; };
+        auto whole_of = [&](const Part& s) -> bool { return s.begin == 0 && s.end == s.chunks; };
+        auto first_of = [&](const Part& s) -> int64_t {
+            return whole_of(s) ? s.row0 : (2 * pair + slot_of(s)) * p.slot_rows;
+        };
+        auto note = [&](const Part& s) {   // for the kernel that joins
+            if (!first || rank != 0 || whole_of(s)) return;
+            int4 mark = p.meta[pair];
+            if (slot_of(s) == 0) {
+                mark.z |= kHeadThere | (s.end == s.chunks ? kHeadEnds : 0);
+            } else {
+                mark.x = static_cast<int32_t>(s.row0);
+                mark.y = s.rows;
+                mark.z |= kTailOpen;
+            }
+            p.meta[pair] = mark;
+        };
+        auto set_lse = [&](const Part& s, float v) {
+            if (half == 0 && part == 0 && in_tile < s.rows) (whole_of(s) ? p.lse : p.piece_lse)[first_of(s) + in_tile] = v;
+        };
+        Part s, n;
+        int tile = 0;
+        bool more = part_at(0, s);
+        if (more) {
+            // the first query's stage has no results to wait for
+            if (warp_wait(smem_addr(&bars->copied[0]), 0, ok) && first) mbar_arrive(smem_addr(&bars->empty[0]));
+            ring.next();
+        }
+        ok = !group_any(kMoveBar, kMoveWarps * 32, !ok);   // all movers leave together
+#pragma unroll 1
+        while (more && ok) {
+            ring.skip(s.end - s.begin - 1);
+            const Ring<kStages> last = ring;    // of the tile's chunks
+            ring.next();                        // of the next query, if there is one
+            more = part_at(tile + 1, n);
+            if (more) warp_wait(smem_addr(&bars->copied[(tile + 1) & 1]), ((tile + 1) >> 1) & 1, ok);
+            // The last value product implies everything before it.  The movers agree on it, so that
+            // a row is written in full or not at all.
+            if (ok) warp_wait(smem_addr(&bars->stats[tile & 1]), (tile >> 1) & 1, ok);
+            if (ok) warp_wait(smem_addr(&bars->empty[last.s]), last.parity, ok);
+            ok = !group_any(kMoveBar, kMoveWarps * 32, !ok);
+            if (!ok) break;
+            tc_fence_after_sync();
+            float inv, lse2;
+            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(inv), "=f"(lse2)
+                         : "r"(smem_addr(smem) + kOffStats + (tile & 1) * 512 + 8 * row) : "memory");
+            const uint32_t stage = smem_addr(smem) + kOffStages + ring.s * kStageBytes;
+            const uint32_t out_row = stage + row * kRowBytes, turn = (row & 7) << 4;
+            const int rows = s.rows - static_cast<int>(rank) * kCtaRows;      // of this CTA
+            if (whole_of(s) && p.wide == 0) {
+                // bf16: eight blocks of 64 dims, as the query's
+#pragma unroll 1
+                for (int d = 0; d < 128; d += 32) {
+                    float t[32];
+                    tmem_ld32(tmem + lanes + 128 * part + d, t);
+                    const uint32_t to = out_row + (4 * half + 2 * part + (d >> 6)) * kBlockBytes + ((d & 32) << 1 ^ turn);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) sts16(to ^ (i << 4), pack8(t + 8 * i, inv));
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(o_free);
+                fence_async_smem();
+                all_sync();
+                if (rows >= kCtaRows) {
+                    if (first) {
+                        tma_store_3d(&out_map, stage, 0, static_cast<int32_t>(s.row0 + rank * kCtaRows), 0);
+                        tma_store_3d(&out_map, stage + kHalfBytes, 0, static_cast<int32_t>(s.row0 + rank * kCtaRows), 4);
+                        bulk_commit();
+                        bulk_wait_read_all();
+                    }
+                } else {
+                    // rows of the request only
+                    uint8_t* const dst = static_cast<uint8_t*>(p.out) + (s.row0 + rank * kCtaRows) * 1024;
+                    copy_rows(stage, dst, 1024, rows, warp - kFirstMove, lane);
+                }
+            } else {
+                // fp32: 256 dims at a time, of which warps of the same lanes' half hold 128 each
+                uint8_t* const dst = (whole_of(s) ? static_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(p.pieces)) +
+                                     (first_of(s) + rank * kCtaRows) * 2048;
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    if (half == h) {
+#pragma unroll 1
+                        for (int d = 0; d < 128; d += 32) {
+                            float t[32];
+                            tmem_ld32(tmem + lanes + 128 * part + d, t);
+                            const uint32_t to = out_row + (4 * part + (d >> 5)) * kBlockBytes + turn;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                sts16(to ^ (i << 4), make_uint4(__float_as_uint(__fmul_rn(t[4 * i], inv)),
+                                                                __float_as_uint(__fmul_rn(t[4 * i + 1], inv)),
+                                                                __float_as_uint(__fmul_rn(t[4 * i + 2], inv)),
+                                                                __float_as_uint(__fmul_rn(t[4 * i + 3], inv))));
+                        }
+                        tc_fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(o_free);
+                    }
+                    all_sync();
+                    copy_rows(stage, dst + h * 1024, 2048, rows, warp - kFirstMove, lane);
+                    if (h == 0) all_sync();   // read before the other half comes
+                }
+            }
+            fence_async_smem();   // what was read is read, before TMA writes there
+            all_sync();
+            if (first && more) mbar_arrive(smem_addr(&bars->empty[ring.s]));
+            set_lse(s, whole_of(s) && p.wide == 0 ? __fmul_rn(lse2, kLn2) : lse2);
+            note(s);
+            s = n;
+            ++tile;
+            ring.next();
+        }
+        if (first) bulk_wait_all();
+        __syncwarp();
+        if (!ok) {
+            // a wait gave up: what this pair has not written is marked
+            Walk walk;
+            walk.init(p, bars);
+            for (int skip = tile; walk.next(p, s);) {
+                if (s.chunks > 0 && skip-- > 0) continue;
+                set_lse(s, __uint_as_float(kUnwritten));
+                note(s);
+            }
+        }
     } else {
-        // ------------------------------------------------------------- softmax, epilogue
-        // Tensor-memory lane L: row L % 64 of this CTA; of a chunk the rows of CTA L / 64; of the
-        // output the dims 256 (L / 64) ...  Two warps share a lane, one for each half of its
-        // columns, so four threads have a row; they exchange maxima and sums.
+        // ------------------------------------------------------------- softmax
+        // Tensor-memory lane L: row L % 64 of this CTA; of a chunk the rows of CTA L / 64.  Two warps
+        // share a lane, one for each half of its columns, so four threads have a row; they
+        // exchange maxima and sums.
         const int quarter = warp & 3, part = warp >> 2;
         const int row = (warp & 1) * 32 + lane;
         const int half = quarter >> 1;
@@ -555,55 +795,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         const int self = (part * 2 + half) * 64;
         const uint32_t s_free = map_rank(smem_addr(&bars->s_free), 0);
         const uint32_t p_full = map_rank(smem_addr(&bars->p_full), 0);
-        const uint32_t q_full = map_rank(smem_addr(&bars->q_full), 0);
         const float scale = __fmul_rn(p.sm_scale, kLog2e);   // logits in powers of two
         const uint32_t stages = smem_addr(smem) + kOffStages;
-        // this thread's 64 bytes of the probabilities; those of the warp's rows leave through them
-        const uint32_t p_half = smem_addr(smem) + kOffP + half * kBlockBytes;
-        const uint32_t prow = p_half + row * kRowBytes + ((part * 4 ^ (row & 7)) << 4);
+        // this thread's 64 bytes of the probabilities
+        const uint32_t prow = smem_addr(smem) + kOffP + half * kBlockBytes + row * kRowBytes + ((part * 4 ^ (row & 7)) << 4);
+        const int32_t column = half * kCtaKeys + part * 32;   // of the chunk
         auto head_sync = [&]() { group_sync(kHeadsBar + (warp & 1), 128); };
         auto head_any = [&](bool mine) -> bool { return group_any(kHeadsBar + (warp & 1), 128, mine); };
-        if (threadIdx.x == 0 && rank == 0) p.meta[pair] = make_int4(0, 0, 0, 0);
-
-        // The next segment with chunks; tiles that see no row are written on the way.
-        auto advance = [&](Segment& n) -> bool {
-            while (walk.next(p, n)) {
-                if (n.chunks > 0) return true;
-                const int rows = min(kCtaRows, n.rows - static_cast<int>(rank) * kCtaRows);
-                const int64_t at = n.r.row0 + n.row0 + rank * kCtaRows;
-                const int64_t bytes = p.wide != 0 ? 2048 : 1024;
-                for (int64_t i = threadIdx.x * INT64_C(16); i < rows * bytes; i += kSoftmaxWarps * 32 * 16)
-                    st16(static_cast<uint8_t*>(p.out) + at * bytes + i, make_uint4(0u, 0u, 0u, 0u));
-                if (static_cast<int>(threadIdx.x) < rows) p.lse[at + threadIdx.x] = -INFINITY;
-            }
-            return false;
-        };
-        // The query tile that is the ring's next item to where q . K reads it.
-        auto query = [&]() {
-            if (ok && warp_wait(smem_addr(&bars->full[ring.s]), ring.parity, ok))
-                take_query(stages + ring.s * kStageBytes, row, part, half, tmem + lanes + kQCol, smem_addr(smem));
-            fence_async_smem();   // what was read is read, before TMA writes there
-            tc_fence_before_sync();
-            ok = !group_any(kSoftmaxBar, kSoftmaxWarps * 32, !ok);
-            if (threadIdx.x == 0 && ok) mbar_arrive(smem_addr(&bars->empty[ring.s]));
-            if (lane == 0 && ok) mbar_arrive_cluster(q_full);
-            ring.next();
-        };
-
-        Segment n;
-        bool more = advance(n);
-        if (more) query();
-        int j = 0;
         uint32_t turns = 0;        // bit s: parity of the chunks so far in stage s
+        int j = 0;
+        Ring<kStages> last;        // the stage of the chunk before
+        Part s;
 #pragma unroll 1
-        while (more) {
-            s = n;
+        for (int tile = 0;; ++tile) {
+            const bool some = part_at(tile, s);
+            ok = !head_any(!ok);       // a row's four warps leave together
+            if (!ok || !some) break;
+            ring.next();               // the query tile
             float m = -INFINITY, l = 0.0f;
-            Ring<kStages> last;        // the stage of the chunk before
-            const int32_t my_row = s.row0 + static_cast<int32_t>(rank) * kCtaRows + row;   // of the request
-            const int32_t see = sees(p, s.r, min(my_row, s.r.rows - 1));
-            const int32_t least = sees(p, s.r, s.row0);   // of the tile's rows
-            const int32_t column = half * kCtaKeys + part * 32;   // of the chunk
+            const uint32_t in_tile = rank * kCtaRows + row;
+            const int32_t see = p.causal == 0 ? s.keys
+                                              : clamped(s.see + (s.offset + in_tile) / static_cast<uint32_t>(p.num_heads), s.keys);
 #pragma unroll 1
             for (int c = s.begin; c < s.end; ++c, ++j) {
                 const bool fresh = c == s.begin;
@@ -621,8 +833,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
                 __syncwarp();
                 if (lane == 0 && ok) mbar_arrive_cluster(s_free);
                 // columns that some row of the tile does not see
-                if (key + 32 > least) {
-                    const int64_t from = least - key;
+                if (key + 32 > s.least) {
+                    const int64_t from = s.least - key;
                     uint32_t odd = 0;
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
@@ -692,7 +904,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
                 f32x2_split(sum2, sum_a, sum_b);
                 l = __fadd_rn(l, __fadd_rn(sum_a, sum_b));
                 // the chunk before is multiplied: its probabilities are read
-                if (!fresh && ok) warp_wait(smem_addr(&bars->empty[last.s]), last.parity, ok);
+                if (j > 0 && ok) warp_wait(smem_addr(&bars->empty[last.s]), last.parity, ok);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) sts16(prow ^ (i << 4), pack8(v + 8 * i));
                 fence_async_smem();
@@ -703,77 +915,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
                 turns ^= 1u << ring.s;
                 ring.next();
             }
-            // q . K of this tile is complete: the next query tile may take its place, and is
-            // multiplied while this one's results are written
-            more = advance(n);
-            if (more) query();
             heads[self] = l;
             head_sync();
             const float total = __fadd_rn(__fadd_rn(heads[0], heads[64]), __fadd_rn(heads[128], heads[192]));
-            // The last value product implies everything before it.  A row's warps agree on it, so
-            // that it is written in full or not at all.  (The barrier also puts the other lanes'
-            // accesses behind lane 0's wait, and the next sums behind the reads of these.)
-            if (ok) warp_wait(smem_addr(&bars->empty[last.s]), last.parity, ok);
-            ok = !head_any(!ok);
-            tc_fence_after_sync();
-            const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
-            const bool whole = s.begin == 0 && s.end == s.chunks;
-            const float lse2 = total == 0.0f ? -INFINITY : __fadd_rn(__fsub_rn(m, kLift), log2f(total));
-            const int64_t first_row = s.r.row0 + s.row0;
-            const int slot = s.begin == 0 ? 1 : 0;
-            if (!whole && threadIdx.x == 0 && rank == 0) {
-                int4 mark = p.meta[pair];
-                if (slot == 0) {
-                    mark.z |= kHeadThere | (s.end == s.chunks ? kHeadEnds : 0);
-                } else {
-                    mark.x = static_cast<int32_t>(first_row);
-                    mark.y = s.rows;
-                    mark.z |= kTailOpen;
-                }
-                p.meta[pair] = mark;
+            head_sync();   // read before they are written again
+            if (half == 0 && part == 0) {
+                const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
+                const float lse2 = total == 0.0f ? -INFINITY : __fadd_rn(__fsub_rn(m, kLift), log2f(total));
+                asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(smem_addr(smem) + kOffStats + (tile & 1) * 512 + 8 * row),
+                             "f"(inv),
+                             "f"(lse2) : "memory");
             }
-            const bool narrow = whole && p.wide == 0;
-            const int64_t at = whole ? first_row : (2 * pair + slot) * p.slot_rows;
-            const int64_t dst_row = narrow ? 1024 : 2048;
-            uint8_t* const dst = (whole ? static_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(p.pieces)) +
-                                 at * dst_row + (2 * half + part) * (dst_row >> 2);
-            const int rows = ok ? s.rows : 0;
-            const int row0 = static_cast<int>(rank) * kCtaRows + (warp & 1) * 32;
-            const int step = narrow ? 32 : 16;
-#pragma unroll 1
-            for (int d = 0; d < 128; d += step) {           // 64 bytes of each row
-                float t[16];
-                tmem_ld16(tmem + lanes + 128 * part + d, t);
-                if (narrow) {
-                    sts16(prow, pack8(t, inv));
-                    sts16(prow ^ 16u, pack8(t + 8, inv));
-                    tmem_ld16(tmem + lanes + 128 * part + d + 16, t);
-                    sts16(prow ^ 32u, pack8(t, inv));
-                    sts16(prow ^ 48u, pack8(t + 8, inv));
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        sts16(prow ^ (i << 4), make_uint4(__float_as_uint(__fmul_rn(t[4 * i], inv)),
-                                                          __float_as_uint(__fmul_rn(t[4 * i + 1], inv)),
-                                                          __float_as_uint(__fmul_rn(t[4 * i + 2], inv)),
-                                                          __float_as_uint(__fmul_rn(t[4 * i + 3], inv))));
-                }
-                __syncwarp();
-                // four lanes write 64 bytes of one row
-                uint8_t* const to = dst + d * (narrow ? 2 : 4) + (lane & 3) * 16;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 8 * i + (lane >> 2), in_cta = (warp & 1) * 32 + r;
-                    const uint4 x = lds16_at(p_half + in_cta * kRowBytes + (((part * 4 + (lane & 3)) ^ (r & 7)) << 4));
-                    if (row0 + r < rows) st16(to + (row0 + r) * dst_row, x);
-                }
-                __syncwarp();
-            }
-            if (half == 0 && part == 0 && row0 + lane < s.rows) {
-                float* const to = whole ? p.lse : p.piece_lse;
-                to[at + row0 + lane] = !ok ? __uint_as_float(kUnwritten) : narrow ? __fmul_rn(lse2, kLn2) : lse2;
-            }
-            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0 && ok) mbar_arrive(smem_addr(&bars->stats[tile & 1]));
         }
     }
     if (!ok) bars->timed_out = 1;
@@ -900,14 +1054,14 @@ __global__ void __launch_bounds__(kJoinRows * 32) merge_kernel(const MergeArgs p
 // ---------------------------------------------------------------- host
 
 // `rows` rows of 512 bf16 (`stride` bytes apart) as a 3-D tensor map of 64 dims x rows x 8 blocks of
-// dims, with boxes of 64 rows of four blocks: one load brings half the dims of 64 rows as four
+// dims, with boxes of 64 rows of `blocks` blocks: one load brings those dims of 64 rows as so many
 // operand blocks.  Rows past the last read as zeros.
-cudaError_t rows_tensor_map(const void* base, int64_t rows, int64_t stride, CUtensorMap* map) {
+cudaError_t rows_tensor_map(const void* base, int64_t rows, int64_t stride, uint32_t blocks, CUtensorMap* map) {
     const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (encode == nullptr) return cudaErrorNotSupported;
     const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), 8};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(stride), 128};
-    const cuuint32_t box[3] = {64, kCtaRows, 4};
+    const cuuint32_t box[3] = {64, kCtaRows, blocks};
     const cuuint32_t step[3] = {1, 1, 1};
     const CUresult r =
         encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step,
@@ -940,13 +1094,17 @@ cudaError_t launch_tiles(TileArgs a, const void* q, const void* kv, int64_t kv_s
     a.pieces = reinterpret_cast<float*>(workspace);
     a.piece_lse = reinterpret_cast<float*>(workspace + n * 2048);
     a.meta = reinterpret_cast<int4*>(workspace + n * 2048 + up16(n * 4));
-    CUtensorMap q_map, k_map;
-    e = rows_tensor_map(q, rows, 1024, &q_map);
+    CUtensorMap q_map, tail_map, k_map, out_map;
+    // no rows: nothing is loaded by their map; fp32 results do not leave by theirs
+    e = rows_tensor_map(q, rows, 1024, 4, &q_map);
+    if (e == cudaSuccess) e = rows_tensor_map(q, rows, 1024, 8 - kQTmemBlocks, &tail_map);
+    if (e == cudaSuccess)
+        e = a.num_rows > 0 ? rows_tensor_map(kv, a.num_rows, kv_stride * 2, 4, &k_map)
+                           : rows_tensor_map(q, rows, 1024, 4, &k_map);
+    if (e == cudaSuccess) e = rows_tensor_map(a.out, rows, 1024, 4, &out_map);
     if (e != cudaSuccess) return e;
-    // no rows: nothing is loaded by the map
-    e = a.num_rows > 0 ? rows_tensor_map(kv, a.num_rows, kv_stride * 2, &k_map) : rows_tensor_map(q, rows, 1024, &k_map);
-    if (e != cudaSuccess) return e;
-    e = launch_kernel(tile_kernel, 2 * static_cast<int64_t>(pairs), kTileThreads, kTileSmem, stream, pdl, a, q_map, k_map);
+    e = launch_kernel(tile_kernel, 2 * static_cast<int64_t>(pairs), kTileThreads, kTileSmem, stream, pdl, a, q_map,
+                      tail_map, k_map, out_map);
     if (e != cudaSuccess) return e;
     const int64_t blocks = static_cast<int64_t>(pairs) * ((a.slot_rows + kJoinRows - 1) / kJoinRows);
     return launch_kernel(tile_join_kernel, blocks, kJoinRows * 32, 0, stream, pdl, a, pairs);
