@@ -345,15 +345,16 @@ __device__ __noinline__ void clear_row(uint32_t half, int row, int lane) {
     if (found) sts16(at, v);
 }
 
-// `rows` rows of 1 KB from a stage (eight swizzled blocks of 128 bytes) to global memory, `stride` bytes
-// apart; eight warps.
-__device__ __forceinline__ void copy_rows(uint32_t stage, uint8_t* dst, int64_t stride, int rows, int warp, int lane) {
-#pragma unroll 2
-    for (int r = warp; r < min(rows, kCtaRows); r += kMoveWarps) {
-        const uint32_t at = stage + (lane >> 3) * kBlockBytes + r * kRowBytes + (((lane ^ r) & 7) << 4);
-        const uint4 a = lds16_at(at), b = lds16_at(at + 4 * kBlockBytes);
-        st16(dst + r * stride + 16 * lane, a);
-        st16(dst + r * stride + 512 + 16 * lane, b);
+// `rows` rows of 256 bytes from two swizzled blocks of 32 rows to global memory, `stride` bytes apart; a
+// warp.
+constexpr uint32_t kMoveBlock = 32 * kRowBytes;
+__device__ __forceinline__ void copy_rows(uint32_t from, uint8_t* dst, int64_t stride, int rows, int lane) {
+    const uint32_t block = from + (lane >> 3 & 1) * kMoveBlock;
+#pragma unroll 4
+    for (int i = 0; i < 16; ++i) {
+        const int r = 2 * i + (lane >> 4);
+        const uint4 x = lds16_at(block + r * kRowBytes + (((lane ^ r) & 7) << 4));
+        if (r < rows) st16(dst + r * stride + 16 * (lane & 15), x);
     }
 }
 
@@ -655,7 +656,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         const uint32_t o_free = map_rank(smem_addr(&bars->o_free), 0);
         const bool first = threadIdx.x == kFirstMove * 32;
         if (first && rank == 0) p.meta[pair] = make_int4(0, 0, 0, 0);
-        auto all_sync = [&]() { group_sync(kMoveBar, kMoveWarps * 32); };
         // Where part `s` goes: the results, or a piece (slot 1: it begins its tile).
         auto slot_of = [&](const Part& s) -> int { return s.begin == 0 ? 1 : 0; };
         auto whole_of = [&](const Part& s) -> bool { return s.begin == 0 && s.end == s.chunks; };
@@ -703,66 +703,64 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             float inv, lse2;
             asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(inv), "=f"(lse2)
                          : "r"(smem_addr(smem) + kOffStats + (tile & 1) * 512 + 8 * row) : "memory");
-            const uint32_t stage = smem_addr(smem) + kOffStages + ring.s * kStageBytes;
-            const uint32_t out_row = stage + row * kRowBytes, turn = (row & 7) << 4;
-            const int rows = s.rows - static_cast<int>(rank) * kCtaRows;      // of this CTA
+            // Each warp by itself: its 32 rows and 128 dims through 8 KB of the stage, in two blocks of
+            // 128 bytes a row, swizzled.
+            const uint32_t mine = smem_addr(smem) + kOffStages + ring.s * kStageBytes + (warp - kFirstMove) * 2 * kMoveBlock;
+            const uint32_t to = mine + lane * kRowBytes + ((lane & 7) << 4);
+            const int row0 = static_cast<int>(rank) * kCtaRows + (warp & 1) * 32;   // of the tile
+            const int rows = min(s.rows - row0, 32);
             if (whole_of(s) && p.wide == 0) {
-                // bf16: eight blocks of 64 dims, as the query's
 #pragma unroll 1
-                for (int d = 0; d < 128; d += 32) {
-                    float t[32];
-                    tmem_ld32(tmem + lanes + 128 * part + d, t);
-                    const uint32_t to = out_row + (4 * half + 2 * part + (d >> 6)) * kBlockBytes + ((d & 32) << 1 ^ turn);
+                for (int b = 0; b < 2; ++b) {       // 64 dims, bf16
+#pragma unroll 1
+                    for (int h = 0; h < 2; ++h) {
+                        float t[32];
+                        tmem_ld32(tmem + lanes + 128 * part + 64 * b + 32 * h, t);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sts16(to ^ (i << 4), pack8(t + 8 * i, inv));
+                        for (int i = 0; i < 4; ++i) sts16((to ^ ((4 * h + i) << 4)) + b * kMoveBlock, pack8(t + 8 * i, inv));
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (rows == 32 && lane == 0) {
+                        tma_store_3d(&out_map, mine + b * kMoveBlock, 0, static_cast<int32_t>(s.row0 + row0),
+                                     4 * half + 2 * part + b);
+                        bulk_commit();
+                    }
                 }
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(o_free);
-                fence_async_smem();
-                all_sync();
-                if (rows >= kCtaRows) {
-                    if (first) {
-                        tma_store_3d(&out_map, stage, 0, static_cast<int32_t>(s.row0 + rank * kCtaRows), 0);
-                        tma_store_3d(&out_map, stage + kHalfBytes, 0, static_cast<int32_t>(s.row0 + rank * kCtaRows), 4);
-                        bulk_commit();
-                        bulk_wait_read_all();
-                    }
-                } else {
-                    // rows of the request only
-                    uint8_t* const dst = static_cast<uint8_t*>(p.out) + (s.row0 + rank * kCtaRows) * 1024;
-                    copy_rows(stage, dst, 1024, rows, warp - kFirstMove, lane);
-                }
+                if (rows < 32)   // the request's only
+                    copy_rows(mine, static_cast<uint8_t*>(p.out) + (s.row0 + row0) * 1024 + (2 * half + part) * 256, 1024,
+                              rows, lane);
             } else {
-                // fp32: 256 dims at a time, of which warps of the same lanes' half hold 128 each
                 uint8_t* const dst = (whole_of(s) ? static_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(p.pieces)) +
-                                     (first_of(s) + rank * kCtaRows) * 2048;
+                                     (first_of(s) + row0) * 2048 + (2 * half + part) * 512;
 #pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
-                    if (half == h) {
+                for (int b = 0; b < 2; ++b) {       // 64 dims, fp32
 #pragma unroll 1
-                        for (int d = 0; d < 128; d += 32) {
-                            float t[32];
-                            tmem_ld32(tmem + lanes + 128 * part + d, t);
-                            const uint32_t to = out_row + (4 * part + (d >> 5)) * kBlockBytes + turn;
+                    for (int h = 0; h < 2; ++h) {
+                        float t[32];
+                        tmem_ld32(tmem + lanes + 128 * part + 64 * b + 32 * h, t);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                sts16(to ^ (i << 4), make_uint4(__float_as_uint(__fmul_rn(t[4 * i], inv)),
-                                                                __float_as_uint(__fmul_rn(t[4 * i + 1], inv)),
-                                                                __float_as_uint(__fmul_rn(t[4 * i + 2], inv)),
-                                                                __float_as_uint(__fmul_rn(t[4 * i + 3], inv))));
-                        }
-                        tc_fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(o_free);
+                        for (int i = 0; i < 8; ++i)
+                            sts16((to ^ (i << 4)) + h * kMoveBlock, make_uint4(__float_as_uint(__fmul_rn(t[4 * i], inv)),
+                                                                               __float_as_uint(__fmul_rn(t[4 * i + 1], inv)),
+                                                                               __float_as_uint(__fmul_rn(t[4 * i + 2], inv)),
+                                                                               __float_as_uint(__fmul_rn(t[4 * i + 3], inv))));
                     }
-                    all_sync();
-                    copy_rows(stage, dst + h * 1024, 2048, rows, warp - kFirstMove, lane);
-                    if (h == 0) all_sync();   // read before the other half comes
+                    __syncwarp();
+                    copy_rows(mine, dst + b * 256, 2048, rows, lane);
+                    __syncwarp();   // read before it is written again
                 }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(o_free);
             }
-            fence_async_smem();   // what was read is read, before TMA writes there
-            all_sync();
+            // what was read is read, before TMA writes there
+            if (lane == 0) bulk_wait_read_all();
+            fence_async_smem();
+            group_sync(kMoveBar, kMoveWarps * 32);
             if (first && more) mbar_arrive(smem_addr(&bars->empty[ring.s]));
             set_lse(s, whole_of(s) && p.wide == 0 ? __fmul_rn(lse2, kLn2) : lse2);
             note(s);
@@ -770,7 +768,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             ++tile;
             ring.next();
         }
-        if (first) bulk_wait_all();
+        if (lane == 0) bulk_wait_all();
         __syncwarp();
         if (!ok) {
             // a wait gave up: what this pair has not written is marked
@@ -1054,14 +1052,15 @@ __global__ void __launch_bounds__(kJoinRows * 32) merge_kernel(const MergeArgs p
 // ---------------------------------------------------------------- host
 
 // `rows` rows of 512 bf16 (`stride` bytes apart) as a 3-D tensor map of 64 dims x rows x 8 blocks of
-// dims, with boxes of 64 rows of `blocks` blocks: one load brings those dims of 64 rows as so many
+// dims, with boxes of `box_rows` rows of `blocks` blocks: one load brings those dims of the rows as so many
 // operand blocks.  Rows past the last read as zeros.
-cudaError_t rows_tensor_map(const void* base, int64_t rows, int64_t stride, uint32_t blocks, CUtensorMap* map) {
+cudaError_t rows_tensor_map(const void* base, int64_t rows, int64_t stride, uint32_t box_rows, uint32_t blocks,
+                            CUtensorMap* map) {
     const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
     if (encode == nullptr) return cudaErrorNotSupported;
     const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), 8};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(stride), 128};
-    const cuuint32_t box[3] = {64, kCtaRows, blocks};
+    const cuuint32_t box[3] = {64, box_rows, blocks};
     const cuuint32_t step[3] = {1, 1, 1};
     const CUresult r =
         encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step,
@@ -1096,12 +1095,12 @@ cudaError_t launch_tiles(TileArgs a, const void* q, const void* kv, int64_t kv_s
     a.meta = reinterpret_cast<int4*>(workspace + n * 2048 + up16(n * 4));
     CUtensorMap q_map, tail_map, k_map, out_map;
     // no rows: nothing is loaded by their map; fp32 results do not leave by theirs
-    e = rows_tensor_map(q, rows, 1024, 4, &q_map);
-    if (e == cudaSuccess) e = rows_tensor_map(q, rows, 1024, 8 - kQTmemBlocks, &tail_map);
+    e = rows_tensor_map(q, rows, 1024, kCtaRows, 4, &q_map);
+    if (e == cudaSuccess) e = rows_tensor_map(q, rows, 1024, kCtaRows, 8 - kQTmemBlocks, &tail_map);
     if (e == cudaSuccess)
-        e = a.num_rows > 0 ? rows_tensor_map(kv, a.num_rows, kv_stride * 2, 4, &k_map)
-                           : rows_tensor_map(q, rows, 1024, 4, &k_map);
-    if (e == cudaSuccess) e = rows_tensor_map(a.out, rows, 1024, 4, &out_map);
+        e = a.num_rows > 0 ? rows_tensor_map(kv, a.num_rows, kv_stride * 2, kCtaKeys, 4, &k_map)
+                           : rows_tensor_map(q, rows, 1024, kCtaRows, 4, &k_map);
+    if (e == cudaSuccess) e = rows_tensor_map(a.out, rows, 1024, 32, 1, &out_map);
     if (e != cudaSuccess) return e;
     e = launch_kernel(tile_kernel, 2 * static_cast<int64_t>(pairs), kTileThreads, kTileSmem, stream, pdl, a, q_map,
                       tail_map, k_map, out_map);
