@@ -669,6 +669,7 @@ GKR_API gkr_status gkr_prompt_attention(const void* q, int32_t num_heads, int64_
     if (st != GKR_OK) return st;
     if (!prompt_rows_ok(num_heads, num_tokens) || num_rows < 0 || num_rows > kMaxPromptRows ||
         kv_stride < 512 || kv_stride > (INT64_C(1) << 34) || kv_stride % 8 != 0 ||
+        num_rows > (INT64_C(1) << 37) / num_heads ||
         num_requests < 0 || num_requests > gkr::kPlanMaxRequests || causal < 0 || causal > 1 ||
         !finite(sm_scale))
         return GKR_EINVAL;

@@ -117,10 +117,7 @@ struct alignas(8) TileBarriers {
     uint64_t part[kParts];         // a part of the pair's work is described
     uint64_t stats[2];             // softmax: a tile's sums and log-sum-exps are there
     uint64_t drained;              // every product that was issued is complete
-    // the pair's first unit: request, tile of it, unit of the tile; how many there are
-    int64_t units, at;
-    int64_t sums[kTileThreads / 32];
-    int32_t request, tile, unit;
+    int64_t sums[kTileThreads / 32];   // of the requests' units, if they are many
     uint32_t tmem_base;
     volatile int32_t timed_out;
     Part parts[kParts];
@@ -131,6 +128,8 @@ static_assert(kTileSmem <= 227 * 1024, "a CTA's shared memory");
 // Arguments of the tile kernel.
 struct TileArgs {
     int32_t num_heads;
+    uint32_t heads_shift;
+    uint64_t heads_magic;        // x / num_heads = (x * heads_magic) >> heads_shift for x < 2^31
     int64_t num_tokens, num_rows;
     const int32_t* starts;       // null: one request, all queries and rows
     const int32_t* kv_starts;
@@ -152,8 +151,10 @@ struct TileArgs {
 // with (x: its first row, y: its rows); slot 0, a tile begun before, which it ended or not.
 constexpr int kTailOpen = 1, kHeadThere = 2, kHeadEnds = 4;
 
-// A unit less than this many for each pair is not worth another piece to join.
-constexpr int64_t kUnitsAPair = 3;
+// Work is counted in units of half a chunk; a tile costs kTileUnits besides its chunks.
+constexpr int kTileUnits = 4;
+// Fewer units than this for each pair are not worth another piece to join.
+constexpr int64_t kUnitsAPair = 6;
 
 // A request's rows and its tiles' work.
 struct Request {
@@ -183,53 +184,54 @@ __device__ __forceinline__ Request request_at(const TileArgs& p, int b, bool& ba
     return r;
 }
 
+// row / num_heads by a multiply and a shift (row < 2^31).
+__device__ __forceinline__ int32_t query_of(const TileArgs& p, int32_t row) {
+    return static_cast<int32_t>((static_cast<uint64_t>(static_cast<uint32_t>(row)) * p.heads_magic) >> p.heads_shift);
+}
 __device__ __forceinline__ int32_t clamped(int64_t see, int32_t keys) {
     return static_cast<int32_t>(min(max(see, INT64_C(0)), static_cast<int64_t>(keys)));
 }
 // How many rows row `row` of a request sees.
 __device__ __forceinline__ int32_t sees(const TileArgs& p, const Request& r, int32_t row) {
     if (p.causal == 0) return r.keys;
-    return clamped(r.past + static_cast<uint32_t>(row) / static_cast<uint32_t>(p.num_heads) + 1, r.keys);
+    return clamped(r.past + query_of(p, row) + 1, r.keys);
+}
+__device__ __forceinline__ int32_t chunks_in(int32_t keys) {
+    return static_cast<int32_t>((static_cast<int64_t>(keys) + kChunk - 1) / kChunk);
 }
 // Chunks of a tile: what its last row sees.
 __device__ __forceinline__ int32_t chunks_of(const TileArgs& p, const Request& r, int32_t tile) {
-    const int32_t see = tile == r.tiles - 1 ? r.keys : sees(p, r, tile * kTileRows + kTileRows - 1);
-    return static_cast<int32_t>((static_cast<int64_t>(see) + kChunk - 1) / kChunk);
+    return chunks_in(tile == r.tiles - 1 ? r.keys : sees(p, r, tile * kTileRows + kTileRows - 1));
 }
 // Units of the request's first `tile` tiles (tile < tiles).  Causal: tile x, but for the last,
 // has max(0, ceil((past + floor((128 x + 127) / H) + 1) / 128)) chunks, which is
 // max(0, floor((x + c) / H)) with c = floor((127 + (past + 128) H) / 128), as a tile and a chunk
 // are both 128; and the sum of max(0, floor(y / H)) over y < z is H a (a - 1) / 2 + a (z - a H), a =
-// floor(z / H).
-__device__ __forceinline__ int64_t floors_below(int64_t z, int64_t h) {
+// floor(z / H).  (z < 2^31: the rows of K times H are at most 2^37.)
+__device__ __forceinline__ int64_t floors_below(const TileArgs& p, int64_t z) {
     if (z <= 0) return 0;
-    const int64_t a = z / h;
-    return h * (a * (a - 1) / 2) + a * (z - a * h);
+    const int64_t a = query_of(p, static_cast<int32_t>(z));
+    return p.num_heads * (a * (a - 1) / 2) + a * (z - a * p.num_heads);
 }
 __device__ __forceinline__ int64_t units_before(const TileArgs& p, const Request& r, int64_t tile) {
-    if (p.causal == 0) return tile * (1 + (static_cast<int64_t>(r.keys) + kChunk - 1) / kChunk);
-    const int64_t h = p.num_heads;
-    const int64_t c = (kTileRows - 1 + (r.past + kChunk) * h) >> 7;
-    return tile + floors_below(tile + c, h) - floors_below(c, h);
+    if (p.causal == 0) return tile * (kTileUnits + 2 * chunks_in(r.keys));
+    const int64_t c = (kTileRows - 1 + (r.past + kChunk) * p.num_heads) >> 7;
+    return kTileUnits * tile + 2 * (floors_below(p, tile + c) - floors_below(p, c));
 }
 __device__ __forceinline__ int64_t units_of(const TileArgs& p, const Request& r) {
     if (r.tiles == 0) return 0;
-    return units_before(p, r, r.tiles - 1) + 1 + (static_cast<int64_t>(r.keys) + kChunk - 1) / kChunk;
+    return units_before(p, r, r.tiles - 1) + kTileUnits + 2 * chunks_in(r.keys);
+}
+// The chunk of a tile where a cut at this unit of it falls.
+__device__ __forceinline__ int32_t chunk_at(int64_t unit) {
+    return unit <= kTileUnits ? 0 : static_cast<int32_t>((unit - kTileUnits + 1) >> 1);
 }
 
 // A pair's parts, one after another.
 struct Walk {
     Request r;
-    int64_t left;
-    int32_t b, tile, unit;
-    __device__ void init(const TileArgs& p, const TileBarriers* bars) {
-        b = bars->request;
-        tile = bars->tile;
-        unit = bars->unit;
-        left = bars->units;
-        bool bad = false;
-        if (left > 0) r = request_at(p, b, bad);
-    }
+    int64_t left, unit;     // units left; units of the tile that are behind
+    int32_t b, tile;
     // The next one; `chunks` 0 is a tile that sees no row here.
     __device__ bool next(const TileArgs& p, Part& s) {
         while (left > 0) {
@@ -246,86 +248,96 @@ struct Walk {
             s.k0 = r.k0;
             s.rows = min(kTileRows, r.rows - row);
             s.keys = r.keys;
-            const uint32_t query = static_cast<uint32_t>(row) / static_cast<uint32_t>(p.num_heads);
-            s.offset = row - static_cast<int32_t>(query) * p.num_heads;
+            const int32_t query = query_of(p, row);
+            s.offset = row - query * p.num_heads;
             s.see = p.causal == 0 ? r.keys : r.past + query + 1;
             s.least = clamped(s.see, r.keys);
             s.chunks = chunks_of(p, r, tile);
-            const int64_t take = min(left, static_cast<int64_t>(1 + s.chunks - unit));
-            s.begin = max(unit, 1) - 1;
-            s.end = static_cast<int32_t>(unit + take) - 1;
+            const int64_t all = kTileUnits + 2 * static_cast<int64_t>(s.chunks), first = unit;
+            const int64_t take = min(left, all - unit);
             left -= take;
-            unit += static_cast<int32_t>(take);
-            if (unit == 1 + s.chunks) {
+            unit += take;
+            s.begin = chunk_at(first);
+            s.end = chunk_at(unit);
+            if (unit == all) {
                 ++tile;
                 unit = 0;
             }
-            if (s.chunks == 0 || s.end > s.begin) return true;
+            if (s.chunks == 0 ? first == 0 : s.end > s.begin) return true;
         }
         return false;
     }
 };
 
-// The pair's first unit and how many it has, into `bars`: all threads sum up the requests' units
-// and find the request; then (after a barrier) a warp finds the tile.
-__device__ __forceinline__ void find_work(const TileArgs& p, TileBarriers* bars, int64_t pair, int64_t pairs) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int run = (p.num_requests + kTileThreads - 1) / kTileThreads;
-    const int first = min(p.num_requests, static_cast<int>(threadIdx.x) * run);
-    const int last = min(p.num_requests, first + run);
-    int64_t mine = 0;
+// The requests' units are summed up by one warp, or, if there are many, first by all warps, each of
+// them a run of requests per thread.
+constexpr int kFewRequests = 64;
+__device__ __forceinline__ int work_groups(const TileArgs& p) { return p.num_requests > kFewRequests ? kTileThreads / 32 : 1; }
+__device__ __forceinline__ int64_t run_units(const TileArgs& p, int group, int lane, int& first, int& last, bool& bad) {
+    const int run = (p.num_requests + 32 * work_groups(p) - 1) / (32 * work_groups(p));
+    first = min(p.num_requests, (32 * group + lane) * run);
+    last = min(p.num_requests, first + run);
+    int64_t units = 0;
+    for (int b = first; b < last; ++b) units += units_of(p, request_at(p, b, bad));
+    return units;
+}
+__device__ __forceinline__ int64_t warp_total(int64_t v) {
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+    return v;
+}
+
+// Where this pair's work begins and how much it is; a warp (sums: of the groups, if there are more
+// than one).
+__device__ __noinline__ void find_work(const TileArgs& p, const int64_t* sums, int64_t pair, int64_t pairs, Walk& walk) {
+    const int lane = threadIdx.x & 31, groups = work_groups(p);
+    int first = 0, last = 0;
     bool bad = false;
-    for (int b = first; b < last; ++b) mine += units_of(p, request_at(p, b, bad));
-    if (bad && blockIdx.x == 0) report(p.err, kErrIndex);
+    int64_t mine = groups == 1 ? run_units(p, 0, lane, first, last, bad) : lane < groups ? sums[lane] : 0;
+    const int64_t total = warp_total(mine);
+    // an even share, the first ones a unit more
+    pairs = max(INT64_C(1), min(pairs, total / kUnitsAPair));
+    const int64_t share = total >> 32 == 0 ? static_cast<uint32_t>(total) / static_cast<uint32_t>(pairs) : total / pairs;
+    const int64_t more = total - share * pairs, x0 = pair * share + min(pair, more);
+    walk.left = pair < pairs ? share + (pair < more ? 1 : 0) : 0;
+    walk.b = p.num_requests;
+    if (walk.left == 0) return;
+    int64_t before = 0;   // units of the groups, then of the lanes, before x0's
+    if (groups > 1) {
+        int g = 0;
+        for (; g < groups - 1 && before + sums[g] <= x0; ++g) before += sums[g];
+        mine = run_units(p, g, lane, first, last, bad);
+    }
     int64_t upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const int64_t o = __shfl_up_sync(kFull, upto, d);
         if (lane >= d) upto += o;
     }
-    if (lane == 31) bars->sums[warp] = upto;
-    __syncthreads();
-    int64_t before = upto - mine, total = 0;
-    for (int w = 0; w < kTileThreads / 32; ++w) {
-        const int64_t s = bars->sums[w];
-        if (w < warp) before += s;
-        total += s;
-    }
-    const int64_t most = (total + kUnitsAPair - 1) / kUnitsAPair;
-    if (most < pairs) pairs = most;
-    const int64_t x0 = pair < pairs ? total * pair / pairs : 0, x1 = pair < pairs ? total * (pair + 1) / pairs : 0;
-    if (threadIdx.x == 0) bars->units = x1 - x0;
-    if (x1 > x0 && x0 >= before && x0 < before + mine) {   // in this thread's run of requests
-        int64_t at = x0 - before;
-        for (int b = first; b < last; ++b) {
+    const int owner = __ffs(__ballot_sync(kFull, before + upto > x0)) - 1;
+    int64_t at = x0 - before - (upto - mine);
+    int b = first;
+    if (lane == owner) {
+        for (; b < last - 1; ++b) {
             const int64_t u = units_of(p, request_at(p, b, bad));
-            if (at < u) {
-                bars->request = b;
-                bars->at = at;
-                break;
-            }
+            if (at < u) break;
             at -= u;
         }
     }
-}
-__device__ __forceinline__ void find_tile(const TileArgs& p, TileBarriers* bars) {
-    const int lane = threadIdx.x & 31;
-    const int64_t at = bars->at;
-    bool bad = false;
-    const Request r = request_at(p, bars->request, bad);
-    int64_t lo = 0, hi = r.tiles;           // units_before(lo) <= at < units_before(hi)
+    walk.b = __shfl_sync(kFull, b, owner);
+    at = __shfl_sync(kFull, at, owner);
+    walk.r = request_at(p, walk.b, bad);
+    int64_t lo = 0, hi = walk.r.tiles;           // units_before(lo) <= at < units_before(hi)
     while (hi - lo > 1) {
-        const int64_t x = lo + (hi - lo) * lane / 32;
-        const uint32_t below = __ballot_sync(kFull, units_before(p, r, x) <= at);   // lane 0 always
+        const int64_t x = lo + ((hi - lo) * lane >> 5);
+        const uint32_t below = __ballot_sync(kFull, units_before(p, walk.r, x) <= at);   // lane 0 always
         const int n = __popc(below);
-        const int64_t l = lo + (hi - lo) * (n - 1) / 32, h = n == 32 ? hi : lo + (hi - lo) * n / 32;
+        const int64_t l = lo + ((hi - lo) * (n - 1) >> 5), h = n == 32 ? hi : lo + ((hi - lo) * n >> 5);
         lo = l;
-        hi = h > l ? h : l + 1;
+        hi = h;
     }
-    if (lane == 0) {
-        bars->tile = static_cast<int32_t>(lo);
-        bars->unit = static_cast<int32_t>(at - units_before(p, r, lo));
-    }
+    walk.tile = static_cast<int32_t>(lo);
+    walk.unit = at - units_before(p, walk.r, lo);
 }
 
 // Values of key row `row` in this CTA's half of the dims (four blocks at `half`) that are not
@@ -407,12 +419,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     }
     pdl_wait_previous();
     pdl_release_next();
-    find_work(p, bars, pair, gridDim.x >> 1);
+    if (work_groups(p) > 1) {
+        int first, last;
+        bool bad = false;
+        const int64_t units = warp_total(run_units(p, warp, lane, first, last, bad));
+        if (lane == 0) bars->sums[warp] = units;
+        if (bad && blockIdx.x == 0) report(p.err, kErrIndex);
+    }
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == 0 && bars->units > 0) find_tile(p, bars);
-    __syncthreads();
-    cluster_sync();   // the other CTA's barriers exist
+    // The other CTA's barriers exist once both have come here; what only loads needs none of them.
+    cluster_arrive();
+    if (warp != kLoadWarp) cluster_wait();
     tc_fence_after_sync();
     // All 512 columns are this CTA's, so they begin at address 0.
     constexpr uint32_t tmem = 0;
@@ -448,7 +466,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             ++loads;
         };
         Walk walk;
-        walk.init(p, bars);
+        find_work(p, bars->sums, pair, gridDim.x >> 1, walk);
         Part s;
         while (ok) {
             const bool some = walk.next(p, s);
@@ -477,6 +495,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         for (int i = max(0, loads - kStages); i < loads; ++i)
             if (!wait_landed(smem_addr(&bars->full[i % kStages]), (i / kStages) & 1)) ok = false;
         __syncwarp();
+        cluster_wait();
     } else if (warp == kRefillWarp) {
         // ------------------------------------------------------------- rows for p . K
         int j = 0, tile = 0, used[kStages] = {0, 0, 0};
@@ -656,6 +675,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         const uint32_t o_free = map_rank(smem_addr(&bars->o_free), 0);
         const bool first = threadIdx.x == kFirstMove * 32;
         if (first && rank == 0) p.meta[pair] = make_int4(0, 0, 0, 0);
+        if (blockIdx.x == 0 && warp == kFirstMove && work_groups(p) == 1) {
+            int from, upto;
+            bool bad = false;
+            run_units(p, 0, lane, from, upto, bad);
+            if (bad) report(p.err, kErrIndex);
+        }
         // Where part `s` goes: the results, or a piece (slot 1: it begins its tile).
         auto slot_of = [&](const Part& s) -> int { return s.begin == 0 ? 1 : 0; };
         auto whole_of = [&](const Part& s) -> bool { return s.begin == 0 && s.end == s.chunks; };
@@ -773,7 +798,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         if (!ok) {
             // a wait gave up: what this pair has not written is marked
             Walk walk;
-            walk.init(p, bars);
+            find_work(p, bars->sums, pair, gridDim.x >> 1, walk);
             for (int skip = tile; walk.next(p, s);) {
                 if (s.chunks > 0 && skip-- > 0) continue;
                 set_lse(s, __uint_as_float(kUnwritten));
@@ -811,9 +836,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             if (!ok || !some) break;
             ring.next();               // the query tile
             float m = -INFINITY, l = 0.0f;
-            const uint32_t in_tile = rank * kCtaRows + row;
+            const int32_t in_tile = static_cast<int32_t>(rank) * kCtaRows + row;
             const int32_t see = p.causal == 0 ? s.keys
-                                              : clamped(s.see + (s.offset + in_tile) / static_cast<uint32_t>(p.num_heads), s.keys);
+                                              : clamped(s.see + query_of(p, s.offset + in_tile), s.keys);
 #pragma unroll 1
             for (int c = s.begin; c < s.end; ++c, ++j) {
                 const bool fresh = c == s.begin;
@@ -983,29 +1008,42 @@ __global__ void __launch_bounds__(kJoinRows * 32) tile_join_kernel(const TileArg
     pdl_release_next();
     const int4 mark = p.meta[g];
     if ((mark.z & kTailOpen) == 0 || r >= mark.y) return;
+    // the pairs that go on with the tile, up to the one that ends it
     int n = 1;
-    while (g + n < pairs && (p.meta[g + n++].z & kHeadEnds) == 0) {}
+    for (bool ended = false; !ended && g + n < pairs; ) {
+        const int left = min(32, pairs - g - n);
+        const uint32_t ends = __ballot_sync(kFull, lane < left && (p.meta[g + n + lane].z & kHeadEnds) != 0);
+        ended = ends != 0u;
+        n += ended ? __ffs(ends) : left;
+    }
     // the first piece ends its pair's run (slot 1), the others begin theirs (slot 0)
     auto piece = [&](int i) -> int64_t { return (2 * static_cast<int64_t>(g + i) + (i == 0 ? 1 : 0)) * p.slot_rows + r; };
-    float m = -INFINITY;
+    // a lane has the log-sum-exps of four pieces (there are at most 128)
+    float lses[4], m = -INFINITY;
     bool unwritten = false;
-    for (int i = lane; i < n; i += 32) {
-        const float x = p.piece_lse[piece(i)];
-        unwritten |= is_unwritten(x);
-        m = fmaxf(m, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        lses[i] = lane + 32 * i < n ? p.piece_lse[piece(lane + 32 * i)] : -INFINITY;
+        unwritten |= is_unwritten(lses[i]);
+        m = fmaxf(m, lses[i]);
     }
     unwritten = __any_sync(kFull, unwritten) != 0;
 #pragma unroll
     for (int x = 16; x >= 1; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
     const float ref = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lses[i] = exp2_approx(__fsub_rn(lses[i], ref));
     float sum = 0.0f;
     Dims acc;
     acc.zero();
-#pragma unroll 2
-    for (int i = 0; i < n; ++i) {
-        const float w = exp2_approx(__fsub_rn(p.piece_lse[piece(i)], ref));
-        sum = __fadd_rn(sum, w);
-        acc.add(p.pieces + piece(i) * 512, lane, w);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll 4
+        for (int i = 32 * j; i < min(n, 32 * j + 32); ++i) {
+            const float w = __shfl_sync(kFull, lses[j], i & 31);
+            sum = __fadd_rn(sum, w);
+            acc.add(p.pieces + piece(i) * 512, lane, w);
+        }
     }
     const int64_t row = mark.x + r;
     if (unwritten) {
@@ -1077,8 +1115,11 @@ int64_t tile_bytes(int32_t pairs, int64_t rows) {
     return n * 2048 + up16(n * 4) + static_cast<int64_t>(pairs) * 16;
 }
 
+constexpr int32_t kMaxPairs = 128;   // the join's lanes hold four pieces each
 cudaError_t tile_pairs(int32_t* pairs) {
-    return resident_pairs(reinterpret_cast<const void*>(tile_kernel), kTileThreads, kTileSmem, pairs);
+    const cudaError_t e = resident_pairs(reinterpret_cast<const void*>(tile_kernel), kTileThreads, kTileSmem, pairs);
+    if (*pairs > kMaxPairs) *pairs = kMaxPairs;
+    return e;
 }
 
 // Attention of the rows of q; args but for what is in the workspace.
@@ -1087,6 +1128,11 @@ cudaError_t launch_tiles(TileArgs a, const void* q, const void* kv, int64_t kv_s
     int32_t pairs = 0;
     cudaError_t e = tile_pairs(&pairs);
     if (e != cudaSuccess) return e;
+    // ceil(2^shift / d) with shift = 32 + ceil(log2(d)): the product's excess over x 2^shift / d is below
+    // 2^31 < 2^shift / d
+    a.heads_shift = 32;
+    while ((1 << (a.heads_shift - 32)) < a.num_heads) ++a.heads_shift;
+    a.heads_magic = ((UINT64_C(1) << a.heads_shift) + a.num_heads - 1) / a.num_heads;
     const int64_t rows = a.num_tokens * a.num_heads;
     a.slot_rows = slot_rows(rows);
     const int64_t n = 2 * static_cast<int64_t>(pairs) * a.slot_rows;

@@ -252,6 +252,13 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::
                      : "memory");
 }
+// The same in two steps.
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 // Arrive on an mbarrier anywhere in the cluster (a map_rank address).  What the arrivals of
 // these kernels announce is read by the tensor cores of the arriving CTA's own SM, for which
 // the writer has fenced it (fence_async_smem); no memory is handed from CTA to CTA, so the

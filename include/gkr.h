@@ -504,7 +504,8 @@ GKR_API gkr_status gkr_kv_slots(const int32_t *block_table, int64_t table_stride
  * q              device, bf16 [num_tokens, num_heads, 512], 16-byte aligned.
  * num_heads      1 .. 4096; num_tokens >= 0, num_heads * num_tokens <= 2147418112.
  * kv             device, bf16 [num_rows, 512], 16-byte aligned, row r at kv + r * kv_stride
- *                elements (kv_stride >= 512, a multiple of 8); num_rows 0 .. 2147418112.
+ *                elements (kv_stride >= 512, a multiple of 8); num_rows 0 .. 2147418112,
+ *                num_heads * num_rows <= 2^37.
  * starts, kv_starts   device, int32 [num_requests + 1], not descending, within the tensors
  *                (values out of range are taken as the nearest in range; GKR_ERR_INDEX).
  * num_requests   0 .. 16384 (0, like no tokens, enqueues nothing).
