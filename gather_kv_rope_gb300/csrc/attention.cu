@@ -336,7 +336,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
             if (ahead < n) {
                 const uint32_t to = ring + (ahead & (kIndexRing - 1)) * 128;
                 const int64_t k = ci * kChunkKeys + key;
-                if (k < p.topk) cp_async4(to, p.indices + qi * p.index_stride + k);
+                if (k < p.topk)
+                    cp_async4(to, k < p.prefix_length ? p.prefix + k
+                                                      : p.indices + qi * p.index_stride + (k - p.prefix_length));
                 else asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(-1) : "memory");
                 if (++ci == cut.per_query) {
                     ci = 0;

@@ -94,6 +94,10 @@ struct AttentionParams {
     int32_t* err;              // nullable
     int32_t pdl;
     int32_t wide = 0;          // 1: out has fp32 rows and lse is in powers of two (no weights)
+    // entries that come first in every query's list: `topk` counts them, `indices` begins behind
+    // them (no weights)
+    const int32_t* prefix = nullptr;
+    int64_t prefix_length = 0;
 };
 
 // Validated arguments of one eviction launch.

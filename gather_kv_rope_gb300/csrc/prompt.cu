@@ -34,8 +34,6 @@
 // columns, values that are not finite are cleared before p . K (a row that does see them has NaN
 // from its logit).
 #include <cmath>
-#include <mutex>
-#include <vector>
 
 #include "attend.cuh"
 #include "device.cuh"
@@ -99,32 +97,6 @@ struct alignas(16) Part {
     int32_t begin, end;      // of them, this pair's
 };
 
-struct alignas(8) TileBarriers {
-    // in the leader: arrivals of both CTAs
-    uint64_t peer_full[kStages];   // rank 1: a query tile or its rows for q . K have landed
-    uint64_t peer_refilled[kStages];   // ... its rows for p . K
-    uint64_t peer_tail;            // ... the query's last dims
-    uint64_t s_free;               // softmax: the logits are read
-    uint64_t p_full;               // softmax: the probabilities are written
-    uint64_t o_free;               // movers: a tile's output is read
-    // in each CTA
-    uint64_t full[kStages];        // a query tile or rows for q . K have landed
-    uint64_t refilled[kStages];    // rows for p . K have
-    uint64_t tail;                 // the query's last dims have
-    uint64_t empty[kStages];       // p . K of the chunk is complete; results have left the stage
-    uint64_t s_full[2];            // the logits of a chunk are complete (even, odd chunks)
-    uint64_t copied[2];            // a query tile is in tensor memory (even, odd tiles)
-    uint64_t part[kParts];         // a part of the pair's work is described
-    uint64_t stats[2];             // softmax: a tile's sums and log-sum-exps are there
-    uint64_t drained;              // every product that was issued is complete
-    int64_t sums[kTileThreads / 32];   // of the requests' units, if they are many
-    uint32_t tmem_base;
-    volatile int32_t timed_out;
-    Part parts[kParts];
-};
-constexpr size_t kTileSmem = kOffBars + sizeof(TileBarriers);
-static_assert(kTileSmem <= 227 * 1024, "a CTA's shared memory");
-
 // Arguments of the tile kernel.
 struct TileArgs {
     int32_t num_heads;
@@ -155,32 +127,39 @@ constexpr int kTailOpen = 1, kHeadThere = 2, kHeadEnds = 4;
 constexpr int kTileUnits = 4;
 // Fewer units than this for each pair are not worth another piece to join.
 constexpr int64_t kUnitsAPair = 6;
+// To write pieces and join them takes as long as about so many units.
+constexpr int64_t kJoinUnits = 8;
+// No pair has a tile of its own where there are more units than this for each.
+constexpr int64_t kWholeUnits = 64;
 
-// A request's rows and its tiles' work.
+// A request: its queries, its rows of K.
 struct Request {
-    int64_t row0;        // first row of q
-    int64_t k0;          // first row of K
-    int32_t rows, keys, tiles;
-    int64_t past;        // keys - queries
+    int32_t q0, queries, k0, keys;
+    int32_t rows, tiles;     // of q
+    __device__ __forceinline__ void derive(const TileArgs& p) {
+        rows = queries * p.num_heads;
+        tiles = static_cast<int32_t>((static_cast<uint32_t>(rows) + kTileRows - 1) / kTileRows);
+    }
+    __device__ __forceinline__ int64_t past() const { return static_cast<int64_t>(keys) - queries; }
 };
 
 __device__ __forceinline__ Request request_at(const TileArgs& p, int b, bool& bad) {
-    int64_t q0 = 0, q1 = p.num_tokens, k0 = 0, k1 = p.num_rows;
-    if (p.starts != nullptr) {
-        const int64_t a = p.starts[b], z = p.starts[b + 1], c = p.kv_starts[b], e = p.kv_starts[b + 1];
-        q0 = min(max(a, INT64_C(0)), p.num_tokens);
-        q1 = min(max(z, q0), p.num_tokens);
-        k0 = min(max(c, INT64_C(0)), p.num_rows);
-        k1 = min(max(e, k0), p.num_rows);
-        bad |= a != q0 || z != q1 || c != k0 || e != k1;
-    }
+    const int32_t tokens = static_cast<int32_t>(p.num_tokens), rows = static_cast<int32_t>(p.num_rows);
     Request r;
-    r.row0 = q0 * p.num_heads;
-    r.k0 = k0;
-    r.rows = static_cast<int32_t>((q1 - q0) * p.num_heads);
-    r.keys = static_cast<int32_t>(k1 - k0);
-    r.tiles = (r.rows + kTileRows - 1) / kTileRows;
-    r.past = (k1 - k0) - (q1 - q0);
+    r.q0 = 0;
+    r.k0 = 0;
+    r.queries = tokens;
+    r.keys = rows;
+    if (p.starts != nullptr) {
+        const int32_t a = p.starts[b], z = p.starts[b + 1], c = p.kv_starts[b], e = p.kv_starts[b + 1];
+        r.q0 = min(max(a, 0), tokens);
+        r.k0 = min(max(c, 0), rows);
+        const int32_t q1 = min(max(z, r.q0), tokens), k1 = min(max(e, r.k0), rows);
+        bad |= a != r.q0 || z != q1 || c != r.k0 || e != k1;
+        r.queries = q1 - r.q0;
+        r.keys = k1 - r.k0;
+    }
+    r.derive(p);
     return r;
 }
 
@@ -194,7 +173,7 @@ __device__ __forceinline__ int32_t clamped(int64_t see, int32_t keys) {
 // How many rows row `row` of a request sees.
 __device__ __forceinline__ int32_t sees(const TileArgs& p, const Request& r, int32_t row) {
     if (p.causal == 0) return r.keys;
-    return clamped(r.past + query_of(p, row) + 1, r.keys);
+    return clamped(r.past() + query_of(p, row) + 1, r.keys);
 }
 __device__ __forceinline__ int32_t chunks_in(int32_t keys) {
     return static_cast<int32_t>((static_cast<int64_t>(keys) + kChunk - 1) / kChunk);
@@ -215,7 +194,7 @@ __device__ __forceinline__ int64_t floors_below(const TileArgs& p, int64_t z) {
 }
 __device__ __forceinline__ int64_t units_before(const TileArgs& p, const Request& r, int64_t tile) {
     if (p.causal == 0) return tile * (kTileUnits + 2 * chunks_in(r.keys));
-    const int64_t c = (kTileRows - 1 + (r.past + kChunk) * p.num_heads) >> 7;
+    const int64_t c = (kTileRows - 1 + (r.past() + kChunk) * p.num_heads) >> 7;
     return kTileUnits * tile + 2 * (floors_below(p, tile + c) - floors_below(p, c));
 }
 __device__ __forceinline__ int64_t units_of(const TileArgs& p, const Request& r) {
@@ -244,13 +223,13 @@ struct Walk {
                 continue;
             }
             const int32_t row = tile * kTileRows;
-            s.row0 = r.row0 + row;
+            s.row0 = static_cast<int64_t>(r.q0) * p.num_heads + row;
             s.k0 = r.k0;
             s.rows = min(kTileRows, r.rows - row);
             s.keys = r.keys;
             const int32_t query = query_of(p, row);
             s.offset = row - query * p.num_heads;
-            s.see = p.causal == 0 ? r.keys : r.past + query + 1;
+            s.see = p.causal == 0 ? r.keys : r.past() + query + 1;
             s.least = clamped(s.see, r.keys);
             s.chunks = chunks_of(p, r, tile);
             const int64_t all = kTileUnits + 2 * static_cast<int64_t>(s.chunks), first = unit;
@@ -268,6 +247,33 @@ struct Walk {
         return false;
     }
 };
+
+struct alignas(8) TileBarriers {
+    // in the leader: arrivals of both CTAs
+    uint64_t peer_full[kStages];   // rank 1: a query tile or its rows for q . K have landed
+    uint64_t peer_refilled[kStages];   // ... its rows for p . K
+    uint64_t peer_tail;            // ... the query's last dims
+    uint64_t s_free;               // softmax: the logits are read
+    uint64_t p_full;               // softmax: the probabilities are written
+    uint64_t o_free;               // movers: a tile's output is read
+    // in each CTA
+    uint64_t full[kStages];        // a query tile or rows for q . K have landed
+    uint64_t refilled[kStages];    // rows for p . K have
+    uint64_t tail;                 // the query's last dims have
+    uint64_t empty[kStages];       // p . K of the chunk is complete; results have left the stage
+    uint64_t s_full[2];            // the logits of a chunk are complete (even, odd chunks)
+    uint64_t copied[2];            // a query tile is in tensor memory (even, odd tiles)
+    uint64_t part[kParts];         // a part of the pair's work is described
+    uint64_t stats[2];             // softmax: a tile's sums and log-sum-exps are there
+    uint64_t drained;              // every product that was issued is complete
+    int64_t sums[kTileThreads / 32];   // of the requests' units, if they are many
+    uint32_t tmem_base;
+    volatile int32_t timed_out;
+    Part parts[kParts];
+    Walk walk;                     // where the pair's work begins
+};
+constexpr size_t kTileSmem = kOffBars + sizeof(TileBarriers);
+static_assert(kTileSmem <= 227 * 1024, "a CTA's shared memory");
 
 // The requests' units are summed up by one warp, or, if there are many, first by all warps, each of
 // them a run of requests per thread.
@@ -287,47 +293,105 @@ __device__ __forceinline__ int64_t warp_total(int64_t v) {
     return v;
 }
 
-// Where this pair's work begins and how much it is; a warp (sums: of the groups, if there are more
-// than one).
-__device__ __noinline__ void find_work(const TileArgs& p, const int64_t* sums, int64_t pair, int64_t pairs, Walk& walk) {
-    const int lane = threadIdx.x & 31, groups = work_groups(p);
-    int first = 0, last = 0;
-    bool bad = false;
-    int64_t mine = groups == 1 ? run_units(p, 0, lane, first, last, bad) : lane < groups ? sums[lane] : 0;
-    const int64_t total = warp_total(mine);
-    // an even share, the first ones a unit more
-    pairs = max(INT64_C(1), min(pairs, total / kUnitsAPair));
-    const int64_t share = total >> 32 == 0 ? static_cast<uint32_t>(total) / static_cast<uint32_t>(pairs) : total / pairs;
-    const int64_t more = total - share * pairs, x0 = pair * share + min(pair, more);
-    walk.left = pair < pairs ? share + (pair < more ? 1 : 0) : 0;
-    walk.b = p.num_requests;
-    if (walk.left == 0) return;
-    int64_t before = 0;   // units of the groups, then of the lanes, before x0's
-    if (groups > 1) {
-        int g = 0;
-        for (; g < groups - 1 && before + sums[g] <= x0; ++g) before += sums[g];
-        mine = run_units(p, g, lane, first, last, bad);
-    }
-    int64_t upto = mine;
+// A lane's value in an inclusive sum over the lanes.
+template <typename T>
+__device__ __forceinline__ T warp_upto(T v, int lane) {
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const int64_t o = __shfl_up_sync(kFull, upto, d);
-        if (lane >= d) upto += o;
+        const T o = __shfl_up_sync(kFull, v, d);
+        if (lane >= d) v += o;
     }
-    const int owner = __ffs(__ballot_sync(kFull, before + upto > x0)) - 1;
-    int64_t at = x0 - before - (upto - mine);
-    int b = first;
-    if (lane == owner) {
-        for (; b < last - 1; ++b) {
-            const int64_t u = units_of(p, request_at(p, b, bad));
-            if (at < u) break;
-            at -= u;
+    return v;
+}
+
+// A pair's even share of the units, the first ones a unit more; false: none.
+__device__ __forceinline__ bool even_share(int64_t total, int64_t pair, int64_t pairs, int64_t& x0, int64_t& units) {
+    pairs = max(INT64_C(1), min(pairs, total / kUnitsAPair));
+    const int64_t share = total >> 32 == 0 ? static_cast<uint32_t>(total) / static_cast<uint32_t>(pairs) : total / pairs;
+    const int64_t more = total - share * pairs;
+    x0 = pair * share + min(pair, more);
+    units = pair >= pairs ? 0 : share + (pair < more ? 1 : 0);
+    return units > 0;
+}
+
+// Where this pair's work begins and how much it is; a warp (sums: of the groups, if there are more
+// than one).  Every instruction here is run for the first time and in a row, so what lanes have read
+// is not read again.
+__device__ __forceinline__ void find_work(const TileArgs& p, const int64_t* sums, int64_t pair, int64_t pairs, Walk& walk) {
+    const int lane = threadIdx.x & 31, groups = work_groups(p);
+    bool bad = false;
+    walk.left = 0;
+    walk.unit = 0;
+    walk.b = p.num_requests;
+    walk.tile = 0;
+    Request mine_r = {};        // of the lane, where each has at most one
+    int64_t before = 0, at;     // units before the group, then within a request
+    int owner, b;
+    if (p.num_requests <= 32) {
+        int64_t mine = 0;
+        int most = 0;
+        if (lane < p.num_requests) {
+            mine_r = request_at(p, lane, bad);
+            mine = units_of(p, mine_r);
+            if (mine_r.tiles > 0) most = kTileUnits + 2 * chunks_in(mine_r.keys);
         }
+        const int64_t upto = warp_upto(mine, lane), total = __shfl_sync(kFull, upto, 31);
+        bool whole = false;
+        if (total <= pairs * kWholeUnits) {
+            // Few tiles: one for each pair, if none of them takes much longer than an even share.
+            const int tiles = warp_upto(mine_r.tiles, lane), all = __shfl_sync(kFull, tiles, 31);
+            most = __reduce_max_sync(kFull, most);
+            whole = all <= pairs &&
+                    most <= static_cast<int>(static_cast<uint32_t>(total) / static_cast<uint32_t>(pairs)) + kJoinUnits;
+            if (whole) {
+                if (pair >= all) return;
+                owner = __ffs(__ballot_sync(kFull, tiles > pair)) - 1;
+                walk.tile = static_cast<int32_t>(pair) - __shfl_sync(kFull, tiles - mine_r.tiles, owner);
+            }
+        }
+        if (!whole) {
+            int64_t x0;
+            if (!even_share(total, pair, pairs, x0, walk.left)) return;
+            owner = __ffs(__ballot_sync(kFull, upto > x0)) - 1;
+            at = x0 - __shfl_sync(kFull, upto - mine, owner);
+        }
+        walk.b = owner;
+        walk.r.q0 = __shfl_sync(kFull, mine_r.q0, owner);
+        walk.r.queries = __shfl_sync(kFull, mine_r.queries, owner);
+        walk.r.k0 = __shfl_sync(kFull, mine_r.k0, owner);
+        walk.r.keys = __shfl_sync(kFull, mine_r.keys, owner);
+        walk.r.derive(p);
+        if (whole) {
+            walk.left = kTileUnits + 2 * static_cast<int64_t>(chunks_of(p, walk.r, walk.tile));
+            return;
+        }
+    } else {
+        int first = 0, last = 0;
+        int64_t mine = groups == 1 ? run_units(p, 0, lane, first, last, bad) : lane < groups ? sums[lane] : 0;
+        int64_t upto = warp_upto(mine, lane), x0;
+        if (!even_share(__shfl_sync(kFull, upto, 31), pair, pairs, x0, walk.left)) return;
+        if (groups > 1) {
+            int g = 0;
+            for (; g < groups - 1 && before + sums[g] <= x0; ++g) before += sums[g];
+            mine = run_units(p, g, lane, first, last, bad);
+            upto = warp_upto(mine, lane);
+        }
+        owner = __ffs(__ballot_sync(kFull, before + upto > x0)) - 1;
+        at = x0 - before - (upto - mine);
+        b = first;
+        if (lane == owner) {
+            for (; b < last - 1; ++b) {
+                const int64_t u = units_of(p, request_at(p, b, bad));
+                if (at < u) break;
+                at -= u;
+            }
+        }
+        walk.b = __shfl_sync(kFull, b, owner);
+        at = __shfl_sync(kFull, at, owner);
+        walk.r = request_at(p, walk.b, bad);
     }
-    walk.b = __shfl_sync(kFull, b, owner);
-    at = __shfl_sync(kFull, at, owner);
-    walk.r = request_at(p, walk.b, bad);
     int64_t lo = 0, hi = walk.r.tiles;           // units_before(lo) <= at < units_before(hi)
+#pragma unroll 1
     while (hi - lo > 1) {
         const int64_t x = lo + ((hi - lo) * lane >> 5);
         const uint32_t below = __ballot_sync(kFull, units_before(p, walk.r, x) <= at);   // lane 0 always
@@ -426,6 +490,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         if (lane == 0) bars->sums[warp] = units;
         if (bad && blockIdx.x == 0) report(p.err, kErrIndex);
     }
+    if (work_groups(p) > 1) __syncthreads();
+    Walk walk;
+    if (warp == kLoadWarp) {
+        find_work(p, bars->sums, pair, gridDim.x >> 1, walk);
+        if (lane == 0) bars->walk = walk;
+    }
     tc_fence_before_sync();
     __syncthreads();
     // The other CTA's barriers exist once both have come here; what only loads needs none of them.
@@ -440,6 +510,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         if (!ok || !warp_wait(smem_addr(&bars->part[tile & (kParts - 1)]), (tile / kParts) & 1, ok)) return false;
         s = bars->parts[tile & (kParts - 1)];
         return s.chunks > 0;
+    };
+    // The last dims of a query tile; a thread.
+    auto load_tail = [&](int64_t row0) {
+        const uint32_t bar = smem_addr(&bars->tail);
+        mbar_expect_tx(bar, kQBytes);
+        tma_load_3d(smem_addr(smem), &tail_map, bar, 0, static_cast<int32_t>(row0 + rank * kCtaRows), kQTmemBlocks);
     };
     Ring<kStages> ring;
 
@@ -465,8 +541,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             ring.next();
             ++loads;
         };
-        Walk walk;
-        find_work(p, bars->sums, pair, gridDim.x >> 1, walk);
+        // The first tile's last dims come from here: they have landed before the refilling warp can ask
+        // for the next ones.
+        bool tail_asked = false;
+        auto tail_landed = [&]() {
+            if (tail_asked && !wait_landed(smem_addr(&bars->tail), 0)) ok = false;
+            tail_asked = false;
+        };
         Part s;
         while (ok) {
             const bool some = walk.next(p, s);
@@ -479,19 +560,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
                 continue;
             }
             if (!some) s.chunks = 0;
+            tail_landed();
             if (lane == 0) {
                 bars->parts[tile & (kParts - 1)] = s;
                 mbar_arrive(smem_addr(&bars->part[tile & (kParts - 1)]));
             }
             __syncwarp();
             if (!some) break;
-            ++tile;
+            if (++tile == 1) {
+                if (lane == 0) load_tail(s.row0);
+                tail_asked = true;
+            }
             load(true, s.row0 + rank * kCtaRows);
 #pragma unroll 1
             for (int c = s.begin; c < s.end && ok; ++c)
                 load(false, s.k0 + static_cast<int64_t>(c) * kChunk + rank * kCtaKeys);
         }
         // what is under way lands before the CTA leaves
+        tail_landed();
         for (int i = max(0, loads - kStages); i < loads; ++i)
             if (!wait_landed(smem_addr(&bars->full[i % kStages]), (i / kStages) & 1)) ok = false;
         __syncwarp();
@@ -501,13 +587,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         int j = 0, tile = 0, used[kStages] = {0, 0, 0};
         Part s;
         for (; part_at(tile, s); ++tile) {
-            // q . K of the tile before is complete: the query's last dims may be replaced
-            if (lane == 0) {
-                const uint32_t bar = smem_addr(&bars->tail);
-                mbar_expect_tx(bar, kQBytes);
-                tma_load_3d(smem_addr(smem), &tail_map, bar, 0, static_cast<int32_t>(s.row0 + rank * kCtaRows),
-                            kQTmemBlocks);
-            }
+            // q . K of the tile before is complete: the query's last dims may be replaced (the first
+            // tile's come with the others)
+            if (tile > 0 && lane == 0) load_tail(s.row0);
             __syncwarp();
             ring.next();   // the query tile
 #pragma unroll 1
@@ -530,7 +612,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int i = 0; i < kStages; ++i)
             if (used[i] > 0 && !wait_landed(smem_addr(&bars->refilled[i]), (used[i] - 1) & 1)) ok = false;
-        if (tile > 0 && !wait_landed(smem_addr(&bars->tail), (tile - 1) & 1)) ok = false;
+        if (tile > 1 && !wait_landed(smem_addr(&bars->tail), (tile - 1) & 1)) ok = false;
         __syncwarp();
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------- products
@@ -797,8 +879,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         __syncwarp();
         if (!ok) {
             // a wait gave up: what this pair has not written is marked
-            Walk walk;
-            find_work(p, bars->sums, pair, gridDim.x >> 1, walk);
+            walk = bars->walk;
             for (int skip = tile; walk.next(p, s);) {
                 if (s.chunks > 0 && skip-- > 0) continue;
                 set_lse(s, __uint_as_float(kUnwritten));
@@ -986,105 +1067,151 @@ struct Dims {
             d[i].w = __fmaf_rn(w, x[i].w, d[i].w);
         }
     }
-    __device__ __forceinline__ void store(uint8_t* row, int lane, float f, bool wide) const {
+    __device__ __forceinline__ void store(uint8_t* row, int lane, float f) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = __fmul_rn(d[i].x, f), b = __fmul_rn(d[i].y, f), c = __fmul_rn(d[i].z, f),
-                        e = __fmul_rn(d[i].w, f);
-            if (wide) *reinterpret_cast<float4*>(row + 512 * i + 16 * lane) = make_float4(a, b, c, e);
-            else st8(row + 256 * i + 8 * lane, make_uint2(pack_bf16x2_rn(a, b), pack_bf16x2_rn(c, e)));
-        }
+        for (int i = 0; i < 4; ++i)
+            st8(row + 256 * i + 8 * lane, make_uint2(pack_bf16x2_rn(__fmul_rn(d[i].x, f), __fmul_rn(d[i].y, f)),
+                                                     pack_bf16x2_rn(__fmul_rn(d[i].z, f), __fmul_rn(d[i].w, f))));
     }
 };
 
-// Joins the pieces of each tile that was cut: out = sum_i exp2(lse_i - lse) rows_i.  A warp takes
-// a row; blocks of tiles that were not cut leave at once.
-constexpr int kJoinRows = 8;
-__global__ void __launch_bounds__(kJoinRows * 32) tile_join_kernel(const TileArgs p, const int32_t pairs) {
-    const int parts = (p.slot_rows + kJoinRows - 1) / kJoinRows;
-    const int g = blockIdx.x / parts, lane = threadIdx.x & 31;
-    const int r = (blockIdx.x - g * parts) * kJoinRows + (threadIdx.x >> 5);
-    pdl_wait_previous();
-    pdl_release_next();
-    const int4 mark = p.meta[g];
-    if ((mark.z & kTailOpen) == 0 || r >= mark.y) return;
-    // the pairs that go on with the tile, up to the one that ends it
-    int n = 1;
-    for (bool ended = false; !ended && g + n < pairs; ) {
-        const int left = min(32, pairs - g - n);
-        const uint32_t ends = __ballot_sync(kFull, lane < left && (p.meta[g + n + lane].z & kHeadEnds) != 0);
-        ended = ends != 0u;
-        n += ended ? __ffs(ends) : left;
-    }
-    // the first piece ends its pair's run (slot 1), the others begin theirs (slot 0)
-    auto piece = [&](int i) -> int64_t { return (2 * static_cast<int64_t>(g + i) + (i == 0 ? 1 : 0)) * p.slot_rows + r; };
-    // a lane has the log-sum-exps of four pieces (there are at most 128)
-    float lses[4], m = -INFINITY;
-    bool unwritten = false;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        lses[i] = lane + 32 * i < n ? p.piece_lse[piece(lane + 32 * i)] : -INFINITY;
-        unwritten |= is_unwritten(lses[i]);
-        m = fmaxf(m, lses[i]);
-    }
-    unwritten = __any_sync(kFull, unwritten) != 0;
-#pragma unroll
-    for (int x = 16; x >= 1; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
-    const float ref = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) lses[i] = exp2_approx(__fsub_rn(lses[i], ref));
-    float sum = 0.0f;
-    Dims acc;
-    acc.zero();
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-#pragma unroll 4
-        for (int i = 32 * j; i < min(n, 32 * j + 32); ++i) {
-            const float w = __shfl_sync(kFull, lses[j], i & 31);
-            sum = __fadd_rn(sum, w);
-            acc.add(p.pieces + piece(i) * 512, lane, w);
-        }
-    }
-    const int64_t row = mark.x + r;
-    if (unwritten) {
-        if (lane == 0) p.lse[row] = __uint_as_float(kUnwritten);
-        return;
-    }
-    const float inv = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
-    acc.store(static_cast<uint8_t*>(p.out) + row * (p.wide != 0 ? 2048 : 1024), lane, inv, p.wide != 0);
-    if (lane == 0) {
-        const float lse2 = sum == 0.0f ? -INFINITY : __fadd_rn(m, log2f(sum));
-        p.lse[row] = p.wide != 0 ? lse2 : __fmul_rn(lse2, kLn2);
-    }
-}
-
-// Joins two results of every row, fp32 with log-sum-exps in powers of two.
-struct MergeArgs {
-    const float *a, *b, *a_lse, *b_lse;
-    int64_t rows;
-    void* out;
+// Joins the pieces of each tile that was cut, out = sum_i exp2(lse_i - lse) rows_i, and, where there are
+// other results of the same rows (`own`), every row with those.  A block reads what the pairs left
+// and goes through the rows that have something to join: a warp takes one, or, where there are few,
+// two, four or eight warps, each of them some of the pieces.  (A block for each pair and eight rows,
+// most of them with nothing to do, and one warp for up to 43 pieces took 20 us where this takes
+// 6.)
+constexpr int kJoinWarps = 8;
+constexpr int32_t kMaxPairs = 128;
+constexpr int kMaxParts = kMaxPairs + 1;    // of a row
+struct JoinArgs {
+    const float *own, *own_lse;       // fp32 rows, log-sum-exps in powers of two; or null
+    const float *whole, *whole_lse;   // with `own`: the rows of the tiles that were not cut
+    void* out;                        // bf16
     float* lse;
+    int32_t pairs;
 };
-__global__ void __launch_bounds__(kJoinRows * 32) merge_kernel(const MergeArgs p) {
-    const int lane = threadIdx.x & 31;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * kJoinRows + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(kJoinWarps * 32, 4) tile_join_kernel(const TileArgs p, const JoinArgs q) {
+    // the cut tiles: first row, rows before (of cut tiles), pair that begins them; all pairs' flags
+    __shared__ int32_t tail_row[kMaxPairs], tail_upto[kMaxPairs + 1], tail_pair[kMaxPairs], flags[kMaxPairs];
+    __shared__ int32_t tails;
+    __shared__ float weights[kJoinWarps][kMaxParts];
+    __shared__ float4 parts[kJoinWarps][128];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait_previous();
     pdl_release_next();
-    if (row >= p.rows) return;
-    const float x = p.a_lse[row], y = p.b_lse[row];
-    if (is_unwritten(x) || is_unwritten(y)) {
-        if (lane == 0) p.lse[row] = __uint_as_float(kUnwritten);
-        return;
+    if (warp == 0) {
+        int n = 0, at = 0;
+        if (lane == 0) tail_upto[0] = 0;
+        int4 marks[kMaxPairs / 32];
+#pragma unroll
+        for (int i = 0; i < kMaxPairs / 32; ++i)
+            marks[i] = 32 * i + lane < q.pairs ? p.meta[32 * i + lane] : make_int4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < kMaxPairs / 32; ++i) {
+            const int g = 32 * i + lane;
+            const bool tail = (marks[i].z & kTailOpen) != 0;
+            const uint32_t which = __ballot_sync(kFull, tail);
+            const int upto = at + warp_upto(tail ? marks[i].y : 0, lane);
+            const int k = n + __popc(which & ((1u << lane) - 1u));
+            flags[g] = marks[i].z;
+            if (tail) {
+                tail_row[k] = marks[i].x;
+                tail_pair[k] = g;
+                tail_upto[k + 1] = upto;
+            }
+            n += __popc(which);
+            at = __shfl_sync(kFull, upto, 31);
+        }
+        if (lane == 0) tails = n;
     }
-    const float m = fmaxf(x, y), ref = m == -INFINITY ? 0.0f : m;
-    const float u = exp2_approx(__fsub_rn(x, ref)), w = exp2_approx(__fsub_rn(y, ref));
-    const float sum = __fadd_rn(u, w);
-    Dims acc;
-    acc.zero();
-    acc.add(p.a + row * 512, lane, u);
-    acc.add(p.b + row * 512, lane, w);
-    acc.store(static_cast<uint8_t*>(p.out) + row * 1024, lane, sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum), false);
-    if (lane == 0) p.lse[row] = sum == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(m, log2f(sum)), kLn2);
+    __syncthreads();
+    const bool merge = q.own != nullptr;
+    const int64_t total = merge ? p.num_tokens * p.num_heads : tail_upto[tails];
+    // warps of a row, rows of a block at a time
+    const int64_t blocks = gridDim.x;
+    const int share = total <= blocks ? 8 : total <= 2 * blocks ? 4 : total <= 4 * blocks ? 2 : 1;
+    const int each = kJoinWarps / share, sub = warp & (share - 1);
+#pragma unroll 1
+    for (int64_t base = blockIdx.x * static_cast<int64_t>(each); base < total; base += blocks * each) {
+        const int64_t item = base + warp / share;
+        const bool some = item < total;
+        int64_t row = item;
+        int g = 0, n = 0, r = 0;      // pair that begins the tile, pieces, row of the piece
+        if (some && tails > 0) {
+            const int32_t* const keys = merge ? tail_row : tail_upto;
+            int lo = 0, hi = tails;   // the first of them past the item
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (keys[mid] <= item) lo = mid + 1;
+                else hi = mid;
+            }
+            const int k = lo - 1;
+            if (k >= 0) {
+                r = static_cast<int>(item - keys[k]);
+                if (r < tail_upto[k + 1] - tail_upto[k]) {
+                    g = tail_pair[k];
+                    row = tail_row[k] + static_cast<int64_t>(r);
+                    // the pairs that go on with the tile, up to the one that ends it
+                    n = 1;
+                    while (g + n < q.pairs && (flags[g + n++] & kHeadEnds) == 0) {}
+                }
+            }
+        }
+        const int count = !some ? 0 : n + (merge ? 1 + (n == 0 ? 1 : 0) : 0);
+        // part i of the row: a piece (the first ends its pair's run, slot 1, the others begin theirs, slot
+        // 0) or the whole tile's row, then the other results'
+        auto piece = [&](int i) -> int64_t { return (2 * static_cast<int64_t>(g + i) + (i == 0 ? 1 : 0)) * p.slot_rows + r; };
+        auto row_of = [&](int i) -> const float* {
+            return (i < n ? p.pieces + piece(i) * 512 : (i == count - 1 ? q.own : q.whole) + row * 512);
+        };
+        auto lse_of = [&](int i) -> float {
+            return i < n ? p.piece_lse[piece(i)] : (i == count - 1 ? q.own_lse : q.whole_lse)[row];
+        };
+        float lses[(kMaxParts + 31) / 32], m = -INFINITY;
+        bool unwritten = false;
+#pragma unroll
+        for (int i = 0; i < (kMaxParts + 31) / 32; ++i) {
+            lses[i] = lane + 32 * i < count ? lse_of(lane + 32 * i) : -INFINITY;
+            unwritten |= is_unwritten(lses[i]);
+            m = fmaxf(m, lses[i]);
+        }
+        unwritten = __any_sync(kFull, unwritten) != 0;
+#pragma unroll
+        for (int x = 16; x >= 1; x >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, x));
+        const float ref = m == -INFINITY ? 0.0f : m;
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < (kMaxParts + 31) / 32; ++i) {
+            const float w = exp2_approx(__fsub_rn(lses[i], ref));
+            if (lane + 32 * i < count) weights[warp][lane + 32 * i] = w;
+            sum = __fadd_rn(sum, w);
+        }
+#pragma unroll
+        for (int x = 16; x >= 1; x >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(kFull, sum, x));
+        __syncwarp();
+        Dims acc;
+        acc.zero();
+#pragma unroll 4
+        for (int i = sub; i < count; i += share) acc.add(row_of(i), lane, weights[warp][i]);
+        if (share > 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) parts[warp][32 * i + lane] = acc.d[i];
+            __syncthreads();
+            if (sub == 0)
+                for (int w = 1; w < share; ++w) acc.add(reinterpret_cast<const float*>(parts[warp + w]), lane, 1.0f);
+            __syncthreads();
+        }
+        if (some && sub == 0) {
+            if (!unwritten) {
+                acc.store(static_cast<uint8_t*>(q.out) + row * 1024, lane, sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum));
+                if (lane == 0) q.lse[row] = sum == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(m, log2f(sum)), kLn2);
+            } else if (lane == 0) {
+                q.lse[row] = __uint_as_float(kUnwritten);
+            }
+        }
+        __syncwarp();   // the weights are read before the next row's are written
+    }
 }
 
 // ---------------------------------------------------------------- host
@@ -1115,15 +1242,15 @@ int64_t tile_bytes(int32_t pairs, int64_t rows) {
     return n * 2048 + up16(n * 4) + static_cast<int64_t>(pairs) * 16;
 }
 
-constexpr int32_t kMaxPairs = 128;   // the join's lanes hold four pieces each
 cudaError_t tile_pairs(int32_t* pairs) {
     const cudaError_t e = resident_pairs(reinterpret_cast<const void*>(tile_kernel), kTileThreads, kTileSmem, pairs);
     if (*pairs > kMaxPairs) *pairs = kMaxPairs;
     return e;
 }
 
-// Attention of the rows of q; args but for what is in the workspace.
-cudaError_t launch_tiles(TileArgs a, const void* q, const void* kv, int64_t kv_stride, uint8_t* workspace,
+// Attention of the rows of q; args but for what is in the workspace.  Joined with other results, if
+// there are any (own; then the tiles leave fp32 rows).
+cudaError_t launch_tiles(TileArgs a, JoinArgs join, const void* q, const void* kv, int64_t kv_stride, uint8_t* workspace,
                          int32_t pdl, cudaStream_t stream) {
     int32_t pairs = 0;
     cudaError_t e = tile_pairs(&pairs);
@@ -1151,25 +1278,52 @@ cudaError_t launch_tiles(TileArgs a, const void* q, const void* kv, int64_t kv_s
     e = launch_kernel(tile_kernel, 2 * static_cast<int64_t>(pairs), kTileThreads, kTileSmem, stream, pdl, a, q_map,
                       tail_map, k_map, out_map);
     if (e != cudaSuccess) return e;
-    const int64_t blocks = static_cast<int64_t>(pairs) * ((a.slot_rows + kJoinRows - 1) / kJoinRows);
-    return launch_kernel(tile_join_kernel, blocks, kJoinRows * 32, 0, stream, pdl, a, pairs);
+    // a block for each row that may have something to join, up to one wave
+    int64_t warps = 0;
+    e = resident_warps(reinterpret_cast<const void*>(tile_join_kernel), kJoinWarps * 32, 0, &warps);
+    if (e != cudaSuccess) return e;
+    const int64_t most = join.own != nullptr ? rows : static_cast<int64_t>(pairs) * a.slot_rows;
+    const int64_t wave = warps / kJoinWarps, blocks = most < wave ? most : wave;
+    join.pairs = pairs;
+    return launch_kernel(tile_join_kernel, blocks, kJoinWarps * 32, 0, stream, pdl, a, join);
 }
 
 // The workspace of a prefix attention: the prefix as bf16 rows, both parts' rows and
 // log-sum-exps, both parts' own workspaces.
 struct PrefixLayout {
+    bool written_out;    // every query's list with the prefix in front of it
     int64_t rows, shared, shared_lse, own, own_lse, tiles, attend, bytes;
 };
+// Two ways: the prefix once for all queries (gathered, tiles of 128 query heads, the queries' own
+// lists, the join: five launches), or, as the sparse attention does, each query's list with the
+// prefix in front of it (two launches, 128 rows of the tensor cores for a query's heads, every record
+// dequantised for every query).  Which takes less by these estimates, in us:
+//   written out: 10.5 and 1.05 for a chunk of 64 records of a pair's run;
+//   shared: 27, the gather 2.1e-4 a record, 1.35 for a chunk of 128 rows of a pair's run and
+//   1.05 for one of 64 own records.
+// Measured, us in a graph, shared and written out (queries x heads, prefix + 100 own): 4 x 16, 4095 32.6
+// and 17.7, 16384 39.5 and 27.5, 65536 64 and 68.5; 16 x 16, 4095 35 and 31, 16384 42 and 73; 8 x 128,
+// 16384 57 and 51, 131072 215 and 242; 64 x 16, 2048 39 and 43, 131072 214 and 1791; 128 x 64, 512 45 and
+// 33, 4095 93 and 140.  Of 90 such sizes the slower way is taken in five, by 7 % at most.
+bool write_out(int32_t num_heads, int64_t num_queries, int64_t prefix_length, int64_t topk, int32_t pairs) {
+    const double own = static_cast<double>(num_queries) * static_cast<double>((topk + 63) / 64) / pairs;
+    const double listed = static_cast<double>(num_queries) * static_cast<double>((prefix_length + topk + 63) / 64) / pairs;
+    const double tiles = static_cast<double>((num_queries * num_heads + kTileRows - 1) / kTileRows);
+    const double shared = tiles * static_cast<double>((prefix_length + kChunk - 1) / kChunk) / pairs;
+    return 10.5 + 1.05 * listed <= 27.0 + 2.1e-4 * static_cast<double>(prefix_length) + 1.35 * shared + 1.05 * own;
+}
 cudaError_t prefix_layout(int32_t num_heads, int64_t num_queries, int64_t prefix_length, int64_t topk,
                           PrefixLayout* w) {
     const int64_t n = num_queries * num_heads;
+    *w = {};
+    int32_t pairs = 0;
+    cudaError_t e = tile_pairs(&pairs);
+    if (e != cudaSuccess) return e;
+    w->written_out = write_out(num_heads, num_queries, prefix_length, topk, pairs);
+    if (w->written_out) return attention_workspace(num_heads, num_queries, prefix_length + topk, &w->bytes);
     const bool both = prefix_length > 0 && topk > 0;
     int64_t at = 0, attend = 0;
-    int32_t pairs = 0;
-    cudaError_t e = cudaSuccess;
-    if (prefix_length > 0) e = tile_pairs(&pairs);
-    if (e == cudaSuccess && (topk > 0 || prefix_length == 0))
-        e = attention_workspace(num_heads, num_queries, topk, &attend);
+    if (topk > 0) e = attention_workspace(num_heads, num_queries, topk, &attend);
     if (e != cudaSuccess) return e;
     auto take = [&](int64_t bytes) {
         const int64_t here = at;
@@ -1181,7 +1335,7 @@ cudaError_t prefix_layout(int32_t num_heads, int64_t num_queries, int64_t prefix
     w->shared_lse = take(both ? n * 4 : 0);
     w->own = take(both ? n * 2048 : 0);
     w->own_lse = take(both ? n * 4 : 0);
-    w->tiles = take(prefix_length > 0 ? tile_bytes(pairs, n) : 0);
+    w->tiles = take(tile_bytes(pairs, n));
     w->attend = take(attend);
     w->bytes = at;
     return cudaSuccess;
@@ -1218,7 +1372,10 @@ cudaError_t launch_prompt_attention(const PromptParams& p, cudaStream_t stream) 
     a.out = p.out;
     a.lse = p.lse;
     a.err = p.err;
-    return launch_tiles(a, p.q, p.kv, p.kv_stride, static_cast<uint8_t*>(p.workspace), p.pdl, stream);
+    JoinArgs join = {};
+    join.out = p.out;
+    join.lse = p.lse;
+    return launch_tiles(a, join, p.q, p.kv, p.kv_stride, static_cast<uint8_t*>(p.workspace), p.pdl, stream);
 }
 
 cudaError_t launch_prefix_attention(const PrefixParams& p, cudaStream_t stream) {
@@ -1230,7 +1387,12 @@ cudaError_t launch_prefix_attention(const PrefixParams& p, cudaStream_t stream) 
     const bool both = p.prefix_length > 0 && o.topk > 0;
     AttentionParams own = o;
     own.workspace = base + w.attend;
-    if (p.prefix_length == 0) return launch_sparse_attention(own, stream);
+    if (w.written_out) {
+        own.prefix = p.prefix;
+        own.prefix_length = p.prefix_length;
+        own.topk += p.prefix_length;
+        return launch_sparse_attention(own, stream);
+    }
     if (both) {
         own.out = base + w.own;
         own.lse = reinterpret_cast<float*>(base + w.own_lse);
@@ -1262,17 +1424,16 @@ cudaError_t launch_prefix_attention(const PrefixParams& p, cudaStream_t stream) 
     a.lse = both ? reinterpret_cast<float*>(base + w.shared_lse) : o.lse;
     a.wide = both ? 1 : 0;
     a.err = o.err;
-    e = launch_tiles(a, o.q, base + w.rows, 512, base + w.tiles, o.pdl, stream);
-    if (e != cudaSuccess || !both) return e;
-    MergeArgs m;
-    m.a = reinterpret_cast<const float*>(base + w.shared);
-    m.b = reinterpret_cast<const float*>(base + w.own);
-    m.a_lse = reinterpret_cast<const float*>(base + w.shared_lse);
-    m.b_lse = reinterpret_cast<const float*>(base + w.own_lse);
-    m.rows = o.num_queries * o.num_heads;
-    m.out = o.out;
-    m.lse = o.lse;
-    return launch_kernel(merge_kernel, (m.rows + kJoinRows - 1) / kJoinRows, kJoinRows * 32, 0, stream, o.pdl, m);
+    JoinArgs join = {};
+    join.out = o.out;
+    join.lse = o.lse;
+    if (both) {
+        join.own = reinterpret_cast<const float*>(base + w.own);
+        join.own_lse = reinterpret_cast<const float*>(base + w.own_lse);
+        join.whole = reinterpret_cast<const float*>(base + w.shared);
+        join.whole_lse = reinterpret_cast<const float*>(base + w.shared_lse);
+    }
+    return launch_tiles(a, join, o.q, base + w.rows, 512, base + w.tiles, o.pdl, stream);
 }
 
 }  // namespace gkr
