@@ -162,7 +162,10 @@ cudaError_t resident_warps(const void* func, int threads, size_t smem, int64_t* 
     if (e != cudaSuccess) return e;
     if (per_sm < 1) per_sm = 1;
     const int64_t w = static_cast<int64_t>(sms) * per_sm * (threads / 32);
-    g_occ.push_back({dev, func, smem, threads, w});
+    try {
+        g_occ.push_back({dev, func, smem, threads, w});
+    } catch (...) {   // asked again next time
+    }
     *warps = w;
     return cudaSuccess;
 }
@@ -195,7 +198,10 @@ cudaError_t resident_pairs(const void* func, int threads, size_t smem, int32_t* 
     e = cudaOccupancyMaxActiveClusters(&n, func, &cfg);
     if (e != cudaSuccess) return e;
     if (n < 1) return cudaErrorInvalidConfiguration;
-    g_pairs.push_back({dev, func, n});
+    try {
+        g_pairs.push_back({dev, func, n});
+    } catch (...) {   // asked again next time
+    }
     *pairs = n;
     return cudaSuccess;
 }

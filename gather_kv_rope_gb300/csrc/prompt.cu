@@ -549,9 +549,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             tail_asked = false;
         };
         Part s;
-        while (ok) {
+        while (true) {
             const bool some = walk.next(p, s);
-            if (some && s.chunks == 0) {   // zeros
+            if (some && s.chunks == 0) {   // zeros, whatever has become of the other tiles
                 const int rows = min(kCtaRows, s.rows - static_cast<int>(rank) * kCtaRows);
                 const int64_t at = s.row0 + rank * kCtaRows, bytes = p.wide != 0 ? 2048 : 1024;
                 for (int64_t i = lane * INT64_C(16); i < rows * bytes; i += 512)
@@ -559,8 +559,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
                 for (int i = lane; i < rows; i += 32) p.lse[at + i] = -INFINITY;
                 continue;
             }
+            if (!ok) {
+                if (!some) break;
+                continue;
+            }
             if (!some) s.chunks = 0;
             tail_landed();
+            if (!ok) continue;
             if (lane == 0) {
                 bars->parts[tile & (kParts - 1)] = s;
                 mbar_arrive(smem_addr(&bars->part[tile & (kParts - 1)]));
@@ -881,7 +886,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             // a wait gave up: what this pair has not written is marked
             walk = bars->walk;
             for (int skip = tile; walk.next(p, s);) {
-                if (s.chunks > 0 && skip-- > 0) continue;
+                if (s.chunks == 0 || skip-- > 0) continue;
                 set_lse(s, __uint_as_float(kUnwritten));
                 note(s);
             }
@@ -982,7 +987,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
                         if (ok) warp_wait(smem_addr(&bars->empty[last.s]), last.parity, ok);
                         tc_fence_after_sync();
 #pragma unroll 1
-                        for (int d = 128 * part; d < 128 * part + 128; d += 32) {
+                        for (int d = 128 * part; d < 128 * part + 128 && ok; d += 32) {
                             float t[32];
                             tmem_ld32(tmem + lanes + d, t);
 #pragma unroll
@@ -1009,8 +1014,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
                 l = __fadd_rn(l, __fadd_rn(sum_a, sum_b));
                 // the chunk before is multiplied: its probabilities are read
                 if (j > 0 && ok) warp_wait(smem_addr(&bars->empty[last.s]), last.parity, ok);
+                if (ok) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) sts16(prow ^ (i << 4), pack8(v + 8 * i));
+                    for (int i = 0; i < 4; ++i) sts16(prow ^ (i << 4), pack8(v + 8 * i));
+                }
                 fence_async_smem();
                 tc_fence_before_sync();
                 __syncwarp();
@@ -1023,7 +1030,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             head_sync();
             const float total = __fadd_rn(__fadd_rn(heads[0], heads[64]), __fadd_rn(heads[128], heads[192]));
             head_sync();   // read before they are written again
-            if (half == 0 && part == 0) {
+            if (half == 0 && part == 0 && ok) {
                 const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
                 const float lse2 = total == 0.0f ? -INFINITY : __fadd_rn(__fsub_rn(m, kLift), log2f(total));
                 asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(smem_addr(smem) + kOffStats + (tile & 1) * 512 + 8 * row),
