@@ -248,7 +248,7 @@ struct Walk {
     }
 };
 
-struct alignas(8) TileBarriers {
+struct alignas(16) TileBarriers {
     // in the leader: arrivals of both CTAs
     uint64_t peer_full[kStages];   // rank 1: a query tile or its rows for q . K have landed
     uint64_t peer_refilled[kStages];   // ... its rows for p . K

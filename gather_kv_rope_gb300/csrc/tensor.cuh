@@ -28,7 +28,6 @@ __device__ __forceinline__ void mbar_init_fence() {
 // has waits that run out: wait_quiet's limit is that many clocks, and a poll does not suspend.
 #ifdef GKR_WAIT_CLOCKS
 constexpr int64_t kWaitClocks = GKR_WAIT_CLOCKS;
-constexpr uint32_t kSuspendNs = 0;
 constexpr int kWaitPolls = 1;
 #else
 constexpr int64_t kWaitClocks = INT64_C(4000000000);   // 2 s at 2 GHz
@@ -37,6 +36,16 @@ constexpr int kWaitPolls = 64;
 #endif
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     uint32_t done;
+#ifdef GKR_WAIT_CLOCKS
+    // (try_wait may suspend for as long as it likes, whatever the hint)
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+#else
     asm volatile(
         "{\n .reg .pred p;\n"
         " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
@@ -44,6 +53,7 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
         : "=r"(done)
         : "r"(bar), "r"(parity), "r"(kSuspendNs)
         : "memory");
+#endif
     return done != 0u;
 }
 __device__ __forceinline__ uint64_t global_ns() {
