@@ -53,10 +53,11 @@ constexpr int kSoftmaxWarps = 8;         // warp w: tensor-memory lanes 32 (w % 
                                          // their columns
 constexpr int kMoveWarps = 8;            // write results, warp w of them as above
 constexpr int kFirstMove = kSoftmaxWarps;
-constexpr int kMmaWarp = kFirstMove + kMoveWarps;   // products (rank 0); rank 1: tells rank 0 what has landed
+constexpr int kMmaWarp = kFirstMove + kMoveWarps;   // products (rank 0)
 constexpr int kLoadWarp = kMmaWarp + 1;  // query tiles and rows for q . K; the pair's work
 constexpr int kRefillWarp = kLoadWarp + 1;   // rows for p . K, the query's last dims
-constexpr int kTileThreads = (kRefillWarp + 1) * 32;
+constexpr int kRelayWarp = kRefillWarp + 1;  // tells rank 0 what has landed
+constexpr int kTileThreads = (kRelayWarp + 1) * 32;
 constexpr uint32_t kBlockBytes = kCtaKeys * kRowBytes;      // 64 dims of 64 rows
 constexpr uint32_t kHalfBytes = 4 * kBlockBytes;            // 256 dims
 constexpr uint32_t kStageBytes = 2 * kHalfBytes;
@@ -250,11 +251,11 @@ struct Walk {
 
 struct alignas(16) TileBarriers {
     // in the leader: arrivals of both CTAs
-    uint64_t peer_full[kStages];   // rank 1: a query tile or its rows for q . K have landed
-    uint64_t peer_refilled[kStages];   // ... its rows for p . K
-    uint64_t peer_tail;            // ... the query's last dims
-    uint64_t s_free;               // softmax: the logits are read
-    uint64_t p_full;               // softmax: the probabilities are written
+    uint64_t q_ready[2];           // relays: a query tile (even, odd) has landed
+    uint64_t tail_ready;           // ... its last dims have
+    uint64_t k_ready[2];           // all that q . K of a chunk (even, odd) waits for.  Relays: its rows
+                                   // have landed; softmax: the logits before them are read
+    uint64_t p_ready[2];           // and p . K.  Relays: its rows; softmax: the probabilities are written
     uint64_t o_free;               // movers: a tile's output is read
     // in each CTA
     uint64_t full[kStages];        // a query tile or rows for q . K have landed
@@ -454,8 +455,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     }
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(smem_addr(&bars->peer_full[s]), 1);
-            mbar_init(smem_addr(&bars->peer_refilled[s]), 1);
             mbar_init(smem_addr(&bars->full[s]), 1);
             mbar_init(smem_addr(&bars->refilled[s]), 1);
             mbar_init(smem_addr(&bars->empty[s]), 1);
@@ -465,11 +464,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             mbar_init(smem_addr(&bars->s_full[s]), 1);
             mbar_init(smem_addr(&bars->copied[s]), 1);
             mbar_init(smem_addr(&bars->stats[s]), kSoftmaxWarps);
+            mbar_init(smem_addr(&bars->q_ready[s]), 2);
+            mbar_init(smem_addr(&bars->k_ready[s]), 2 + 2 * kSoftmaxWarps);
+            mbar_init(smem_addr(&bars->p_ready[s]), 2 + 2 * kSoftmaxWarps);
         }
-        mbar_init(smem_addr(&bars->peer_tail), 1);
+        mbar_init(smem_addr(&bars->tail_ready), 2);
         mbar_init(smem_addr(&bars->tail), 1);
-        mbar_init(smem_addr(&bars->s_free), 2 * kSoftmaxWarps);
-        mbar_init(smem_addr(&bars->p_full), 2 * kSoftmaxWarps);
         mbar_init(smem_addr(&bars->o_free), 2 * kMoveWarps);
         mbar_init(smem_addr(&bars->drained), 1);
         bars->timed_out = 0;
@@ -619,37 +619,73 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             if (used[i] > 0 && !wait_landed(smem_addr(&bars->refilled[i]), (used[i] - 1) & 1)) ok = false;
         if (tile > 1 && !wait_landed(smem_addr(&bars->tail), (tile - 1) & 1)) ok = false;
         __syncwarp();
+    } else if (warp == kRelayWarp) {
+        // ------------------------------------------------------------- what has landed
+        // In the order in which the products need it.  No CTA's relay is a phase ahead of the other's: before
+        // the next arrival at a barrier comes one that the products of the phase before must have
+        // preceded (rows for p . K land after q . K).
+        const uint32_t q_ready = map_rank(smem_addr(&bars->q_ready[0]), 0);
+        const uint32_t tail_ready = map_rank(smem_addr(&bars->tail_ready), 0);
+        const uint32_t k_ready = map_rank(smem_addr(&bars->k_ready[0]), 0);
+        const uint32_t p_ready = map_rank(smem_addr(&bars->p_ready[0]), 0);
+        uint32_t turns = 0;        // bit s: parity of the chunks that p has met in stage s
+        int jq = 0, jo = 0;
+        Ring<kStages> ro;          // the stage of chunk jo; `ring`: of the next item of the loads
+        auto pass_on = [&](uint64_t* bar, uint32_t parity, uint32_t to) -> bool {
+            if (!warp_wait(smem_addr(bar), parity, ok)) return false;
+            if (lane == 0) mbar_arrive_cluster(to);
+            return true;
+        };
+        auto refilled = [&]() -> bool {
+            if (!pass_on(&bars->refilled[ro.s], turns >> ro.s & 1u, p_ready + 8 * (jo & 1))) return false;
+            turns ^= 1u << ro.s;
+            ro.next();
+            ++jo;
+            return true;
+        };
+        Part s;
+        for (int tile = 0; part_at(tile, s); ++tile) {
+            if (!pass_on(&bars->full[ring.s], ring.parity, q_ready + 8 * (tile & 1))) break;
+            ring.next();
+            if (tile > 0 && !refilled()) break;   // of the tile before
+            ro = ring;
+            if (!pass_on(&bars->tail, tile & 1, tail_ready)) break;
+#pragma unroll 1
+            for (int c = s.begin; c < s.end; ++c, ++jq) {
+                if (!pass_on(&bars->full[ring.s], ring.parity, k_ready + 8 * (jq & 1))) break;
+                ring.next();
+                if (c > s.begin && !refilled()) break;
+            }
+            if (!ok) break;
+        }
+        if (ok && jo < jq) refilled();
     } else if (warp == kMmaWarp) {
         // ------------------------------------------------------------- products
-        // The whole warp runs this, one lane issues (elect_lane).  In rank 1 it passes on, in the
-        // same order, that this CTA's loads have landed.  q . K is one chunk ahead of p . K within
-        // a tile; between tiles p . K of the last chunk comes first, as it and the writing of the
-        // results take longer than what the next tile needs until its first p . K.
-        const uint32_t elected = elect_lane();
-        const uint64_t q_desc = sw128_desc(smem_addr(smem));
-        const uint64_t k_desc0 = sw128_desc(smem_addr(smem + kOffStages));
-        const uint64_t v_desc0 = sw128_mn_desc(smem_addr(smem + kOffStages), kBlockBytes);
-        const uint64_t p_desc0 = sw128_desc(smem_addr(smem + kOffP));
-        const uint32_t q_lo = static_cast<uint32_t>(q_desc), k_lo = static_cast<uint32_t>(k_desc0);
-        const uint32_t v_lo = static_cast<uint32_t>(v_desc0), p_lo = static_cast<uint32_t>(p_desc0);
-        uint32_t turns = 0;                   // bit s: parity of the chunks that p has met in stage s
-        int jq = 0, jo = 0;                   // chunks multiplied by q, by p
-        int tq = 0, to = 0, left_q = 0, left_next = 0, left_o = 0;   // parts begun, and what is left of them
-        bool some = true, opened = false, fresh = true;   // opened: the next part's query is on its way
-        Ring<kStages> rq;                     // the stage of chunk jq; `ring`: of chunk jo
-        Part s;
+        // The whole warp runs this, one lane issues (elect_lane).  q . K is one chunk ahead of p . K
+        // within a tile; between tiles p . K of the last chunk comes first, as it and the writing of
+        // the results take longer than what the next tile needs until its first p . K.  A product
+        // waits for one barrier: three of them took 400 cycles a chunk.
+        if (rank == 0) {
+            const uint32_t elected = elect_lane();
+            const uint64_t q_desc = sw128_desc(smem_addr(smem));
+            const uint64_t k_desc0 = sw128_desc(smem_addr(smem + kOffStages));
+            const uint64_t v_desc0 = sw128_mn_desc(smem_addr(smem + kOffStages), kBlockBytes);
+            const uint64_t p_desc0 = sw128_desc(smem_addr(smem + kOffP));
+            const uint32_t q_lo = static_cast<uint32_t>(q_desc), k_lo = static_cast<uint32_t>(k_desc0);
+            const uint32_t v_lo = static_cast<uint32_t>(v_desc0), p_lo = static_cast<uint32_t>(p_desc0);
+            int jq = 0, jo = 0;                   // chunks multiplied by q, by p
+            int tq = 0, to = 0, left_q = 0, left_next = 0, left_o = 0;   // parts begun, and what is left of them
+            bool some = true, opened = false, fresh = true;   // opened: the next part's query is on its way
+            Ring<kStages> rq;                     // the stage of chunk jq; `ring`: of chunk jo
+            Part s;
 #pragma unroll 1
-        while (true) {
-            if (some && left_q == 0 && !opened && jq - jo < 2) {
-                some = part_at(tq, s);
-                if (!ok) break;
-                if (!some) continue;
-                left_next = s.end - s.begin;
-                if (!warp_wait(smem_addr(&bars->full[rq.s]), rq.parity, ok)) break;
-                if (rank != 0) {
-                    if (lane == 0) mbar_arrive_cluster(map_rank(smem_addr(&bars->peer_full[rq.s]), 0));
-                } else {
-                    if (!warp_wait(smem_addr(&bars->peer_full[rq.s]), rq.parity, ok)) break;
+            while (true) {
+                if (some && left_q == 0 && !opened && jq - jo < 2) {
+                    some = part_at(tq, s);
+                    if (!ok) break;
+                    if (!some) continue;
+                    left_next = s.end - s.begin;
+                    if (!warp_wait(smem_addr(&bars->q_ready[tq & 1]), (tq >> 1) & 1, ok)) break;
                     // q . K of the tile before has read its query
                     if (jq > 0 && !warp_wait(smem_addr(&bars->s_full[(jq - 1) & 1]), ((jq - 1) >> 1) & 1, ok)) break;
                     tc_fence_after_sync();
@@ -663,27 +699,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
                     }
                     __syncwarp();
                     mma_commit_pair(smem_addr(&bars->copied[tq & 1]), elected);
-                }
-                rq.next();
-                opened = true;
-            } else if (some && jq - jo < 2 && !(opened && jo < jq)) {
-                if (opened) {
-                    if (!warp_wait(smem_addr(&bars->tail), tq & 1, ok)) break;
-                    if (rank != 0) {
-                        if (lane == 0) mbar_arrive_cluster(map_rank(smem_addr(&bars->peer_tail), 0));
-                    } else if (!warp_wait(smem_addr(&bars->peer_tail), tq & 1, ok)) {
-                        break;
+                    rq.next();
+                    opened = true;
+                } else if (some && jq - jo < 2 && !(opened && jo < jq)) {
+                    if (opened) {
+                        if (!warp_wait(smem_addr(&bars->tail_ready), tq & 1, ok)) break;
+                        opened = false;
+                        left_q = left_next;
+                        ++tq;
                     }
-                    opened = false;
-                    left_q = left_next;
-                    ++tq;
-                }
-                if (!warp_wait(smem_addr(&bars->full[rq.s]), rq.parity, ok)) break;
-                if (rank != 0) {
-                    if (lane == 0) mbar_arrive_cluster(map_rank(smem_addr(&bars->peer_full[rq.s]), 0));
-                } else {
-                    if (!warp_wait(smem_addr(&bars->peer_full[rq.s]), rq.parity, ok)) break;
-                    if (jq > 0 && !warp_wait(smem_addr(&bars->s_free), (jq - 1) & 1, ok)) break;
+                    if (!warp_wait(smem_addr(&bars->k_ready[jq & 1]), (jq >> 1) & 1, ok)) break;
                     tc_fence_after_sync();
                     const uint32_t b = k_lo + rq.s * (kStageBytes >> 4);
                     if (elected) {
@@ -700,25 +725,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
                     }
                     __syncwarp();
                     mma_commit_pair(smem_addr(&bars->s_full[jq & 1]), elected);
-                }
-                rq.next();
-                ++jq;
-                --left_q;
-            } else if (jo < jq) {
-                if (left_o == 0) {
-                    if (!part_at(to, s)) break;
-                    left_o = s.end - s.begin;
-                    ring.next();
-                    ++to;
-                    fresh = true;
-                }
-                const uint32_t turn = turns >> ring.s & 1u;
-                if (!warp_wait(smem_addr(&bars->refilled[ring.s]), turn, ok)) break;
-                if (rank != 0) {
-                    if (lane == 0) mbar_arrive_cluster(map_rank(smem_addr(&bars->peer_refilled[ring.s]), 0));
-                } else {
-                    if (!warp_wait(smem_addr(&bars->peer_refilled[ring.s]), turn, ok)) break;
-                    if (!warp_wait(smem_addr(&bars->p_full), jo & 1, ok)) break;
+                    rq.next();
+                    ++jq;
+                    --left_q;
+                } else if (jo < jq) {
+                    if (left_o == 0) {
+                        if (!part_at(to, s)) break;
+                        left_o = s.end - s.begin;
+                        ring.next();
+                        ++to;
+                        fresh = true;
+                    }
+                    if (!warp_wait(smem_addr(&bars->p_ready[jo & 1]), (jo >> 1) & 1, ok)) break;
                     if (fresh && to > 1 && !warp_wait(smem_addr(&bars->o_free), to & 1, ok)) break;   // of part to - 2
                     tc_fence_after_sync();
                     const uint32_t b = v_lo + ring.s * (kStageBytes >> 4);
@@ -734,23 +752,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
                     }
                     __syncwarp();
                     mma_commit_pair(smem_addr(&bars->empty[ring.s]), elected);
+                    ring.next();
+                    ++jo;
+                    --left_o;
+                    fresh = false;
+                } else {
+                    break;
                 }
-                turns ^= 1u << ring.s;
-                ring.next();
-                ++jo;
-                --left_o;
-                fresh = false;
-            } else {
-                break;
             }
-        }
-        // whatever ended the loop, no product is under way when the pair leaves
-        if (rank == 0) {
+            // whatever ended the loop, no product is under way when the pair leaves
             mma_commit_pair(smem_addr(&bars->drained), elected);
             if (!wait_landed(smem_addr(&bars->drained), 0)) ok = false;
             __syncwarp();
         }
-    } else if (warp >= kFirstMove) {
+    } else if (warp >= kFirstMove && warp < kMmaWarp) {
         // ------------------------------------------------------------- results
         // Warp w has tensor-memory lanes 32 (w % 4) .. and half w / 4 of what is in them: lane L is
         // row L % 64 of this CTA and of the output the dims 256 (L / 64) ...  The rows leave
@@ -902,8 +917,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
         float* const heads = reinterpret_cast<float*>(smem + kOffHeads) + row;
         const int self = (part * 2 + half) * 64;
-        const uint32_t s_free = map_rank(smem_addr(&bars->s_free), 0);
-        const uint32_t p_full = map_rank(smem_addr(&bars->p_full), 0);
+        const uint32_t k_ready = map_rank(smem_addr(&bars->k_ready[0]), 0);
+        const uint32_t p_ready = map_rank(smem_addr(&bars->p_ready[0]), 0);
         const float scale = __fmul_rn(p.sm_scale, kLog2e);   // logits in powers of two
         const uint32_t stages = smem_addr(smem) + kOffStages;
         // this thread's 64 bytes of the probabilities
@@ -913,6 +928,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         auto head_any = [&](bool mine) -> bool { return group_any(kHeadsBar + (warp & 1), 128, mine); };
         uint32_t turns = 0;        // bit s: parity of the chunks so far in stage s
         int j = 0;
+        if (lane == 0 && ok) mbar_arrive_cluster(k_ready);   // no logits before the first chunk's
         Ring<kStages> last;        // the stage of the chunk before
         Part s;
 #pragma unroll 1
@@ -940,7 +956,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
                 tmem_ld32(tmem + lanes + kSCol + 32 * part, v);
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0 && ok) mbar_arrive_cluster(s_free);
+                if (lane == 0 && ok) mbar_arrive_cluster(k_ready + 8 * ((j + 1) & 1));
                 // columns that some row of the tile does not see
                 if (key + 32 > s.least) {
                     const int64_t from = s.least - key;
@@ -1021,7 +1037,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
                 fence_async_smem();
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0 && ok) mbar_arrive_cluster(p_full);
+                if (lane == 0 && ok) mbar_arrive_cluster(p_ready + 8 * (j & 1));
                 last = ring;
                 turns ^= 1u << ring.s;
                 ring.next();
