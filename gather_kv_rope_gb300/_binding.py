@@ -705,21 +705,28 @@ def kv_evict(indices: torch.Tensor, weights: torch.Tensor, keep: int, recent: in
     return kept, kept_weights, evicted
 
 
-def _vector(t: torch.Tensor, name: str, length: int | None = None, dtype=torch.int32) -> int:
+_I32 = torch.int32
+
+
+def _vector(t: torch.Tensor, name: str, length: int | None = None, dtype=_I32) -> int:
     """Length of a contiguous 1-D tensor, checked against `length` where that is given."""
-    if t.dtype != dtype or t.dim() != 1 or not t.is_contiguous() \
-            or (length is not None and t.shape[0] != length):
+    shape = t.shape
+    if t.dtype is not dtype or len(shape) != 1 or not t.is_contiguous() \
+            or (length is not None and shape[0] != length):
         n = "" if length is None else f" [{length}]"
         raise ValueError(f"{name} must be a contiguous 1-D {dtype} tensor{n}".replace("torch.", ""))
-    return t.shape[0]
+    return shape[0]
 
 
-def _out_vector(t, length: int, dtype: torch.dtype, name: str, like: torch.Tensor):
-    """A given 1-D output after its checks, or a new one beside `like`."""
-    if t is None:
-        return torch.empty(length, dtype=dtype, device=like.device)
-    _vector(t, name, length, dtype)
-    return t
+def _device_of(*ts: torch.Tensor) -> torch.device:
+    """The CUDA device that all of them (None: skipped) are on."""
+    index = ts[0].get_device()
+    for t in ts:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"all tensors must be on {ts[0].device}; got one on {t.device}")
+    if index < 0 or not ts[0].is_cuda:
+        raise ValueError("this call needs CUDA tensors (there is no CPU path)")
+    return ts[0].device
 
 
 def kv_allocate(past: torch.Tensor, added: torch.Tensor, block_table: torch.Tensor,
@@ -743,38 +750,65 @@ def kv_allocate(past: torch.Tensor, added: torch.Tensor, block_table: torch.Tens
     has slot -1, and err_flag ERR_SLOT.  The lengths stay on the GPU; nothing is kept."""
     B = _vector(past, "past")
     _vector(added, "added", B)
-    stride = _rows(block_table, torch.int32, "block_table")
-    if block_table.shape[0] != B:
+    stride = _rows(block_table, _I32, "block_table")
+    rows, W = block_table.shape
+    if rows != B:
         raise ValueError("block_table must have a row for each request")
     F = _vector(free_pages, "free_pages")
     num_tokens = int(num_tokens)
-    _check(0 <= num_tokens < 1 << 31, "num_tokens must be in [0, 2^31)")
-    slot_mapping = _out_vector(slot_mapping, num_tokens, torch.int64, "slot_mapping", past)
-    positions = _out_vector(positions, num_tokens, torch.int64, "positions", past)
-    starts = _out_vector(starts, B + 1, torch.int32, "starts", past)
-    taken = _out_vector(taken, 1, torch.int32, "taken", past)
+    if not 0 <= num_tokens < 1 << 31:
+        raise ValueError("num_tokens must be in [0, 2^31)")
+    if slot_mapping is not None:
+        _vector(slot_mapping, "slot_mapping", num_tokens, torch.int64)
+    if positions is not None:
+        _vector(positions, "positions", num_tokens, torch.int64)
+    if starts is not None:
+        _vector(starts, "starts", B + 1)
+    if taken is not None:
+        _vector(taken, "taken", 1)
     _check_err_flag(err_flag)
-    dev = _same_cuda_device(past, added, block_table, free_pages, slot_mapping, positions, starts,
-                            taken, err_flag)
+    dev = _device_of(past, added, block_table, free_pages, slot_mapping, positions, starts, taken,
+                     err_flag)
+    if slot_mapping is None:
+        slot_mapping = torch.empty(num_tokens, dtype=torch.int64, device=dev)
+    if positions is None:
+        positions = torch.empty(num_tokens, dtype=torch.int64, device=dev)
+    if starts is None:
+        starts = torch.empty(B + 1, dtype=_I32, device=dev)
+    if taken is None:
+        taken = torch.empty(1, dtype=_I32, device=dev)
     _call(dev, lib().gkr_kv_allocate, past.data_ptr(), added.data_ptr(), B, block_table.data_ptr(),
-          stride, block_table.shape[1], free_pages.data_ptr(), F, int(block_size), num_tokens,
+          stride, W, free_pages.data_ptr(), F, int(block_size), num_tokens,
           slot_mapping.data_ptr(), positions.data_ptr(), starts.data_ptr(), taken.data_ptr(),
           _ptr(err_flag), _opts(launch_opts))
     return slot_mapping, positions, starts, taken
 
 
-def _slots(block_table, lengths, block_size, width, first, indices, starts, err_flag, launch_opts):
+def _slots(block_table, lengths, block_size, width, first, indices, starts, packed, err_flag,
+           launch_opts):
     B = _vector(lengths, "lengths")
-    stride = _rows(block_table, torch.int32, "block_table")
-    if block_table.shape[0] != B:
+    stride = _rows(block_table, _I32, "block_table")
+    rows, W = block_table.shape
+    if rows != B:
         raise ValueError("block_table must have a row for each request")
     if first is not None:
         _vector(first, "first", B)
+    shape = (width,) if packed else (B, width)
+    if indices is not None and (indices.dtype is not _I32 or indices.shape != shape
+                                or not indices.is_contiguous()):
+        raise ValueError(f"indices must be a contiguous int32 tensor {list(shape)}")
+    if starts is not None:
+        _vector(starts, "starts", B + 1)
     _check_err_flag(err_flag)
-    dev = _same_cuda_device(lengths, block_table, first, indices, starts, err_flag)
-    _call(dev, lib().gkr_kv_slots, block_table.data_ptr(), stride, block_table.shape[1],
-          lengths.data_ptr(), _ptr(first), B, int(block_size), width, indices.data_ptr(),
-          _ptr(starts), _ptr(err_flag), _opts(launch_opts))
+    dev = _device_of(lengths, block_table, first, indices, starts, err_flag)
+    if indices is None:
+        indices = torch.empty(shape, dtype=_I32, device=dev)
+    if packed and starts is None:
+        starts = torch.empty(B + 1, dtype=_I32, device=dev)
+    _call(dev, lib().gkr_kv_slots, block_table.data_ptr(), stride, W, lengths.data_ptr(),
+          _ptr(first), B, int(block_size), width, indices.data_ptr(), _ptr(starts),
+          _ptr(err_flag), _opts(launch_opts))
+    return indices, starts
 
 
 def kv_slots(block_table: torch.Tensor, lengths: torch.Tensor, block_size: int, width: int,
@@ -789,10 +823,8 @@ def kv_slots(block_table: torch.Tensor, lengths: torch.Tensor, block_size: int, 
     A position without a page gets -1, and err_flag ERR_INDEX, as where a row is too short."""
     width = int(width)
     _check(0 <= width < 1 << 31, "width must be in [0, 2^31)")
-    indices = _buffer(indices, lengths.shape[0] if lengths.dim() == 1 else 0, width, torch.int32,
-                      "indices", lengths)
-    _slots(block_table, lengths, block_size, width, first, indices, None, err_flag, launch_opts)
-    return indices
+    return _slots(block_table, lengths, block_size, width, first, indices, None, False, err_flag,
+                  launch_opts)[0]
 
 
 def kv_slots_packed(block_table: torch.Tensor, lengths: torch.Tensor, block_size: int, total: int,
@@ -804,11 +836,8 @@ def kv_slots_packed(block_table: torch.Tensor, lengths: torch.Tensor, block_size
     returns for them, with these starts, are what prompt_attention takes as kv and kv_starts."""
     total = int(total)
     _check(0 <= total < 1 << 31, "total must be in [0, 2^31)")
-    indices = _out_vector(indices, total, torch.int32, "indices", lengths)
-    starts = _out_vector(starts, lengths.shape[0] + 1 if lengths.dim() == 1 else 1, torch.int32,
-                         "starts", lengths)
-    _slots(block_table, lengths, block_size, total, first, indices, starts, err_flag, launch_opts)
-    return indices, starts
+    return _slots(block_table, lengths, block_size, total, first, indices, starts, True, err_flag,
+                  launch_opts)
 
 
 @functools.lru_cache(maxsize=256)
@@ -845,29 +874,35 @@ def prefix_attention_workspace(num_heads: int, num_queries: int, prefix_length: 
                              _device_index(device))
 
 
-def _attention_outputs(q, out, lse):
-    """q bf16 [n, H, 512] and the outputs beside it, checked or new."""
+def _attention_args(q, out, lse, workspace):
+    """Checks of q bf16 [n, H, 512] and of what the caller gave beside it."""
     shape = q.shape
-    if q.dtype != torch.bfloat16 or len(shape) != 3 or shape[2] != HEAD_DIM \
+    if q.dtype is not torch.bfloat16 or len(shape) != 3 or shape[2] != HEAD_DIM \
             or not q.is_contiguous():
         raise ValueError("q must be a contiguous bf16 tensor [queries, heads, 512]")
+    if out is not None and (out.dtype is not torch.bfloat16 or not out.is_contiguous()
+                            or out.shape != shape):
+        raise ValueError("out must be a contiguous bf16 tensor of q's shape")
+    if lse is not None and (lse.dtype is not torch.float32 or not lse.is_contiguous()
+                            or lse.shape != shape[:2]):
+        raise ValueError("lse must be a contiguous fp32 tensor [queries, heads]")
+    if workspace is not None and (workspace.dtype is not torch.uint8
+                                  or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    return shape[0], shape[1]
+
+
+def _attention_buffers(q, n, H, out, lse, workspace, size, dev):
+    """What the caller did not give, allocated (size: bytes of workspace)."""
     if out is None:
         out = torch.empty_like(q)
-    elif out.dtype != torch.bfloat16 or not out.is_contiguous() or out.shape != shape:
-        raise ValueError("out must be a contiguous bf16 tensor of q's shape")
     if lse is None:
-        lse = torch.empty(shape[0], shape[1], dtype=torch.float32, device=q.device)
-    elif lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != shape[:2]:
-        raise ValueError("lse must be a contiguous fp32 tensor [queries, heads]")
-    return out, lse
-
-
-def _work_buffer(workspace, size: int, dev):
+        lse = torch.empty(n, H, dtype=torch.float32, device=dev)
     if workspace is None:
-        return torch.empty(size, dtype=torch.uint8, device=dev) if size else None
-    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 tensor")
-    return workspace
+        if size == 0:
+            return out, lse, None, 0
+        return out, lse, torch.empty(size, dtype=torch.uint8, device=dev), size
+    return out, lse, workspace, workspace.numel()
 
 
 def prompt_attention(q: torch.Tensor, kv: torch.Tensor, starts: torch.Tensor, sm_scale: float,
@@ -892,10 +927,10 @@ def prompt_attention(q: torch.Tensor, kv: torch.Tensor, starts: torch.Tensor, sm
     out[i, h] = softmax over the rows it sees of (sm_scale * q[i, h] . K) times K, lse[i, h] the
     log of the softmax's sum; zeros and -inf for a query that sees none.  Queries of no
     request are left as they are.  Returns (out, lse)."""
-    out, lse = _attention_outputs(q, out, lse)
-    T, H, _ = q.shape
+    T, H = _attention_args(q, out, lse, workspace)
     stride = _rows(kv, torch.bfloat16, "kv")
-    if kv.shape[1] != HEAD_DIM or (stride % 8 and kv.shape[0] > 1):
+    N, width = kv.shape
+    if width != HEAD_DIM or (stride % 8 and N > 1):
         raise ValueError("kv must be bf16 [rows, 512], rows a multiple of 8 elements apart")
     if stride % 8:
         stride = HEAD_DIM
@@ -906,14 +941,13 @@ def prompt_attention(q: torch.Tensor, kv: torch.Tensor, starts: torch.Tensor, sm
     else:
         _vector(kv_starts, "kv_starts", B + 1)
     _check_err_flag(err_flag)
-    dev = _same_cuda_device(q, kv, starts, kv_starts, out, lse, err_flag, workspace)
-    if workspace is None and T:
-        workspace = _work_buffer(None, _prompt_workspace(H, T, dev.index), dev)
-    workspace = _work_buffer(workspace, 0, dev)
-    _call(dev, lib().gkr_prompt_attention, q.data_ptr(), H, T, kv.data_ptr(), stride, kv.shape[0],
+    dev = _device_of(q, kv, starts, kv_starts, out, lse, err_flag, workspace)
+    size = _prompt_workspace(H, T, dev.index) if workspace is None and T else 0
+    out, lse, workspace, size = _attention_buffers(q, T, H, out, lse, workspace, size, dev)
+    _call(dev, lib().gkr_prompt_attention, q.data_ptr(), H, T, kv.data_ptr(), stride, N,
           starts.data_ptr(), kv_starts.data_ptr(), B, 1 if causal else 0, float(sm_scale),
-          out.data_ptr(), lse.data_ptr(), _ptr(workspace),
-          0 if workspace is None else workspace.numel(), _ptr(err_flag), _opts(launch_opts))
+          out.data_ptr(), lse.data_ptr(), _ptr(workspace), size, _ptr(err_flag),
+          _opts(launch_opts))
     return out, lse
 
 
@@ -933,22 +967,20 @@ def prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, prefix: torch.Tenso
     q, k_cache, sm_scale, out and lse are sparse_attention's.  Returns (out, lse)."""
     desc = _cache_desc(k_cache)
     _check(desc.record == MXFP4, "prefix_attention reads the MXFP4 records (272 bytes)")
-    out, lse = _attention_outputs(q, out, lse)
-    Q, H, _ = q.shape
+    Q, H = _attention_args(q, out, lse, workspace)
     L = _vector(prefix, "prefix")
-    istride = _rows(indices, torch.int32, "indices")
+    istride = _rows(indices, _I32, "indices")
     rows, K = indices.shape
     if rows != Q:
         raise ValueError("indices must have a row for each query")
     if not 1 <= H <= 128:
         raise ValueError("prefix_attention takes 1 to 128 heads")
     _check_err_flag(err_flag)
-    dev = _same_cuda_device(q, k_cache, prefix, indices, out, lse, err_flag, workspace)
-    if workspace is None and Q:
-        workspace = _work_buffer(None, _prefix_workspace(H, Q, L, K, dev.index), dev)
-    workspace = _work_buffer(workspace, 0, dev)
+    dev = _device_of(q, k_cache, prefix, indices, out, lse, err_flag, workspace)
+    size = _prefix_workspace(H, Q, L, K, dev.index) if workspace is None and Q else 0
+    out, lse, workspace, size = _attention_buffers(q, Q, H, out, lse, workspace, size, dev)
     _call(dev, lib().gkr_prefix_attention, q.data_ptr(), H, k_cache.data_ptr(), ctypes.byref(desc),
           prefix.data_ptr(), L, indices.data_ptr(), istride, Q, K, float(sm_scale),
-          out.data_ptr(), lse.data_ptr(), _ptr(workspace),
-          0 if workspace is None else workspace.numel(), _ptr(err_flag), _opts(launch_opts))
+          out.data_ptr(), lse.data_ptr(), _ptr(workspace), size, _ptr(err_flag),
+          _opts(launch_opts))
     return out, lse
