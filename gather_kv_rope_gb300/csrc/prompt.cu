@@ -19,20 +19,33 @@
 //     by the other 64 rows' half of this CTA's dims for p . K (a product of the pair takes half
 //     of its columns from each CTA, at the same address in both).
 //   * The next query tile passes through the ring like a chunk; the tensor cores copy it on to
-//     tensor memory.  Its stage then takes the results of the tile before, which leave by TMA
-//     stores.  So neither passes through registers on the way that every product's operands
-//     take: loads, stores and tensor-memory accesses of the warps share one pipe of 128 bytes a
+//     tensor memory (tcgen05.cp).  Its stage then takes the results of the tile before, which leave
+//     by TMA stores of eight warps of their own.  So neither is on the softmax's way, and little of
+//     it on that of the warps' loads, stores and tensor-memory accesses: one pipe of 128 bytes a
 //     cycle, which a tile's query and results took for 9000 cycles.
 //   * q . K of the next chunk is issued before p . K of this one, so that the softmax of a chunk
 //     has the time of two products.  The probabilities have one buffer, and so have the logits.
-//   * Work: a unit for each tile (its loads and its epilogue) and one for each of its chunks, all
-//     tiles in a row, cut evenly over the pairs.  Each CTA finds its cut from the requests'
-//     lengths by itself (closed sums, no plan to launch).  The pieces of a tile that is cut go
-//     to the workspace (fp32 rows and their log-sum-exp) and a second kernel joins them.
+//   * The thread that issues the products waits for one barrier before each, at which the softmax
+//     and a warp of each CTA that relays what has landed arrive: three barriers took 400
+//     cycles a chunk.  Its loops are unrolled: rolled up they cost a quarter of the rate.
+//   * Work: units for each tile (its loads and its epilogue, as long as two chunks) and for each of
+//     its chunks, all tiles in a row, cut evenly over the pairs.  One warp of each CTA finds the cut
+//     from the requests' lengths by itself (closed sums, no plan to launch).  The pieces of a tile
+//     that is cut go to the workspace (fp32 rows and their log-sum-exp) and a second kernel joins
+//     them.  Where there are few tiles and none much longer than an even share, each pair has
+//     a whole one.
 // What a row does not see: columns past its last row are -inf before the softmax.  Their
 // probabilities are 0, but 0 times an infinity or NaN is NaN, so in a chunk with such
 // columns, values that are not finite are cleared before p . K (a row that does see them has NaN
 // from its logit).
+//
+// Measured (in a graph): 8192 tokens of 64 heads 2.26 to 2.35 ms, 1945 to 1870 TFLOP/s, 99 to 95 % of the
+// measured burst rate (at the power cap, over seconds, 2.55 ms, 1720); 2 x 1024 queries of 128 heads
+// behind 7168 rows 2.13 ms; 2048 tokens of 128 heads 0.37 ms, 1460.  A chunk takes 2213 cycles in the
+// middle of a tile, a tile about 5500 more: the first softmax and the reading of the results, one
+// after the other, and loads that wait for the stage that the results are in.  Tried without gain: the
+// output freed in two halves, p . K of the last chunk before the next query is copied or in the order
+// in which they are ready, 16-row steps of p . K left out where no row is seen.
 #include <cmath>
 
 #include "attend.cuh"
@@ -124,11 +137,15 @@ struct TileArgs {
 // with (x: its first row, y: its rows); slot 0, a tile begun before, which it ended or not.
 constexpr int kTailOpen = 1, kHeadThere = 2, kHeadEnds = 4;
 
-// Work is counted in units of half a chunk; a tile costs kTileUnits besides its chunks.
+// Work is counted in units of half a chunk; a tile costs kTileUnits besides its chunks (measured 5500
+// cycles, a chunk 2213: with 2 units, 8192 x 64 heads took 2.64 ms instead of 2.31, as the pairs that
+// have the short tiles at a prompt's beginning came last).
 constexpr int kTileUnits = 4;
-// Fewer units than this for each pair are not worth another piece to join.
+// Fewer units than this for each pair are not worth another piece to join (one query of 128 heads, 4096
+// rows: 20.2 us, with 12 units 23.5).
 constexpr int64_t kUnitsAPair = 6;
-// To write pieces and join them takes as long as about so many units.
+// To write pieces and join them takes as long as about so many units (511 tokens of 16 heads: whole
+// tiles 17.3 us, cut 25.6; 200 of 32 13.8 and 18.2).
 constexpr int64_t kJoinUnits = 8;
 // No pair has a tile of its own where there are more units than this for each.
 constexpr int64_t kWholeUnits = 64;
@@ -663,8 +680,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         // ------------------------------------------------------------- products
         // The whole warp runs this, one lane issues (elect_lane).  q . K is one chunk ahead of p . K
         // within a tile; between tiles p . K of the last chunk comes first, as it and the writing of
-        // the results take longer than what the next tile needs until its first p . K.  A product
-        // waits for one barrier: three of them took 400 cycles a chunk.
+        // the results take longer than what the next tile needs until its first p . K.
         if (rank == 0) {
             const uint32_t elected = elect_lane();
             const uint64_t q_desc = sw128_desc(smem_addr(smem));
