@@ -204,6 +204,9 @@ __device__ __forceinline__ void query_to_tmem(uint32_t tile, int row, int first,
     tmem_st_wait();
 }
 
+// kParted: part of a prefix attention, with a prefix in front of the lists or fp32 rows as results (a form of
+// its own, as the tests for them cost the plain one 1 to 3 %).
+template <bool kParted>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     attend_kernel(const AttentionParams p, const Cut cut, const __grid_constant__ CUtensorMap q_map) {
     extern __shared__ uint8_t smem_raw[];
@@ -337,8 +340,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 const uint32_t to = ring + (ahead & (kIndexRing - 1)) * 128;
                 const int64_t k = ci * kChunkKeys + key;
                 if (k < p.topk)
-                    cp_async4(to, k < p.prefix_length ? p.prefix + k
-                                                      : p.indices + qi * p.index_stride + (k - p.prefix_length));
+                    cp_async4(to, !kParted              ? p.indices + qi * p.index_stride + k
+                                  : k < p.prefix_length ? p.prefix + k
+                                                        : p.indices + qi * p.index_stride + (k - p.prefix_length));
                 else asm volatile("st.shared.b32 [%0], %1;" ::"r"(to), "r"(-1) : "memory");
                 if (++ci == cut.per_query) {
                     ci = 0;
@@ -621,7 +625,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 tc_fence_after_sync();
                 const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
                 const bool whole = seg == 0 && ci + 1 == cut.per_query;
-                const bool narrow = whole && p.wide == 0;
+                const bool narrow = whole && (!kParted || p.wide == 0);
                 const float lse2 =
                     total == 0.0f ? -INFINITY : __fadd_rn(__fsub_rn(m, kLift), log2f(total));
                 // A piece that does not begin its query is its pair's first: slot 0.  Rows leave
@@ -1157,7 +1161,7 @@ __global__ void __launch_bounds__(kWeightThreads, 1)
 
 cudaError_t make_cut(int64_t num_queries, int64_t topk, int32_t num_heads, Cut* cut) {
     int32_t pairs = 0;
-    const cudaError_t e = resident_pairs(reinterpret_cast<const void*>(attend_kernel), kAttendThreads, kAttendSmem, &pairs);
+    const cudaError_t e = resident_pairs(reinterpret_cast<const void*>(attend_kernel<false>), kAttendThreads, kAttendSmem, &pairs);
     if (e != cudaSuccess) return e;
     cut->per_query = topk == 0 ? 1 : (topk + kChunkKeys - 1) / kChunkKeys;
     cut->total = num_queries * cut->per_query;
@@ -1244,8 +1248,14 @@ cudaError_t launch_sparse_attention(const AttentionParams& p, cudaStream_t strea
     CUtensorMap q_map;
     e = q_tensor_map(p, kPairHeads, &q_map);
     if (e != cudaSuccess) return e;
-    e = launch_kernel(attend_kernel, 2 * static_cast<int64_t>(cut.pairs), kAttendThreads, kAttendSmem,
-                      stream, p.pdl, p, cut, q_map);
+    const bool parted = p.wide != 0 || p.prefix_length > 0;
+    if (parted) {   // the kernel's limit of shared memory is set with this
+        int32_t pairs = 0;
+        e = resident_pairs(reinterpret_cast<const void*>(attend_kernel<true>), kAttendThreads, kAttendSmem, &pairs);
+        if (e != cudaSuccess) return e;
+    }
+    e = launch_kernel(parted ? attend_kernel<true> : attend_kernel<false>, 2 * static_cast<int64_t>(cut.pairs),
+                      kAttendThreads, kAttendSmem, stream, p.pdl, p, cut, q_map);
     if (e != cudaSuccess) return e;
     Cuts cuts;
     const int most = find_cuts(cut, &cuts);
