@@ -718,6 +718,14 @@ def _vector(t: torch.Tensor, name: str, length: int | None = None, dtype=_I32) -
     return shape[0]
 
 
+def _int32_size(n: int, name: str) -> int:
+    """A size that C takes as int32: ctypes would cut a larger one to its low bits."""
+    n = int(n)
+    if not 1 <= n < 1 << 31:
+        raise ValueError(f"{name} must be in [1, 2^31)")
+    return n
+
+
 def _device_of(*ts: torch.Tensor) -> torch.device:
     """The CUDA device that all of them (None: skipped) are on."""
     index = ts[0].get_device()
@@ -755,6 +763,7 @@ def kv_allocate(past: torch.Tensor, added: torch.Tensor, block_table: torch.Tens
     if rows != B:
         raise ValueError("block_table must have a row for each request")
     F = _vector(free_pages, "free_pages")
+    block_size = _int32_size(block_size, "block_size")
     num_tokens = int(num_tokens)
     if not 0 <= num_tokens < 1 << 31:
         raise ValueError("num_tokens must be in [0, 2^31)")
@@ -778,7 +787,7 @@ def kv_allocate(past: torch.Tensor, added: torch.Tensor, block_table: torch.Tens
     if taken is None:
         taken = torch.empty(1, dtype=_I32, device=dev)
     _call(dev, lib().gkr_kv_allocate, past.data_ptr(), added.data_ptr(), B, block_table.data_ptr(),
-          stride, W, free_pages.data_ptr(), F, int(block_size), num_tokens,
+          stride, W, free_pages.data_ptr(), F, block_size, num_tokens,
           slot_mapping.data_ptr(), positions.data_ptr(), starts.data_ptr(), taken.data_ptr(),
           _ptr(err_flag), _opts(launch_opts))
     return slot_mapping, positions, starts, taken
@@ -791,6 +800,7 @@ def _slots(block_table, lengths, block_size, width, first, indices, starts, pack
     rows, W = block_table.shape
     if rows != B:
         raise ValueError("block_table must have a row for each request")
+    block_size = _int32_size(block_size, "block_size")
     if first is not None:
         _vector(first, "first", B)
     shape = (width,) if packed else (B, width)
@@ -806,7 +816,7 @@ def _slots(block_table, lengths, block_size, width, first, indices, starts, pack
     if packed and starts is None:
         starts = torch.empty(B + 1, dtype=_I32, device=dev)
     _call(dev, lib().gkr_kv_slots, block_table.data_ptr(), stride, W, lengths.data_ptr(),
-          _ptr(first), B, int(block_size), width, indices.data_ptr(), _ptr(starts),
+          _ptr(first), B, block_size, width, indices.data_ptr(), _ptr(starts),
           _ptr(err_flag), _opts(launch_opts))
     return indices, starts
 
@@ -864,14 +874,15 @@ def _device_index(device) -> int:
 
 def prompt_attention_workspace(num_heads: int, num_tokens: int, device=None) -> int:
     """Bytes of workspace a prompt_attention call of these sizes needs on a device."""
-    return _prompt_workspace(int(num_heads), int(num_tokens), _device_index(device))
+    return _prompt_workspace(_int32_size(num_heads, "num_heads"), int(num_tokens),
+                             _device_index(device))
 
 
 def prefix_attention_workspace(num_heads: int, num_queries: int, prefix_length: int, topk: int,
                                device=None) -> int:
     """Bytes of workspace a prefix_attention call of these sizes needs on a device."""
-    return _prefix_workspace(int(num_heads), int(num_queries), int(prefix_length), int(topk),
-                             _device_index(device))
+    return _prefix_workspace(_int32_size(num_heads, "num_heads"), int(num_queries),
+                             int(prefix_length), int(topk), _device_index(device))
 
 
 def _attention_args(q, out, lse, workspace):

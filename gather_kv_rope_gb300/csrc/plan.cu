@@ -13,8 +13,9 @@
 // does everything: every block sums the lengths of all requests for itself (a few KB from L2) and
 // then finds the request of each of its rows by bisection in shared memory.  Measured in a graph:
 // decoding 64 requests 3.7 us, 524288 tokens of 512 requests 7.8 (their bytes take 1.2), 64 lists of
-// 8191 slots 2.9, 8 packed ones of up to 131072 5.0; a call from Python takes 10 to 19.  New pages are read from the free list, not from the table that other blocks are
-// writing.  No atomics but for the error bits: the same call gives the same bytes.
+// 8191 slots 2.9, 8 packed ones of up to 131072 5.0; a call from Python takes 10 to 25, the host's time.
+// New pages are read from the free list, not from the table that other blocks are writing.  No atomics but
+// for the error bits: the same call gives the same bytes.
 #include "device.cuh"
 #include "launch.h"
 

@@ -209,3 +209,19 @@ def test_binding_rejects_bad_tensors(gkr):
             gkr.kv_allocate(*ok, **kw)
     with pytest.raises(ValueError):
         gkr.kv_slots(i32(2, 8), i32(2), 64, 5, indices=i32(2, 6))
+
+
+@pytest.mark.parametrize("wrapped", [2 ** 32 + 64, 2 ** 31, 0, -64])
+def test_binding_refuses_sizes_past_32_bits(gkr, wrapped):
+    """What C takes as int32 is checked before it could be cut to its low bits (2^32 + 64: 64)."""
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)   # noqa: E731
+    with pytest.raises(ValueError, match="block_size"):
+        gkr.kv_allocate(i32(2), i32(2), i32(2, 8), i32(4), wrapped, 5)
+    with pytest.raises(ValueError, match="block_size"):
+        gkr.kv_slots(i32(2, 8), i32(2), wrapped, 5)
+    with pytest.raises(ValueError, match="block_size"):
+        gkr.kv_slots_packed(i32(2, 8), i32(2), wrapped, 5)
+    with pytest.raises(ValueError, match="num_heads"):
+        gkr.prompt_attention_workspace(wrapped, 4, "cuda:0")
+    with pytest.raises(ValueError, match="num_heads"):
+        gkr.prefix_attention_workspace(wrapped, 4, 5, 6, "cuda:0")
