@@ -101,5 +101,11 @@ __device__ __forceinline__ uint4 pack8(const float* v, float f) {
                       pack_bf16x2_rn(__fmul_rn(v[6], f), __fmul_rn(v[7], f)));
 }
 
+// The sum of those eight as they are after the rounding; its two halves are still to be added.
+__device__ __forceinline__ uint64_t sum_rounded(uint4 w) {
+    auto two = [](uint32_t x) { return f32x2(__uint_as_float(x << 16), __uint_as_float(x & 0xFFFF0000u)); };
+    return add_f32x2(add_f32x2(two(w.x), two(w.y)), add_f32x2(two(w.z), two(w.w)));
+}
+
 }  // namespace
 }  // namespace gkr

@@ -204,8 +204,9 @@ __device__ __forceinline__ void query_to_tmem(uint32_t tile, int row, int first,
     tmem_st_wait();
 }
 
-// kParted: part of a prefix attention, with a prefix in front of the lists or fp32 rows as results (a form of
-// its own, as the tests for them cost the plain one 1 to 3 %).
+// kParted: part of a prefix attention, with a prefix in front of the lists or fp32 rows as results, divided by
+// the sum of the probabilities as rounded, as the tiles' are (a form of its own, as the tests for them
+// cost the plain one 1 to 3 %, and its results stay what they were).
 template <bool kParted>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
     attend_kernel(const AttentionParams p, const Cut cut, const __grid_constant__ CUtensorMap q_map) {
@@ -528,7 +529,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
         };
         if (threadIdx.x == kPollThread && ok) fetch_next(qi);
         query(qi);
-        float m = -INFINITY, l = 0.0f;
+        float m = -INFINITY, l = 0.0f, rounded = 0.0f;   // rounded: see the tiles' softmax (kParted)
         bool fresh = true;         // no chunk of this query is in the accumulator
         int64_t seg = ci;          // the segment's first chunk
 #pragma unroll 1
@@ -569,6 +570,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 const float fix = rise ? exp2_approx(__fsub_rn(m, top)) : 1.0f;
                 if (rise) m = top;
                 l = __fmul_rn(l, fix);
+                if constexpr (kParted) rounded = __fmul_rn(rounded, fix);
                 if (!fresh) {
                     // the products of the chunk before are in the accumulator
                     if (ok) warp_wait(smem_addr(&bars->stage_empty[(j - 1) % kStages]), ((j - 1) / kStages) & 1, ok);
@@ -601,20 +603,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
             l = __fadd_rn(l, __fadd_rn(sum_a, sum_b));
             const uint32_t prow = smem_addr(smem + kOffP) + (j & 1) * kPBytes + row * kRowBytes +
                                   ((half * 4 + part * 2 ^ (row & 7)) << 4);
-            sts16(prow, pack8(v));
-            sts16(prow ^ 16u, pack8(v + 8));
+            const uint4 w0 = pack8(v), w1 = pack8(v + 8);
+            sts16(prow, w0);
+            sts16(prow ^ 16u, w1);
             fence_async_smem();
             tc_fence_before_sync();
             __syncwarp();
             if (lane == 0 && ok) mbar_arrive_cluster(p_full + 8 * (j & 1));
+            if constexpr (kParted) {
+                f32x2_split(add_f32x2(sum_rounded(w0), sum_rounded(w1)), sum_a, sum_b);
+                rounded = __fadd_rn(rounded, __fadd_rn(sum_a, sum_b));
+            }
             fresh = false;
             if (last) {
                 // q . K of this query is complete: the next one may take its place, and is
                 // multiplied while this one is written out
                 if (j + 1 < n) query(qi + 1);
                 sums[self] = l;
+                if constexpr (kParted) maxima[self] = rounded;   // free until the next chunk's
                 head_sync();
                 const float total = __fadd_rn(__fadd_rn(sums[0], sums[64]), __fadd_rn(sums[128], sums[192]));
+                float divisor = total;
+                if constexpr (kParted)
+                    divisor = __fadd_rn(__fadd_rn(maxima[0], maxima[64]), __fadd_rn(maxima[128], maxima[192]));
                 // The last value product implies everything before it: each of its chunks passed
                 // only arrivals of warps that had all they waited for.  A head's warps agree on
                 // it, so that its row is written in full or not at all.  (The barrier also puts
@@ -623,7 +634,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 if (lane == 0) wait_quiet(smem_addr(&bars->stage_empty[j % kStages]), (j / kStages) & 1, ok);
                 ok = !head_any(!ok);
                 tc_fence_after_sync();
-                const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
+                const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, divisor);
                 const bool whole = seg == 0 && ci + 1 == cut.per_query;
                 const bool narrow = whole && (!kParted || p.wide == 0);
                 const float lse2 =
@@ -681,6 +692,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 tc_fence_before_sync();
                 m = -INFINITY;
                 l = 0.0f;
+                if constexpr (kParted) rounded = 0.0f;
                 fresh = true;
                 seg = 0;
             }
@@ -1248,7 +1260,7 @@ cudaError_t launch_sparse_attention(const AttentionParams& p, cudaStream_t strea
     CUtensorMap q_map;
     e = q_tensor_map(p, kPairHeads, &q_map);
     if (e != cudaSuccess) return e;
-    const bool parted = p.wide != 0 || p.prefix_length > 0;
+    const bool parted = p.parted != 0;
     if (parted) {   // the kernel's limit of shared memory is set with this
         int32_t pairs = 0;
         e = resident_pairs(reinterpret_cast<const void*>(attend_kernel<true>), kAttendThreads, kAttendSmem, &pairs);

@@ -93,9 +93,10 @@ struct AttentionParams {
     void* workspace;           // attention_workspace() bytes
     int32_t* err;              // nullable
     int32_t pdl;
-    int32_t wide = 0;          // 1: out has fp32 rows and lse is in powers of two (no weights)
+    int32_t parted = 0;        // 1: part of a prefix attention (no weights), and only then:
+    int32_t wide = 0;          // 1: out has fp32 rows and lse is in powers of two
     // entries that come first in every query's list: `topk` counts them, `indices` begins behind
-    // them (no weights)
+    // them
     const int32_t* prefix = nullptr;
     int64_t prefix_length = 0;
 };

@@ -34,14 +34,22 @@
 //     that is cut go to the workspace (fp32 rows and their log-sum-exp) and a second kernel joins
 //     them.  Where there are few tiles and none much longer than an even share, each pair has
 //     a whole one.
+// The tensor cores take the probabilities as bf16 (A and B of a product have one type, and the rows are
+// bf16).  The reference lags the maximum, so the largest one is no power of two, and where one row of K has
+// most of the weight its rounding, up to 2^-9, is the result's as well.  So results are divided by the
+// sum of the probabilities as they were rounded, in which such a rounding cancels, and only the
+// log-sum-exp comes from the sum of what was not: the results of 128 queries of 128 heads behind 16384
+// records are then 0.0017 off (root mean square, relative; rounding them to bf16 alone takes 0.0016), before it
+// was 0.0022.  It costs 1.3 % where the power cap is near (8192 x 64 heads 2.25 -> 2.28 ms), else
+// nothing (4096 x 64 0.627 and 0.625), as the second sum is taken once the products may begin.
 // What a row does not see: columns past its last row are -inf before the softmax.  Their
 // probabilities are 0, but 0 times an infinity or NaN is NaN, so in a chunk with such
 // columns, values that are not finite are cleared before p . K (a row that does see them has NaN
 // from its logit).
 //
-// Measured (in a graph): 8192 tokens of 64 heads 2.26 to 2.35 ms, 1945 to 1870 TFLOP/s, 99 to 95 % of the
-// measured burst rate (at the power cap, over seconds, 2.55 ms, 1720); 2 x 1024 queries of 128 heads
-// behind 7168 rows 2.13 ms; 2048 tokens of 128 heads 0.37 ms, 1460.  A chunk takes 2213 cycles in the
+// Measured (in a graph): 8192 tokens of 64 heads 2.28 to 2.36 ms, 1930 to 1865 TFLOP/s, 98 to 95 % of the
+// measured burst rate (at the power cap, over seconds, 2.54 to 2.67 ms, 1730 to 1650); 2 x 1024 queries of 128 heads
+// behind 7168 rows 2.13 ms; 2048 tokens of 128 heads 0.37 ms, 1460.  A chunk took 2213 cycles (without the second sum) in the
 // middle of a tile, a tile about 5500 more: the first softmax and the reading of the results, one
 // after the other, and loads that wait for the stage that the results are in.  Tried without gain: the
 // output freed in two halves, p . K of the last chunk before the next query is copied or in the order
@@ -953,7 +961,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             ok = !head_any(!ok);       // a row's four warps leave together
             if (!ok || !some) break;
             ring.next();               // the query tile
-            float m = -INFINITY, l = 0.0f;
+            float m = -INFINITY, l = 0.0f, rounded = 0.0f;   // rounded: the sum of what p . K multiplies
             const int32_t in_tile = static_cast<int32_t>(rank) * kCtaRows + row;
             const int32_t see = p.causal == 0 ? s.keys
                                               : clamped(s.see + query_of(p, s.offset + in_tile), s.keys);
@@ -1014,6 +1022,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
                     const float fix = rise ? exp2_approx(__fsub_rn(m, top)) : 1.0f;
                     if (rise) m = top;
                     l = __fmul_rn(l, fix);
+                    rounded = __fmul_rn(rounded, fix);
                     if (!fresh) {
                         // the products of the chunk before are in the accumulator
                         if (ok) warp_wait(smem_addr(&bars->empty[last.s]), last.parity, ok);
@@ -1046,14 +1055,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
                 l = __fadd_rn(l, __fadd_rn(sum_a, sum_b));
                 // the chunk before is multiplied: its probabilities are read
                 if (j > 0 && ok) warp_wait(smem_addr(&bars->empty[last.s]), last.parity, ok);
+                uint4 w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = pack8(v + 8 * i);
                 if (ok) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) sts16(prow ^ (i << 4), pack8(v + 8 * i));
+                    for (int i = 0; i < 4; ++i) sts16(prow ^ (i << 4), w[i]);
                 }
                 fence_async_smem();
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0 && ok) mbar_arrive_cluster(p_ready + 8 * (j & 1));
+                f32x2_split(add_f32x2(add_f32x2(sum_rounded(w[0]), sum_rounded(w[1])),
+                                      add_f32x2(sum_rounded(w[2]), sum_rounded(w[3]))), sum_a, sum_b);
+                rounded = __fadd_rn(rounded, __fadd_rn(sum_a, sum_b));
                 last = ring;
                 turns ^= 1u << ring.s;
                 ring.next();
@@ -1062,8 +1077,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             head_sync();
             const float total = __fadd_rn(__fadd_rn(heads[0], heads[64]), __fadd_rn(heads[128], heads[192]));
             head_sync();   // read before they are written again
+            heads[self] = rounded;
+            head_sync();
+            const float divisor = __fadd_rn(__fadd_rn(heads[0], heads[64]), __fadd_rn(heads[128], heads[192]));
+            head_sync();
             if (half == 0 && part == 0 && ok) {
-                const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, total);
+                // both sums are 0 or neither is: what is not flushed is a normal bf16
+                const float inv = total == 0.0f ? 0.0f : __fdiv_rn(1.0f, divisor);
                 const float lse2 = total == 0.0f ? -INFINITY : __fadd_rn(__fsub_rn(m, kLift), log2f(total));
                 asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(smem_addr(smem) + kOffStats + (tile & 1) * 512 + 8 * row),
                              "f"(inv),
@@ -1425,6 +1445,7 @@ cudaError_t launch_prefix_attention(const PrefixParams& p, cudaStream_t stream) 
     uint8_t* const base = static_cast<uint8_t*>(o.workspace);
     const bool both = p.prefix_length > 0 && o.topk > 0;
     AttentionParams own = o;
+    own.parted = 1;
     own.workspace = base + w.attend;
     if (w.written_out) {
         own.prefix = p.prefix;

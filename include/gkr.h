@@ -496,7 +496,8 @@ GKR_API gkr_status gkr_kv_slots(const int32_t *block_table, int64_t table_stride
  *   s[k] = sm_scale * q[i, h] . K[k],  lse = log(sum exp(s[k])),
  *   out = bf16(sum exp(s[k] - lse) K[k]).
  * A query without rows gets zeros and lse -inf.  Queries of no request are left as they are.
- * Arithmetic as for gkr_sparse_attention; a row that a query does not see (another request's, a
+ * Arithmetic as for gkr_sparse_attention, but results are divided by the sum of the probabilities
+ * as rounded (lse is of those before), so that a large one's rounding cancels; a row that a query does not see (another request's, a
  * later one, one behind the last) has no influence on it, whatever it holds.  A row with an
  * infinity or a NaN makes the queries that see it NaN (where their logit for it is -inf, NaN or
  * what they would be without it).
