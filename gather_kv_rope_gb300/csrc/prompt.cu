@@ -48,12 +48,13 @@
 // from its logit).
 //
 // Measured (in a graph): 8192 tokens of 64 heads 2.28 to 2.36 ms, 1930 to 1865 TFLOP/s, 98 to 95 % of the
-// measured burst rate (at the power cap, over seconds, 2.54 to 2.67 ms, 1730 to 1650); 2 x 1024 queries of 128 heads
-// behind 7168 rows 2.13 ms; 2048 tokens of 128 heads 0.37 ms, 1460.  A chunk took 2213 cycles (without the second sum) in the
-// middle of a tile, a tile about 5500 more: the first softmax and the reading of the results, one
-// after the other, and loads that wait for the stage that the results are in.  Tried without gain: the
-// output freed in two halves, p . K of the last chunk before the next query is copied or in the order
-// in which they are ready, 16-row steps of p . K left out where no row is seen.
+// measured burst rate (at the power cap, over seconds, 2.54 to 2.67 ms, 1730 to 1650); 2 x 1024 queries of
+// 128 heads behind 7168 rows 2.13 ms; 2048 tokens of 128 heads 0.38 to 0.40 ms, 1420 to 1350.  A chunk
+// took 2213 cycles (without the second sum) in the middle of a tile, a tile about 5500 more: the first
+// softmax and the reading of the results, one after the other, and loads that wait for the stage that the
+// results are in.  Tried without gain: the output freed in two halves, p . K of the last chunk before the
+// next query is copied or in the order in which they are ready, 16-row steps of p . K left out where no
+// row is seen.
 #include <cmath>
 
 #include "attend.cuh"
