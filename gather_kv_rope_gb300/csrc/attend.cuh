@@ -20,6 +20,9 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // their range: probabilities stay below 2^(kLag + kLift) = 2^48, and an output of fewer than
 // 2^24 records below 2^55 each cannot overflow.
 constexpr float kLag = 32.0f;
+// Where the reference moves up by 2^-by, what is in the accumulator is multiplied by 2^(by / 2) twice: its terms may
+// lie 2^(kLag + kLift) above the old reference and still count where 2^by is below what fp32 holds (one
+// factor lost what had weights of up to 2^-117).  The sums of the probabilities end far above that.
 // Probabilities are taken as exp2(s - m + kLift): bf16 ends at 2^-133, and without the lift terms
 // that the output still shows (it ends there too) would be rounded away before they are
 // multiplied by a record's values and summed.

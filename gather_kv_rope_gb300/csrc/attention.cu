@@ -567,23 +567,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kAttendThreads, 1)
                 top = fmaxf(fmaxf(maxima[0], maxima[64]), fmaxf(maxima[128], maxima[192]));
                 head_sync();   // read before they are written again
                 const bool rise = top > m + kLag || (m == -INFINITY && top > m);
-                const float fix = rise ? exp2_approx(__fsub_rn(m, top)) : 1.0f;
+                const float root = rise ? exp2_approx(__fmul_rn(__fsub_rn(m, top), 0.5f)) : 1.0f;
                 if (rise) m = top;
-                l = __fmul_rn(l, fix);
-                if constexpr (kParted) rounded = __fmul_rn(rounded, fix);
+                l = __fmul_rn(l, __fmul_rn(root, root));
+                if constexpr (kParted) rounded = __fmul_rn(rounded, __fmul_rn(root, root));
                 if (!fresh) {
                     // the products of the chunk before are in the accumulator
                     if (ok) warp_wait(smem_addr(&bars->stage_empty[(j - 1) % kStages]), ((j - 1) / kStages) & 1, ok);
                     tc_fence_after_sync();
 #pragma unroll 1
-                    for (int c = 128 * part; c < 128 * part + 128; c += 32) {
+                    for (int i = 0; i < 256; i += 32) {   // the columns twice, a factor each time
+                        const int c = 128 * part + (i & 127);
                         float t[32];
                         tmem_ld32(tmem + lanes + c, t);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) t[i] = __fmul_rn(t[i], fix);
+                        for (int k = 0; k < 32; ++k) t[k] = __fmul_rn(t[k], root);
                         tmem_st32(tmem + lanes + c, t);
+                        tmem_st_wait();
                     }
-                    tmem_st_wait();
                 }
             }
             const float ref = m == -INFINITY ? 0.0f : __fsub_rn(m, kLift);

@@ -1020,10 +1020,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
                     top = fmaxf(fmaxf(heads[0], heads[64]), fmaxf(heads[128], heads[192]));
                     head_sync();   // read before they are written again
                     const bool rise = top > m + kLag || (m == -INFINITY && top > m);
-                    const float fix = rise ? exp2_approx(__fsub_rn(m, top)) : 1.0f;
+                    const float root = rise ? exp2_approx(__fmul_rn(__fsub_rn(m, top), 0.5f)) : 1.0f;
                     if (rise) m = top;
-                    l = __fmul_rn(l, fix);
-                    rounded = __fmul_rn(rounded, fix);
+                    l = __fmul_rn(__fmul_rn(l, root), root);
+                    rounded = __fmul_rn(__fmul_rn(rounded, root), root);
                     if (!fresh) {
                         // the products of the chunk before are in the accumulator
                         if (ok) warp_wait(smem_addr(&bars->empty[last.s]), last.parity, ok);
@@ -1033,7 +1033,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
                             float t[32];
                             tmem_ld32(tmem + lanes + d, t);
 #pragma unroll
-                            for (int i = 0; i < 32; ++i) t[i] = __fmul_rn(t[i], fix);
+                            for (int i = 0; i < 32; ++i) t[i] = __fmul_rn(__fmul_rn(t[i], root), root);
                             tmem_st32(tmem + lanes + d, t);
                         }
                         tmem_st_wait();
