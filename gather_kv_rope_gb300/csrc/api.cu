@@ -632,7 +632,8 @@ GKR_API gkr_status gkr_kv_slots(const int32_t* block_table, int64_t table_stride
     // blocks of a launch
     if (!packed_rows && width > 0 && num_requests > kMaxIndex / ((width + 2047) / 2048))
         return GKR_EINVAL;
-    if (!packed_rows && (num_requests == 0 || width == 0)) return GKR_OK;
+    // without room for entries only the lengths are looked at, for the error bits
+    if (!packed_rows && (num_requests == 0 || (width == 0 && !err_flag))) return GKR_OK;
     if ((num_requests > 0 && (!lengths || (table_width > 0 && !block_table))) ||
         (width > 0 && !indices))
         return GKR_EINVAL;

@@ -316,7 +316,7 @@ cudaError_t launch_allocate(const AllocateParams& p, cudaStream_t stream) {
 cudaError_t launch_slots(const SlotsParams& p, cudaStream_t stream) {
     if (p.starts == nullptr) {
         constexpr int64_t kPer = kPlanThreads * kRowEntries;
-        const int64_t parts = (p.width + kPer - 1) / kPer;
+        const int64_t parts = p.width > 0 ? (p.width + kPer - 1) / kPer : 1;   // 1: only errors, no entries
         return launch_kernel(slots_kernel, p.num_requests * parts, kPlanThreads, 0, stream, p.pdl, p, parts);
     }
     return launch_rows(packed_slots_kernel<1>, packed_slots_kernel<kLongRun>, p, p.width, stream);

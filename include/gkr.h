@@ -476,7 +476,8 @@ GKR_API gkr_status gkr_kv_allocate(const int32_t *past, const int32_t *added,
  *   [num_requests + 1] says where each begins (num_requests <= 16384).
  * A position without a page, or whose slot is no int32, gets -1; positions that `width` has no
  * room for are left out; negative lengths and firsts count as 0; GKR_ERR_INDEX for each.
- * width 0 .. 2^31 - 1.  The other arguments are gkr_kv_allocate's.
+ * width 0 .. 2^31 - 1 (0: errors are reported all the same; without starts and err_flag
+ * nothing is enqueued, as for no requests).  The other arguments are gkr_kv_allocate's.
  */
 GKR_API gkr_status gkr_kv_slots(const int32_t *block_table, int64_t table_stride,
                                 int32_t table_width, const int32_t *lengths,
