@@ -937,7 +937,8 @@ def prompt_attention(q: torch.Tensor, kv: torch.Tensor, starts: torch.Tensor, sm
 
     out[i, h] = softmax over the rows it sees of (sm_scale * q[i, h] . K) times K, lse[i, h] the
     log of the softmax's sum; zeros and -inf for a query that sees none.  Queries of no
-    request are left as they are.  Returns (out, lse)."""
+    request are left as they are.  Sums cannot overflow while the number of rows that a query
+    sees times their largest magnitude is below 2^80.  Returns (out, lse)."""
     T, H = _attention_args(q, out, lse, workspace)
     stride = _rows(kv, torch.bfloat16, "kv")
     N, width = kv.shape

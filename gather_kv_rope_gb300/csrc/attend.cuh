@@ -17,8 +17,8 @@ constexpr float kLn2 = 0.69314718055994530942f;
 // any of the 32 heads of a warp: rescaling the accumulator takes longer than a chunk's softmax
 // (1400 cycles), and at 8, with the logits of heavy-tailed latents, every second chunk had some
 // head that rose.  The reference does not touch the precision of floating-point terms, only
-// their range: probabilities stay below 2^(kLag + kLift) = 2^48, and an output of fewer than
-// 2^24 records below 2^55 each cannot overflow.
+// their range: probabilities stay below 2^(kLag + kLift) = 2^48, so an output cannot overflow while the
+// number of rows times the largest value is below 2^80 (2^24 records, the most of a list: 2^55 each).
 constexpr float kLag = 32.0f;
 // Where the reference moves up by 2^-by, what is in the accumulator is multiplied by 2^(by / 2) twice: its terms may
 // lie 2^(kLag + kLift) above the old reference and still count where 2^by is below what fp32 holds (one

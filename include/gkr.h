@@ -365,8 +365,9 @@ GKR_API gkr_status gkr_sparse_logits(const void *q, int32_t num_heads, const voi
  * invalid entries are not touched.  Entries may repeat; each counts.
  * Arithmetic: bf16 products with fp32 sums, fp32 softmax statistics; the probabilities are
  * rounded to bf16 (relative to a running maximum) for the value product.  Records' values below
- * 2^55 cannot overflow the accumulator, however many are listed.  Results do not
- * depend on the order of execution: every sum has a fixed order.
+ * 2^55 cannot overflow the accumulator, however many are listed (2^24 at most).  A probability
+ * below 2^-142 of the row's largest may count as 0 (what values up to 2^9 make of it is below
+ * bf16's smallest).  Results do not depend on the order of execution: every sum has a fixed order.
  * Should a wait give up (GKR_ERR_TIMEOUT), each row of out is either right or not written, and
  * the lse of one that is not is a NaN; the weights of a query with such a head are left as they
  * are, and any other entry has its weight added or is left.
@@ -498,10 +499,12 @@ GKR_API gkr_status gkr_kv_slots(const int32_t *block_table, int64_t table_stride
  *   out = bf16(sum exp(s[k] - lse) K[k]).
  * A query without rows gets zeros and lse -inf.  Queries of no request are left as they are.
  * Arithmetic as for gkr_sparse_attention, but results are divided by the sum of the probabilities
- * as rounded (lse is of those before), so that a large one's rounding cancels; a row that a query does not see (another request's, a
- * later one, one behind the last) has no influence on it, whatever it holds.  A row with an
- * infinity or a NaN makes the queries that see it NaN (where their logit for it is -inf, NaN or
- * what they would be without it).
+ * as rounded (lse is of those before), so that a large one's rounding cancels; and the accumulator
+ * cannot overflow while the number of rows that a query sees times their largest magnitude is
+ * below 2^80 (past that a result may be infinite or NaN).  A row that a query does not see
+ * (another request's, a later one, one behind the last) has no influence on it, whatever it holds.
+ * A row with an infinity or a NaN makes the queries that see it NaN (where their logit for it is
+ * -inf, NaN or what they would be without it).
  *
  * q              device, bf16 [num_tokens, num_heads, 512], 16-byte aligned.
  * num_heads      1 .. 4096; num_tokens >= 0, num_heads * num_tokens <= 2147418112.
