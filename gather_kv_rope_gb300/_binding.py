@@ -709,13 +709,26 @@ _I32 = torch.int32
 
 
 def _vector(t: torch.Tensor, name: str, length: int | None = None, dtype=_I32) -> int:
-    """Length of a contiguous 1-D tensor, checked against `length` where that is given."""
+    """Length of a contiguous 1-D tensor, checked against `length` where that is given; below
+    2^31, as C takes most of them as int32."""
     shape = t.shape
     if t.dtype is not dtype or len(shape) != 1 or not t.is_contiguous() \
-            or (length is not None and shape[0] != length):
+            or shape[0] >= 1 << 31 or (length is not None and shape[0] != length):
         n = "" if length is None else f" [{length}]"
-        raise ValueError(f"{name} must be a contiguous 1-D {dtype} tensor{n}".replace("torch.", ""))
+        raise ValueError(f"{name} must be a contiguous 1-D {dtype} tensor{n} of fewer than 2^31 "
+                         "elements".replace("torch.", ""))
     return shape[0]
+
+
+def _table(block_table: torch.Tensor, requests: int) -> tuple[int, int]:
+    """Row stride and width of a block table."""
+    stride = _rows(block_table, _I32, "block_table")
+    rows, width = block_table.shape
+    if rows != requests:
+        raise ValueError("block_table must have a row for each request")
+    if width >= 1 << 31:                  # C takes it as int32
+        raise ValueError("block_table must have fewer than 2^31 columns")
+    return stride, width
 
 
 def _int32_size(n: int, name: str) -> int:
@@ -758,10 +771,7 @@ def kv_allocate(past: torch.Tensor, added: torch.Tensor, block_table: torch.Tens
     has slot -1, and err_flag ERR_SLOT.  The lengths stay on the GPU; nothing is kept."""
     B = _vector(past, "past")
     _vector(added, "added", B)
-    stride = _rows(block_table, _I32, "block_table")
-    rows, W = block_table.shape
-    if rows != B:
-        raise ValueError("block_table must have a row for each request")
+    stride, W = _table(block_table, B)
     F = _vector(free_pages, "free_pages")
     block_size = _int32_size(block_size, "block_size")
     num_tokens = int(num_tokens)
@@ -796,10 +806,7 @@ def kv_allocate(past: torch.Tensor, added: torch.Tensor, block_table: torch.Tens
 def _slots(block_table, lengths, block_size, width, first, indices, starts, packed, err_flag,
            launch_opts):
     B = _vector(lengths, "lengths")
-    stride = _rows(block_table, _I32, "block_table")
-    rows, W = block_table.shape
-    if rows != B:
-        raise ValueError("block_table must have a row for each request")
+    stride, W = _table(block_table, B)
     block_size = _int32_size(block_size, "block_size")
     if first is not None:
         _vector(first, "first", B)
