@@ -44,8 +44,9 @@
 // nothing (4096 x 64 0.627 and 0.625), as the second sum is taken once the products may begin.
 // What a row does not see: columns past its last row are -inf before the softmax.  Their
 // probabilities are 0, but 0 times an infinity or NaN is NaN, so in a chunk with such
-// columns, values that are not finite are cleared before p . K (a row that does see them has NaN
-// from its logit).
+// columns, values that are not finite are cleared before p . K.  A row that does see them has NaN from
+// its logit, unless that is -inf: then its result is finite, where in a chunk that every row of the tile
+// sees in full, and that nothing is cleared in, it is NaN.
 //
 // Measured (in a graph): 8192 tokens of 64 heads 2.28 to 2.36 ms, 1930 to 1865 TFLOP/s, 98 to 95 % of the
 // measured burst rate (at the power cap, over seconds, 2.54 to 2.67 ms, 1730 to 1650); 2 x 1024 queries of
