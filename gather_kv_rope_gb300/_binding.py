@@ -977,7 +977,8 @@ def prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, prefix: torch.Tenso
                      launch_opts: LaunchOpts | None = None) -> tuple[torch.Tensor, torch.Tensor]:
     """sparse_attention for queries that share a prefix: query i attends to the records that
     `prefix` lists, the same for every query, and to those of its own row of `indices`, in one
-    softmax.  The prefix is read and dequantised once for all queries.
+    softmax.  The prefix is read and dequantised once for all queries, or, where few queries or a
+    short prefix make that faster, as the beginning of each query's list.
 
     prefix     int32 [L], contiguous;  indices  int32 [Q, K], rows contiguous.  -1 (or an index
                outside the cache) is no entry in either; L or K may be 0.

@@ -12,8 +12,9 @@
 // The outputs are a few bytes a token, so latencies bound all but the largest calls, and one launch
 // does everything: every block sums the lengths of all requests for itself (a few KB from L2) and
 // then finds the request of each of its rows by bisection in shared memory.  Measured in a graph:
-// decoding 64 requests 3.7 us, 524288 tokens of 512 requests 7.8 (their bytes take 1.2), 64 lists of
-// 8191 slots 2.9, 8 packed ones of up to 131072 5.0; a call from Python takes 10 to 25, the host's time.
+// decoding 64 requests 3.5 to 3.7 us, 524288 tokens of 512 requests 7.5 to 7.8 (their bytes take 1.2), 64 lists
+// of 8191 slots 2.5 to 3.0, 8 packed ones of up to 131072 4.9 to 5.0; a call from Python takes 10 to 26, the
+// host's time.
 // New pages are read from the free list, not from the table that other blocks are writing.  No atomics but
 // for the error bits: the same call gives the same bytes.
 #include "device.cuh"
@@ -103,8 +104,8 @@ struct Split {   // x / bs by a shift where bs is a power of two
 };
 
 // A thread takes kRun consecutive rows: one bisection, and one page for as long as they lie in it.  One
-// row where there are threads for all: decoding 64 requests took 6.4 us with four, 4.1 with
-// one; 524288 tokens of 512 requests 7.8 with four, 8.9 with one.
+// row where there are threads for all: decoding 64 requests takes 3.5 us with one, 5.9 with four, 512
+// requests 4.1 and 7.0; 512 requests of 1024 tokens 7.9 and 7.4, of 8192 34 and 29, 16384 of 512 186 and 124.
 constexpr int64_t kLongRun = 4;
 template <int kRun>
 __global__ void __launch_bounds__(kPlanThreads) allocate_kernel(const AllocateParams p) {

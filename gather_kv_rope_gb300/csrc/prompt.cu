@@ -33,7 +33,9 @@
 //     from the requests' lengths by itself (closed sums, no plan to launch).  The pieces of a tile
 //     that is cut go to the workspace (fp32 rows and their log-sum-exp) and a second kernel joins
 //     them.  Where there are few tiles and none much longer than an even share, each pair has
-//     a whole one.
+//     a whole one; that is looked at for up to 32 requests, one a lane, while more are always cut (one
+//     query of 128 heads and 300 rows a request: 32 requests 14.7 us, 33 20.4, 64 25.2; 1500
+//     rows: 28.1, 30.3, 47.1).
 // The tensor cores take the probabilities as bf16 (A and B of a product have one type, and the rows are
 // bf16).  The reference lags the maximum, so the largest one is no power of two, and where one row of K has
 // most of the weight its rounding, up to 2^-9, is the result's as well.  So results are divided by the
@@ -48,9 +50,9 @@
 // its logit, unless that is -inf: then its result is finite, where in a chunk that every row of the tile
 // sees in full, and that nothing is cleared in, it is NaN.
 //
-// Measured (in a graph): 8192 tokens of 64 heads 2.28 to 2.36 ms, 1930 to 1865 TFLOP/s, 98 to 95 % of the
-// measured burst rate (at the power cap, over seconds, 2.54 to 2.67 ms, 1730 to 1650); 2 x 1024 queries of
-// 128 heads behind 7168 rows 2.13 ms; 2048 tokens of 128 heads 0.38 to 0.40 ms, 1420 to 1350.  A chunk
+// Measured (in a graph): 8192 tokens of 64 heads 2.27 to 2.36 ms, 1940 to 1865 TFLOP/s, 99 to 95 % of the
+// measured burst rate (at the power cap, over seconds, 2.54 to 2.73 ms, 1730 to 1610); 2 x 1024 queries of
+// 128 heads behind 7168 rows 2.08 to 2.14 ms; 2048 tokens of 128 heads 0.38 to 0.40 ms, 1420 to 1350.  A chunk
 // took 2213 cycles (without the second sum) in the middle of a tile, a tile about 5500 more: the first
 // softmax and the reading of the results, one after the other, and loads that wait for the stage that the
 // results are in.  Tried without gain: the output freed in two halves, p . K of the last chunk before the
@@ -1362,10 +1364,12 @@ struct PrefixLayout {
 //   written out: 10.5 and 1.05 for a chunk of 64 records of a pair's run;
 //   shared: 27, the gather 2.1e-4 a record, 1.35 for a chunk of 128 rows of a pair's run and
 //   1.05 for one of 64 own records.
-// Measured, us in a graph, shared and written out (queries x heads, prefix + 100 own): 4 x 16, 4095 32.6
-// and 17.7, 16384 39.5 and 27.5, 65536 64 and 68.5; 16 x 16, 4095 35 and 31, 16384 42 and 73; 8 x 128,
-// 16384 57 and 51, 131072 215 and 242; 64 x 16, 2048 39 and 43, 131072 214 and 1791; 128 x 64, 512 45 and
-// 33, 4095 93 and 140.  Of 90 such sizes the slower way is taken in five, by 7 % at most.
+// Measured, us in a graph, shared and written out (queries x heads, prefix + 100 own): 4 x 16, 4095 30.0
+// and 16.0, 16384 37.2 and 26.8, 65536 57 and 68; 16 x 16, 4095 31.5 and 30.1, 16384 38 and 72; 64 x 16,
+// 2048 33 and 42, 131072 205 and 1801; 16 x 128, 16384 67 and 77; 64 x 64, 2048 43.7 and 42.8; 128 x 64,
+// 512 43.5 and 31.8, 4095 83 and 140.  Of 90 sizes (1 to 128 queries, 16, 64, 128 heads, 512 to 131072
+// records) the slower way is taken in two: 64 x 64, 2048, by 2 %, and 128 x 128, 2048, by 21 % (98 and 81), as the
+// estimates leave out what the fp32 rows of many heads and their join take.
 bool write_out(int32_t num_heads, int64_t num_queries, int64_t prefix_length, int64_t topk, int32_t pairs) {
     const double own = static_cast<double>(num_queries) * static_cast<double>((topk + 63) / 64) / pairs;
     const double listed = static_cast<double>(num_queries) * static_cast<double>((prefix_length + topk + 63) / 64) / pairs;

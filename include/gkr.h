@@ -538,8 +538,9 @@ GKR_API gkr_status gkr_prompt_attention_workspace(int32_t num_heads, int64_t num
  * prefix_attention: gkr_sparse_attention for queries that share a prefix (an extension of the
  * library): query i attends to the records prefix[0 .. prefix_length - 1], the same for every
  * query, and to those that its row of indices lists, in one softmax.  The prefix's records are
- * read and dequantised for all queries at once.  -1 and invalid indices as there, in
- * both lists; either may be empty.
+ * read and dequantised for all queries at once, or, where few queries or a short prefix make that
+ * faster, as the beginning of each query's list.  -1 and invalid indices as there, in both lists;
+ * either may be empty.  Results are divided by the sum of the probabilities as rounded.
  *
  * prefix         device, int32 [prefix_length]; prefix_length 0 .. 2^24.
  * out            not overlapping q (GKR_EINVAL) or any other input.
