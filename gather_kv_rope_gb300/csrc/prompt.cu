@@ -464,6 +464,11 @@ __device__ __forceinline__ void copy_rows(uint32_t from, uint8_t* dst, int64_t s
     }
 }
 
+template <int64_t kClocks>
+struct Clocks {
+    static constexpr int64_t value = kClocks;
+};
+
 // Named barriers: the four softmax warps of each half of the rows; the movers.
 constexpr int kHeadsBar = 1, kMoveBar = 3;
 
@@ -534,12 +539,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     // All 512 columns are this CTA's, so they begin at address 0.
     constexpr uint32_t tmem = 0;
     bool ok = bars->tmem_base == 0 && (smem_addr(smem) & 1023u) == 0u;
-    // Part `tile` of the pair's work; a warp.  False after the last, or once a wait gave up.
-    auto part_at = [&](int tile, Part& s) -> bool {
-        if (!ok || !warp_wait(smem_addr(&bars->part[tile & (kParts - 1)]), (tile / kParts) & 1, ok)) return false;
+    // Part `tile` of the pair's work; a warp.  False after the last, or once a wait gave up.  The movers wait for it
+    // as long as the part before takes to load.
+    auto part_within = [&](auto limit, int tile, Part& s) -> bool {
+        if (!ok || !warp_wait<decltype(limit)::value>(smem_addr(&bars->part[tile & (kParts - 1)]), (tile / kParts) & 1, ok))
+            return false;
         s = bars->parts[tile & (kParts - 1)];
         return s.chunks > 0;
     };
+    auto part_at = [&](int tile, Part& s) -> bool { return part_within(Clocks<kWaitClocks>(), tile, s); };
     // The last dims of a query tile; a thread.
     auto load_tail = [&](int64_t row0) {
         const uint32_t bar = smem_addr(&bars->tail);
@@ -846,7 +854,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             ring.skip(s.end - s.begin - 1);
             const Ring<kStages> last = ring;    // of the tile's chunks
             ring.next();                        // of the next query, if there is one
-            more = part_at(tile + 1, n);
+            more = part_within(Clocks<kLongWaitClocks>(), tile + 1, n);
             if (more) warp_wait(smem_addr(&bars->copied[(tile + 1) & 1]), ((tile + 1) >> 1) & 1, ok);
             // The last value product implies everything before it.  The movers agree on it, so that
             // a row is written in full or not at all.
