@@ -35,7 +35,7 @@
 //     them.  Where there are few tiles and none much longer than an even share, each pair has
 //     a whole one; that is looked at for up to 32 requests, one a lane, while more are always cut (one
 //     query of 128 heads and 300 rows a request: 32 requests 14.7 us, 33 20.4, 64 25.2; 1500
-//     rows: 28.1, 30.3, 47.1).
+//     rows: 28.1, 30.3, 47.1).  A share of more than 131072 rows is taken in runs (kRunChunks).
 // The tensor cores take the probabilities as bf16 (A and B of a product have one type, and the rows are
 // bf16).  The reference lags the maximum, so the largest one is no power of two, and where one row of K has
 // most of the weight its rounding, up to 2^-9, is the result's as well.  So results are divided by the
@@ -110,7 +110,16 @@ constexpr uint32_t kOffHeads = kOffStages + kStages * kStageBytes;   // [4][64] 
 constexpr uint32_t kOffStats = kOffHeads + 256 * 4;         // [2][64] a tile's 1 / sum and log-sum-exp of a row
 constexpr uint32_t kOffBars = kOffStats + 2 * 64 * 8;
 
-// A pair's part of one tile, as its roles need it.
+// A pair takes its share of a tile in runs of at most so many chunks, each with an accumulator of its own, and joins
+// them in fp32 rows in the workspace.  The tensor cores cut off what a sum of theirs cannot hold, all
+// in one direction, on average half of its last bit for every 16 rows: in one run, results over a million rows
+// came out 0.4 % too small, over 64 million 24 %; over 131072 it is 0.08 %, and a run costs what a tile does besides
+// its chunks, 0.2 %.  That is a form of the kernel of its own (kLong), for calls with more rows than a run has, as
+// the code that joins costs short calls 1 to 5 % (511 tokens of 16 heads 15.5 and 16.2 us, one query of each of 64
+// requests over 4096 rows, 16 heads, 62.5 and 63.5).
+constexpr int kRunChunks = 1024;
+
+// A run of a pair's share of one tile, as its roles need it.
 constexpr int kParts = 4;                // in the ring: the loads are never two tiles ahead
 struct alignas(16) Part {
     int64_t row0;            // the tile's first row of q
@@ -120,7 +129,8 @@ struct alignas(16) Part {
     int32_t rows, keys;      // rows of the tile; rows of K
     int32_t least;           // rows that all of the tile's rows see
     int32_t chunks;          // of the tile; 0: no more parts
-    int32_t begin, end;      // of them, this pair's
+    int32_t from, to;        // of them, this pair's
+    int32_t begin, end;      // and the run's
 };
 
 // Arguments of the tile kernel.
@@ -241,8 +251,14 @@ struct Walk {
     Request r;
     int64_t left, unit;     // units left; units of the tile that are behind
     int32_t b, tile;
-    // The next one; `chunks` 0 is a tile that sees no row here.
+    // The one after `s` (at first one of no chunks); `chunks` 0 is a tile that sees no row here.
+    template <bool kLong>
     __device__ bool next(const TileArgs& p, Part& s) {
+        if (kLong && s.end < s.to) {
+            s.begin = s.end;
+            s.end = min(s.to, s.begin + kRunChunks);
+            return true;
+        }
         while (left > 0) {
             if (tile >= r.tiles) {
                 if (++b >= p.num_requests) return false;
@@ -266,13 +282,14 @@ struct Walk {
             const int64_t take = min(left, all - unit);
             left -= take;
             unit += take;
-            s.begin = chunk_at(first);
-            s.end = chunk_at(unit);
+            s.from = s.begin = chunk_at(first);
+            s.to = chunk_at(unit);
+            s.end = kLong ? min(s.to, s.begin + kRunChunks) : s.to;
             if (unit == all) {
                 ++tile;
                 unit = 0;
             }
-            if (s.chunks == 0 ? first == 0 : s.end > s.begin) return true;
+            if (s.chunks == 0 ? first == 0 : s.to > s.from) return true;
         }
         return false;
     }
@@ -464,14 +481,10 @@ __device__ __forceinline__ void copy_rows(uint32_t from, uint8_t* dst, int64_t s
     }
 }
 
-template <int64_t kClocks>
-struct Clocks {
-    static constexpr int64_t value = kClocks;
-};
-
 // Named barriers: the four softmax warps of each half of the rows; the movers.
 constexpr int kHeadsBar = 1, kMoveBar = 3;
 
+template <bool kLong>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     tile_kernel(const TileArgs p, const __grid_constant__ CUtensorMap q_map,
                 const __grid_constant__ CUtensorMap tail_map, const __grid_constant__ CUtensorMap k_map,
@@ -539,15 +552,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     // All 512 columns are this CTA's, so they begin at address 0.
     constexpr uint32_t tmem = 0;
     bool ok = bars->tmem_base == 0 && (smem_addr(smem) & 1023u) == 0u;
-    // Part `tile` of the pair's work; a warp.  False after the last, or once a wait gave up.  The movers wait for it
-    // as long as the part before takes to load.
-    auto part_within = [&](auto limit, int tile, Part& s) -> bool {
-        if (!ok || !warp_wait<decltype(limit)::value>(smem_addr(&bars->part[tile & (kParts - 1)]), (tile / kParts) & 1, ok))
-            return false;
+    // Part `tile` of the pair's work; a warp.  False after the last, or once a wait gave up.
+    auto part_at = [&](int tile, Part& s) -> bool {
+        if (!ok || !warp_wait(smem_addr(&bars->part[tile & (kParts - 1)]), (tile / kParts) & 1, ok)) return false;
         s = bars->parts[tile & (kParts - 1)];
         return s.chunks > 0;
     };
-    auto part_at = [&](int tile, Part& s) -> bool { return part_within(Clocks<kWaitClocks>(), tile, s); };
     // The last dims of a query tile; a thread.
     auto load_tail = [&](int64_t row0) {
         const uint32_t bar = smem_addr(&bars->tail);
@@ -586,8 +596,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             tail_asked = false;
         };
         Part s;
+        s.end = s.to = 0;
         while (true) {
-            const bool some = walk.next(p, s);
+            const bool some = walk.next<kLong>(p, s);
             if (some && s.chunks == 0) {   // zeros, whatever has become of the other tiles
                 const int rows = min(kCtaRows, s.rows - static_cast<int>(rank) * kCtaRows);
                 const int64_t at = s.row0 + rank * kCtaRows, bytes = p.wide != 0 ? 2048 : 1024;
@@ -819,16 +830,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             run_units(p, 0, lane, from, upto, bad);
             if (bad) report(p.err, kErrIndex);
         }
-        // Where part `s` goes: the results, or a piece (slot 1: it begins its tile).
-        auto slot_of = [&](const Part& s) -> int { return s.begin == 0 ? 1 : 0; };
-        auto whole_of = [&](const Part& s) -> bool { return s.begin == 0 && s.end == s.chunks; };
-        auto first_of = [&](const Part& s) -> int64_t {
-            return whole_of(s) ? s.row0 : (2 * pair + slot_of(s)) * p.slot_rows;
-        };
+        // Where run `s` goes: the results, or, where it does not end a whole tile, a piece (slot 1: of a share that
+        // begins its tile; only the last one stays there).
+        auto piece_of = [&](const Part& s) -> int64_t { return (2 * pair + (s.from == 0 ? 1 : 0)) * p.slot_rows; };
+        auto whole_of = [&](const Part& s) -> bool { return s.from == 0 && s.end == s.chunks; };
+        auto first_of = [&](const Part& s) -> int64_t { return whole_of(s) ? s.row0 : piece_of(s); };
         auto note = [&](const Part& s) {   // for the kernel that joins
-            if (!first || rank != 0 || whole_of(s)) return;
+            if (!first || rank != 0 || whole_of(s) || s.end < s.to) return;
             int4 mark = p.meta[pair];
-            if (slot_of(s) == 0) {
+            if (s.from != 0) {
                 mark.z |= kHeadThere | (s.end == s.chunks ? kHeadEnds : 0);
             } else {
                 mark.x = static_cast<int32_t>(s.row0);
@@ -854,7 +864,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             ring.skip(s.end - s.begin - 1);
             const Ring<kStages> last = ring;    // of the tile's chunks
             ring.next();                        // of the next query, if there is one
-            more = part_within(Clocks<kLongWaitClocks>(), tile + 1, n);
+            more = part_at(tile + 1, n);
             if (more) warp_wait(smem_addr(&bars->copied[(tile + 1) & 1]), ((tile + 1) >> 1) & 1, ok);
             // The last value product implies everything before it.  The movers agree on it, so that
             // a row is written in full or not at all.
@@ -872,7 +882,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
             const uint32_t to = mine + lane * kRowBytes + ((lane & 7) << 4);
             const int row0 = static_cast<int>(rank) * kCtaRows + (warp & 1) * 32;   // of the tile
             const int rows = min(s.rows - row0, 32);
-            if (whole_of(s) && p.wide == 0) {
+            if ((!kLong || s.begin == s.from) && whole_of(s) && p.wide == 0) {
 #pragma unroll 1
                 for (int b = 0; b < 2; ++b) {       // 64 dims, bf16
 #pragma unroll 1
@@ -896,7 +906,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
                 if (rows < 32)   // the request's only
                     copy_rows(mine, static_cast<uint8_t*>(p.out) + (s.row0 + row0) * 1024 + (2 * half + part) * 256, 1024,
                               rows, lane);
-            } else {
+            } else if (!kLong || s.begin == s.from) {
                 uint8_t* const dst = (whole_of(s) ? static_cast<uint8_t*>(p.out) : reinterpret_cast<uint8_t*>(p.pieces)) +
                                      (first_of(s) + row0) * 2048 + (2 * half + part) * 512;
 #pragma unroll 1
@@ -919,6 +929,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(o_free);
+            } else {
+                // Joined with the share's runs before; each thread its row's 128 dims.
+                const int64_t at = piece_of(s) + in_tile;
+                const bool mine = in_tile < s.rows;
+                const float old = mine ? p.piece_lse[at] : -INFINITY;
+                const float top = fmaxf(old, lse2), ref = top == -INFINITY ? 0.0f : top;
+                const float w_old = exp2_approx(__fsub_rn(old, ref)), w_new = exp2_approx(__fsub_rn(lse2, ref));
+                const float sum = __fadd_rn(w_old, w_new), one = sum == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum);
+                lse2 = sum == 0.0f ? -INFINITY : __fadd_rn(top, log2f(sum));
+                const int dim = 256 * half + 128 * part;
+                float* const from = p.pieces + at * 512 + dim;
+                uint8_t* const to_row = static_cast<uint8_t*>(p.out) + (s.row0 + in_tile) * (p.wide != 0 ? 2048 : 1024);
+#pragma unroll 1
+                for (int d = 0; d < 128; d += 16) {
+                    float t[16];
+                    tmem_ld16(tmem + lanes + 128 * part + d, t);
+                    if (mine) {
+#pragma unroll
+                        for (int i = 0; i < 16; i += 4) {
+                            const float4 x = *reinterpret_cast<const float4*>(from + d + i);
+                            const float o[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                t[i + k] = __fmul_rn(__fadd_rn(__fmul_rn(__fmul_rn(t[i + k], inv), w_new), __fmul_rn(o[k], w_old)), one);
+                        }
+                        if (whole_of(s) && p.wide == 0) {
+                            st16(to_row + 2 * (dim + d), pack8(t));
+                            st16(to_row + 2 * (dim + d) + 16, pack8(t + 8));
+                        } else {
+                            float* const to = whole_of(s) ? reinterpret_cast<float*>(to_row) + dim : from;
+#pragma unroll
+                            for (int i = 0; i < 16; i += 4)
+                                *reinterpret_cast<float4*>(to + d + i) = make_float4(t[i], t[i + 1], t[i + 2], t[i + 3]);
+                        }
+                    }
+                    __syncwarp();
+                }
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(o_free);
             }
             // what was read is read, before TMA writes there
             if (lane == 0) bulk_wait_read_all();
@@ -936,7 +986,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         if (!ok) {
             // a wait gave up: what this pair has not written is marked
             walk = bars->walk;
-            for (int skip = tile; walk.next(p, s);) {
+            s.end = s.to = 0;
+            for (int skip = tile; walk.next<kLong>(p, s);) {
                 if (s.chunks == 0 || skip-- > 0) continue;
                 set_lse(s, __uint_as_float(kUnwritten));
                 note(s);
@@ -1314,7 +1365,7 @@ int64_t tile_bytes(int32_t pairs, int64_t rows) {
 }
 
 cudaError_t tile_pairs(int32_t* pairs) {
-    const cudaError_t e = resident_pairs(reinterpret_cast<const void*>(tile_kernel), kTileThreads, kTileSmem, pairs);
+    const cudaError_t e = resident_pairs(reinterpret_cast<const void*>(tile_kernel<false>), kTileThreads, kTileSmem, pairs);
     if (*pairs > kMaxPairs) *pairs = kMaxPairs;
     return e;
 }
@@ -1346,8 +1397,14 @@ cudaError_t launch_tiles(TileArgs a, JoinArgs join, const void* q, const void* k
                            : rows_tensor_map(q, rows, 1024, kCtaRows, 4, &k_map);
     if (e == cudaSuccess) e = rows_tensor_map(a.out, rows, 1024, 32, 1, &out_map);
     if (e != cudaSuccess) return e;
-    e = launch_kernel(tile_kernel, 2 * static_cast<int64_t>(pairs), kTileThreads, kTileSmem, stream, pdl, a, q_map,
-                      tail_map, k_map, out_map);
+    const bool longer = a.num_rows > static_cast<int64_t>(kRunChunks) * kChunk;   // some tile's share may take runs
+    if (longer) {   // the kernel's limit of shared memory is set with this
+        int32_t same = 0;
+        e = resident_pairs(reinterpret_cast<const void*>(tile_kernel<true>), kTileThreads, kTileSmem, &same);
+        if (e != cudaSuccess) return e;
+    }
+    e = launch_kernel(longer ? tile_kernel<true> : tile_kernel<false>, 2 * static_cast<int64_t>(pairs), kTileThreads,
+                      kTileSmem, stream, pdl, a, q_map, tail_map, k_map, out_map);
     if (e != cudaSuccess) return e;
     // a block for each row that may have something to join, up to one wave
     int64_t warps = 0;

@@ -34,8 +34,6 @@ constexpr int64_t kWaitClocks = INT64_C(4000000000);   // 2 s at 2 GHz
 constexpr uint32_t kSuspendNs = 20000;
 constexpr int kWaitPolls = 64;
 #endif
-// Of a wait that takes as long as a tile: one over 2^31 rows (128 in at most 3000 clocks) ends before.
-constexpr int64_t kLongWaitClocks = kWaitClocks > 0 ? 16 * kWaitClocks : kWaitClocks;
 __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
     uint32_t done;
 #ifdef GKR_WAIT_CLOCKS
@@ -192,19 +190,17 @@ __device__ __forceinline__ void wait_quiet(uint32_t bar, uint32_t parity, bool& 
     if (ok && !mbar_try_wait(bar, parity)) ok = mbar_wait_slow(bar, parity, kWaitClocks);
 }
 // The same for a converged warp, with one outcome: every lane waits, a vote decides.
-template <int64_t kLimit>
 __device__ __noinline__ bool warp_wait_slow(uint32_t bar, uint32_t parity) {
     const int64_t t0 = clock64();
     do {
 #pragma unroll 1
         for (int i = 0; i < kWaitPolls; ++i)
             if (__all_sync(kFull, mbar_try_wait(bar, parity))) return true;
-    } while (__all_sync(kFull, clock64() - t0 <= kLimit));
+    } while (__all_sync(kFull, clock64() - t0 <= kWaitClocks));
     return false;
 }
-template <int64_t kLimit = kWaitClocks>
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, bool& ok) {
-    if (!__all_sync(kFull, mbar_try_wait(bar, parity))) ok = warp_wait_slow<kLimit>(bar, parity);
+    if (!__all_sync(kFull, mbar_try_wait(bar, parity))) ok = warp_wait_slow(bar, parity);
     return ok;
 }
 // The wait for copies and products that are under way when a CTA leaves: with the full limit in
