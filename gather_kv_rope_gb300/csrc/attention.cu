@@ -32,7 +32,8 @@
 //   * Work: the chunks of all queries in a row, cut evenly over the pairs, or whole queries
 //     where that costs no more (make_cut).  A query that lies inside one pair's run is
 //     finished there; the pieces of a cut one go to the workspace (fp32 rows and their
-//     log-sum-exp) and a second kernel joins them.
+//     log-sum-exp) and a second kernel joins them.  Where a run of one query were too long for one
+//     accumulator, the cut is over more pairs than the device holds at once (kRunChunks).
 // Measured: 128 queries x 128 heads x 2048 entries 76.8 us, 895 TFLOP/s, 46 % of the measured
 // matrix rate.  A chunk of 64 records takes 2000 cycles, its products alone 1165 (64 columns a
 // product run at 63 % of the rate of 256).  What is left is shared out: issue slots are 70 %
@@ -102,7 +103,13 @@ struct Cut {
         const int64_t b = each > 0 ? each * per_query * g : total * g / pairs;
         return b < total ? b : total;
     }
+    // The pair that takes a chunk, where the cut is even: the last g with total * g / pairs < chunk + 1.
+    __device__ int64_t pair_of(int64_t chunk) const { return ((chunk + 1) * pairs - 1) / total; }
 };
+// Chunks of a query that one accumulator sums, at most.  The tensor cores cut off what a sum of theirs cannot hold, all in
+// one direction, on average half of its last bit for every 16 records: over a million records results came out
+// 0.4 % too small, over 131072 it is 0.08 %.  Longer queries are cut over more pairs than the device holds at once.
+constexpr int64_t kRunChunks = 2048;
 
 // Shared memory of a CTA, from a 1024-byte boundary.
 constexpr uint32_t kOffNext = kQBytes;                      // the next query's first blocks
@@ -738,6 +745,22 @@ struct Cuts {
     int32_t n;
     int32_t query[kMaxPairs - 1];
     int16_t first[kMaxPairs - 1], pairs[kMaxPairs - 1];
+    // entry c: its query, first pair, pieces
+    __device__ int find(int c, int64_t& q, int& g) const {
+        q = query[c];
+        g = first[c];
+        return pairs[c];
+    }
+};
+// The same of every query, where there are more pairs; those of one pair are whole.
+struct ManyCuts {
+    Cut cut;
+    __device__ int find(int c, int64_t& q, int& g) const {
+        q = c;
+        const int64_t a = cut.pair_of(q * cut.per_query), z = cut.pair_of((q + 1) * cut.per_query - 1);
+        g = static_cast<int>(a);
+        return z > a ? static_cast<int>(z - a) + 1 : 0;
+    }
 };
 
 // Joins the pieces of each cut query: out = sum_i exp2(lse_i - lse) rows_i.  A block takes one
@@ -745,16 +768,19 @@ struct Cuts {
 // fourth piece and add up in shared memory.  A few pieces are a matter of throughput, many of
 // latency, so the first loads do not wait for the log-sum-exps.
 constexpr int kJoinFirst = 4;
-template <int kGroups>
+template <int kGroups, typename CutsOf>
 __global__ void __launch_bounds__(128 * kGroups)
-    join_kernel(const AttentionParams p, const int32_t pairs, const __grid_constant__ Cuts cuts) {
+    join_kernel(const AttentionParams p, const int32_t pairs, const __grid_constant__ CutsOf cuts) {
     __shared__ float4 part[kGroups][kGroups > 1 ? 128 : 1];
     const int32_t c = blockIdx.x / p.num_heads;
     const int32_t head = blockIdx.x - c * p.num_heads;
-    const int g0 = cuts.first[c], n = cuts.pairs[c];
+    int64_t query;
+    int g0;
+    const int n = cuts.find(c, query, g0);
     const int d = threadIdx.x & 127, group = threadIdx.x >> 7;
     pdl_wait_previous();
     pdl_release_next();
+    if (n == 0) return;
     const float* const rows = static_cast<const float*>(p.workspace);
     const float* const lses = rows + 2 * static_cast<int64_t>(pairs) * p.num_heads * 512 + head;
     // the first piece ends its pair's run (slot 1), the others begin theirs (slot 0)
@@ -815,7 +841,7 @@ __global__ void __launch_bounds__(128 * kGroups)
     const float lse2 = sum == 0.0f ? -INFINITY : __fadd_rn(m, log2f(sum));
     const uint2 v = make_uint2(pack_bf16x2_rn(__fmul_rn(acc.x, inv), __fmul_rn(acc.y, inv)),
                                pack_bf16x2_rn(__fmul_rn(acc.z, inv), __fmul_rn(acc.w, inv)));
-    const int64_t at = static_cast<int64_t>(cuts.query[c]) * p.num_heads + head;
+    const int64_t at = query * p.num_heads + head;
     if (unwritten) {
         if (threadIdx.x == 0) p.lse[at] = __uint_as_float(kUnwritten);
         return;
@@ -1198,6 +1224,11 @@ cudaError_t make_cut(int64_t num_queries, int64_t topk, int32_t num_heads, Cut* 
         cut->each = each;
         cut->pairs = static_cast<int32_t>((num_queries + each - 1) / each);
     }
+    const int64_t run = cut->each > 0 ? cut->each * cut->per_query : (cut->total + pairs - 1) / pairs;
+    if (cut->per_query > kRunChunks && run > kRunChunks) {
+        cut->each = 0;
+        cut->pairs = static_cast<int32_t>(pairs * ((cut->total + pairs * kRunChunks - 1) / (pairs * kRunChunks)));
+    }
     return cudaSuccess;
 }
 
@@ -1270,13 +1301,19 @@ cudaError_t launch_sparse_attention(const AttentionParams& p, cudaStream_t strea
     e = launch_kernel(parted ? attend_kernel<true> : attend_kernel<false>, 2 * static_cast<int64_t>(cut.pairs),
                       kAttendThreads, kAttendSmem, stream, p.pdl, p, cut, q_map);
     if (e != cudaSuccess) return e;
-    Cuts cuts;
-    const int most = find_cuts(cut, &cuts);
-    if (cuts.n > 0) {
-        const int64_t blocks = static_cast<int64_t>(cuts.n) * p.num_heads;
-        e = most >= kManyPieces ? launch_kernel(join_kernel<4>, blocks, 512, 0, stream, p.pdl, p, cut.pairs, cuts)
-                                : launch_kernel(join_kernel<1>, blocks, 128, 0, stream, p.pdl, p, cut.pairs, cuts);
+    if (cut.pairs > kMaxPairs) {
+        const ManyCuts cuts = {cut};
+        e = launch_kernel(join_kernel<4, ManyCuts>, p.num_queries * p.num_heads, 512, 0, stream, p.pdl, p, cut.pairs, cuts);
         if (e != cudaSuccess) return e;
+    } else {
+        Cuts cuts;
+        const int most = find_cuts(cut, &cuts);
+        if (cuts.n > 0) {
+            const int64_t blocks = static_cast<int64_t>(cuts.n) * p.num_heads;
+            e = most >= kManyPieces ? launch_kernel(join_kernel<4, Cuts>, blocks, 512, 0, stream, p.pdl, p, cut.pairs, cuts)
+                                    : launch_kernel(join_kernel<1, Cuts>, blocks, 128, 0, stream, p.pdl, p, cut.pairs, cuts);
+            if (e != cudaSuccess) return e;
+        }
     }
     if (p.weights == nullptr || p.topk == 0) return e;
     const int n_pad = (p.num_heads + 15) / 16 * 16;   // columns of the product

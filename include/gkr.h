@@ -367,7 +367,9 @@ GKR_API gkr_status gkr_sparse_logits(const void *q, int32_t num_heads, const voi
  * rounded to bf16 (relative to a running maximum) for the value product.  Records' values below
  * 2^55 cannot overflow the accumulator, however many are listed (2^24 at most).  A probability
  * below 2^-142 of the row's largest may count as 0 (what values up to 2^9 make of it is below
- * bf16's smallest).  Results do not depend on the order of execution: every sum has a fixed order.
+ * bf16's smallest).  The hardware's sums are cut off and not rounded, so an accumulator sums at
+ * most 131072 records, and such runs are joined with fp32 roundings.  Results do not depend on the
+ * order of execution: every sum has a fixed order.
  * Should a wait give up (GKR_ERR_TIMEOUT), each row of out is either right or not written, and
  * the lse of one that is not is a NaN; the weights of a query with such a head are left as they
  * are, and any other entry has its weight added or is left.
